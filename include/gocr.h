@@ -351,6 +351,59 @@ int gocr_op_attention_ranges(int dtype, const void* q_hi, const void* q_lo, cons
  * GOCR_EINVAL for negative sizes, B < 1, or a null output. */
 int gocr_three_stream_ranges(int P, int N, int B, int32_t* lim, int32_t* lo2, int32_t* hi2, int32_t* pos);
 
+/* ---- training and scoring operators (device pointers) -------------------
+ *
+ * The two ends of a decoder's training step and its attention over packed
+ * sequences, forward (which also scores and prefills) and backward.  For all
+ * of them: row-major arrays, device memory of the current device, `stream` a
+ * stream of the current device (GOCR_EINVAL otherwise); operands aligned to 16
+ * bytes; nothing is allocated, kept between calls or synchronised, so a call
+ * can be captured into a graph; a workspace need not be cleared and belongs to
+ * one call at a time.  The same inputs give the same bits.  Outputs must not
+ * overlap inputs.  Zero rows (T = 0) are allowed: gradients of weights are
+ * then zero.  Errors: GOCR_EINVAL (null pointer, shape, alignment, stream),
+ * GOCR_ECAPACITY (workspace), GOCR_ECUDA (launch). */
+
+/* y[T, H] = scale * row(ids[t]), rounded once to dtype: row(id) is embed[id]
+ * for 0 <= id < V, mask_embed for id = -1 (the [M] row; zero when mask_embed
+ * is NULL), and zero for every other id (padding).  embed [V, H], mask_embed
+ * [H] and y in dtype, ids int32[T] (device).  H % 8 == 0. */
+int gocr_op_embed(int dtype, const void* embed, const void* mask_embed, const int32_t* ids, void* y, int T, int H,
+                  int V, float scale, void* stream);
+
+/* Gradient of gocr_op_embed: d_embed[V, H] (dense: rows of tokens that do not
+ * occur are zero) and d_mask[H] (NULL: not wanted) from dy[T, H], all in
+ * dtype.  Positions are sorted by token; a row's sum runs over its positions
+ * in increasing order in pieces of 16, in fp32, and is rounded once. */
+size_t gocr_op_embed_backward_workspace(int T, int H);
+int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* d_embed, void* d_mask, int T, int H,
+                           int V, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy of a linear head: z = x w^T with x [T, H] and w [V, H]
+ * in bf16 (fp32 sums), lse[t] = log sum_v exp z[t, v], loss[t] = lse[t] -
+ * z[t, labels[t]].  A label outside 0..V-1 marks a row without a target: its
+ * loss is zero (lse is written all the same).  The logits are not stored.  H %
+ * 8 == 0, any V. */
+size_t gocr_op_linear_ce_workspace(int T, int V);
+int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,
+                      int H, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of sum_t dloss[t] loss[t]: dx[T, H] and dw[V, H] in bf16, from the
+ * forward call's lse.  dloss[t] is the row's weight in the training loss (of a
+ * clean or a corrupted stream's mean, say); rows without a target add nothing
+ * (their dloss and lse are not read).  z is computed again in pieces of the
+ * vocabulary; (softmax - one-hot) dloss is rounded to bf16 for the products,
+ * whose sums are in fp32. */
+size_t gocr_op_linear_ce_backward_workspace(int T, int V, int H);
+int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w, const int32_t* labels,
+                               const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Synchronises `stream` and reports whether a kernel of these operators on the
+ * current device gave up a wait since the last report (GOCR_EDEVICE; the
+ * outputs of such a call are not valid). */
+int gocr_op_status(void* stream);
+
 /* ---- allocation-free GEMM ------------------------------------------------ */
 
 /* Bytes of the device scratch array behind gocr_op_linear_static (per GPU). */

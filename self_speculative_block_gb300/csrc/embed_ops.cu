@@ -1,0 +1,417 @@
+// Token embedding and its gradient, for training and scoring.
+//
+//   y_t  = s * row(id_t)      row: E[id], the [M] row for id = -1, else zero
+//   dE_v = s * sum of dy_t over id_t = v;  d[M] likewise
+//
+// Both are bound by memory: the forward call reads the distinct rows and
+// writes T rows, the backward call reads T rows of dy and writes the dense
+// V x H gradient, which is most of its bytes.  The sum of a row runs over the
+// token's positions in increasing order, in fixed pieces, in fp32 and without
+// atomics, so the gradient's bits are the same on every call.
+//
+// Backward, three launches:
+//   sort  a cluster of SORT_CTAS CTAs sorts the positions by token (stable
+//         radix sort, digits of at most 9 bits, counts exchanged over
+//         distributed shared memory), while the other CTAs of the launch write
+//         the zeros of the whole gradient: the sort's latency hides behind the
+//         launch's V x H writes;
+//   sum   a CTA sums the runs of equal tokens in a piece of PIECE sorted
+//         positions; a run inside the piece is written, a run that crosses a
+//         border of the piece leaves an fp32 partial row;
+//   join  the piece where a crossing run begins adds up its partial rows.
+// A frequent token ([M] above all) is one run over many pieces, so no CTA ever
+// walks more than PIECE rows of dy.
+#include "../../include/gocr.h"
+#include "kernels.cuh"
+
+#include <cooperative_groups.h>
+
+using namespace gocr;
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int SORT_CTAS = 8;
+constexpr int SORT_THREADS = 512;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int MAX_DIGITS = 512;
+constexpr int PIECE = 16;
+
+// 16 bytes of a row in fp32
+template <typename T> struct Vec;
+template <> struct Vec<bf16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void load(const bf16* p, float* v) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(bf16* p, const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(const float* p, float* v) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+
+// One warp per row.
+template <typename T>
+__global__ void __launch_bounds__(256) embed_rows_kernel(const T* __restrict__ embed, const T* __restrict__ mask,
+                                                         const int* __restrict__ ids, T* __restrict__ y, int rows,
+                                                         int H, int V, float scale) {
+  constexpr int N = Vec<T>::N;
+  const int lane = threadIdx.x & 31;
+  const long long nw = (long long)gridDim.x * 8;
+  for (long long t = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); t < rows; t += nw) {
+    const int id = ids[t];
+    const T* src = (unsigned)id < (unsigned)V ? embed + (size_t)id * H : (id == TOK_MASK ? mask : nullptr);
+    T* dst = y + (size_t)t * H;
+#pragma unroll 4
+    for (int c = lane * N; c < H; c += 32 * N) {
+      float v[N];
+      if (src) {
+        Vec<T>::load(src + c, v);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= scale;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+      }
+      Vec<T>::store(dst + c, v);
+    }
+  }
+}
+
+// Sort key of a position: its token, V for [M], V + 1 for a row without a
+// gradient (an id outside the table, or [M] when no [M] gradient is wanted).
+__device__ __forceinline__ int key_of(int id, int V, bool mask) {
+  return (unsigned)id < (unsigned)V ? id : (id == TOK_MASK && mask ? V : V + 1);
+}
+
+struct SortArgs {
+  const int* ids;
+  int* key[2];   // [T] sorted keys; the last pass's output is key[1]
+  int* pos[2];   // [T] positions in that order
+  int T, V, mask, passes, digit_bits;
+  void* d_embed; size_t embed_bytes;  // zeroed by the launch's other CTAs (multiples of 16 bytes)
+  void* d_mask; size_t mask_bytes;
+};
+
+__global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(SortArgs a) {
+  if (blockIdx.x >= SORT_CTAS) {  // whole clusters
+    const size_t n = a.embed_bytes / 16, step = (size_t)(gridDim.x - SORT_CTAS) * SORT_THREADS;
+    const size_t first = (size_t)(blockIdx.x - SORT_CTAS) * SORT_THREADS + threadIdx.x;
+    uint4* d = reinterpret_cast<uint4*>(a.d_embed);
+    for (size_t i = first; i < n; i += step) d[i] = make_uint4(0, 0, 0, 0);
+    if (a.d_mask) {
+      uint4* m = reinterpret_cast<uint4*>(a.d_mask);
+      for (size_t i = first; i < a.mask_bytes / 16; i += step) m[i] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  __shared__ int cnt[SORT_WARPS][MAX_DIGITS];  // keys of (warp, digit), then the warp's next place
+  __shared__ int cta_cnt[MAX_DIGITS];
+  __shared__ int scan[MAX_DIGITS];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int D = 1 << a.digit_bits;
+  // warp w of CTA c owns the positions [(16 c + w) share, + share): the order
+  // of (CTA, warp, position) is the order of the positions
+  const int share = ((a.T + SORT_CTAS * SORT_WARPS - 1) / (SORT_CTAS * SORT_WARPS) + 31) & ~31;
+  const long long lo_ = (long long)(rank * SORT_WARPS + warp) * share;
+  const int lo = lo_ < a.T ? (int)lo_ : a.T;
+  const int hi = lo_ + share < a.T ? (int)(lo_ + share) : a.T;
+  const unsigned below = (1u << lane) - 1u;
+  for (int p = 0; p < a.passes; ++p) {
+    const int shift = p * a.digit_bits;
+    // the output of pass p is buffer (passes - p) & 1, so that the last one is 1
+    const int* kin = a.key[(a.passes - p + 1) & 1];
+    const int* pin = a.pos[(a.passes - p + 1) & 1];
+    int* kout = a.key[(a.passes - p) & 1];
+    int* pout = a.pos[(a.passes - p) & 1];
+    for (int d = lane; d < D; d += 32) cnt[warp][d] = 0;
+    __syncwarp();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      const int k = in ? (p == 0 ? key_of(a.ids[i], a.V, a.mask) : __ldcg(kin + i)) : 0;
+      const int dg = in ? (k >> shift) & (D - 1) : D;
+      const unsigned same = __match_any_sync(0xffffffffu, dg);
+      if (in && (same & below) == 0) cnt[warp][dg] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int d = tid; d < D; d += SORT_THREADS) {  // before warp w in this CTA
+      int s = 0;
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const int c = cnt[w][d];
+        cnt[w][d] = s;
+        s += c;
+      }
+      cta_cnt[d] = s;
+    }
+    cluster.sync();
+    int before = 0, total = 0;  // digit tid: keys of the CTAs before this one, of all CTAs
+    if (tid < D)
+      for (int c = 0; c < SORT_CTAS; ++c) {
+        const int v = *cluster.map_shared_rank(&cta_cnt[tid], c);
+        if (c < rank) before += v;
+        total += v;
+      }
+    scan[tid] = tid < D ? total : 0;  // SORT_THREADS = MAX_DIGITS
+    __syncthreads();
+    for (int o = 1; o < MAX_DIGITS; o <<= 1) {
+      const int v = tid >= o ? scan[tid - o] : 0;
+      __syncthreads();
+      scan[tid] += v;
+      __syncthreads();
+    }
+    if (tid < D) {
+      const int base = scan[tid] - total + before;
+      for (int w = 0; w < SORT_WARPS; ++w) cnt[w][tid] += base;
+    }
+    __syncthreads();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      const int k = in ? (p == 0 ? key_of(a.ids[i], a.V, a.mask) : __ldcg(kin + i)) : 0;
+      const int at = in ? (p == 0 ? i : __ldcg(pin + i)) : 0;
+      const int dg = in ? (k >> shift) & (D - 1) : D;
+      const unsigned same = __match_any_sync(0xffffffffu, dg);
+      const int mine = __popc(same & below);
+      int place = 0;
+      if (in) place = cnt[warp][dg] + mine;
+      __syncwarp();
+      if (in && mine == 0) cnt[warp][dg] += __popc(same);
+      __syncwarp();
+      if (in) {
+        kout[place] = k;
+        pout[place] = at;
+      }
+    }
+    __threadfence();
+    cluster.sync();  // the pass's output, and every read of cta_cnt, is complete
+  }
+}
+
+struct SumArgs {
+  const void* dy;
+  const int* key;
+  const int* pos;
+  void* d_embed;
+  void* d_mask;
+  float* part;  // [pieces][2][H]: the run that comes into the piece, the run that goes out of it
+  int T, H, V;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ T* grad_row(const SumArgs& a, int key) {
+  return key < a.V ? reinterpret_cast<T*>(a.d_embed) + (size_t)key * a.H
+                   : (key == a.V ? reinterpret_cast<T*>(a.d_mask) : nullptr);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
+  constexpr int N = Vec<T>::N;
+  __shared__ int keys[PIECE + 2];  // keys[1 + i] of the piece's positions, and its neighbours'
+  __shared__ int poss[PIECE];
+  const int b = blockIdx.x * PIECE, n = min(PIECE, a.T - b);
+  for (int i = threadIdx.x; i < PIECE + 2; i += blockDim.x) {
+    const int at = b + i - 1;
+    keys[i] = at >= 0 && at < a.T ? a.key[at] : -1;
+    if (i < PIECE) poss[i] = b + i < a.T ? a.pos[b + i] : 0;
+  }
+  __syncthreads();
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
+  if (c >= a.H) return;
+  const T* dy = reinterpret_cast<const T*>(a.dy) + c;
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+  bool from_before = keys[0] == keys[1];
+  constexpr int B = 8;  // rows fetched at a time
+  for (int i0 = 0; i0 < n; i0 += B) {
+    float v[B][N];
+#pragma unroll
+    for (int u = 0; u < B; ++u)
+      if (i0 + u < n && keys[1 + i0 + u] <= a.V) Vec<T>::load(dy + (size_t)poss[i0 + u] * a.H, v[u]);
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      const int i = i0 + u;
+      if (i >= n) break;
+      const int k = keys[1 + i];
+      if (k > a.V) return;  // rows without a gradient come last
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] += v[u][j];
+      const bool goes_on = keys[2 + i] == k;
+      if (goes_on && i + 1 < n) continue;
+      if (from_before || goes_on) {
+        // a run that comes in (and perhaps goes on) is the first partial, a
+        // run that begins here and goes on the second
+        float* p = a.part + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * a.H + c;
+#pragma unroll
+        for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] *= a.scale;
+        Vec<T>::store(grad_row<T>(a, k) + c, acc);
+      }
+      from_before = false;
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a) {
+  __shared__ int s_last;  // the last piece of the run
+  const int b = blockIdx.x * PIECE, e = b + PIECE;
+  if (e >= a.T) return;  // the last piece has no run that goes on
+  const int k = a.key[e - 1];
+  if (k > a.V || a.key[e] != k) return;
+  if (b > 0 && a.key[b - 1] == k) return;  // the run began before this piece
+  const int pieces = (a.T + PIECE - 1) / PIECE;
+  if (threadIdx.x == 0) s_last = 0x7fffffff;
+  __syncthreads();
+  for (int j0 = blockIdx.x + 1; j0 < pieces; j0 += blockDim.x) {
+    const int j = j0 + threadIdx.x;
+    // the run ends in piece j when the position after the piece is not its own
+    if (j < pieces && ((j + 1) * (long long)PIECE >= a.T || a.key[(j + 1) * PIECE] != k)) atomicMin(&s_last, j);
+    __syncthreads();
+    if (s_last != 0x7fffffff) break;
+    __syncthreads();
+  }
+  const int last = s_last;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
+  if (c >= a.H) return;
+  float4 s = *reinterpret_cast<const float4*>(a.part + ((size_t)blockIdx.x * 2 + 1) * a.H + c);
+#pragma unroll 8
+  for (int j = blockIdx.x + 1; j <= last; ++j) {
+    const float4 v = *reinterpret_cast<const float4*>(a.part + (size_t)j * 2 * a.H + c);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  T* d = grad_row<T>(a, k) + c;
+  d[0] = from_f32<T>(s.x * a.scale);
+  d[1] = from_f32<T>(s.y * a.scale);
+  d[2] = from_f32<T>(s.z * a.scale);
+  d[3] = from_f32<T>(s.w * a.scale);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t sort_bytes(int T) { return 4 * up256((size_t)T * 4); }
+
+int check_shape(int dtype, int T, int H, int V) {
+  if (dtype != GOCR_DTYPE_F32 && dtype != GOCR_DTYPE_BF16) return op_fail(GOCR_EINVAL, "bad dtype");
+  if (T < 0 || T > (1 << 28) || H < 8 || H % 8 || H > (1 << 20) || V < 1 || V > (1 << 28))
+    return op_fail(GOCR_EINVAL, "bad shape T=%d H=%d V=%d", T, H, V);
+  return GOCR_OK;
+}
+
+template <typename T>
+int embed_backward(const SortArgs& so, const SumArgs& su, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  // the clusters past the first write zeros: two CTAs per SM
+  const size_t fill = (so.embed_bytes / 16 + SORT_THREADS * 4 - 1) / (SORT_THREADS * 4);
+  const size_t most = 2 * SM_COUNT - SORT_CTAS;
+  const unsigned ctas = (unsigned)(fill < most ? fill : most);
+  cfg.gridDim = dim3(SORT_CTAS + (ctas + SORT_CTAS - 1) / SORT_CTAS * SORT_CTAS);
+  cfg.blockDim = dim3(SORT_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = SORT_CTAS;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, embed_sort_kernel, so);
+  if (int rc = op_launched("embedding sort")) return rc;
+  if (!su.T) return GOCR_OK;
+  const unsigned pieces = (unsigned)((su.T + PIECE - 1) / PIECE);
+  const int vecs = su.H / Vec<T>::N;
+  const int th = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
+  embed_sum_kernel<T><<<dim3(pieces, (vecs + th - 1) / th), th, 0, s>>>(su);
+  if (int rc = op_launched("embedding sum")) return rc;
+  if (pieces > 1) {
+    const int v4 = su.H / 4, tj = v4 >= 256 ? 256 : (v4 + 31) / 32 * 32;
+    embed_join_kernel<T><<<dim3(pieces - 1, (v4 + tj - 1) / tj), tj, 0, s>>>(su);
+    return op_launched("embedding join");
+  }
+  return GOCR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gocr_op_embed(int dtype, const void* embed, const void* mask_embed, const int32_t* ids, void* y, int T, int H,
+                  int V, float scale, void* stream) {
+  if (int rc = check_shape(dtype, T, H, V)) return rc;
+  if (!embed || (T && (!ids || !y))) return op_fail(GOCR_EINVAL, "null pointer");
+  if (((uintptr_t)embed | (uintptr_t)mask_embed | (uintptr_t)y) & 15)
+    return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (int rc = op_stream_check(s)) return rc;
+  if (!T) return GOCR_OK;
+  const int grid = T <= 8 * 8 * SM_COUNT ? (T + 7) / 8 : 8 * SM_COUNT;
+  if (dtype == GOCR_DTYPE_BF16)
+    embed_rows_kernel<bf16><<<grid, 256, 0, s>>>((const bf16*)embed, (const bf16*)mask_embed, ids, (bf16*)y, T, H, V, scale);
+  else
+    embed_rows_kernel<float><<<grid, 256, 0, s>>>((const float*)embed, (const float*)mask_embed, ids, (float*)y, T, H, V, scale);
+  return op_launched("embedding");
+}
+
+size_t gocr_op_embed_backward_workspace(int T, int H) {
+  if (T < 0 || H < 1) return 0;
+  return sort_bytes(T) + (size_t)((T + PIECE - 1) / PIECE) * 2 * H * 4 + 256;
+}
+
+int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* d_embed, void* d_mask, int T, int H,
+                           int V, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_shape(dtype, T, H, V)) return rc;
+  if (!d_embed || !workspace || (T && (!dy || !ids))) return op_fail(GOCR_EINVAL, "null pointer");
+  if (((uintptr_t)dy | (uintptr_t)d_embed | (uintptr_t)d_mask | (uintptr_t)workspace) & 15)
+    return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if (workspace_bytes < gocr_op_embed_backward_workspace(T, H)) return op_fail(GOCR_ECAPACITY, "workspace too small");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (int rc = op_stream_check(s)) return rc;
+  const size_t es = dtype == GOCR_DTYPE_BF16 ? 2 : 4;
+  SortArgs so{};
+  char* ws = (char*)workspace;
+  const size_t arr = up256((size_t)T * 4);
+  so.ids = ids;
+  for (int i = 0; i < 2; ++i) {
+    so.key[i] = (int*)(ws + i * arr);
+    so.pos[i] = (int*)(ws + (2 + i) * arr);
+  }
+  so.T = T; so.V = V; so.mask = d_mask != nullptr;
+  int bits = 1;
+  while ((1ll << bits) < (long long)V + 2) ++bits;
+  so.passes = (bits + 8) / 9;
+  so.digit_bits = (bits + so.passes - 1) / so.passes;
+  so.d_embed = d_embed; so.embed_bytes = (size_t)V * H * es;
+  so.d_mask = d_mask; so.mask_bytes = (size_t)H * es;
+  SumArgs su{dy, so.key[1], so.pos[1], d_embed, d_mask, (float*)(ws + 4 * arr), T, H, V, scale};
+  return dtype == GOCR_DTYPE_BF16 ? embed_backward<bf16>(so, su, s) : embed_backward<float>(so, su, s);
+}
+
+}  // extern "C"

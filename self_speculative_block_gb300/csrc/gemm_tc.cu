@@ -121,6 +121,20 @@ bool encode_tmap_bf16(void* out, const void* ptr, int rows, int cols, int box_ro
   return tmap_2d(reinterpret_cast<CUtensorMap*>(out), ptr, rows, cols, box_rows);
 }
 
+bool encode_tmap(void* out, const void* ptr, bool f32, int rank, const unsigned long long* dims,
+                 const unsigned long long* strides, const unsigned* box) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!encoder()) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; }
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return g_encode(reinterpret_cast<CUtensorMap*>(out),
+                  f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                  const_cast<void*>(ptr), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shared memory: the ring (>= stages * (A tile + B tile), and, after the
 // mainloop, the partial tile, the reduced rows and the epilogue scratch at
 // the offsets of gemm_y_layout), in the early exchange layout the peers'

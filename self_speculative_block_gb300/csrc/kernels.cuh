@@ -97,6 +97,11 @@ int gemm_kgroup(int N, int K, bool two_groups);
 // 128-byte-swizzled TMA descriptor (CUtensorMap, 128 bytes at `out`) of a
 // row-major bf16 matrix [rows, cols] with boxes of 64 columns x box_rows.
 bool encode_tmap_bf16(void* out, const void* ptr, int rows, int cols, int box_rows);
+// 128-byte-swizzled TMA descriptor of a tensor of 2 or 3 dimensions, bf16 or
+// fp32 (dims and box innermost first, strides in bytes of dimension 1 and 2;
+// box[0] x element size = 128 bytes).  Encoded anew at each call.
+bool encode_tmap(void* out, const void* ptr, bool f32, int rank, const unsigned long long* dims,
+                 const unsigned long long* strides, const unsigned* box);
 int gemm_kchunk(int N, int K);
 size_t gemm_ws_floats(int T, int N, int K);
 int gemm_counter_ints(int T, int N);
@@ -251,6 +256,18 @@ __device__ __forceinline__ void trace_at(const Args& a, int word, int slot0 = 0)
 
 // Library-level error message returned by gocr_last_error(NULL).
 void set_lib_error(const char* msg);
+
+// Host side of the single-kernel entry points in files of their own.
+// op_fail records a message and returns `code`; op_stream_check refuses a
+// stream of another device than the current one (the kernels' attributes are
+// set on the current device); op_launched turns the last launch's error into a
+// status.
+int op_fail(int code, const char* fmt, ...);
+int op_stream_check(cudaStream_t s);
+int op_launched(const char* what);
+// Error word of the file's kernels with bounded waits (a DevErr; read and
+// cleared on an idle stream).
+cudaError_t take_linear_ce_error(int* out);
 
 // Ask for the largest shared-memory carveout for kernel `fn` on the current
 // device (once).  Every kernel of the decode path runs with the same SM

@@ -36,7 +36,10 @@ EXPORTS = ("gocr_create", "gocr_prefill", "gocr_decode", "gocr_decode_batch", "g
            "gocr_set_draft_override", "gocr_debug_forward", "gocr_debug_forward_batch", "gocr_read_kv", "gocr_get_state",
            "gocr_get_option", "gocr_read_trace", "gocr_last_error", "gocr_free",
            "gocr_op_linear_workspace", "gocr_op_linear", "gocr_op_linear_planes", "gocr_op_attention",
-           "gocr_op_linear_static", "gocr_op_attention_ranges", "gocr_three_stream_ranges")
+           "gocr_op_linear_static", "gocr_op_attention_ranges", "gocr_three_stream_ranges",
+           "gocr_op_embed", "gocr_op_embed_backward_workspace", "gocr_op_embed_backward",
+           "gocr_op_linear_ce_workspace", "gocr_op_linear_ce", "gocr_op_linear_ce_backward_workspace",
+           "gocr_op_linear_ce_backward", "gocr_op_status")
 
 
 class GocrError(RuntimeError):
@@ -93,7 +96,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"libgocr.so is not built ({path}); run the package build first")
     lib = ctypes.CDLL(path)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     P32 = ctypes.POINTER(ctypes.c_int32)
     sig = {
         "gocr_create": (i32, [ctypes.POINTER(Config), ctypes.POINTER(Weights), vp, ALLOC_FN, FREE_FN, vp,
@@ -120,6 +123,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gocr_op_linear_static": (i32, [i32, vp, vp, vp, i32, i32, i32, vp]),
         "gocr_op_attention_ranges": (i32, [i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]),
         "gocr_three_stream_ranges": (i32, [i32, i32, i32, P32, P32, P32, P32]),
+        "gocr_op_embed": (i32, [i32, vp, vp, vp, vp, i32, i32, i32, f32, vp]),
+        "gocr_op_embed_backward_workspace": (sz, [i32, i32]),
+        "gocr_op_embed_backward": (i32, [i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, sz, vp]),
+        "gocr_op_linear_ce_workspace": (sz, [i32, i32]),
+        "gocr_op_linear_ce": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
+        "gocr_op_linear_ce_backward_workspace": (sz, [i32, i32, i32]),
+        "gocr_op_linear_ce_backward": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
+        "gocr_op_status": (i32, [vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -453,3 +464,122 @@ def op_attention(q, kc, vc, lim, dtype: int, lo2=None, hi2=None):
     _check(lib.gocr_op_attention_ranges(dtype, ptr(qh), ptr(ql), ptr(kh), ptr(kl), ptr(vh), ptr(vl), o.data_ptr(),
                                         lim.data_ptr(), ptr(lo2), ptr(hi2), T, Hq, Hkv, d, cap, stream))
     return o
+
+
+# ----------------------------------------------------------------------------
+# training and scoring operators
+# ----------------------------------------------------------------------------
+
+def _want(name: str, t, shape, *dtypes, device=None):
+    """Check one operand: a contiguous CUDA tensor of this shape (None = any size) and one of the dtypes."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be [{', '.join('*' if w is None else str(w) for w in shape)}], got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    _on_device(name, t, device)
+
+
+def _on_device(name: str, t, device):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands are on {device}")
+
+
+def _workspace(ws, need: int, device):
+    torch = _torch()
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _want("workspace", ws, (None,), torch.uint8, device=device)
+    return ws
+
+
+def _stream(device):
+    return _torch().cuda.current_stream(device).cuda_stream
+
+
+def op_embed(ids, embed, mask_embed=None, scale: float = 1.0):
+    """y[T, H] = scale * the rows of embed [V, H] (bf16 or fp32) that ids (int32
+    [T]) name; id -1 is the [M] row mask_embed [H] (zero without one), any
+    other id outside the table a row of zeros."""
+    torch = _torch()
+    _want("embed", embed, (None, None), torch.bfloat16, torch.float32)
+    dev, (V, H) = embed.device, embed.shape
+    _want("ids", ids, (None,), torch.int32, device=dev)
+    if mask_embed is not None:
+        _want("mask_embed", mask_embed, (H,), embed.dtype, device=dev)
+    T = ids.shape[0]
+    with torch.cuda.device(dev):
+        y = torch.empty((T, H), dtype=embed.dtype, device=dev)
+        _check(load().gocr_op_embed(_dt(embed), embed.data_ptr(), mask_embed.data_ptr() if mask_embed is not None else None,
+                                    ids.data_ptr(), y.data_ptr(), T, H, V, scale, _stream(dev)))
+    return y
+
+
+def op_embed_backward(dy, ids, vocab: int, scale: float = 1.0, mask: bool = False, workspace=None):
+    """Gradient of op_embed from dy [T, H]: (d_embed [vocab, H], d_mask [H] when
+    mask else None), dense, in dy's dtype, fp32 sums in a fixed order."""
+    torch = _torch()
+    lib = load()
+    _want("dy", dy, (None, None), torch.bfloat16, torch.float32)
+    dev, (T, H) = dy.device, dy.shape
+    _want("ids", ids, (T,), torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        d_embed = torch.empty((vocab, H), dtype=dy.dtype, device=dev)
+        d_mask = torch.empty((H,), dtype=dy.dtype, device=dev) if mask else None
+        ws = _workspace(workspace, lib.gocr_op_embed_backward_workspace(T, H), dev)
+        _check(lib.gocr_op_embed_backward(_dt(dy), dy.data_ptr(), ids.data_ptr(), d_embed.data_ptr(),
+                                          d_mask.data_ptr() if mask else None, T, H, vocab, scale, ws.data_ptr(),
+                                          ws.numel(), _stream(dev)))
+    return d_embed, d_mask
+
+
+def op_linear_ce(x, w, labels, workspace=None):
+    """(loss [T], lse [T]) fp32 of the softmax cross entropy of x w^T: x [T, H]
+    and w [V, H] bf16, labels int32 [T] (outside 0..V-1: no target, loss 0).
+    The logits are not stored."""
+    torch = _torch()
+    lib = load()
+    _want("x", x, (None, None), torch.bfloat16)
+    dev, (T, H) = x.device, x.shape
+    _want("w", w, (None, H), torch.bfloat16, device=dev)
+    _want("labels", labels, (T,), torch.int32, device=dev)
+    V = w.shape[0]
+    with torch.cuda.device(dev):
+        loss = torch.empty((T,), dtype=torch.float32, device=dev)
+        lse = torch.empty((T,), dtype=torch.float32, device=dev)
+        ws = _workspace(workspace, lib.gocr_op_linear_ce_workspace(T, V), dev)
+        _check(lib.gocr_op_linear_ce(x.data_ptr(), w.data_ptr(), labels.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                     T, V, H, ws.data_ptr(), ws.numel(), _stream(dev)))
+    return loss, lse
+
+
+def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None):
+    """(dx [T, H], dw [V, H]) bf16: the gradient of sum(dloss * loss) of
+    op_linear_ce, from its lse; dloss fp32 [T] holds the rows' weights."""
+    torch = _torch()
+    lib = load()
+    _want("x", x, (None, None), torch.bfloat16)
+    dev, (T, H) = x.device, x.shape
+    _want("w", w, (None, H), torch.bfloat16, device=dev)
+    _want("labels", labels, (T,), torch.int32, device=dev)
+    _want("dloss", dloss, (T,), torch.float32, device=dev)
+    _want("lse", lse, (T,), torch.float32, device=dev)
+    V = w.shape[0]
+    with torch.cuda.device(dev):
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        ws = _workspace(workspace, lib.gocr_op_linear_ce_backward_workspace(T, V, H), dev)
+        _check(lib.gocr_op_linear_ce_backward(dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
+                                              lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(),
+                                              ws.numel(), _stream(dev)))
+    return dx, dw
+
+
+def op_status(device="cuda") -> None:
+    """Wait for the device's current stream; raise when a kernel of these
+    operators gave up a wait since the last call."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        _check(load().gocr_op_status(_stream(torch.cuda.current_device())))
