@@ -379,6 +379,33 @@ size_t gocr_op_embed_backward_workspace(int T, int H);
 int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* d_embed, void* d_mask, int T, int H,
                            int V, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Causal attention over packed sequences with grouped heads, bf16: sequence s
+ * is rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 (device int32[n_seq + 1],
+ * non-decreasing, within 0..T; empty sequences allowed; the values stay on the
+ * device), and row i of a sequence reads its rows 0..i: o = softmax(scale q
+ * k^T) v, lse = the log of the row's sum of exponentials.  q [T, Hq, d] with
+ * rows ldq elements apart, k and v [T, Hkv, d] with rows ldk and ldv apart (so
+ * the three may be column ranges of one fused projection; pitches % 8 == 0);
+ * o [T, Hq, d] bf16 and lse [Hq, T] fp32 dense.  d 64 or 128, Hq % Hkv == 0,
+ * scale > 0.  Rows that belong to no sequence are not read into any result,
+ * whatever they hold, and their o and lse are left as they were; nothing of
+ * one sequence reaches another, non-finite values included.  Within a
+ * sequence, a non-finite v or do may reach the other rows of its block of 128. */
+int gocr_op_attention_packed(const void* q, const void* k, const void* v, void* o, float* lse,
+                             const int32_t* cu_seqlens, int n_seq, int T, int Hq, int Hkv, int d, long long ldq,
+                             long long ldk, long long ldv, float scale, void* stream);
+
+/* Gradient of gocr_op_attention_packed from d_o [T, Hq, d] and the forward
+ * call's o and lse: dq [T, Hq, d], dk and dv [T, Hkv, d] bf16, dense (rows that
+ * belong to no sequence are left as they were).  dk and dv sum over the q
+ * heads of the group; all sums are in fp32, in a fixed order. */
+size_t gocr_op_attention_packed_backward_workspace(int T, int Hq);
+int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void* k, const void* v, const void* o,
+                                      const float* lse, const int32_t* cu_seqlens, void* dq, void* dk, void* dv,
+                                      int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk,
+                                      long long ldv, float scale, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
 /* Softmax cross entropy of a linear head: z = x w^T with x [T, H] and w [V, H]
  * in bf16 (fp32 sums), lse[t] = log sum_v exp z[t, v], loss[t] = lse[t] -
  * z[t, labels[t]].  A label outside 0..V-1 marks a row without a target: its

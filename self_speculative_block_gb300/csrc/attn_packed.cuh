@@ -1,0 +1,119 @@
+// Shared parts of the packed-sequence attention kernels (forward in
+// attn_packed.cu, backward in attn_packed_bwd.cu).
+//
+// Rows of several sequences lie one after the other: sequence s is rows
+// cu[s] .. cu[s + 1] - 1 of q, k, v and o.  Row i of a sequence reads rows
+// 0 .. i of the same sequence.  q head h reads k/v head h / (Hq / Hkv).
+#pragma once
+#include "kernels.cuh"
+#include "tc.cuh"
+
+#include <cuda.h>
+
+namespace gocr {
+namespace packed {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// 2^x of the special-function unit (relative error 2^-22; subnormal results
+// become zero, which is below every rounding here).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct Block {
+  int row0;   // first row of the sequence
+  int len;    // its rows
+  int at;     // first row (within the sequence) of this block of `size` rows
+};
+
+// The b-th block of `size` rows over all sequences, in a sequence's order or
+// its last block first (the order of falling work: the last query rows read
+// the most keys, the first keys are read by the most rows); one warp, all
+// lanes get the answer.  len = 0: there is no such block.  Whatever cu holds,
+// the rows stay within 0 .. T - 1.
+template <bool LAST_FIRST>
+__device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int size, int b) {
+  const int lane = threadIdx.x & 31;
+  Block r{0, 0, 0};
+  int seen = 0;
+  for (int s0 = 0; s0 < n_seq; s0 += 32) {
+    const int s = s0 + lane;
+    int lo = 0, len = 0;
+    if (s < n_seq) {
+      lo = min(max(cu[s], 0), T);
+      len = max(min(cu[s + 1], T) - lo, 0);
+    }
+    const int n = (len + size - 1) / size;
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, seen + inc > b);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      const int i = b - (seen + inc - n);
+      r.row0 = __shfl_sync(0xffffffffu, lo, src);
+      r.len = __shfl_sync(0xffffffffu, len, src);
+      r.at = __shfl_sync(0xffffffffu, (LAST_FIRST ? n - 1 - i : i) * size, src);
+      return r;
+    }
+    seen += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return r;
+}
+
+// Most blocks of `size` rows that n_seq sequences of T rows in all can have.
+inline long long max_blocks(int n_seq, int T, int size) { return (long long)n_seq + T / size; }
+
+// A tile of 128 rows x D bf16 in shared memory: D / 64 boxes of 128 rows x 128
+// bytes, swizzled, as TMA writes them.
+template <int D> constexpr int TILE_BYTES = 128 * D * 2;
+constexpr int BOX_BYTES = 128 * 128;
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const void* map, int head, int row, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(dst + c * BOX_BYTES, map, c * 64, head, row, bar);
+}
+
+// Rows n .. 127 of a tile become zero: they belong to another sequence or to
+// nobody and may hold anything, and a product that runs over rows would carry
+// their NaN or infinity into this sequence.  One warp.
+template <int D> __device__ __forceinline__ void zero_rows(uint8_t* tile, int n) {
+  const int lane = threadIdx.x & 31;
+  for (int i = n * 8 + lane; i < 128 * 8; i += 32)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) *reinterpret_cast<uint4*>(tile + c * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// A operand step ks (16 elements of D) of a K-major tile, B operand likewise;
+// step ks (16 rows) of a tile read N-major (its D columns are N, its rows K).
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int ks) {
+  return tc::sdesc_sw128(tile + (ks >> 2) * BOX_BYTES + (ks & 3) * 32);
+}
+__device__ __forceinline__ uint64_t desc_n(uint32_t tile, int ks) {
+  return tc::sdesc_sw128_mn(tile + ks * 2048, BOX_BYTES);
+}
+
+// 3-D TMA map over [T, heads, D] bf16 rows `ld` elements apart: boxes of 64
+// columns x 1 head x 128 rows.
+inline bool map_rows(CUtensorMap* m, const void* p, int T, int heads, int D, long long ld) {
+  const unsigned long long dims[3] = {(unsigned long long)D, (unsigned long long)heads, (unsigned long long)T};
+  const unsigned long long st[2] = {(unsigned long long)D * 2, (unsigned long long)ld * 2};
+  const unsigned box[3] = {64, 1, 128};
+  return encode_tmap(m, p, false, 3, dims, st, box);
+}
+
+}  // namespace packed
+}  // namespace gocr

@@ -1,0 +1,592 @@
+// Causal attention over packed sequences with grouped heads, backward.
+//
+//   P_ij = exp(c q_i . k_j - lse_i)      delta_i = do_i . o_i
+//   dP_ij = do_i . v_j                   dS_ij = P_ij (dP_ij - delta_i)
+//   dv_j = sum_i P_ij do_i               dk_j = c sum_i dS_ij q_i      dq_i = c sum_j dS_ij k_j
+//
+// dk and dv also sum over the q heads of the group.  Three launches: delta;
+// then dk and dv, one CTA per (128 keys, k/v head) walking the q heads and the
+// query blocks that see the keys; then dq, one CTA per (128 query rows, q
+// head) walking the keys.  S and dP are computed twice, seven products of 128
+// x 128 x D a block pair instead of five; in return every sum has one owner:
+// no atomics, no fp32 dq in memory, and the same bits on every call.
+//
+// All products run on tcgen05 with fp32 accumulators in tensor memory.  The
+// dk/dv kernel works on the transposed blocks (a lane is a key): P^T and dS^T
+// (bf16, relative 2^-8, as the tensor cores take them) go back to tensor memory
+// over the scores they came from and are the A operands of dV += P^T dO and dK
+// += dS^T Q; dO and Q serve as they lie, K-major for S^T and dP^T and N-major
+// here.  The dq kernel has lanes of query rows and dQ += dS K.  Eight warps do
+// the elementwise work, two to a lane quarter with 64 columns each; it
+// overlaps the products: P^T with dK and dP^T, dS^T with dV and the next S^T.
+#include "../../include/gocr.h"
+#include "attn_packed.cuh"
+
+using namespace gocr;
+using namespace gocr::packed;
+
+namespace {
+
+constexpr int THREADS = 320;  // eight elementwise warps, a TMA and an MMA warp
+constexpr int EW = 8;         // elementwise warps
+
+static __device__ int g_error;  // DevErr of a wait that gave up
+
+struct BwdArgs {
+  const int* cu;
+  const float* lse;
+  const float* delta;
+  bf16* dq; bf16* dk; bf16* dv;
+  int n_seq, T, Hq, Hkv;
+  float scale;
+};
+
+// delta[h][t] = sum_d do o: D / 8 lanes per (t, h)
+template <int D>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const bf16* o, const bf16* d_o, float* delta, int T, int Hq) {
+  constexpr int L = D / 8;
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / L;
+  const int l = threadIdx.x % L;
+  const bool in = i < (long long)T * Hq;
+  float s = 0.f;
+  if (in) {
+    const uint4 x = *reinterpret_cast<const uint4*>(o + i * D + l * 8), y = *reinterpret_cast<const uint4*>(d_o + i * D + l * 8);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+      s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+    }
+  }
+#pragma unroll
+  for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if (in && l == 0) delta[(i % Hq) * T + i / Hq] = s;
+}
+
+// The 32 columns of an accumulator row, times f, as bf16 to dst (16-byte aligned).
+__device__ __forceinline__ void store32(uint32_t taddr, float f, bf16* dst, bool in) {
+  uint32_t w[32];
+  tc::tmem_ld32_nowait(taddr, w);
+  tc::tmem_wait_ld();
+  if (in)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = pack2(__uint_as_float(w[g * 8 + 2 * e]) * f, __uint_as_float(w[g * 8 + 2 * e + 1]) * f);
+      *reinterpret_cast<uint4*>(dst + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
+// 64 packed values (32 columns) of an elementwise thread back to tensor memory.
+// The two column halves of a block keep to their own columns, [0, 32) and
+// [64, 96), so neither overwrites scores that the other has yet to read; step
+// ks of the product (16 of the 128 columns, 8 packed) then starts here:
+__device__ __forceinline__ uint32_t packed_col(int ks) { return (ks >> 2) * 64 + (ks & 3) * 8; }
+
+// ---------------------------------------------------------------- dk, dv
+
+template <int D> struct DkvGeo {
+  static constexpr int TILE = TILE_BYTES<D>;
+  static constexpr int OFF_K = 0, OFF_V = TILE;
+  static constexpr int OFF_Q = 2 * TILE;   // [2]
+  static constexpr int OFF_DO = 4 * TILE;  // [2]
+  static constexpr int OFF_ROW = 6 * TILE; // float [2 stages][lse, delta][128]
+  static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * 128 * 4;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const BwdArgs a) {
+  using G = DkvGeo<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* rows = reinterpret_cast<float*>(sm + G::OFF_ROW);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + G::OFF_BAR);
+  uint64_t* q_full = kv_full + 1;    // [2]
+  uint64_t* q_empty = q_full + 2;    // [2]
+  uint64_t* do_full = q_empty + 2;   // [2]
+  uint64_t* do_empty = do_full + 2;  // [2]
+  uint64_t* row_full = do_empty + 2; // [2] lse and delta of the stage; ragged tiles zeroed
+  uint64_t* s_full = row_full + 2;
+  uint64_t* p_full = s_full + 1;
+  uint64_t* dp_full = p_full + 1;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* done = ds_full + 1;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int kvh = blockIdx.x % a.Hkv;
+  const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, blockIdx.x / a.Hkv);
+  if (blk.len == 0) return;
+  const int group = a.Hq / a.Hkv;
+  const int kb = blk.at / 128, nqb = (blk.len + 127) / 128;
+  const int per = nqb - kb;         // query blocks of a head that see these keys
+  const int n = group * per;
+  const int tail = blk.len - (nqb - 1) * 128;  // rows of the last query block within the sequence
+
+  if (tid == 0) {
+    tc::mbar_init(kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(q_full + s, 1);
+      tc::mbar_init(q_empty + s, 1);
+      tc::mbar_init(do_full + s, 1);
+      tc::mbar_init(do_empty + s, 1);
+      tc::mbar_init(row_full + s, 1);
+    }
+    tc::mbar_init(s_full, 1);
+    tc::mbar_init(p_full, EW);
+    tc::mbar_init(dp_full, 1);
+    tc::mbar_init(ds_full, EW);
+    tc::mbar_init(done, 1);
+    tc::fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 9) tc::tmem_alloc(holder, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *holder;
+  constexpr uint32_t DP = 128, DV = 256, DK = 256 + D;  // S^T at 0
+  bool ok = true;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      tc::mbar_expect_tx(kv_full, 2 * G::TILE);
+      load_tile<D>(sm + G::OFF_K, &mk, kvh, blk.row0 + blk.at, kv_full);
+      load_tile<D>(sm + G::OFF_V, &mv, kvh, blk.row0 + blk.at, kv_full);
+    }
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1, ph = (it >> 1) & 1;
+      const int head = kvh * group + it / per, at = (kb + it % per) * 128;
+      const bool ragged = at + 128 > blk.len;
+      uint8_t* q = sm + G::OFF_Q + st * G::TILE;
+      uint8_t* d_o = sm + G::OFF_DO + st * G::TILE;
+      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(q_empty + st, ph ^ 1)))) break;
+      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(do_empty + st, ph ^ 1)))) break;
+      if (lane == 0) {
+        tc::mbar_expect_tx(q_full + st, G::TILE);
+        load_tile<D>(q, &mq, head, blk.row0 + at, q_full + st);
+        tc::mbar_expect_tx(do_full + st, G::TILE);
+        load_tile<D>(d_o, &mdo, head, blk.row0 + at, do_full + st);
+      }
+      // the stage is free: dK of its last block, after every read of its rows, has completed
+      float* lse = rows + st * 256;
+      for (int i = lane; i < 128; i += 32) {
+        const bool in = at + i < blk.len;
+        const size_t src = (size_t)head * a.T + blk.row0 + at + i;
+        lse[i] = in ? a.lse[src] * LOG2E : 0.f;
+        lse[128 + i] = in ? a.delta[src] : 0.f;
+      }
+      if (ragged) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(q_full + st, ph) && tc::mbar_wait_ns(do_full + st, ph));
+        if (!ok) break;
+        zero_rows<D>(q, tail);
+        zero_rows<D>(d_o, tail);
+        tc::fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(row_full + st);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
+      constexpr uint32_t idesc_g = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
+      const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
+      const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
+      auto wait = [&](uint64_t* bar, int ph) {
+        const bool w = tc::mbar_wait_ns(bar, ph);
+        tc::fence_after_sync();
+        return w;
+      };
+      auto block = [&](uint32_t dst, uint32_t x, uint32_t y, uint64_t* bar) {  // dst = x y^T over D
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) tc::mma_bf16(tmem + dst, desc_k(x, ks), desc_k(y, ks), idesc_s, ks > 0 ? 1u : 0u);
+        tc::mma_commit(bar);
+      };
+      auto add = [&](uint32_t dst, uint32_t src, uint32_t y, bool first) {  // dst += src y over 128 rows
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_bf16_ta(tmem + dst, tmem + src + packed_col(ks), desc_n(y, ks), idesc_g, !first || ks > 0 ? 1u : 0u);
+      };
+      ok = wait(kv_full, 0) && wait(q_full, 0);
+      if (ok) {
+        block(0, k, q, s_full);
+        if ((ok = wait(do_full, 0))) block(DP, v, d_o, dp_full);
+      }
+      for (int it = 0; it < n && ok; ++it) {
+        const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
+        if (!(ok = wait(p_full, it & 1))) break;
+        add(DV, 0, d_o + st * G::TILE, it == 0);
+        tc::mma_commit(do_empty + st);
+        if (it + 1 < n) {
+          if (!(ok = wait(q_full + nx, nph))) break;
+          block(0, k, q + nx * G::TILE, s_full);
+        }
+        if (!(ok = wait(ds_full, it & 1))) break;
+        add(DK, DP, q + st * G::TILE, it == 0);
+        tc::mma_commit(q_empty + st);
+        if (it + 1 < n) {
+          if (!(ok = wait(do_full + nx, nph))) break;
+          block(DP, v, d_o + nx * G::TILE, dp_full);
+        }
+      }
+      if (ok) tc::mma_commit(done);
+    }
+  } else {
+    const int half = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int key = blk.at + (warp & 3) * 32 + lane;  // within the sequence
+    const uint32_t ts = tmem + lanes + half * 64, tp = ts + DP;
+    const float sl2 = a.scale * LOG2E;
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1;
+      const int at = (kb + it % per) * 128 + half * 64;  // first query row of this thread's columns
+      const float4* lse = reinterpret_cast<const float4*>(rows + st * 256 + half * 64);
+      const float4* del = lse + 32;
+      ok = tc::mbar_wait_ns(row_full + st, (it >> 1) & 1) && tc::mbar_wait_ns(s_full, it & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc::fence_after_sync();
+      // query column i is visible from `lo` on (causal) and below `hi` (the end of the sequence)
+      const int lo = key - at, hi = blk.len - at;
+      const bool cut = at < blk.at + 128 || hi < 64;  // uniform
+      float p[64];
+      {
+        uint32_t u[64];
+        tc::tmem_ld32_nowait(ts, u);
+        tc::tmem_ld32_nowait(ts + 32, u + 32);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const float4 r = lse[i / 4];
+          p[i] = ex2(fmaf(__uint_as_float(u[i]), sl2, -r.x));
+          p[i + 1] = ex2(fmaf(__uint_as_float(u[i + 1]), sl2, -r.y));
+          p[i + 2] = ex2(fmaf(__uint_as_float(u[i + 2]), sl2, -r.z));
+          p[i + 3] = ex2(fmaf(__uint_as_float(u[i + 3]), sl2, -r.w));
+        }
+        if (cut)
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < lo || i >= hi) p[i] = 0.f;
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+        tc::tmem_st32(ts, w);
+        tc::tmem_wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(p_full);
+      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(dp_full, it & 1)))) break;
+      tc::fence_after_sync();
+      {
+        uint32_t u[64];
+        tc::tmem_ld32_nowait(tp, u);
+        tc::tmem_ld32_nowait(tp + 32, u + 32);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const float4 r = del[i / 4];
+          p[i] *= __uint_as_float(u[i]) - r.x;
+          p[i + 1] *= __uint_as_float(u[i + 1]) - r.y;
+          p[i + 2] *= __uint_as_float(u[i + 2]) - r.z;
+          p[i + 3] *= __uint_as_float(u[i + 3]) - r.w;
+        }
+        if (cut)
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < lo || i >= hi) p[i] = 0.f;
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+        tc::tmem_st32(tp, w);
+        tc::tmem_wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(ds_full);
+    }
+    if (ok) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(done, 0));
+      tc::fence_after_sync();
+      const bool in = ok && key < blk.len;
+      const size_t at = ((size_t)(blk.row0 + key) * a.Hkv + kvh) * D + half * (D / 2);
+      const uint32_t tv = tmem + lanes + DV + half * (D / 2), tk = tmem + lanes + DK + half * (D / 2);
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        store32(tv + c, 1.f, a.dv + at + c, in);
+        store32(tk + c, a.scale, a.dk + at + c, in);
+      }
+    }
+  }
+  if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- dq
+
+template <int D> struct DqGeo {
+  static constexpr int TILE = TILE_BYTES<D>;
+  static constexpr int OFF_Q = 0, OFF_DO = TILE;
+  static constexpr int OFF_K = 2 * TILE;  // [2]
+  static constexpr int OFF_V = 4 * TILE;  // [2]
+  static constexpr int OFF_BAR = 6 * TILE;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const BwdArgs a) {
+  using G = DqGeo<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + G::OFF_BAR);
+  uint64_t* k_full = q_full + 1;    // [2]
+  uint64_t* k_empty = k_full + 2;   // [2]
+  uint64_t* v_full = k_empty + 2;   // [2]
+  uint64_t* v_empty = v_full + 2;   // [2]
+  uint64_t* k_tail = v_empty + 2;
+  uint64_t* s_full = k_tail + 1;    // [2]
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* dp_free = dp_full + 1;
+  uint64_t* ds_full = dp_free + 1;  // [2]
+  uint64_t* done = ds_full + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int head = blockIdx.x % a.Hq;
+  const Block blk = find_block<true>(a.cu, a.n_seq, a.T, 128, blockIdx.x / a.Hq);
+  if (blk.len == 0) return;
+  const int kvh = head / (a.Hq / a.Hkv);
+  const int n = blk.at / 128 + 1;
+  const int tail = blk.len - blk.at;  // rows of the last key block within the sequence, if < 128
+
+  if (tid == 0) {
+    tc::mbar_init(q_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(k_full + s, 1);
+      tc::mbar_init(k_empty + s, 1);
+      tc::mbar_init(v_full + s, 1);
+      tc::mbar_init(v_empty + s, 1);
+      tc::mbar_init(s_full + s, 1);
+      tc::mbar_init(ds_full + s, EW);
+    }
+    tc::mbar_init(k_tail, 1);
+    tc::mbar_init(dp_full, 1);
+    tc::mbar_init(dp_free, EW);
+    tc::mbar_init(done, 1);
+    tc::fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 9) tc::tmem_alloc(holder, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *holder;
+  constexpr uint32_t DP = 256, DQ = 384;  // S at 0 and 128
+  bool ok = true;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      tc::mbar_expect_tx(q_full, 2 * G::TILE);
+      load_tile<D>(sm + G::OFF_Q, &mq, head, blk.row0 + blk.at, q_full);
+      load_tile<D>(sm + G::OFF_DO, &mdo, head, blk.row0 + blk.at, q_full);
+      for (int it = 0; it < n; ++it) {
+        const int st = it & 1, ph = (it >> 1) & 1;
+        if (!(ok = tc::mbar_wait_ns(k_empty + st, ph ^ 1))) break;
+        tc::mbar_expect_tx(k_full + st, G::TILE);
+        load_tile<D>(sm + G::OFF_K + st * G::TILE, &mk, kvh, blk.row0 + it * 128, k_full + st);
+        if (!(ok = tc::mbar_wait_ns(v_empty + st, ph ^ 1))) break;
+        tc::mbar_expect_tx(v_full + st, G::TILE);
+        load_tile<D>(sm + G::OFF_V + st * G::TILE, &mv, kvh, blk.row0 + it * 128, v_full + st);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && tail < 128) {  // nothing behind the sequence in dQ += dS K
+      const int st = (n - 1) & 1;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(k_full + st, ((n - 1) >> 1) & 1));
+      zero_rows<D>(sm + G::OFF_K + st * G::TILE, tail);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(k_tail);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
+      constexpr uint32_t idesc_g = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
+      const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
+      const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
+      auto wait = [&](uint64_t* bar, int ph) {
+        const bool w = tc::mbar_wait_ns(bar, ph);
+        tc::fence_after_sync();
+        return w;
+      };
+      auto block = [&](uint32_t dst, uint32_t x, uint32_t y, uint64_t* bar) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) tc::mma_bf16(tmem + dst, desc_k(x, ks), desc_k(y, ks), idesc_s, ks > 0 ? 1u : 0u);
+        tc::mma_commit(bar);
+      };
+      ok = wait(q_full, 0) && wait(k_full, 0);
+      if (ok) {
+        block(0, q, k, s_full);
+        if ((ok = wait(v_full, 0))) {
+          block(DP, d_o, v, dp_full);
+          tc::mma_commit(v_empty);
+        }
+      }
+      for (int it = 0; it < n && ok; ++it) {
+        const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
+        if (it + 1 < n) {
+          // the other score buffer: its dS was consumed by dQ(it - 1), issued before
+          if (!(ok = wait(k_full + nx, nph))) break;
+          block(nx * 128, q, k + nx * G::TILE, s_full + nx);
+          if (!(ok = wait(v_full + nx, nph) && wait(dp_free, it & 1))) break;
+          block(DP, d_o, v + nx * G::TILE, dp_full);
+          tc::mma_commit(v_empty + nx);
+        }
+        if (!(ok = wait(ds_full + st, (it >> 1) & 1))) break;
+        if (it + 1 == n && tail < 128 && !(ok = wait(k_tail, 0))) break;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_bf16_ta(tmem + DQ, tmem + st * 128 + packed_col(ks), desc_n(k + st * G::TILE, ks), idesc_g,
+                          it > 0 || ks > 0 ? 1u : 0u);
+        tc::mma_commit(k_empty + st);
+      }
+      if (ok) tc::mma_commit(done);
+    }
+  } else {
+    const int half = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int row = blk.at + (warp & 3) * 32 + lane;  // within the sequence
+    const bool in = row < blk.len;
+    const size_t t = (size_t)blk.row0 + row;
+    const float lse = in ? a.lse[(size_t)head * a.T + t] * LOG2E : 0.f;
+    const float del = in ? a.delta[(size_t)head * a.T + t] : 0.f;
+    const float sl2 = a.scale * LOG2E;
+    const uint32_t tp = tmem + lanes + DP + half * 64;
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1;
+      const uint32_t ts = tmem + lanes + st * 128 + half * 64;
+      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(s_full + st, (it >> 1) & 1)))) break;
+      tc::fence_after_sync();
+      float p[64];
+      {
+        uint32_t u[64];
+        tc::tmem_ld32_nowait(ts, u);
+        tc::tmem_ld32_nowait(ts + 32, u + 32);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; ++i) p[i] = ex2(fmaf(__uint_as_float(u[i]), sl2, -lse));
+      }
+      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(dp_full, it & 1)))) break;
+      tc::fence_after_sync();
+      {
+        uint32_t u[64];
+        tc::tmem_ld32_nowait(tp, u);
+        tc::tmem_ld32_nowait(tp + 32, u + 32);
+        tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(dp_free);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) p[i] *= __uint_as_float(u[i]) - del;
+      }
+      if (it + 1 == n) {  // the diagonal block; the end of the sequence lies past the row
+        const int see = min(row, blk.len - 1) - it * 128 - half * 64;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i > see) p[i] = 0.f;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+      tc::tmem_st32(ts, w);
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(ds_full + st);
+    }
+    if (ok) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(done, 0));
+      tc::fence_after_sync();
+      const uint32_t tq = tmem + lanes + DQ + half * (D / 2);
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) store32(tq + c, a.scale, a.dq + (t * a.Hq + head) * D + half * (D / 2) + c, ok && in);
+    }
+  }
+  if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+int backward(const CUtensorMap* m, const BwdArgs& a, const bf16* o, const bf16* d_o, float* delta, cudaStream_t s) {
+  const void* kf[2] = {reinterpret_cast<const void*>(&attn_dkv_kernel<D>), reinterpret_cast<const void*>(&attn_dq_kernel<D>)};
+  if (!kernel_smem_at_least(kf[0], DkvGeo<D>::SMEM) || !kernel_smem_at_least(kf[1], DqGeo<D>::SMEM))
+    return op_fail(GOCR_ECUDA, "kernel configuration rejected");
+  const long long threads = (long long)a.T * a.Hq * (D / 8);
+  attn_delta_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(o, d_o, delta, a.T, a.Hq);
+  if (int rc = op_launched("attention_packed delta")) return rc;
+  const long long blocks = max_blocks(a.n_seq, a.T, 128);
+  attn_dkv_kernel<D><<<(unsigned)(blocks * a.Hkv), THREADS, DkvGeo<D>::SMEM, s>>>(m[0], m[1], m[2], m[3], a);
+  if (int rc = op_launched("attention_packed dk, dv")) return rc;
+  attn_dq_kernel<D><<<(unsigned)(blocks * a.Hq), THREADS, DqGeo<D>::SMEM, s>>>(m[0], m[1], m[2], m[3], a);
+  return op_launched("attention_packed dq");
+}
+
+}  // namespace
+
+namespace gocr {
+cudaError_t take_attn_packed_bwd_error(int* out) {
+  const int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_error, sizeof(int));
+  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_error, &zero, sizeof(int));
+  return e;
+}
+}  // namespace gocr
+
+extern "C" {
+
+size_t gocr_op_attention_packed_backward_workspace(int T, int Hq) {
+  if (T < 0 || Hq < 1) return 0;
+  return (((size_t)T * Hq * 4 + 255) & ~(size_t)255) + 256;
+}
+
+int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void* k, const void* v, const void* o,
+                                      const float* lse, const int32_t* cu_seqlens, void* dq, void* dk, void* dv,
+                                      int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk,
+                                      long long ldv, float scale, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  if (int rc = attn_packed_check(n_seq, T, Hq, Hkv, d, ldq, ldk, ldv, scale)) return rc;
+  if (!cu_seqlens || !workspace || (T && (!d_o || !q || !k || !v || !o || !lse || !dq || !dk || !dv)))
+    return op_fail(GOCR_EINVAL, "null pointer");
+  if (((uintptr_t)d_o | (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o | (uintptr_t)dq | (uintptr_t)dk |
+       (uintptr_t)dv | (uintptr_t)workspace) & 15)
+    return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if (workspace_bytes < gocr_op_attention_packed_backward_workspace(T, Hq)) return op_fail(GOCR_ECAPACITY, "workspace too small");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (int rc = op_stream_check(s)) return rc;
+  if (!T || !n_seq) return GOCR_OK;
+  CUtensorMap m[4];
+  if (!map_rows(&m[0], q, T, Hq, d, ldq) || !map_rows(&m[1], k, T, Hkv, d, ldk) || !map_rows(&m[2], v, T, Hkv, d, ldv) ||
+      !map_rows(&m[3], d_o, T, Hq, d, (long long)Hq * d))
+    return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
+  float* delta = (float*)workspace;
+  const BwdArgs a{cu_seqlens, lse, delta, (bf16*)dq, (bf16*)dk, (bf16*)dv, n_seq, T, Hq, Hkv, scale};
+  return d == 128 ? backward<128>(m, a, (const bf16*)o, (const bf16*)d_o, delta, s)
+                  : backward<64>(m, a, (const bf16*)o, (const bf16*)d_o, delta, s);
+}
+
+}  // extern "C"

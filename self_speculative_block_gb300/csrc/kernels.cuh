@@ -268,6 +268,11 @@ int op_launched(const char* what);
 // Error word of the file's kernels with bounded waits (a DevErr; read and
 // cleared on an idle stream).
 cudaError_t take_linear_ce_error(int* out);
+cudaError_t take_attn_packed_error(int* out);
+cudaError_t take_attn_packed_bwd_error(int* out);
+// Argument checks that the packed attention calls share.
+int attn_packed_check(int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk, long long ldv,
+                      float scale);
 
 // Ask for the largest shared-memory carveout for kernel `fn` on the current
 // device (once).  Every kernel of the decode path runs with the same SM

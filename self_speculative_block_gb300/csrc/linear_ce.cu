@@ -21,7 +21,7 @@
 //          for dw (M-major), W and x N-major, so nothing is transposed.
 // The vocabulary goes by in pieces whose g fits the workspace (and L2); the
 // tiles of both products of a piece share one launch, the longer ones first.
-// g is rounded to bf16 (relative 2^-9) because the tensor cores take it so;
+// g is rounded to bf16 (relative 2^-8) because the tensor cores take it so;
 // every sum is in fp32.  Nothing is added by atomics across CTAs, so the same
 // inputs give the same bits.
 #include "../../include/gocr.h"

@@ -47,12 +47,16 @@ using namespace gocr;
 extern "C" int gocr_op_status(void* stream) {
   if (int rc = op_stream_check((cudaStream_t)stream)) return rc;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
-  int ce = 0;
+  int ce = 0, af = 0, ab = 0;
   if (e == cudaSuccess) e = take_linear_ce_error(&ce);
+  if (e == cudaSuccess) e = take_attn_packed_error(&af);
+  if (e == cudaSuccess) e = take_attn_packed_bwd_error(&ab);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return op_fail(GOCR_ECUDA, "status read failed: %s", cudaGetErrorString(e));
   }
-  if (ce) return op_fail(GOCR_EDEVICE, "a wait inside a linear_ce kernel gave up");
+  if (ce || af || ab)
+    return op_fail(GOCR_EDEVICE, "a wait inside a kernel of %s gave up",
+                   ce ? "linear_ce" : (af ? "attention_packed" : "attention_packed_backward"));
   return GOCR_OK;
 }

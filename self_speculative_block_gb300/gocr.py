@@ -39,7 +39,8 @@ EXPORTS = ("gocr_create", "gocr_prefill", "gocr_decode", "gocr_decode_batch", "g
            "gocr_op_linear_static", "gocr_op_attention_ranges", "gocr_three_stream_ranges",
            "gocr_op_embed", "gocr_op_embed_backward_workspace", "gocr_op_embed_backward",
            "gocr_op_linear_ce_workspace", "gocr_op_linear_ce", "gocr_op_linear_ce_backward_workspace",
-           "gocr_op_linear_ce_backward", "gocr_op_status")
+           "gocr_op_linear_ce_backward", "gocr_op_attention_packed", "gocr_op_attention_packed_backward_workspace",
+           "gocr_op_attention_packed_backward", "gocr_op_status")
 
 
 class GocrError(RuntimeError):
@@ -96,7 +97,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"libgocr.so is not built ({path}); run the package build first")
     lib = ctypes.CDLL(path)
-    vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    vp, i32, sz, f32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_longlong
     P32 = ctypes.POINTER(ctypes.c_int32)
     sig = {
         "gocr_create": (i32, [ctypes.POINTER(Config), ctypes.POINTER(Weights), vp, ALLOC_FN, FREE_FN, vp,
@@ -130,6 +131,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gocr_op_linear_ce": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
         "gocr_op_linear_ce_backward_workspace": (sz, [i32, i32, i32]),
         "gocr_op_linear_ce_backward": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
+        "gocr_op_attention_packed": (i32, [vp] * 6 + [i32] * 5 + [i64] * 3 + [f32, vp]),
+        "gocr_op_attention_packed_backward_workspace": (sz, [i32, i32]),
+        "gocr_op_attention_packed_backward": (i32, [vp] * 10 + [i32] * 5 + [i64] * 3 + [f32, vp, sz, vp]),
         "gocr_op_status": (i32, [vp]),
     }
     for name, (res, args) in sig.items():
@@ -534,6 +538,82 @@ def op_embed_backward(dy, ids, vocab: int, scale: float = 1.0, mask: bool = Fals
                                           d_mask.data_ptr() if mask else None, T, H, vocab, scale, ws.data_ptr(),
                                           ws.numel(), _stream(dev)))
     return d_embed, d_mask
+
+
+def _rows(name: str, t, T, heads, d, device):
+    """Check a [T, heads, d] bf16 operand whose rows may lie apart; returns the row pitch."""
+    torch = _torch()
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{T}, {'*' if heads is None else heads}, {d}], got {list(t.shape)}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a row of {name} must be contiguous, got strides {t.stride()}")
+    _on_device(name, t, device)
+    return t.stride(0) if T > 1 else t.shape[1] * d
+
+
+def _packed_args(q, k, v, cu_seqlens, scale):
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, d], got {list(q.shape)}")
+    dev, (T, Hq, d) = q.device, q.shape
+    ld = [_rows("q", q, T, None, d, dev), _rows("k", k, T, None, d, dev)]
+    ld.append(_rows("v", v, T, k.shape[1], d, dev))
+    _want("cu_seqlens", cu_seqlens, (None,), torch.int32, device=dev)
+    if cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must hold at least one entry")
+    sizes = (cu_seqlens.shape[0] - 1, T, Hq, k.shape[1], d, *ld, d ** -0.5 if scale is None else scale)
+    return dev, T, Hq, k.shape[1], d, sizes
+
+
+def op_attention_packed(q, k, v, cu_seqlens, scale=None, o=None, lse=None):
+    """Causal attention over packed sequences with grouped heads: q [T, Hq, d],
+    k and v [T, Hkv, d] bf16 (rows may be views of one fused projection);
+    sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32, on the
+    device); scale defaults to 1 / sqrt(d).  Returns (o [T, Hq, d] bf16, lse
+    [Hq, T] fp32), written into o and lse when given; rows of no sequence are
+    not written."""
+    torch = _torch()
+    dev, T, Hq, Hkv, d, sizes = _packed_args(q, k, v, cu_seqlens, scale)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _want("o", o, (T, Hq, d), torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        else:
+            _want("lse", lse, (Hq, T), torch.float32, device=dev)
+        _check(load().gocr_op_attention_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                               cu_seqlens.data_ptr(), *sizes, _stream(dev)))
+    return o, lse
+
+
+def op_attention_packed_backward(do, q, k, v, o, lse, cu_seqlens, scale=None, workspace=None, dq=None, dk=None,
+                                 dv=None):
+    """Gradient of op_attention_packed from do [T, Hq, d] and the forward
+    call's o and lse: (dq [T, Hq, d], dk, dv [T, Hkv, d]) bf16, written into
+    dq, dk and dv when given; rows of no sequence are not written."""
+    torch = _torch()
+    lib = load()
+    dev, T, Hq, Hkv, d, sizes = _packed_args(q, k, v, cu_seqlens, scale)
+    _want("do", do, (T, Hq, d), torch.bfloat16, device=dev)
+    _want("o", o, (T, Hq, d), torch.bfloat16, device=dev)
+    _want("lse", lse, (Hq, T), torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        out = []
+        for name, t, heads in (("dq", dq, Hq), ("dk", dk, Hkv), ("dv", dv, Hkv)):
+            if t is None:
+                t = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev)
+            else:
+                _want(name, t, (T, heads, d), torch.bfloat16, device=dev)
+            out.append(t)
+        ws = _workspace(workspace, lib.gocr_op_attention_packed_backward_workspace(T, Hq), dev)
+        _check(lib.gocr_op_attention_packed_backward(
+            do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(),
+            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), *sizes, ws.data_ptr(), ws.numel(), _stream(dev)))
+    return tuple(out)
 
 
 def op_linear_ce(x, w, labels, workspace=None):

@@ -97,3 +97,51 @@ def test_wrappers_check_tensors():
         gocr.op_linear_ce(torch.zeros(64, 4, dtype=torch.bfloat16).T, b, i)
     with pytest.raises(ValueError, match="dy must be"):
         gocr.op_embed_backward(torch.zeros(4, 64, dtype=torch.float16), i, 10)
+
+
+def test_attention_packed_refusals(lib):
+    def call(q=P, k=P, v=P, o=P, lse=P, cu=P, n=2, T=8, Hq=4, Hkv=2, d=64, ldq=256, ldk=128, ldv=128, scale=0.125):
+        return lib.gocr_op_attention_packed(q, k, v, o, lse, cu, n, T, Hq, Hkv, d, ldq, ldk, ldv, scale, None)
+    for k in ("q", "k", "v", "o", "lse", "cu"):
+        assert call(**{k: None}) == EINVAL and "null" in _message(lib)
+    for bad in (dict(n=-1), dict(T=-1), dict(Hq=3), dict(Hkv=0), dict(d=96), dict(Hq=2048, Hkv=1, ldq=1 << 18)):
+        assert call(**bad) == EINVAL and "shape" in _message(lib)
+    for bad in (dict(ldq=255), dict(ldq=248), dict(ldk=64), dict(ldv=132), dict(ldk=1 << 40)):
+        assert call(**bad) == EINVAL and "pitch" in _message(lib)
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(scale=bad) == EINVAL and "scale" in _message(lib)
+    for k in ("q", "k", "v", "o"):
+        assert call(**{k: ODD}) == EINVAL and "aligned" in _message(lib)
+
+
+def test_attention_packed_backward_refusals(lib):
+    need = lib.gocr_op_attention_packed_backward_workspace(8, 4)
+    assert need > 0 and lib.gocr_op_attention_packed_backward_workspace(8, 0) == 0
+    names = ("d_o", "q", "k", "v", "o", "lse", "cu", "dq", "dk", "dv")
+
+    def call(n=2, T=8, Hq=4, Hkv=2, d=64, ld=(256, 128, 128), scale=0.125, ws=P, nb=need, **ptr):
+        return lib.gocr_op_attention_packed_backward(*[ptr.get(k, P) for k in names], n, T, Hq, Hkv, d, *ld, scale, ws,
+                                                     nb, None)
+    for k in names:
+        assert call(**{k: None}) == EINVAL and "null" in _message(lib)
+    assert call(ws=None) == EINVAL
+    for k in names:
+        if k not in ("lse", "cu"):
+            assert call(**{k: ODD}) == EINVAL and "aligned" in _message(lib)
+    assert call(d=32) == EINVAL and call(ld=(256, 128, 100)) == EINVAL and call(scale=-0.5) == EINVAL
+    assert call(nb=need - 1) == ECAPACITY and "workspace" in _message(lib)
+
+
+def test_attention_packed_wrapper_checks_rows():
+    torch = pytest.importorskip("torch")
+    from self_speculative_block_gb300 import gocr
+    q = torch.zeros(8, 4, 64, dtype=torch.bfloat16)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="contiguous"):
+        gocr.op_attention_packed(torch.zeros(8, 64, 4, dtype=torch.bfloat16).transpose(1, 2), q, q, cu)
+    with pytest.raises(ValueError, match="q must be"):
+        gocr.op_attention_packed(q[0], q, q, cu)
+    with pytest.raises(ValueError, match="bfloat16"):
+        gocr.op_attention_packed(q.float(), q, q, cu)
+    with pytest.raises(ValueError, match="CUDA"):
+        gocr.op_attention_packed(q, q, q, cu)
