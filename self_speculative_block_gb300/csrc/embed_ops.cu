@@ -13,16 +13,18 @@
 //   sort  a cluster of SORT_CTAS CTAs sorts the positions by token (stable
 //         radix sort, digits of at most 9 bits, counts exchanged over
 //         distributed shared memory), while the other CTAs of the launch write
-//         the zeros of the whole gradient: the sort's latency hides behind the
-//         launch's V x H writes;
-//   sum   a CTA sums the runs of equal tokens in a piece of PIECE sorted
-//         positions; a run inside the piece is written, a run that crosses a
-//         border of the piece leaves an fp32 partial row;
-//   join  the piece where a crossing run begins adds up its partial rows.
-// A frequent token ([M] above all) is one run over many pieces, so no CTA ever
-// walks more than PIECE rows of dy.
+//         the zeros of the whole gradient by bulk copies: the sort's latency
+//         hides behind the launch's V x H writes;
+//   sum   a CTA takes PIECE sorted positions.  A run of equal tokens is summed
+//         and written by the piece in which it begins, unless it is longer
+//         than LONG: each piece then leaves an fp32 partial row of it;
+//   join  one CTA per (long run, 128 columns) adds up the partial rows, eight
+//         warps a share each.
+// A frequent token ([M] above all) is one long run, so no CTA ever walks more
+// than PIECE + LONG rows of dy.
 #include "../../include/gocr.h"
 #include "kernels.cuh"
+#include "tc.cuh"
 
 #include <cooperative_groups.h>
 
@@ -36,13 +38,14 @@ constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_DIGITS = 512;
 constexpr int PIECE = 16;
+constexpr int LONG = 16;
+constexpr int FILL_BYTES = 16384;  // one bulk copy of zeros
 
 // 16 bytes of a row in fp32
 template <typename T> struct Vec;
 template <> struct Vec<bf16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const bf16* p, float* v) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+  static __device__ __forceinline__ void unpack(const uint4& u, float* v) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -62,9 +65,9 @@ template <> struct Vec<bf16> {
 };
 template <> struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const float* p, float* v) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* v) {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
   }
   static __device__ __forceinline__ void store(float* p, const float* v) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(256) embed_rows_kernel(const T* __restrict__ e
     for (int c = lane * N; c < H; c += 32 * N) {
       float v[N];
       if (src) {
-        Vec<T>::load(src + c, v);
+        Vec<T>::unpack(*reinterpret_cast<const uint4*>(src + c), v);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= scale;
       } else {
@@ -112,23 +115,38 @@ struct SortArgs {
   int T, V, mask, passes, digit_bits;
   void* d_embed; size_t embed_bytes;  // zeroed by the launch's other CTAs (multiples of 16 bytes)
   void* d_mask; size_t mask_bytes;
+  int* n_long;                        // zeroed: the long runs that the sum kernel lists
 };
 
+// n bytes of zeros (a multiple of 16) at d, by the CTAs of the launch past the sort's.
+__device__ __forceinline__ void fill_zero(uint8_t* d, size_t n, const uint8_t* zeros) {
+  const size_t step = (size_t)(gridDim.x - SORT_CTAS) * FILL_BYTES;
+  for (size_t i = (size_t)(blockIdx.x - SORT_CTAS) * FILL_BYTES; i < n; i += step) {
+    const uint32_t b = (uint32_t)(n - i < FILL_BYTES ? n - i : FILL_BYTES);
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d + i), "r"(tc::smem_u32(zeros)), "r"(b)
+                 : "memory");
+  }
+}
+
 __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(SortArgs a) {
+  __shared__ __align__(16) int cnt[SORT_WARPS][MAX_DIGITS];  // keys of (warp, digit), then the warp's next place
+  __shared__ int cta_cnt[MAX_DIGITS];
+  __shared__ int scan[MAX_DIGITS];
+  static_assert(sizeof(cnt) >= FILL_BYTES, "the zeros' source");
   if (blockIdx.x >= SORT_CTAS) {  // whole clusters
-    const size_t n = a.embed_bytes / 16, step = (size_t)(gridDim.x - SORT_CTAS) * SORT_THREADS;
-    const size_t first = (size_t)(blockIdx.x - SORT_CTAS) * SORT_THREADS + threadIdx.x;
-    uint4* d = reinterpret_cast<uint4*>(a.d_embed);
-    for (size_t i = first; i < n; i += step) d[i] = make_uint4(0, 0, 0, 0);
-    if (a.d_mask) {
-      uint4* m = reinterpret_cast<uint4*>(a.d_mask);
-      for (size_t i = first; i < a.mask_bytes / 16; i += step) m[i] = make_uint4(0, 0, 0, 0);
+    uint4* z = reinterpret_cast<uint4*>(&cnt[0][0]);
+    for (int i = threadIdx.x; i < FILL_BYTES / 16; i += SORT_THREADS) z[i] = make_uint4(0, 0, 0, 0);
+    tc::fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      fill_zero(reinterpret_cast<uint8_t*>(a.d_embed), a.embed_bytes, reinterpret_cast<const uint8_t*>(z));
+      if (a.d_mask) fill_zero(reinterpret_cast<uint8_t*>(a.d_mask), a.mask_bytes, reinterpret_cast<const uint8_t*>(z));
+      tc::bulk_commit();
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     return;
   }
-  __shared__ int cnt[SORT_WARPS][MAX_DIGITS];  // keys of (warp, digit), then the warp's next place
-  __shared__ int cta_cnt[MAX_DIGITS];
-  __shared__ int scan[MAX_DIGITS];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_long = 0;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -218,56 +236,90 @@ struct SumArgs {
   const int* pos;
   void* d_embed;
   void* d_mask;
-  float* part;  // [pieces][2][H]: the run that comes into the piece, the run that goes out of it
+  float* part;   // [pieces][2][H] of long runs: the one that comes into the piece, the one that begins in it
+  int* n_long;
+  int* run;      // [n_long] the pieces in which a long run begins
   int T, H, V;
   float scale;
 };
 
 template <typename T>
 __device__ __forceinline__ T* grad_row(const SumArgs& a, int key) {
-  return key < a.V ? reinterpret_cast<T*>(a.d_embed) + (size_t)key * a.H
-                   : (key == a.V ? reinterpret_cast<T*>(a.d_mask) : nullptr);
+  return key < a.V ? reinterpret_cast<T*>(a.d_embed) + (size_t)key * a.H : reinterpret_cast<T*>(a.d_mask);
 }
+
+// Rows of dy fetched at a time by a thread.
+constexpr int BATCH = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ int keys[PIECE + 2];  // keys[1 + i] of the piece's positions, and its neighbours'
-  __shared__ int poss[PIECE];
+  constexpr int WIN = LONG + PIECE + LONG;  // positions b - LONG .. b + PIECE + LONG - 1
+  __shared__ int keys[WIN + 1];             // and the next one
+  __shared__ int poss[PIECE + LONG];        // of positions b ..
+  __shared__ int edge[4];  // the runs of the piece's first and last position: first position, and past the last
+  if (threadIdx.x == 0) tc::grid_dep_launch();
+  if (threadIdx.x < 4) edge[threadIdx.x] = threadIdx.x & 1 ? PIECE + LONG + 1 : -LONG;
+  tc::grid_dep_wait();
   const int b = blockIdx.x * PIECE, n = min(PIECE, a.T - b);
-  for (int i = threadIdx.x; i < PIECE + 2; i += blockDim.x) {
-    const int at = b + i - 1;
+  for (int i = threadIdx.x; i < WIN + 1; i += blockDim.x) {
+    const int at = b - LONG + i;
     keys[i] = at >= 0 && at < a.T ? a.key[at] : -1;
-    if (i < PIECE) poss[i] = b + i < a.T ? a.pos[b + i] : 0;
+    if (i < PIECE + LONG) poss[i] = b + i < a.T ? a.pos[b + i] : 0;
   }
   __syncthreads();
+  const int* k0 = keys + LONG;  // k0[i]: position b + i
+  for (int i0 = (threadIdx.x & ~31) - LONG + 1; i0 <= PIECE + LONG; i0 += blockDim.x) {
+    const int i = i0 + (threadIdx.x & 31);
+    const bool start = i <= PIECE + LONG && k0[i] != k0[i - 1];
+    const int far = 1 << 20;
+    const int s0 = __reduce_max_sync(0xffffffffu, start && i <= 0 ? i : -far);
+    const int e0 = __reduce_min_sync(0xffffffffu, start && i > 0 ? i : far);
+    const int s1 = __reduce_max_sync(0xffffffffu, start && i < n ? i : -far);
+    const int e1 = __reduce_min_sync(0xffffffffu, start && i >= n ? i : far);
+    if ((threadIdx.x & 31) == 0) {
+      atomicMax(&edge[0], s0);
+      atomicMin(&edge[1], e0);
+      atomicMax(&edge[2], s1);
+      atomicMin(&edge[3], e1);
+    }
+  }
+  __syncthreads();
+  // A run is long when it has more than LONG positions; the window shows that
+  // much of it, so every piece that it touches comes to the same verdict.
+  const bool comes = k0[-1] == k0[0], in = comes && edge[1] - edge[0] > LONG;
+  const int first = comes ? min(edge[1], n) : 0;  // the first run that begins in the piece
+  int end = n;  // the last run that begins here is summed to its end, unless it is long
+  if (first < n && edge[3] > n) {
+    if (edge[3] - edge[2] <= LONG) end = edge[3];
+    else if (blockIdx.y == 0 && threadIdx.x == 0 && k0[n - 1] <= a.V) a.run[atomicAdd(a.n_long, 1)] = blockIdx.x;
+  }
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
   if (c >= a.H) return;
   const T* dy = reinterpret_cast<const T*>(a.dy) + c;
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
-  bool from_before = keys[0] == keys[1];
-  constexpr int B = 8;  // rows fetched at a time
-  for (int i0 = 0; i0 < n; i0 += B) {
-    float v[B][N];
+  for (int i0 = in ? 0 : first; i0 < end; i0 += BATCH) {
+    uint4 v[BATCH];
 #pragma unroll
-    for (int u = 0; u < B; ++u)
-      if (i0 + u < n && keys[1 + i0 + u] <= a.V) Vec<T>::load(dy + (size_t)poss[i0 + u] * a.H, v[u]);
+    for (int u = 0; u < BATCH; ++u)
+      if (i0 + u < end && k0[i0 + u] <= a.V) v[u] = *reinterpret_cast<const uint4*>(dy + (size_t)poss[i0 + u] * a.H);
 #pragma unroll
-    for (int u = 0; u < B; ++u) {
+    for (int u = 0; u < BATCH; ++u) {
       const int i = i0 + u;
-      if (i >= n) break;
-      const int k = keys[1 + i];
+      if (i >= end) break;
+      const int k = k0[i];
       if (k > a.V) return;  // rows without a gradient come last
+      float x[N];
+      Vec<T>::unpack(v[u], x);
 #pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] += v[u][j];
-      const bool goes_on = keys[2 + i] == k;
-      if (goes_on && i + 1 < n) continue;
-      if (from_before || goes_on) {
-        // a run that comes in (and perhaps goes on) is the first partial, a
-        // run that begins here and goes on the second
-        float* p = a.part + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * a.H + c;
+      for (int j = 0; j < N; ++j) acc[j] += x[j];
+      const bool goes_on = k0[i + 1] == k;
+      if (goes_on && i + 1 < end) continue;
+      const bool comes_in = in && i < n && k == k0[-1];
+      if (comes_in || goes_on) {
+        float* p = a.part + ((size_t)blockIdx.x * 2 + (comes_in ? 0 : 1)) * a.H + c;
 #pragma unroll
         for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
       } else {
@@ -275,46 +327,63 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
         for (int j = 0; j < N; ++j) acc[j] *= a.scale;
         Vec<T>::store(grad_row<T>(a, k) + c, acc);
       }
-      from_before = false;
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[j] = 0.f;
     }
   }
 }
 
+// The long runs: warp w adds the w-th eighth of a run's partial rows, four
+// columns a lane, and warp 0 the eight sums.
 template <typename T>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a) {
-  __shared__ int s_last;  // the last piece of the run
-  const int b = blockIdx.x * PIECE, e = b + PIECE;
-  if (e >= a.T) return;  // the last piece has no run that goes on
-  const int k = a.key[e - 1];
-  if (k > a.V || a.key[e] != k) return;
-  if (b > 0 && a.key[b - 1] == k) return;  // the run began before this piece
-  const int pieces = (a.T + PIECE - 1) / PIECE;
-  if (threadIdx.x == 0) s_last = 0x7fffffff;
-  __syncthreads();
-  for (int j0 = blockIdx.x + 1; j0 < pieces; j0 += blockDim.x) {
-    const int j = j0 + threadIdx.x;
-    // the run ends in piece j when the position after the piece is not its own
-    if (j < pieces && ((j + 1) * (long long)PIECE >= a.T || a.key[(j + 1) * PIECE] != k)) atomicMin(&s_last, j);
+  __shared__ float4 sums[8][32];
+  __shared__ int s_last;
+  tc::grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pieces = (a.T + PIECE - 1) / PIECE, n = *a.n_long;
+  const int c = blockIdx.y * 128 + lane * 4;
+  for (int r = blockIdx.x; r < n; r += gridDim.x) {
+    const int first = a.run[r];
+    const int k = a.key[(first + 1) * PIECE - 1];
+    if (threadIdx.x == 0) s_last = pieces - 1;
     __syncthreads();
-    if (s_last != 0x7fffffff) break;
-    __syncthreads();
-  }
-  const int last = s_last;
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
-  if (c >= a.H) return;
-  float4 s = *reinterpret_cast<const float4*>(a.part + ((size_t)blockIdx.x * 2 + 1) * a.H + c);
+    // the run ends in the first piece whose next position is not its own
+    for (int j0 = first + 1; j0 < pieces; j0 += 1024) {
+      int at = pieces;
+#pragma unroll
+      for (int u = 3; u >= 0; --u) {
+        const int j = j0 + u * 256 + threadIdx.x;
+        if (j < pieces - 1 && a.key[(j + 1) * PIECE] != k) at = j;
+      }
+      if (at < pieces) atomicMin(&s_last, at);
+      if (__syncthreads_or(at < pieces)) break;
+    }
+    const int m = s_last - first, share = (m + 8) / 8;  // m + 1 partial rows
+    const int lo = warp * share, hi = min(lo + share, m + 1);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.H) {
 #pragma unroll 8
-  for (int j = blockIdx.x + 1; j <= last; ++j) {
-    const float4 v = *reinterpret_cast<const float4*>(a.part + (size_t)j * 2 * a.H + c);
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      for (int j = lo; j < hi; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part + ((size_t)(first + j) * 2 + (j == 0 ? 1 : 0)) * a.H + c);
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < a.H) {
+      for (int w = 1; w < 8; ++w) {
+        const float4 v = sums[w][lane];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+      T* d = grad_row<T>(a, k) + c;
+      d[0] = from_f32<T>(s.x * a.scale);
+      d[1] = from_f32<T>(s.y * a.scale);
+      d[2] = from_f32<T>(s.z * a.scale);
+      d[3] = from_f32<T>(s.w * a.scale);
+    }
+    __syncthreads();
   }
-  T* d = grad_row<T>(a, k) + c;
-  d[0] = from_f32<T>(s.x * a.scale);
-  d[1] = from_f32<T>(s.y * a.scale);
-  d[2] = from_f32<T>(s.z * a.scale);
-  d[3] = from_f32<T>(s.w * a.scale);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -330,8 +399,8 @@ int check_shape(int dtype, int T, int H, int V) {
 template <typename T>
 int embed_backward(const SortArgs& so, const SumArgs& su, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  // the clusters past the first write zeros: two CTAs per SM
-  const size_t fill = (so.embed_bytes / 16 + SORT_THREADS * 4 - 1) / (SORT_THREADS * 4);
+  // the clusters past the first write zeros, two CTAs per SM at most
+  const size_t fill = (so.embed_bytes + FILL_BYTES - 1) / FILL_BYTES;
   const size_t most = 2 * SM_COUNT - SORT_CTAS;
   const unsigned ctas = (unsigned)(fill < most ? fill : most);
   cfg.gridDim = dim3(SORT_CTAS + (ctas + SORT_CTAS - 1) / SORT_CTAS * SORT_CTAS);
@@ -349,11 +418,11 @@ int embed_backward(const SortArgs& so, const SumArgs& su, cudaStream_t s) {
   const unsigned pieces = (unsigned)((su.T + PIECE - 1) / PIECE);
   const int vecs = su.H / Vec<T>::N;
   const int th = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
-  embed_sum_kernel<T><<<dim3(pieces, (vecs + th - 1) / th), th, 0, s>>>(su);
+  launch_k(embed_sum_kernel<T>, dim3(pieces, (vecs + th - 1) / th), dim3(th), 0, s, true, su);
   if (int rc = op_launched("embedding sum")) return rc;
-  if (pieces > 1) {
-    const int v4 = su.H / 4, tj = v4 >= 256 ? 256 : (v4 + 31) / 32 * 32;
-    embed_join_kernel<T><<<dim3(pieces - 1, (v4 + tj - 1) / tj), tj, 0, s>>>(su);
+  if (su.T > LONG) {
+    const unsigned runs = (unsigned)(su.T / LONG < 64 ? su.T / LONG : 64);
+    launch_k(embed_join_kernel<T>, dim3(runs, (su.H + 127) / 128), dim3(256), 0, s, true, su);
     return op_launched("embedding join");
   }
   return GOCR_OK;
@@ -382,7 +451,8 @@ int gocr_op_embed(int dtype, const void* embed, const void* mask_embed, const in
 
 size_t gocr_op_embed_backward_workspace(int T, int H) {
   if (T < 0 || H < 1) return 0;
-  return sort_bytes(T) + (size_t)((T + PIECE - 1) / PIECE) * 2 * H * 4 + 256;
+  const size_t pieces = (size_t)(T + PIECE - 1) / PIECE;
+  return sort_bytes(T) + pieces * 2 * H * 4 + up256(pieces * 4 + 4) + 256;
 }
 
 int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* d_embed, void* d_mask, int T, int H,
@@ -410,7 +480,10 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
   so.digit_bits = (bits + so.passes - 1) / so.passes;
   so.d_embed = d_embed; so.embed_bytes = (size_t)V * H * es;
   so.d_mask = d_mask; so.mask_bytes = (size_t)H * es;
-  SumArgs su{dy, so.key[1], so.pos[1], d_embed, d_mask, (float*)(ws + 4 * arr), T, H, V, scale};
+  float* part = (float*)(ws + 4 * arr);
+  int* n_long = (int*)(part + (size_t)((T + PIECE - 1) / PIECE) * 2 * H);
+  so.n_long = n_long;
+  SumArgs su{dy, so.key[1], so.pos[1], d_embed, d_mask, part, n_long, n_long + 1, T, H, V, scale};
   return dtype == GOCR_DTYPE_BF16 ? embed_backward<bf16>(so, su, s) : embed_backward<float>(so, su, s);
 }
 

@@ -166,9 +166,15 @@ def _p32(a: np.ndarray):
 # torch plumbing (device memory and streams only)
 # ----------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def to_device(a: np.ndarray, dtype: str, device):
@@ -474,34 +480,56 @@ def op_attention(q, kc, vc, lim, dtype: int, lo2=None, hi2=None):
 # training and scoring operators
 # ----------------------------------------------------------------------------
 
-def _want(name: str, t, shape, *dtypes, device=None):
-    """Check one operand: a contiguous CUDA tensor of this shape (None = any size) and one of the dtypes."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be [{', '.join('*' if w is None else str(w) for w in shape)}], got {list(t.shape)}")
+def _want(name: str, t, shape: tuple, dtype, device):
+    """Check one operand: a contiguous CUDA tensor of this shape, dtype and device."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    _on_device(name, t, device)
-
-
-def _on_device(name: str, t, device):
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands are on {device}")
+
+
+def _lead(name: str, t, dims: int, *dtypes):
+    """Check the type and rank of the operand that the others follow."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be a tensor of {dims} dimensions, got {list(t.shape)}")
+
+
+class _On:
+    """The device's current stream; makes the device current where another one is."""
+
+    __slots__ = ("index", "other")
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError(f"the operands must be CUDA tensors, got {device}")
+        self.index = device.index
+
+    def __enter__(self):
+        torch = _torch()
+        self.other = None
+        if torch.cuda.current_device() != self.index:
+            self.other = torch.cuda.device(self.index)
+            self.other.__enter__()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+        return raw(self.index) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
 
 
 def _workspace(ws, need: int, device):
     torch = _torch()
     if ws is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
-    _want("workspace", ws, (None,), torch.uint8, device=device)
+    _want("workspace", ws, (ws.numel(),), torch.uint8, device)
     return ws
-
-
-def _stream(device):
-    return _torch().cuda.current_stream(device).cuda_stream
 
 
 def op_embed(ids, embed, mask_embed=None, scale: float = 1.0):
@@ -509,16 +537,16 @@ def op_embed(ids, embed, mask_embed=None, scale: float = 1.0):
     [T]) name; id -1 is the [M] row mask_embed [H] (zero without one), any
     other id outside the table a row of zeros."""
     torch = _torch()
-    _want("embed", embed, (None, None), torch.bfloat16, torch.float32)
-    dev, (V, H) = embed.device, embed.shape
-    _want("ids", ids, (None,), torch.int32, device=dev)
+    _lead("embed", embed, 2, torch.bfloat16, torch.float32)
+    dev, (V, H), T = embed.device, embed.shape, ids.numel()
+    _want("embed", embed, (V, H), embed.dtype, dev)
+    _want("ids", ids, (T,), torch.int32, dev)
     if mask_embed is not None:
-        _want("mask_embed", mask_embed, (H,), embed.dtype, device=dev)
-    T = ids.shape[0]
-    with torch.cuda.device(dev):
+        _want("mask_embed", mask_embed, (H,), embed.dtype, dev)
+    with _On(dev) as stream:
         y = torch.empty((T, H), dtype=embed.dtype, device=dev)
         _check(load().gocr_op_embed(_dt(embed), embed.data_ptr(), mask_embed.data_ptr() if mask_embed is not None else None,
-                                    ids.data_ptr(), y.data_ptr(), T, H, V, scale, _stream(dev)))
+                                    ids.data_ptr(), y.data_ptr(), T, H, V, scale, stream))
     return y
 
 
@@ -527,16 +555,17 @@ def op_embed_backward(dy, ids, vocab: int, scale: float = 1.0, mask: bool = Fals
     mask else None), dense, in dy's dtype, fp32 sums in a fixed order."""
     torch = _torch()
     lib = load()
-    _want("dy", dy, (None, None), torch.bfloat16, torch.float32)
+    _lead("dy", dy, 2, torch.bfloat16, torch.float32)
     dev, (T, H) = dy.device, dy.shape
-    _want("ids", ids, (T,), torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    _want("dy", dy, (T, H), dy.dtype, dev)
+    _want("ids", ids, (T,), torch.int32, dev)
+    with _On(dev) as stream:
         d_embed = torch.empty((vocab, H), dtype=dy.dtype, device=dev)
         d_mask = torch.empty((H,), dtype=dy.dtype, device=dev) if mask else None
         ws = _workspace(workspace, lib.gocr_op_embed_backward_workspace(T, H), dev)
         _check(lib.gocr_op_embed_backward(_dt(dy), dy.data_ptr(), ids.data_ptr(), d_embed.data_ptr(),
                                           d_mask.data_ptr() if mask else None, T, H, vocab, scale, ws.data_ptr(),
-                                          ws.numel(), _stream(dev)))
+                                          ws.numel(), stream))
     return d_embed, d_mask
 
 
@@ -549,21 +578,22 @@ def _rows(name: str, t, T, heads, d, device):
         raise ValueError(f"{name} must be [{T}, {'*' if heads is None else heads}, {d}], got {list(t.shape)}")
     if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
         raise ValueError(f"the heads of a row of {name} must be contiguous, got strides {t.stride()}")
-    _on_device(name, t, device)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q is on {device}")
     return t.stride(0) if T > 1 else t.shape[1] * d
 
 
 def _packed_args(q, k, v, cu_seqlens, scale):
     torch = _torch()
-    if q.dim() != 3:
-        raise ValueError(f"q must be [T, Hq, d], got {list(q.shape)}")
+    _lead("q", q, 3, torch.bfloat16)
     dev, (T, Hq, d) = q.device, q.shape
     ld = [_rows("q", q, T, None, d, dev), _rows("k", k, T, None, d, dev)]
     ld.append(_rows("v", v, T, k.shape[1], d, dev))
-    _want("cu_seqlens", cu_seqlens, (None,), torch.int32, device=dev)
-    if cu_seqlens.shape[0] < 1:
+    n = cu_seqlens.numel()
+    _want("cu_seqlens", cu_seqlens, (n,), torch.int32, dev)
+    if n < 1:
         raise ValueError("cu_seqlens must hold at least one entry")
-    sizes = (cu_seqlens.shape[0] - 1, T, Hq, k.shape[1], d, *ld, d ** -0.5 if scale is None else scale)
+    sizes = (n - 1, T, Hq, k.shape[1], d, *ld, d ** -0.5 if scale is None else scale)
     return dev, T, Hq, k.shape[1], d, sizes
 
 
@@ -576,17 +606,17 @@ def op_attention_packed(q, k, v, cu_seqlens, scale=None, o=None, lse=None):
     not written."""
     torch = _torch()
     dev, T, Hq, Hkv, d, sizes = _packed_args(q, k, v, cu_seqlens, scale)
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         if o is None:
             o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
         else:
-            _want("o", o, (T, Hq, d), torch.bfloat16, device=dev)
+            _want("o", o, (T, Hq, d), torch.bfloat16, dev)
         if lse is None:
             lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
         else:
-            _want("lse", lse, (Hq, T), torch.float32, device=dev)
+            _want("lse", lse, (Hq, T), torch.float32, dev)
         _check(load().gocr_op_attention_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                               cu_seqlens.data_ptr(), *sizes, _stream(dev)))
+                                               cu_seqlens.data_ptr(), *sizes, stream))
     return o, lse
 
 
@@ -598,21 +628,21 @@ def op_attention_packed_backward(do, q, k, v, o, lse, cu_seqlens, scale=None, wo
     torch = _torch()
     lib = load()
     dev, T, Hq, Hkv, d, sizes = _packed_args(q, k, v, cu_seqlens, scale)
-    _want("do", do, (T, Hq, d), torch.bfloat16, device=dev)
-    _want("o", o, (T, Hq, d), torch.bfloat16, device=dev)
-    _want("lse", lse, (Hq, T), torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    _want("do", do, (T, Hq, d), torch.bfloat16, dev)
+    _want("o", o, (T, Hq, d), torch.bfloat16, dev)
+    _want("lse", lse, (Hq, T), torch.float32, dev)
+    with _On(dev) as stream:
         out = []
         for name, t, heads in (("dq", dq, Hq), ("dk", dk, Hkv), ("dv", dv, Hkv)):
             if t is None:
                 t = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev)
             else:
-                _want(name, t, (T, heads, d), torch.bfloat16, device=dev)
+                _want(name, t, (T, heads, d), torch.bfloat16, dev)
             out.append(t)
         ws = _workspace(workspace, lib.gocr_op_attention_packed_backward_workspace(T, Hq), dev)
         _check(lib.gocr_op_attention_packed_backward(
             do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(),
-            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), *sizes, ws.data_ptr(), ws.numel(), _stream(dev)))
+            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), *sizes, ws.data_ptr(), ws.numel(), stream))
     return tuple(out)
 
 
@@ -622,17 +652,17 @@ def op_linear_ce(x, w, labels, workspace=None):
     The logits are not stored."""
     torch = _torch()
     lib = load()
-    _want("x", x, (None, None), torch.bfloat16)
-    dev, (T, H) = x.device, x.shape
-    _want("w", w, (None, H), torch.bfloat16, device=dev)
-    _want("labels", labels, (T,), torch.int32, device=dev)
-    V = w.shape[0]
-    with torch.cuda.device(dev):
+    _lead("x", x, 2, torch.bfloat16)
+    dev, (T, H), V = x.device, x.shape, w.shape[0]
+    _want("x", x, (T, H), torch.bfloat16, dev)
+    _want("w", w, (V, H), torch.bfloat16, dev)
+    _want("labels", labels, (T,), torch.int32, dev)
+    with _On(dev) as stream:
         loss = torch.empty((T,), dtype=torch.float32, device=dev)
         lse = torch.empty((T,), dtype=torch.float32, device=dev)
         ws = _workspace(workspace, lib.gocr_op_linear_ce_workspace(T, V), dev)
         _check(lib.gocr_op_linear_ce(x.data_ptr(), w.data_ptr(), labels.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                                     T, V, H, ws.data_ptr(), ws.numel(), _stream(dev)))
+                                     T, V, H, ws.data_ptr(), ws.numel(), stream))
     return loss, lse
 
 
@@ -641,19 +671,19 @@ def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None):
     op_linear_ce, from its lse; dloss fp32 [T] holds the rows' weights."""
     torch = _torch()
     lib = load()
-    _want("x", x, (None, None), torch.bfloat16)
-    dev, (T, H) = x.device, x.shape
-    _want("w", w, (None, H), torch.bfloat16, device=dev)
-    _want("labels", labels, (T,), torch.int32, device=dev)
-    _want("dloss", dloss, (T,), torch.float32, device=dev)
-    _want("lse", lse, (T,), torch.float32, device=dev)
-    V = w.shape[0]
-    with torch.cuda.device(dev):
+    _lead("x", x, 2, torch.bfloat16)
+    dev, (T, H), V = x.device, x.shape, w.shape[0]
+    _want("x", x, (T, H), torch.bfloat16, dev)
+    _want("w", w, (V, H), torch.bfloat16, dev)
+    _want("labels", labels, (T,), torch.int32, dev)
+    _want("dloss", dloss, (T,), torch.float32, dev)
+    _want("lse", lse, (T,), torch.float32, dev)
+    with _On(dev) as stream:
         dx, dw = torch.empty_like(x), torch.empty_like(w)
         ws = _workspace(workspace, lib.gocr_op_linear_ce_backward_workspace(T, V, H), dev)
         _check(lib.gocr_op_linear_ce_backward(dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
                                               lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(),
-                                              ws.numel(), _stream(dev)))
+                                              ws.numel(), stream))
     return dx, dw
 
 
@@ -662,4 +692,4 @@ def op_status(device="cuda") -> None:
     operators gave up a wait since the last call."""
     torch = _torch()
     with torch.cuda.device(device):
-        _check(load().gocr_op_status(_stream(torch.cuda.current_device())))
+        _check(load().gocr_op_status(torch.cuda.current_stream().cuda_stream))
