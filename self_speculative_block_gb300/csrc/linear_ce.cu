@@ -6,24 +6,30 @@
 //
 // All of it is matrix products on tcgen05: 2 T V H operations forward, 6 T V H
 // backward (z again, dx, dw).  One persistent kernel shape serves the three
-// products: a CTA per SM walks 128 x 256 output tiles, a TMA warp keeps a ring
-// of 64-deep stages full, one thread issues the MMAs into one of two tensor
-// memory accumulators, and four warps (one row a thread) run the epilogue of
-// the other:
-//   STATS  (z) the row's maximum, sum of exponentials over the tile's 256
-//          columns, and the label's z: 8 bytes per row and tile leave the SM.
-//          A second kernel joins them in tile order;
+// products: a pair of CTAs walks 256 x 256 output tiles (128 rows a CTA; each
+// CTA stages its rows of A and half the columns of B, so a byte of shared
+// memory feeds twice the operations of a single CTA's tile), a TMA warp keeps
+// a ring of 64-deep stages full, one thread of the pair issues the MMAs into
+// one of two tensor memory accumulators, and four warps a CTA (one row a
+// thread) run the epilogue of the other:
+//   STATS  (z) the row's maximum and sum of exponentials over the tile's 256
+//          columns without the label's: 8 bytes per row and tile leave the SM.
+//          A second kernel joins them in tile order with the label's z, which
+//          it computes in fp32, and takes the loss as log(1 + exp(lse of the
+//          others - z of the label)): a confident row's small loss keeps its
+//          precision, where lse - z would cancel;
 //   GRAD   (z) g in bf16, stored to the piece of the vocabulary in the
 //          workspace;
-//   PROD   dx += g W (fp32, each tile owned by one CTA, or by one CTA per
-//          slice of the contraction in a slab of its own) and dw = g^T x (bf16)
-//          of the piece, both read g as it lies: rows for dx (K-major), columns
-//          for dw (M-major), W and x N-major, so nothing is transposed.
-// The vocabulary goes by in pieces whose g fits the workspace (and L2); the
-// tiles of both products of a piece share one launch, the longer ones first.
-// g is rounded to bf16 (relative 2^-8) because the tensor cores take it so;
-// every sum is in fp32.  Nothing is added by atomics across CTAs, so the same
-// inputs give the same bits.
+//   PROD   dx += g W (fp32 slabs) and dw = g^T x (bf16) of the piece, both read
+//          g as it lies: rows for dx (K-major), columns for dw (M-major), W and
+//          x N-major, so nothing is transposed.
+// The vocabulary goes by in pieces whose g fits the workspace.  In PROD every
+// pair gets the same number of K steps: its share of the dw tiles, which are
+// not split, and a range of the dx tiles' steps, which may end inside a tile;
+// the parts of a tile go to slabs of their own that a last kernel adds up in
+// order.  g is rounded to bf16 (relative 2^-8) because the tensor cores take
+// it so; every sum is in fp32.  Nothing is added by atomics across CTAs in an
+// order that could change, so the same inputs give the same bits.
 #include "../../include/gocr.h"
 #include "kernels.cuh"
 #include "tc.cuh"
@@ -34,9 +40,11 @@ using namespace gocr;
 
 namespace {
 
-constexpr int TM = 128, TN = 256, TK = 64;
-constexpr int STAGES = 4;
-constexpr int A_BYTES = TM * TK * 2, B_BYTES = TN * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int TM = 256, TN = 256, TK = 64;  // of a pair
+constexpr int RM = TM / 2, RN = TN / 2;     // rows of A and columns of B that one CTA stages
+constexpr int STAGES = 6;
+constexpr int A_BYTES = RM * TK * 2, B_BYTES = RN * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int PAIRS = SM_COUNT / 2;
 constexpr int BOX = 64 * 128;            // one box of 64 rows x 64 columns
 constexpr int STORE_BYTES = 32 * 128;    // one epilogue box: 32 rows x 128 bytes
 constexpr int OFF_STORE = STAGES * STAGE_BYTES;
@@ -57,6 +65,22 @@ struct Maps {
   CUtensorMap out1;     // PROD: dw
 };
 
+// How PROD's work is dealt to the pairs.  Pairs 0 .. c - 1 take one dw tile
+// more than the others; the dx steps (tiles in order, `steps` each) are cut
+// into ranges of q_hi steps for those pairs and q_lo for the others.
+struct Deal {
+  int c, q_hi, q_lo;
+  int steps, tiles;        // dx: K steps of a tile, tiles
+  __host__ __device__ int begin(int p) const {
+    const int s = p < c ? p * q_hi : c * q_hi + (p - c) * q_lo;
+    return s < steps * tiles ? s : steps * tiles;
+  }
+  __host__ __device__ int pair_of(int s) const { return s < c * q_hi ? s / q_hi : c + (s - c * q_hi) / q_lo; }
+  // parts of dx tile t, and which of them pair p has
+  __host__ __device__ int parts(int t) const { return pair_of((t + 1) * steps - 1) - pair_of(t * steps) + 1; }
+  __host__ __device__ int part(int t, int p) const { return p - pair_of(t * steps); }
+};
+
 struct Args {
   int T, H, V;
   int v0, vc;           // GRAD, PROD: the piece of the vocabulary
@@ -64,48 +88,55 @@ struct Args {
   const float* lse;
   const float* dloss;
   float2* part;         // STATS: [T][vocabulary tiles] (maximum, sum)
-  float* zlab;          // STATS: [T] z of the label
-  int m_tiles, n_tiles;               // STATS, GRAD, and dx
-  int splits, split_k, slab_rows;     // dx: slices of the contraction, in K steps
-  int add;                            // dx: add to the slab (a later piece)
-  int m_tiles1;                       // dw
-  int tiles0, tiles;                  // tiles of the first product, of both
+  int m_tiles, n_tiles; // STATS, GRAD; n_tiles also of PROD
+  int tiles;            // STATS, GRAD: all; PROD: dw
+  Deal deal, before;    // PROD: this piece's, the earlier pieces' (tiles = 0: this is the first)
+  int slab_rows;
 };
 
 struct Tile {
   int prod;             // PROD: 0 dx, 1 dw
   int m0, n0, k0, ks;   // first row, column, K step; K steps
-  int nb;               // 64-column blocks of B
-  int row_out;          // dx: first row in the slabs
+  int half;             // 128 columns of B instead of 256
+  int row_out, add;     // dx: first row in the slabs; add to them
 };
 
-template <int KIND> __device__ __forceinline__ Tile tile_of(const Args& a, int i) {
-  Tile t;
-  t.prod = 0; t.k0 = 0; t.row_out = 0; t.nb = TN / 64;
+// The pair's i-th tile; false past the last one.
+template <int KIND> __device__ __forceinline__ bool tile_of(const Args& a, int pair, int i, Tile& t) {
+  t.prod = 0; t.k0 = 0; t.row_out = 0; t.half = 0; t.add = 0;
   if (KIND != PROD) {
-    // rows fastest: the CTAs of a wave share a few tiles of w
-    t.m0 = (i % a.m_tiles) * TM;
-    t.n0 = (i / a.m_tiles) * TN;
+    // rows fastest: the pairs of a wave share a few tiles of w
+    const int x = pair + i * PAIRS;
+    if (x >= a.tiles) return false;
+    t.m0 = (x % a.m_tiles) * TM;
+    t.n0 = (x / a.m_tiles) * TN;
     t.ks = (a.H + TK - 1) / TK;
-    return t;
+    return true;
   }
-  if (i < a.tiles0) {
-    const int s = i % a.splits, r = i / a.splits;
-    const int steps = (a.vc + TK - 1) / TK;
-    t.m0 = (r / a.n_tiles) * TM;
-    t.n0 = (r % a.n_tiles) * TN;
-    t.k0 = s * a.split_k;
-    t.ks = max(0, min(a.split_k, steps - t.k0));
-    t.row_out = s * a.slab_rows + t.m0;
+  const Deal& d = a.deal;
+  const int b = d.begin(pair), e = d.begin(pair + 1);
+  const int first = b / d.steps;
+  const int n_dx = e > b ? (e - 1) / d.steps - first + 1 : 0;
+  if (i < n_dx) {
+    const int x = first + i;
+    const int lo = max(b, x * d.steps), hi = min(e, (x + 1) * d.steps);
+    const int part = d.part(x, pair);
+    t.m0 = (x / a.n_tiles) * TM;
+    t.n0 = (x % a.n_tiles) * TN;
+    t.k0 = lo - x * d.steps;
+    t.ks = hi - lo;
+    t.row_out = part * a.slab_rows + t.m0;
+    t.add = a.before.tiles && part < a.before.parts(x);
   } else {
-    i -= a.tiles0;
+    const int x = pair + (i - n_dx) * PAIRS;
+    if (x >= a.tiles) return false;
     t.prod = 1;
-    t.m0 = (i / a.n_tiles) * TM;
-    t.n0 = (i % a.n_tiles) * TN;
+    t.m0 = (x / a.n_tiles) * TM;
+    t.n0 = (x % a.n_tiles) * TN;
     t.ks = (a.T + TK - 1) / TK;
   }
-  t.nb = min(TN / 64, (a.H - t.n0 + 63) / 64);
-  return t;
+  t.half = a.H - t.n0 <= RN;
+  return true;
 }
 
 __device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
@@ -118,68 +149,79 @@ template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
-  uint64_t* empty = full + STAGES;
-  uint64_t* acc_full = empty + STAGES;  // [2]
-  uint64_t* acc_free = acc_full + 2;    // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BAR);  // the even CTA's: both CTAs' loads of a stage
+  uint64_t* empty = full + STAGES;      // each CTA's: the stage has been read
+  uint64_t* acc_full = empty + STAGES;  // [2], each CTA's
+  uint64_t* acc_free = acc_full + 2;    // [2], the even CTA's: the epilogue warps of both
   uint32_t* holder = reinterpret_cast<uint32_t*>(acc_free + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
 
   if (tid == 0) {
+    tc::grid_dep_launch();
     for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(full + s, 1);
       tc::mbar_init(empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(acc_full + b, 1);
-      tc::mbar_init(acc_free + b, 4);
+      tc::mbar_init(acc_free + b, 8);
     }
     tc::fence_mbar_init();
   }
   __syncwarp();
-  if (warp == 1) tc::tmem_alloc(holder, 512);
+  if (warp == 1) tc::tmem_alloc_pair(holder, 512);
   tc::fence_before_sync();
   __syncthreads();
+  __syncwarp();
+  tc::cluster_arrive_release();  // barriers of both CTAs are initialised
+  tc::cluster_wait_acquire();
   tc::fence_after_sync();
   const uint32_t tmem = *holder;
+  tc::grid_dep_wait();
   bool ok = true;
+  Tile t;
 
   if (warp == 0) {
     if (lane == 0) {
       int st = 0, ph = 0;
-      for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
-        const Tile t = tile_of<KIND>(a, i);
-        const uint32_t bytes = A_BYTES + t.nb * BOX;
+      for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
+        const uint32_t bytes = A_BYTES + (t.half ? BOX : B_BYTES);
+        const int m = t.m0 + rank * RM, n = t.n0 + rank * (t.half ? 64 : RN);
         for (int k = 0; k < t.ks; ++k) {
           if (!(ok = tc::mbar_wait_ns(empty + st, ph ^ 1))) break;
           uint8_t* sa = sm + st * STAGE_BYTES;
           uint8_t* sb = sa + A_BYTES;
           const int kk = (t.k0 + k) * TK;
-          tc::mbar_expect_tx(full + st, bytes);
+          if (rank == 0) tc::mbar_expect_tx(full + st, 2 * bytes);
+          const uint32_t bar = tc::mapa(tc::smem_u32(full + st), 0);
           if (KIND != PROD) {
-            tc::tma_load_2d(sa, &maps.a0, kk, t.m0, full + st);
-            tc::tma_load_2d(sb, &maps.b0, kk, a.v0 + t.n0, full + st);
-          } else if (t.prod == 0) {
-            tc::tma_load_2d(sa, &maps.a0, kk, t.m0, full + st);
-            for (int b = 0; b < t.nb; ++b) tc::tma_load_2d(sb + b * BOX, &maps.b0, t.n0 + b * 64, a.v0 + kk, full + st);
+            tc::tma_load_2d_pair(sa, &maps.a0, kk, m, bar);
+            tc::tma_load_2d_pair(sb, &maps.b0, kk, a.v0 + n, bar);
           } else {
-            tc::tma_load_2d(sa, &maps.a1, t.m0, kk, full + st);
-            tc::tma_load_2d(sa + BOX, &maps.a1, t.m0 + 64, kk, full + st);
-            for (int b = 0; b < t.nb; ++b) tc::tma_load_2d(sb + b * BOX, &maps.b1, t.n0 + b * 64, kk, full + st);
+            if (t.prod == 0) {
+              tc::tma_load_2d_pair(sa, &maps.a0, kk, m, bar);
+            } else {
+              tc::tma_load_2d_pair(sa, &maps.a1, m, kk, bar);
+              tc::tma_load_2d_pair(sa + BOX, &maps.a1, m + 64, kk, bar);
+            }
+            const CUtensorMap* mb = t.prod ? &maps.b1 : &maps.b0;
+            const int row = t.prod ? kk : a.v0 + kk;
+            tc::tma_load_2d_pair(sb, mb, n, row, bar);
+            if (!t.half) tc::tma_load_2d_pair(sb + BOX, mb, n + 64, row, bar);
           }
           if (++st == STAGES) { st = 0; ph ^= 1; }
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int st = 0, ph = 0, acc = 0, aph = 0;
-      for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
-        const Tile t = tile_of<KIND>(a, i);
+      for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
         if (!(ok = tc::mbar_wait_ns(acc_free + acc, aph ^ 1))) break;
         tc::fence_after_sync();
         const uint32_t d = tmem + acc * TN;
-        uint32_t idesc = tc::idesc_bf16(TM, t.nb * 64);
+        uint32_t idesc = tc::idesc_bf16(TM, t.half ? RN : TN);
         if (KIND == PROD) idesc |= tc::IDESC_B_MN | (t.prod ? tc::IDESC_A_MN : 0u);
         for (int k = 0; k < t.ks; ++k) {
           if (!(ok = tc::mbar_wait_ns(full + st, ph))) break;
@@ -189,13 +231,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           for (int j = 0; j < TK / 16; ++j) {
             const uint64_t ad = KIND == PROD && t.prod ? tc::sdesc_sw128_mn(sa + j * 2048, BOX) : tc::sdesc_sw128(sa + j * 32);
             const uint64_t bd = KIND == PROD ? tc::sdesc_sw128_mn(sb + j * 2048, BOX) : tc::sdesc_sw128(sb + j * 32);
-            tc::mma_bf16(d, ad, bd, idesc, k > 0 || j > 0 ? 1u : 0u);
+            tc::mma_bf16_pair(d, ad, bd, idesc, k > 0 || j > 0 ? 1u : 0u);
           }
-          tc::mma_commit(empty + st);
+          tc::mma_commit_pair(empty + st);
           if (++st == STAGES) { st = 0; ph ^= 1; }
         }
         if (!ok) break;
-        tc::mma_commit(acc_full + acc);
+        tc::mma_commit_pair(acc_full + acc);
         acc ^= 1;
         if (acc == 0) aph ^= 1;
       }
@@ -204,13 +246,14 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
     const int q = warp & 3;  // the tensor memory lanes this warp may read: 32 q ..
     uint8_t* box = sm + OFF_STORE + q * 2 * STORE_BYTES;
     int acc = 0, aph = 0, buf = 0;
-    for (int i = blockIdx.x; i < a.tiles; i += gridDim.x) {
-      const Tile t = tile_of<KIND>(a, i);
+    for (int i = 0; tile_of<KIND>(a, pair, i, t); ++i) {
       // one verdict a warp: its lanes leave the loop together
       if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(acc_full + acc, aph)))) break;
       tc::fence_after_sync();
       const uint32_t src = tmem + acc * TN + ((uint32_t)(q * 32) << 16);
-      const int row = t.m0 + q * 32 + lane;
+      const int row0 = t.m0 + rank * RM + q * 32;  // the warp's first row
+      const int row = row0 + lane;
+      const uint32_t freed = tc::mapa(tc::smem_u32(acc_free + acc), 0);
       if (KIND == STATS) {
         const bool in = row < a.T;
         const int label = in ? a.labels[row] : -1;
@@ -225,6 +268,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             for (int j = 0; j < 32; ++j)
               if (col + j >= a.V) v[j] = -INFINITY;
           }
+          const unsigned at = (unsigned)label - (unsigned)col;
+          if (__any_sync(0xffffffffu, at < 32u)) {  // the label's column is the join kernel's
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = at == (unsigned)j ? -INFINITY : v[j];
+          }
           float mc = v[0];
 #pragma unroll
           for (int j = 1; j < 32; ++j) mc = fmaxf(mc, v[j]);
@@ -238,17 +286,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           }
           s = fmaf(s, m == -INFINITY ? 0.f : exp2f(fmaf(m, LOG2E, -ref)), e0 + e1);
           m = mn;
-          const unsigned at = (unsigned)(label - col);
-          if (__any_sync(0xffffffffu, at < 32u)) {
-            float z = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z = at == (unsigned)j ? v[j] : z;
-            if (at < 32u && label < a.V) a.zlab[row] = z;
-          }
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(acc_free + acc);
+        if (lane == 0) tc::mbar_arrive_cluster(freed);
         if (in) a.part[(size_t)row * a.n_tiles + t.n0 / TN] = make_float2(m, s);
       } else if (KIND == GRAD) {
         int label = -1;
@@ -295,17 +336,17 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (t.m0 + q * 32 < a.T) tc::tma_store_2d(&maps.out0, bx, t.n0 + c, t.m0 + q * 32);
+            if (row0 < a.T) tc::tma_store_2d(&maps.out0, bx, t.n0 + c, row0);
             tc::bulk_commit();
           }
           buf ^= 1;
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(acc_free + acc);
+        if (lane == 0) tc::mbar_arrive_cluster(freed);
       } else {
         const int step = t.prod ? 64 : 32;  // columns of one box
-        for (int c = 0; c < t.nb * 64 && t.n0 + c < a.H; c += step) {
+        for (int c = 0; c < TN && t.n0 + c < a.H; c += step) {
           if (lane == 0) bulk_wait_read1();
           __syncwarp();
           uint8_t* bx = box + buf * STORE_BYTES;
@@ -315,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
 #pragma unroll
             for (int g = 0; g < 8; ++g)
               *reinterpret_cast<float4*>(bx + box_at(lane, g)) =
-                  t.ks > 0 ? make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                  make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -336,12 +377,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
+            const int out = t.row_out + rank * RM + q * 32;
             if (t.prod) {
-              if (a.v0 + t.m0 + q * 32 < a.V) tc::tma_store_2d(&maps.out1, bx, t.n0 + c, a.v0 + t.m0 + q * 32);
-            } else if (a.add) {
-              tc::tma_add_2d(&maps.out0, bx, t.n0 + c, t.row_out + q * 32);
+              if (a.v0 + row0 < a.V) tc::tma_store_2d(&maps.out1, bx, t.n0 + c, a.v0 + row0);
+            } else if (t.add) {
+              tc::tma_add_2d(&maps.out0, bx, t.n0 + c, out);
             } else {
-              tc::tma_store_2d(&maps.out0, bx, t.n0 + c, t.row_out + q * 32);
+              tc::tma_store_2d(&maps.out0, bx, t.n0 + c, out);
             }
             tc::bulk_commit();
           }
@@ -349,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(acc_free + acc);
+        if (lane == 0) tc::mbar_arrive_cluster(freed);
       }
       acc ^= 1;
       if (acc == 0) aph ^= 1;
@@ -359,17 +401,41 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
   tc::fence_before_sync();
   __syncthreads();
+  __syncwarp();
+  tc::cluster_arrive_release();  // the other CTA still reads this one's shared memory and barriers
+  tc::cluster_wait_acquire();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc_pair(tmem, 512);
   }
 }
 
-// One warp per row: the tiles' (maximum, sum) in a fixed order.
-__global__ void __launch_bounds__(256) linear_ce_join_kernel(const float2* part, const float* zlab, const int* labels,
-                                                             float* loss, float* lse, int T, int V, int n_tiles) {
+// One warp per row: the tiles' (maximum, sum) of the columns that are not the
+// label, in a fixed order, and the label's z = x . w in fp32.
+__global__ void __launch_bounds__(256) linear_ce_join_kernel(const float2* part, const bf16* x, const bf16* w,
+                                                             const int* labels, float* loss, float* lse, int T, int V,
+                                                             int H, int n_tiles) {
+  tc::grid_dep_wait();
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= T) return;
+  const int label = labels[t];
+  const bool has = (unsigned)label < (unsigned)V;
+  float z = 0.f;
+  if (has) {
+    const uint4* xr = reinterpret_cast<const uint4*>(x + (size_t)t * H);
+    const uint4* wr = reinterpret_cast<const uint4*>(w + (size_t)label * H);
+    for (int i = lane; i < H / 8; i += 32) {
+      const uint4 p = xr[i], q = wr[i];
+      const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z = fmaf(__uint_as_float(ps[e] << 16), __uint_as_float(qs[e] << 16), z);
+        z = fmaf(__uint_as_float(ps[e] & 0xffff0000u), __uint_as_float(qs[e] & 0xffff0000u), z);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
   const float2* p = part + (size_t)t * n_tiles;
   float m = -INFINITY;
   for (int i = lane; i < n_tiles; i += 32) m = fmaxf(m, p[i].x);
@@ -383,19 +449,32 @@ __global__ void __launch_bounds__(256) linear_ce_join_kernel(const float2* part,
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) {
-    const float l = m + logf(s);
-    lse[t] = l;
-    loss[t] = (unsigned)labels[t] < (unsigned)V ? l - zlab[t] : 0.f;
+    const float others = m + logf(s);  // -infinity when the label is the only column
+    float l = 0.f, all = others;
+    if (has) {
+      const float d = others - z;      // loss = log(1 + exp(d))
+      l = (d > 0.f ? d : 0.f) + log1pf(expf(-fabsf(d)));
+      if (d != d) l = d;               // a NaN (or infinite) logit
+      all = z + l;
+      if (d > 0.f) all = others + log1pf(expf(-d));
+    }
+    lse[t] = all;
+    loss[t] = l;
   }
 }
 
-// dx = the sum of the slabs, in slab order.
-__global__ void __launch_bounds__(256) linear_ce_dx_kernel(const float* slabs, bf16* dx, int T, int H, int splits,
-                                                           size_t slab) {
+// dx = the sum of the tile's parts, in slab order.
+__global__ void __launch_bounds__(256) linear_ce_dx_kernel(const float* slabs, bf16* dx, int T, int H, int n_tiles,
+                                                           size_t slab, Deal last, Deal before) {
+  tc::grid_dep_wait();
   const size_t n = (size_t)T * H / 8, step = (size_t)gridDim.x * 256;
   for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += step) {
+    const int row = (int)(i * 8 / H), col = (int)(i * 8 % H);
+    const int tile = row / TM * n_tiles + col / TN;
+    int parts = last.parts(tile);
+    if (before.tiles) parts = max(parts, before.parts(tile));
     float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
-    for (int s = 0; s < splits; ++s) {
+    for (int s = 0; s < parts; ++s) {
       const float4* p = reinterpret_cast<const float4*>(slabs + s * slab + i * 8);
       const float4 x = p[0], y = p[1];
       u.x += x.x; u.y += x.y; u.z += x.z; u.w += x.w;
@@ -417,46 +496,90 @@ bool map2(CUtensorMap* m, const void* p, int rows, int cols, size_t ld, int box_
   return encode_tmap(m, p, false, 2, dims, st, box);
 }
 
-// Columns of one piece's g: G_BYTES of workspace, so that a piece is read back
-// from L2, but at least MIN_PIECE columns, which keep the contraction of dx and
-// the tiles of dw long enough to fill the SMs.
+// Columns of one piece's g: G_BYTES of workspace, but at least MIN_PIECE
+// columns, which keep the contraction of dx and the tiles of dw long enough to
+// fill the SMs.
 constexpr size_t G_BYTES = 64u << 20;
 constexpr int MIN_PIECE = 4096;
+// A dw tile's epilogue in K steps, for the balance between the pairs.
+constexpr int DW_EXTRA = 4;
+constexpr int MAX_PARTS = 32;
 
-struct Plan2 {
-  int piece, splits, slab_rows;
+struct BackwardPlan {
+  int piece, slabs, slab_rows;
+  Deal full, last;         // of the pieces before the last (tiles = 0: none), of the last
   size_t off_slab, bytes;
 };
 
-Plan2 backward_plan(int T, int V, int H) {
-  Plan2 p;
+Deal deal_of(int T, int vc, int H) {
+  Deal d;
+  const int nt = cdiv(H, TN);
+  d.steps = cdiv(vc, TK);
+  d.tiles = cdiv(T, TM) * nt;
+  const long long dx = (long long)d.steps * d.tiles;
+  const int dw = cdiv(vc, TM) * nt, cost = cdiv(T, TK) + DW_EXTRA;
+  const int lo = dw / PAIRS;
+  d.c = dw % PAIRS;
+  const long long each = (dx + (long long)dw * cost + PAIRS - 1) / PAIRS;
+  // no more than MAX_PARTS - 1 ranges to a tile, so that its parts fit the slabs
+  const int least = cdiv(d.steps, MAX_PARTS - 2);
+  long long q_hi = each - (lo + 1LL) * cost, q_lo = each - (long long)lo * cost;
+  if (q_lo < least) q_lo = least;
+  if (q_hi < least) q_hi = 0;
+  const long long rest = dx - d.c * q_hi;  // what the others take, whatever the first took
+  if (q_lo * (PAIRS - d.c) < rest) q_lo = (rest + PAIRS - d.c - 1) / (PAIRS - d.c);
+  d.q_hi = (int)q_hi;
+  d.q_lo = (int)q_lo;
+  return d;
+}
+
+// Ranges of at least q steps cut a tile into at most this many parts.
+int most_parts(const Deal& d) {
+  const int q = d.c && d.q_hi && d.q_hi < d.q_lo ? d.q_hi : d.q_lo;
+  return cdiv(d.steps - 1, q) + 1;
+}
+
+BackwardPlan backward_plan(int T, int V, int H) {
+  BackwardPlan p;
   const int v_all = cdiv(V, TN) * TN;
   long long c = (long long)(G_BYTES / 2 / (T < 1 ? 1 : T)) / TN * TN;
   if (c < MIN_PIECE) c = MIN_PIECE;
   p.piece = c < v_all ? (int)c : v_all;
-  // few tiles of dx: slices of the contraction, at least 512 deep, so that
-  // dx alone has a tile for every SM
-  const int tiles = cdiv(T < 1 ? 1 : T, TM) * cdiv(H, TN);
-  int s = cdiv(SM_COUNT, tiles);
-  if (s > p.piece / 512) s = p.piece / 512;
-  if (s > 32) s = 32;
-  p.splits = s < 1 ? 1 : s;
-  p.slab_rows = cdiv(T, TM) * TM;
+  const int n = cdiv(V, p.piece), rows = T < 1 ? 1 : T;
+  p.last = deal_of(rows, V - (n - 1) * p.piece, H);
+  p.full = deal_of(rows, p.piece, H);
+  if (n == 1) p.full.tiles = 0;
+  p.slabs = most_parts(p.last);
+  if (n > 1 && most_parts(p.full) > p.slabs) p.slabs = most_parts(p.full);
+  p.slab_rows = cdiv(rows, TM) * TM;
   p.off_slab = up256((size_t)T * p.piece * 2);
-  p.bytes = p.off_slab + (size_t)p.splits * p.slab_rows * H * 4 + 256;
+  p.bytes = p.off_slab + (size_t)p.slabs * p.slab_rows * H * 4 + 256;
   return p;
 }
 
 int check_shape(int T, int V, int H) {
-  if (T < 0 || T > (1 << 24) || V < 1 || V > (1 << 24) || H < 8 || H % 8 || H > (1 << 16))
+  if (T < 0 || T > (1 << 22) || V < 1 || V > (1 << 22) || H < 8 || H % 8 || H > (1 << 15))
     return op_fail(GOCR_EINVAL, "bad shape T=%d V=%d H=%d", T, V, H);
   return GOCR_OK;
 }
 
-template <int KIND> int launch(const Maps& m, const Args& a, cudaStream_t s) {
+template <int KIND> int launch(const Maps& m, const Args& a, int pairs, cudaStream_t s) {
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&linear_ce_kernel<KIND>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
-  linear_ce_kernel<KIND><<<a.tiles < SM_COUNT ? a.tiles : SM_COUNT, THREADS, SMEM, s>>>(m, a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (pairs < PAIRS ? pairs : PAIRS));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, linear_ce_kernel<KIND>, m, a);
   return op_launched("linear_ce");
 }
 
@@ -477,7 +600,7 @@ extern "C" {
 
 size_t gocr_op_linear_ce_workspace(int T, int V) {
   if (T < 0 || V < 1) return 0;
-  return up256((size_t)T * cdiv(V, TN) * 8) + up256((size_t)T * 4) + 256;
+  return up256((size_t)T * cdiv(V, TN) * 8) + 256;
 }
 
 int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,
@@ -496,10 +619,10 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
   a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(V, TN);
   a.tiles = a.m_tiles * a.n_tiles;
   a.part = (float2*)workspace;
-  a.zlab = (float*)((char*)workspace + up256((size_t)T * a.n_tiles * 8));
-  if (!map2(&m.a0, x, T, H, H, TM) || !map2(&m.b0, w, V, H, H, TN)) return bad_map();
-  if (int rc = launch<STATS>(m, a, s)) return rc;
-  linear_ce_join_kernel<<<cdiv(T, 8), 256, 0, s>>>(a.part, a.zlab, labels, loss, lse, T, V, a.n_tiles);
+  if (!map2(&m.a0, x, T, H, H, RM) || !map2(&m.b0, w, V, H, H, RN)) return bad_map();
+  if (int rc = launch<STATS>(m, a, a.tiles, s)) return rc;
+  launch_k(linear_ce_join_kernel, dim3(cdiv(T, 8)), dim3(256), 0, s, true, (const float2*)a.part, (const bf16*)x,
+           (const bf16*)w, labels, loss, lse, T, V, H, a.n_tiles);
   return op_launched("linear_ce join");
 }
 
@@ -516,7 +639,7 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
     return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)dx | (uintptr_t)dw | (uintptr_t)workspace) & 15)
     return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
-  const Plan2 p = backward_plan(T, V, H);
+  const BackwardPlan p = backward_plan(T, V, H);
   if (workspace_bytes < p.bytes) return op_fail(GOCR_ECAPACITY, "workspace too small");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
@@ -526,11 +649,11 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
   }
   float* slabs = (float*)((char*)workspace + p.off_slab);
   Maps z{}, pr{};
-  if (!map2(&z.a0, x, T, H, H, TM) || !map2(&z.b0, w, V, H, H, TN) || !map2(&pr.b0, w, V, H, H, 64) ||
+  if (!map2(&z.a0, x, T, H, H, RM) || !map2(&z.b0, w, V, H, H, RN) || !map2(&pr.b0, w, V, H, H, 64) ||
       !map2(&pr.b1, x, T, H, H, 64) || !map2(&pr.out1, dw, V, H, H, 32))
     return bad_map();
   {
-    const unsigned long long dims[2] = {(unsigned long long)H, (unsigned long long)p.splits * p.slab_rows},
+    const unsigned long long dims[2] = {(unsigned long long)H, (unsigned long long)p.slabs * p.slab_rows},
                              st[1] = {(unsigned long long)H * 4};
     const unsigned box[2] = {32, 32};
     if (!encode_tmap(&pr.out0, slabs, true, 2, dims, st, box)) return bad_map();
@@ -540,25 +663,24 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
     a.T = T; a.H = H; a.V = V;
     a.labels = labels; a.lse = lse; a.dloss = dloss;
     a.v0 = v0; a.vc = V - v0 < p.piece ? V - v0 : p.piece;
-    if (!map2(&z.out0, workspace, T, a.vc, p.piece, 32) || !map2(&pr.a0, workspace, T, a.vc, p.piece, TM) ||
+    if (!map2(&z.out0, workspace, T, a.vc, p.piece, 32) || !map2(&pr.a0, workspace, T, a.vc, p.piece, RM) ||
         !map2(&pr.a1, workspace, T, a.vc, p.piece, 64))
       return bad_map();
     a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(a.vc, TN);
     a.tiles = a.m_tiles * a.n_tiles;
-    if (int rc = launch<GRAD>(z, a, s)) return rc;
+    if (int rc = launch<GRAD>(z, a, a.tiles, s)) return rc;
     a.n_tiles = cdiv(H, TN);
-    a.m_tiles1 = cdiv(a.vc, TM);
-    a.splits = p.splits;
-    a.split_k = cdiv(cdiv(a.vc, TK), p.splits);
+    a.tiles = cdiv(a.vc, TM) * a.n_tiles;
+    a.deal = v0 + p.piece < V ? p.full : p.last;
+    a.before = p.full;
+    if (v0 == 0) a.before.tiles = 0;
     a.slab_rows = p.slab_rows;
-    a.add = v0 > 0;
-    a.tiles0 = a.m_tiles * a.n_tiles * a.splits;
-    a.tiles = a.tiles0 + a.m_tiles1 * a.n_tiles;
-    if (int rc = launch<PROD>(pr, a, s)) return rc;
+    if (int rc = launch<PROD>(pr, a, PAIRS, s)) return rc;
   }
   const size_t vecs = (size_t)T * H / 8;
   const unsigned blocks = (unsigned)(vecs / 256 + 1 < 8u * SM_COUNT ? vecs / 256 + 1 : 8u * SM_COUNT);
-  linear_ce_dx_kernel<<<blocks, 256, 0, s>>>(slabs, (bf16*)dx, T, H, p.splits, (size_t)p.slab_rows * H);
+  launch_k(linear_ce_dx_kernel, dim3(blocks), dim3(256), 0, s, true, (const float*)slabs, (bf16*)dx, T, H, cdiv(H, TN),
+           (size_t)p.slab_rows * H, p.last, p.full);
   return op_launched("linear_ce dx");
 }
 
