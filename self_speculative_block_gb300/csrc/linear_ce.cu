@@ -42,14 +42,15 @@ namespace {
 
 constexpr int TM = 256, TN = 256, TK = 64;  // of a pair
 constexpr int RM = TM / 2, RN = TN / 2;     // rows of A and columns of B that one CTA stages
-constexpr int STAGES = 6;
-constexpr int A_BYTES = RM * TK * 2, B_BYTES = RN * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int A_BYTES = RM * TK * 2, B_BYTES = RN * TK * 2;
+constexpr int RING = 6 * (A_BYTES + B_BYTES);
+constexpr int MAX_STAGES = 16;
 constexpr int PAIRS = SM_COUNT / 2;
 constexpr int BOX = 64 * 128;            // one box of 64 rows x 64 columns
 constexpr int STORE_BYTES = 32 * 128;    // one epilogue box: 32 rows x 128 bytes
-constexpr int OFF_STORE = STAGES * STAGE_BYTES;
+constexpr int OFF_STORE = RING;
 constexpr int OFF_BAR = OFF_STORE + 4 * 2 * STORE_BYTES;
-constexpr int SMEM = OFF_BAR + 256 + 1024;
+constexpr int SMEM = OFF_BAR + 512 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 constexpr int THREADS = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr float LOG2E = 1.4426950408889634f;
@@ -89,6 +90,9 @@ struct Args {
   const float* dloss;
   float2* part;         // STATS: [T][vocabulary tiles] (maximum, sum)
   int m_tiles, n_tiles; // STATS, GRAD; n_tiles also of PROD
+  int tn;               // STATS, GRAD: columns of a tile
+  int stages;           // of the ring
+  int a_rows;           // rows of A that a CTA stages at most: 128, or fewer for few rows
   int tiles;            // STATS, GRAD: all; PROD: dw
   Deal deal, before;    // PROD: this piece's, the earlier pieces' (tiles = 0: this is the first)
   int slab_rows;
@@ -109,8 +113,9 @@ template <int KIND> __device__ __forceinline__ bool tile_of(const Args& a, int p
     const int x = pair + i * PAIRS;
     if (x >= a.tiles) return false;
     t.m0 = (x % a.m_tiles) * TM;
-    t.n0 = (x / a.m_tiles) * TN;
+    t.n0 = (x / a.m_tiles) * a.tn;
     t.ks = (a.H + TK - 1) / TK;
+    t.half = a.tn == RN;
     return true;
   }
   const Deal& d = a.deal;
@@ -150,16 +155,18 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + OFF_BAR);  // the even CTA's: both CTAs' loads of a stage
-  uint64_t* empty = full + STAGES;      // each CTA's: the stage has been read
-  uint64_t* acc_full = empty + STAGES;  // [2], each CTA's
+  uint64_t* empty = full + MAX_STAGES;  // each CTA's: the stage has been read
+  uint64_t* acc_full = empty + MAX_STAGES;  // [2], each CTA's
   uint64_t* acc_free = acc_full + 2;    // [2], the even CTA's: the epilogue warps of both
   uint32_t* holder = reinterpret_cast<uint32_t*>(acc_free + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+  const int a_bytes = a.a_rows * 128;
+  const int stage_bytes = a_bytes + (KIND != PROD && a.tn == RN ? BOX : B_BYTES);
 
   if (tid == 0) {
     tc::grid_dep_launch();
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < a.stages; ++s) {
       tc::mbar_init(full + s, 1);
       tc::mbar_init(empty + s, 1);
     }
@@ -186,17 +193,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
     if (lane == 0) {
       int st = 0, ph = 0;
       for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
-        const uint32_t bytes = A_BYTES + (t.half ? BOX : B_BYTES);
+        // few rows: the odd CTA has none; what its part of A then holds only
+        // reaches accumulator rows that nobody reads
+        const bool with_a = KIND == PROD || a.a_rows == RM || rank == 0;
+        const uint32_t bytes = 2 * (t.half ? BOX : B_BYTES) + (KIND == PROD || a.a_rows == RM ? 2 * A_BYTES : a_bytes);
         const int m = t.m0 + rank * RM, n = t.n0 + rank * (t.half ? 64 : RN);
         for (int k = 0; k < t.ks; ++k) {
           if (!(ok = tc::mbar_wait_ns(empty + st, ph ^ 1))) break;
-          uint8_t* sa = sm + st * STAGE_BYTES;
-          uint8_t* sb = sa + A_BYTES;
+          uint8_t* sa = sm + st * stage_bytes;
+          uint8_t* sb = sa + a_bytes;
           const int kk = (t.k0 + k) * TK;
-          if (rank == 0) tc::mbar_expect_tx(full + st, 2 * bytes);
+          if (rank == 0) tc::mbar_expect_tx(full + st, bytes);
           const uint32_t bar = tc::mapa(tc::smem_u32(full + st), 0);
           if (KIND != PROD) {
-            tc::tma_load_2d_pair(sa, &maps.a0, kk, m, bar);
+            if (with_a) tc::tma_load_2d_pair(sa, &maps.a0, kk, m, bar);
             tc::tma_load_2d_pair(sb, &maps.b0, kk, a.v0 + n, bar);
           } else {
             if (t.prod == 0) {
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             tc::tma_load_2d_pair(sb, mb, n, row, bar);
             if (!t.half) tc::tma_load_2d_pair(sb + BOX, mb, n + 64, row, bar);
           }
-          if (++st == STAGES) { st = 0; ph ^= 1; }
+          if (++st == a.stages) { st = 0; ph ^= 1; }
         }
       }
     }
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         for (int k = 0; k < t.ks; ++k) {
           if (!(ok = tc::mbar_wait_ns(full + st, ph))) break;
           tc::fence_after_sync();
-          const uint32_t sa = tc::smem_u32(sm + st * STAGE_BYTES), sb = sa + A_BYTES;
+          const uint32_t sa = tc::smem_u32(sm + st * stage_bytes), sb = sa + a_bytes;
 #pragma unroll
           for (int j = 0; j < TK / 16; ++j) {
             const uint64_t ad = KIND == PROD && t.prod ? tc::sdesc_sw128_mn(sa + j * 2048, BOX) : tc::sdesc_sw128(sa + j * 32);
@@ -234,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             tc::mma_bf16_pair(d, ad, bd, idesc, k > 0 || j > 0 ? 1u : 0u);
           }
           tc::mma_commit_pair(empty + st);
-          if (++st == STAGES) { st = 0; ph ^= 1; }
+          if (++st == a.stages) { st = 0; ph ^= 1; }
         }
         if (!ok) break;
         tc::mma_commit_pair(acc_full + acc);
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         const bool in = row < a.T;
         const int label = in ? a.labels[row] : -1;
         float m = -INFINITY, s = 0.f;
-        for (int c = 0; c < TN; c += 32) {
+        for (int c = 0; c < a.tn; c += 32) {
           const int col = t.n0 + c;
           if (col >= a.V) break;
           float v[32];
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(freed);
-        if (in) a.part[(size_t)row * a.n_tiles + t.n0 / TN] = make_float2(m, s);
+        if (in) a.part[(size_t)row * a.n_tiles + t.n0 / a.tn] = make_float2(m, s);
       } else if (KIND == GRAD) {
         int label = -1;
         float f = 0.f, ref = 0.f;
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         }
         const int col0 = a.v0 + t.n0;
         const bool has = label >= 0;
-        for (int c = 0; c < TN; c += 64) {
+        for (int c = 0; c < a.tn; c += 64) {
           if (t.n0 + c >= a.vc) break;
           if (lane == 0) bulk_wait_read1();
           __syncwarp();
@@ -410,53 +420,61 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   }
 }
 
-// One warp per row: the tiles' (maximum, sum) of the columns that are not the
+// Sum or maximum over the 128 threads of a CTA, in a fixed order.
+template <bool MAX> __device__ __forceinline__ float cta_reduce(float v, float* tmp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return MAX ? fmaxf(fmaxf(tmp[0], tmp[1]), fmaxf(tmp[2], tmp[3])) : (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+}
+
+// One CTA per row: the tiles' (maximum, sum) of the columns that are not the
 // label, in a fixed order, and the label's z = x . w in fp32.
-__global__ void __launch_bounds__(256) linear_ce_join_kernel(const float2* part, const bf16* x, const bf16* w,
-                                                             const int* labels, float* loss, float* lse, int T, int V,
-                                                             int H, int n_tiles) {
+__global__ void __launch_bounds__(128) linear_ce_join_kernel(const float2* part, const bf16* x, const bf16* w,
+                                                             const int* labels, float* loss, float* lse, int V, int H,
+                                                             int n_tiles) {
+  __shared__ float tmp[3][4];
+  const int t = blockIdx.x, tid = threadIdx.x;
   tc::grid_dep_wait();
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (t >= T) return;
   const int label = labels[t];
   const bool has = (unsigned)label < (unsigned)V;
+  const float2* p = part + (size_t)t * n_tiles;
+  float m = -INFINITY;
+  for (int i = tid; i < n_tiles; i += 128) m = fmaxf(m, p[i].x);
   float z = 0.f;
   if (has) {
     const uint4* xr = reinterpret_cast<const uint4*>(x + (size_t)t * H);
     const uint4* wr = reinterpret_cast<const uint4*>(w + (size_t)label * H);
-    for (int i = lane; i < H / 8; i += 32) {
-      const uint4 p = xr[i], q = wr[i];
-      const uint32_t ps[4] = {p.x, p.y, p.z, p.w}, qs[4] = {q.x, q.y, q.z, q.w};
+    for (int i = tid; i < H / 8; i += 128) {
+      const uint4 u = xr[i], v = wr[i];
+      const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        z = fmaf(__uint_as_float(ps[e] << 16), __uint_as_float(qs[e] << 16), z);
-        z = fmaf(__uint_as_float(ps[e] & 0xffff0000u), __uint_as_float(qs[e] & 0xffff0000u), z);
+        z = fmaf(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16), z);
+        z = fmaf(__uint_as_float(us[e] & 0xffff0000u), __uint_as_float(vs[e] & 0xffff0000u), z);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   }
-  const float2* p = part + (size_t)t * n_tiles;
-  float m = -INFINITY;
-  for (int i = lane; i < n_tiles; i += 32) m = fmaxf(m, p[i].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = cta_reduce<true>(m, tmp[0]);
   float s = 0.f;
-  for (int i = lane; i < n_tiles; i += 32) {
+  for (int i = tid; i < n_tiles; i += 128) {
     const float2 v = p[i];
     s += v.x == m ? v.y : v.y * expf(v.x - m);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) {
+  s = cta_reduce<false>(s, tmp[1]);
+  z = cta_reduce<false>(z, tmp[2]);
+  if (tid == 0) {
     const float others = m + logf(s);  // -infinity when the label is the only column
     float l = 0.f, all = others;
     if (has) {
       const float d = others - z;      // loss = log(1 + exp(d))
       l = (d > 0.f ? d : 0.f) + log1pf(expf(-fabsf(d)));
       if (d != d) l = d;               // a NaN (or infinite) logit
-      all = z + l;
-      if (d > 0.f) all = others + log1pf(expf(-d));
+      all = d > 0.f ? others + log1pf(expf(-d)) : z + l;
     }
     lse[t] = all;
     loss[t] = l;
@@ -563,6 +581,21 @@ int check_shape(int T, int V, int H) {
   return GOCR_OK;
 }
 
+// Columns of a tile of the z products: 128 where tiles of 256 would leave half
+// the pairs without one (193 rows x 8,191 x 512: 66 -> 53 us with the gradient),
+// else 256.  An MMA of 128 columns takes nearly the time of one of 256: 33 rows
+// x 65,536 x 1,536 took 57 us with tiles of 128, 43 with 256.
+int z_columns(int T, int vc) { return 2LL * cdiv(T, TM) * cdiv(vc, TN) <= PAIRS ? RN : TN; }
+
+// Few rows: only those that there are are staged, so that the ring holds more
+// of w, whose reading bounds the call.
+void set_ring(Args& a, bool z) {
+  a.a_rows = z && a.T < RM ? cdiv(a.T, 8) * 8 : RM;
+  const int stage = a.a_rows * 128 + (z && a.tn == RN ? BOX : B_BYTES);
+  const int n = RING / stage;
+  a.stages = n < MAX_STAGES ? n : MAX_STAGES;
+}
+
 template <int KIND> int launch(const Maps& m, const Args& a, int pairs, cudaStream_t s) {
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&linear_ce_kernel<KIND>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
@@ -600,7 +633,7 @@ extern "C" {
 
 size_t gocr_op_linear_ce_workspace(int T, int V) {
   if (T < 0 || V < 1) return 0;
-  return up256((size_t)T * cdiv(V, TN) * 8) + 256;
+  return up256((size_t)T * cdiv(V, z_columns(T, V)) * 8) + 256;
 }
 
 int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,
@@ -616,13 +649,15 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
   Args a{};
   a.T = T; a.H = H; a.V = V;
   a.labels = labels;
-  a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(V, TN);
+  a.tn = z_columns(T, V);
+  set_ring(a, true);
+  a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(V, a.tn);
   a.tiles = a.m_tiles * a.n_tiles;
   a.part = (float2*)workspace;
-  if (!map2(&m.a0, x, T, H, H, RM) || !map2(&m.b0, w, V, H, H, RN)) return bad_map();
+  if (!map2(&m.a0, x, T, H, H, a.a_rows) || !map2(&m.b0, w, V, H, H, a.tn / 2)) return bad_map();
   if (int rc = launch<STATS>(m, a, a.tiles, s)) return rc;
-  launch_k(linear_ce_join_kernel, dim3(cdiv(T, 8)), dim3(256), 0, s, true, (const float2*)a.part, (const bf16*)x,
-           (const bf16*)w, labels, loss, lse, T, V, H, a.n_tiles);
+  launch_k(linear_ce_join_kernel, dim3(T), dim3(128), 0, s, true, (const float2*)a.part, (const bf16*)x, (const bf16*)w, labels,
+           loss, lse, V, H, a.n_tiles);
   return op_launched("linear_ce join");
 }
 
@@ -649,7 +684,12 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
   }
   float* slabs = (float*)((char*)workspace + p.off_slab);
   Maps z{}, pr{};
-  if (!map2(&z.a0, x, T, H, H, RM) || !map2(&z.b0, w, V, H, H, RN) || !map2(&pr.b0, w, V, H, H, 64) ||
+  Args common{};
+  common.T = T; common.H = H; common.V = V;
+  common.labels = labels; common.lse = lse; common.dloss = dloss;
+  common.tn = z_columns(T, p.piece);
+  set_ring(common, true);
+  if (!map2(&z.a0, x, T, H, H, common.a_rows) || !map2(&z.b0, w, V, H, H, common.tn / 2) || !map2(&pr.b0, w, V, H, H, 64) ||
       !map2(&pr.b1, x, T, H, H, 64) || !map2(&pr.out1, dw, V, H, H, 32))
     return bad_map();
   {
@@ -659,16 +699,15 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
     if (!encode_tmap(&pr.out0, slabs, true, 2, dims, st, box)) return bad_map();
   }
   for (int v0 = 0; v0 < V; v0 += p.piece) {
-    Args a{};
-    a.T = T; a.H = H; a.V = V;
-    a.labels = labels; a.lse = lse; a.dloss = dloss;
+    Args a = common;
     a.v0 = v0; a.vc = V - v0 < p.piece ? V - v0 : p.piece;
     if (!map2(&z.out0, workspace, T, a.vc, p.piece, 32) || !map2(&pr.a0, workspace, T, a.vc, p.piece, RM) ||
         !map2(&pr.a1, workspace, T, a.vc, p.piece, 64))
       return bad_map();
-    a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(a.vc, TN);
+    a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(a.vc, a.tn);
     a.tiles = a.m_tiles * a.n_tiles;
     if (int rc = launch<GRAD>(z, a, a.tiles, s)) return rc;
+    set_ring(a, false);
     a.n_tiles = cdiv(H, TN);
     a.tiles = cdiv(a.vc, TM) * a.n_tiles;
     a.deal = v0 + p.piece < V ? p.full : p.last;
