@@ -4,21 +4,27 @@
 //   dP_ij = do_i . v_j                   dS_ij = P_ij (dP_ij - delta_i)
 //   dv_j = sum_i P_ij do_i               dk_j = c sum_i dS_ij q_i      dq_i = c sum_j dS_ij k_j
 //
-// dk and dv also sum over the q heads of the group.  Three launches: delta;
-// then dk and dv, one CTA per (128 keys, k/v head) walking the q heads and the
-// query blocks that see the keys; then dq, one CTA per (128 query rows, q
-// head) walking the keys.  S and dP are computed twice, seven products of 128
-// x 128 x D a block pair instead of five; in return every sum has one owner:
-// no atomics, no fp32 dq in memory, and the same bits on every call.
+// dk and dv also sum over the q heads of the group.  Two launches: delta, then
+// one of two kinds of CTA: for dk and dv one per (128 keys, k/v head), which
+// walks the q heads and the query blocks that see the keys; for dq one per (128
+// query rows, q head), which walks the keys.  S and dP are computed by both,
+// seven products of 128 x 128 x D a block pair instead of five; in return every
+// sum has one owner: no atomics, no fp32 dq in memory, and the same bits on
+// every call.  The longest CTAs come first and the short dq ones fill up.
 //
-// All products run on tcgen05 with fp32 accumulators in tensor memory.  The
-// dk/dv kernel works on the transposed blocks (a lane is a key): P^T and dS^T
-// (bf16, relative 2^-8, as the tensor cores take them) go back to tensor memory
-// over the scores they came from and are the A operands of dV += P^T dO and dK
-// += dS^T Q; dO and Q serve as they lie, K-major for S^T and dP^T and N-major
-// here.  The dq kernel has lanes of query rows and dQ += dS K.  Eight warps do
-// the elementwise work, two to a lane quarter with 64 columns each; it
-// overlaps the products: P^T with dK and dP^T, dS^T with dV and the next S^T.
+// All products run on tcgen05 with fp32 accumulators in tensor memory.  A dk/dv
+// CTA works on the transposed blocks (a lane is a key): P^T and dS^T (bf16,
+// relative 2^-8, as the tensor cores take them) go back to tensor memory over
+// the scores they came from and are the A operands of dV += P^T dO and dK +=
+// dS^T Q; dO and Q serve as they lie, K-major for S^T and dP^T and N-major
+// here.  A dq CTA has lanes of query rows and dQ += dS K.  Eight warps do the
+// elementwise work, two to a lane quarter with 64 columns each; it overlaps the
+// products: P^T with dK and dP^T, dS^T with dV and the next S^T.
+//
+// delta from o takes o's rounding to bf16 into every dS of the row.  That
+// matters where a row sees few keys (o is then large), so for the first 128
+// rows of a sequence, whose keys are one block, both kinds of CTA take delta_i
+// = sum_j P_ij dP_ij in fp32 instead.
 #include "../../include/gocr.h"
 #include "attn_packed.cuh"
 
@@ -29,6 +35,11 @@ namespace {
 
 constexpr int THREADS = 320;  // eight elementwise warps, a TMA and an MMA warp
 constexpr int EW = 8;         // elementwise warps
+constexpr int BAR_OFF = 7 * 128 * 128 * 2;  // behind seven tiles of D = 128
+constexpr int SMEM = BAR_OFF + 256 + 1024;
+
+// Barrier of the elementwise warps.
+__device__ __forceinline__ void elementwise_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 static __device__ int g_error;  // DevErr of a wait that gave up
 
@@ -45,6 +56,7 @@ struct BwdArgs {
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const bf16* o, const bf16* d_o, float* delta, int T, int Hq) {
   constexpr int L = D / 8;
+  if (threadIdx.x == 0) tc::grid_dep_launch();
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / L;
   const int l = threadIdx.x % L;
   const bool in = i < (long long)T * Hq;
@@ -89,22 +101,36 @@ __device__ __forceinline__ uint32_t packed_col(int ks) { return (ks >> 2) * 64 +
 template <int D> struct DkvGeo {
   static constexpr int TILE = TILE_BYTES<D>;
   static constexpr int OFF_K = 0, OFF_V = TILE;
-  static constexpr int OFF_Q = 2 * TILE;   // [2]
-  static constexpr int OFF_DO = 4 * TILE;  // [2]
-  static constexpr int OFF_ROW = 6 * TILE; // float [2 stages][lse, delta][128]
-  static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * 128 * 4;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int OFF_Q = 2 * TILE;    // [2]
+  static constexpr int OFF_DO = 4 * TILE;   // [2]
+  static constexpr int OFF_ROW = 6 * TILE;  // float [2 stages][lse, delta][128]
+  static constexpr int OFF_RED = OFF_ROW + 2 * 2 * 128 * 4;  // float [2 halves][4 warps][64]
+  static_assert(OFF_RED + 2 * 4 * 64 * 4 <= BAR_OFF, "shared memory");
 };
 
+// Sums over the warp's lanes of 32 values: lane l gets that of value l.  Each
+// step hands half of the values that are left to the lane that keeps them.
+__device__ __forceinline__ float lane_sums(float* x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return x[0];
+}
+
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
-    attn_dkv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const BwdArgs a) {
+__device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                        const CUtensorMap& mdo, const BwdArgs& a, const Block& blk, int kvh) {
   using G = DkvGeo<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   float* rows = reinterpret_cast<float*>(sm + G::OFF_ROW);
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + G::OFF_BAR);
+  float* red = reinterpret_cast<float*>(sm + G::OFF_RED);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + BAR_OFF);
   uint64_t* q_full = kv_full + 1;    // [2]
   uint64_t* q_empty = q_full + 2;    // [2]
   uint64_t* do_full = q_empty + 2;   // [2]
@@ -118,9 +144,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const int kvh = blockIdx.x % a.Hkv;
-  const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, blockIdx.x / a.Hkv);
-  if (blk.len == 0) return;
   const int group = a.Hq / a.Hkv;
   const int kb = blk.at / 128, nqb = (blk.len + 127) / 128;
   const int per = nqb - kb;         // query blocks of a head that see these keys
@@ -149,6 +172,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *holder;
+  tc::grid_dep_wait();  // delta
   constexpr uint32_t DP = 128, DV = 256, DK = 256 + D;  // S^T at 0
   bool ok = true;
 
@@ -286,6 +310,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::tmem_ld32_nowait(tp, u);
         tc::tmem_ld32_nowait(tp + 32, u + 32);
         tc::tmem_wait_ld();
+        if (at - half * 64 == 0) {  // the first query block: these keys are all that its rows see
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = c + i < lo || c + i >= hi ? 0.f : p[c + i] * __uint_as_float(u[c + i]);
+            red[(half * 4 + (warp & 3)) * 64 + c + lane] = lane_sums(x);
+          }
+          elementwise_sync();
+          if ((warp & 3) < 2) {
+            const int c = (warp & 3) * 32 + lane;
+            const float* r = red + half * 256 + c;
+            rows[st * 256 + 128 + half * 64 + c] = (r[0] + r[64]) + (r[128] + r[192]);
+          }
+          elementwise_sync();
+        }
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
           const float4 r = del[i / 4];
@@ -335,23 +375,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int D> struct DqGeo {
   static constexpr int TILE = TILE_BYTES<D>;
   static constexpr int OFF_Q = 0, OFF_DO = TILE;
-  static constexpr int OFF_K = 2 * TILE;  // [2]
-  static constexpr int OFF_V = 4 * TILE;  // [2]
-  static constexpr int OFF_BAR = 6 * TILE;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int OFF_K = 2 * TILE;  // [3]: S(it + 1) runs while dQ(it) still needs K(it)
+  static constexpr int OFF_V = 5 * TILE;  // [2]
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
-    attn_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const BwdArgs a) {
+__device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                       const CUtensorMap& mdo, const BwdArgs& a, const Block& blk, int head) {
   using G = DqGeo<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + G::OFF_BAR);
-  uint64_t* k_full = q_full + 1;    // [2]
-  uint64_t* k_empty = k_full + 2;   // [2]
-  uint64_t* v_full = k_empty + 2;   // [2]
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + BAR_OFF);
+  uint64_t* k_full = q_full + 1;    // [3]
+  uint64_t* k_empty = k_full + 3;   // [3]
+  uint64_t* v_full = k_empty + 3;   // [2]
   uint64_t* v_empty = v_full + 2;   // [2]
   uint64_t* k_tail = v_empty + 2;
   uint64_t* s_full = k_tail + 1;    // [2]
@@ -360,20 +395,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* ds_full = dp_free + 1;  // [2]
   uint64_t* done = ds_full + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
+  __shared__ float row_sum[2][128];  // the first block's delta, by column half
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const int head = blockIdx.x % a.Hq;
-  const Block blk = find_block<true>(a.cu, a.n_seq, a.T, 128, blockIdx.x / a.Hq);
-  if (blk.len == 0) return;
   const int kvh = head / (a.Hq / a.Hkv);
   const int n = blk.at / 128 + 1;
   const int tail = blk.len - blk.at;  // rows of the last key block within the sequence, if < 128
 
   if (tid == 0) {
     tc::mbar_init(q_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 3; ++s) {
       tc::mbar_init(k_full + s, 1);
       tc::mbar_init(k_empty + s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       tc::mbar_init(v_full + s, 1);
       tc::mbar_init(v_empty + s, 1);
       tc::mbar_init(s_full + s, 1);
@@ -391,6 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *holder;
+  tc::grid_dep_wait();  // delta
   constexpr uint32_t DP = 256, DQ = 384;  // S at 0 and 128
   bool ok = true;
 
@@ -401,9 +437,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       load_tile<D>(sm + G::OFF_DO, &mdo, head, blk.row0 + blk.at, q_full);
       for (int it = 0; it < n; ++it) {
         const int st = it & 1, ph = (it >> 1) & 1;
-        if (!(ok = tc::mbar_wait_ns(k_empty + st, ph ^ 1))) break;
-        tc::mbar_expect_tx(k_full + st, G::TILE);
-        load_tile<D>(sm + G::OFF_K + st * G::TILE, &mk, kvh, blk.row0 + it * 128, k_full + st);
+        const int ks = it % 3;
+        if (!(ok = tc::mbar_wait_ns(k_empty + ks, (it / 3 & 1) ^ 1))) break;
+        tc::mbar_expect_tx(k_full + ks, G::TILE);
+        load_tile<D>(sm + G::OFF_K + ks * G::TILE, &mk, kvh, blk.row0 + it * 128, k_full + ks);
         if (!(ok = tc::mbar_wait_ns(v_empty + st, ph ^ 1))) break;
         tc::mbar_expect_tx(v_full + st, G::TILE);
         load_tile<D>(sm + G::OFF_V + st * G::TILE, &mv, kvh, blk.row0 + it * 128, v_full + st);
@@ -411,9 +448,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     ok = __all_sync(0xffffffffu, ok);
     if (ok && tail < 128) {  // nothing behind the sequence in dQ += dS K
-      const int st = (n - 1) & 1;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(k_full + st, ((n - 1) >> 1) & 1));
-      zero_rows<D>(sm + G::OFF_K + st * G::TILE, tail);
+      const int ks = (n - 1) % 3;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(k_full + ks, (n - 1) / 3 & 1));
+      zero_rows<D>(sm + G::OFF_K + ks * G::TILE, tail);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(k_tail);
@@ -443,11 +480,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       for (int it = 0; it < n && ok; ++it) {
-        const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
+        const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1, ks0 = it % 3, ks1 = (it + 1) % 3;
         if (it + 1 < n) {
           // the other score buffer: its dS was consumed by dQ(it - 1), issued before
-          if (!(ok = wait(k_full + nx, nph))) break;
-          block(nx * 128, q, k + nx * G::TILE, s_full + nx);
+          if (!(ok = wait(k_full + ks1, (it + 1) / 3 & 1))) break;
+          block(nx * 128, q, k + ks1 * G::TILE, s_full + nx);
           if (!(ok = wait(v_full + nx, nph) && wait(dp_free, it & 1))) break;
           block(DP, d_o, v + nx * G::TILE, dp_full);
           tc::mma_commit(v_empty + nx);
@@ -456,9 +493,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (it + 1 == n && tail < 128 && !(ok = wait(k_tail, 0))) break;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16_ta(tmem + DQ, tmem + st * 128 + packed_col(ks), desc_n(k + st * G::TILE, ks), idesc_g,
+          tc::mma_bf16_ta(tmem + DQ, tmem + st * 128 + packed_col(ks), desc_n(k + ks0 * G::TILE, ks), idesc_g,
                           it > 0 || ks > 0 ? 1u : 0u);
-        tc::mma_commit(k_empty + st);
+        tc::mma_commit(k_empty + ks0);
       }
       if (ok) tc::mma_commit(done);
     }
@@ -469,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool in = row < blk.len;
     const size_t t = (size_t)blk.row0 + row;
     const float lse = in ? a.lse[(size_t)head * a.T + t] * LOG2E : 0.f;
-    const float del = in ? a.delta[(size_t)head * a.T + t] : 0.f;
+    float del = in ? a.delta[(size_t)head * a.T + t] : 0.f;
     const float sl2 = a.scale * LOG2E;
     const uint32_t tp = tmem + lanes + DP + half * 64;
     for (int it = 0; it < n; ++it) {
@@ -496,14 +533,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(dp_free);
+        // the diagonal block holds the end of the sequence, too: it lies past every row
+        const int see = it + 1 == n ? min(row, blk.len - 1) - it * 128 - half * 64 : 64;
+        if (n == 1) {  // all the keys that the row sees
+          float x = 0.f;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i <= see) x = fmaf(p[i], __uint_as_float(u[i]), x);
+          row_sum[half][(warp & 3) * 32 + lane] = x;
+          elementwise_sync();
+          del = row_sum[0][(warp & 3) * 32 + lane] + row_sum[1][(warp & 3) * 32 + lane];
+        }
 #pragma unroll
         for (int i = 0; i < 64; ++i) p[i] *= __uint_as_float(u[i]) - del;
-      }
-      if (it + 1 == n) {  // the diagonal block; the end of the sequence lies past the row
-        const int see = min(row, blk.len - 1) - it * 128 - half * 64;
+        if (it + 1 == n)
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (i > see) p[i] = 0.f;
+          for (int i = 0; i < 64; ++i)
+            if (i > see) p[i] = 0.f;
       }
       uint32_t w[32];
 #pragma unroll
@@ -532,18 +578,36 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                           const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                           const BwdArgs a, int n_dkv) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  int b = blockIdx.x;
+  if (b < n_dkv) {
+    const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, b / a.Hkv);
+    if (blk.len) dkv_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hkv);
+    else tc::grid_dep_wait();
+  } else {
+    b -= n_dkv;
+    const Block blk = find_block<true>(a.cu, a.n_seq, a.T, 128, b / a.Hq);
+    if (blk.len) dq_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hq);
+    else tc::grid_dep_wait();
+  }
+}
+
+template <int D>
 int backward(const CUtensorMap* m, const BwdArgs& a, const bf16* o, const bf16* d_o, float* delta, cudaStream_t s) {
-  const void* kf[2] = {reinterpret_cast<const void*>(&attn_dkv_kernel<D>), reinterpret_cast<const void*>(&attn_dq_kernel<D>)};
-  if (!kernel_smem_at_least(kf[0], DkvGeo<D>::SMEM) || !kernel_smem_at_least(kf[1], DqGeo<D>::SMEM))
+  if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_packed_bwd_kernel<D>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
   const long long threads = (long long)a.T * a.Hq * (D / 8);
-  attn_delta_kernel<D><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(o, d_o, delta, a.T, a.Hq);
+  launch_k(attn_delta_kernel<D>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, false, o, d_o, delta, a.T, a.Hq);
   if (int rc = op_launched("attention_packed delta")) return rc;
   const long long blocks = max_blocks(a.n_seq, a.T, 128);
-  attn_dkv_kernel<D><<<(unsigned)(blocks * a.Hkv), THREADS, DkvGeo<D>::SMEM, s>>>(m[0], m[1], m[2], m[3], a);
-  if (int rc = op_launched("attention_packed dk, dv")) return rc;
-  attn_dq_kernel<D><<<(unsigned)(blocks * a.Hq), THREADS, DqGeo<D>::SMEM, s>>>(m[0], m[1], m[2], m[3], a);
-  return op_launched("attention_packed dq");
+  launch_k(attn_packed_bwd_kernel<D>, dim3((unsigned)(blocks * (a.Hkv + a.Hq))), dim3(THREADS), SMEM, s, true, m[0], m[1],
+           m[2], m[3], a, (int)(blocks * a.Hkv));
+  return op_launched("attention_packed backward");
 }
 
 }  // namespace
