@@ -23,7 +23,12 @@ using namespace gocr::packed;
 namespace {
 
 constexpr int QT = 256;        // query rows of a CTA
-constexpr int THREADS = 320;   // two softmax groups of four warps, a TMA and an MMA warp
+// Two softmax groups of four warps, and a group with the TMA and the MMA warp.
+// A softmax thread holds a row's 128 scores: its group takes 208 registers a
+// thread of the 168 x 384 that the block is launched with, the third 88.
+constexpr int THREADS = 384;
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+static_assert(2 * SOFTMAX_REGS + OTHER_REGS <= 3 * 168, "registers of the block at launch");
 constexpr float GROW = 8.f;    // log2 of the growth of a row's maximum that rescales O
 
 static __device__ int g_error;  // DevErr of a wait that gave up
@@ -96,7 +101,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *holder;
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp >= 8) {
+    fewer_registers<OTHER_REGS>();
+    if (warp == 8) {
     // K(0), V(0), K(1), V(1), ... through the ring
     if (lane == 0) {
       tc::mbar_expect_tx(q_full, (n1 ? 2 : 1) * TILE_BYTES<D>);
@@ -119,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(v_tail);
     }
-  } else if (warp == 9) {
+    } else if (warp == 9) {
     if (lane == 0) {
       constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
       constexpr uint32_t idesc_o = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const uint32_t v = tile_of(2 * it + 1);
         const bool more = it + 1 < n;
-        if (more && !(ok = wait_full(2 * it + 2))) break;
+        bool have_k = false;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int nj = j ? n1 : n0;
@@ -162,15 +169,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int ks = 0; ks < 8; ++ks)
             tc::mma_bf16_ta(tmem + F::O_COL + j * D, tmem + j * 128 + ks * 8, desc_n(v, ks), idesc_o,
                             it > 0 || ks > 0 ? 1u : 0u);
-          if (it + 1 < nj) scores(j, it + 1);
-          else tc::mma_commit(o_full + j);
+          if (it + 1 < nj) {
+            if (!have_k && !(ok = wait_full(2 * it + 2))) break;
+            have_k = true;
+            scores(j, it + 1);
+          } else {
+            tc::mma_commit(o_full + j);
+          }
         }
         if (!ok) break;
         tc::mma_commit(empty + (2 * it + 1) % SLOTS);
         if (more) tc::mma_commit(empty + (2 * it + 2) % SLOTS);
       }
     }
+    }
   } else {
+    more_registers<SOFTMAX_REGS>();
     const int j = warp >> 2;
     const int nj = j ? n1 : n0;
     const int row = blk.at + j * 128 + (warp & 3) * 32 + lane;  // within the sequence
@@ -191,13 +205,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = 0; i < 128; ++i)
           if (i > see) u[i] = 0xff800000u;  // -infinity
       }
-      float mx = __uint_as_float(u[0]), my = __uint_as_float(u[1]);
+      float m4[4];
 #pragma unroll
-      for (int i = 2; i < 128; i += 2) {
-        mx = fmaxf(mx, __uint_as_float(u[i]));
-        my = fmaxf(my, __uint_as_float(u[i + 1]));
-      }
-      mx = fmaxf(mx, my);
+      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 4]));
+#pragma unroll
+      for (int i = 8; i < 128; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(u[i + e])), __uint_as_float(u[i + e + 4]));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       if (it == 0) {
         ref = mx == -INFINITY ? 0.f : mx;
         ref2 = ref * sl2;
@@ -221,16 +236,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      float s0 = 0.f, s1 = 0.f;
+      const F2 scale2 = f2(sl2, sl2), ref22 = f2(-ref2, -ref2);
+      F2 s4[4] = {f2(l, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
       for (int i = 0; i < 128; i += 2) {
-        const float p0 = ex2(fmaf(__uint_as_float(u[i]), sl2, -ref2));
-        const float p1 = ex2(fmaf(__uint_as_float(u[i + 1]), sl2, -ref2));
-        s0 += p0;
-        s1 += p1;
-        u[i / 2] = pack2(p0, p1);
+        float x, y;
+        split(fma2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), scale2, ref22), x, y);
+        x = ex2(x);
+        y = ex2(y);
+        s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], f2(x, y));
+        u[i / 2] = pack2(x, y);
       }
-      l += s0 + s1;
+      {
+        float x, y;
+        split(add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])), x, y);
+        l = x + y;
+      }
       tc::tmem_st32(ts, u);
       tc::tmem_st32(ts + 32, u + 32);
       tc::tmem_wait_st();
