@@ -2,18 +2,25 @@
 //
 //   S_ij = c q_i . k_j (j <= i),  lse_i = log sum_j exp S_ij,  o_i = sum_j exp(S_ij - lse_i) v_j
 //
-// One CTA per (256 query rows of a sequence, q head): two tiles of 128 rows
-// share the K/V ring that a TMA warp fills.  Both products run on tcgen05: S =
-// Q K^T (128 x 128 x D) into tensor memory, P (bf16) back into tensor memory
-// over S, O += P V with P read from there and V N-major as it lies.  A softmax
-// thread owns a row: its 128 scores come from its own tensor memory lane, so
-// the running maximum and sum need no exchange.  While one tile's softmax
-// runs, the tensor cores work for the other.  O stays in tensor memory and is
-// rescaled only when a row's maximum grows by more than 2^8 over the one its
-// exponentials refer to (the sum and O use the same reference, so nothing is
-// lost; P is at most 2^8).  P is rounded to bf16 (relative 2^-8) since the
-// tensor cores take it so; scores, maxima, sums and O are fp32.  No partial
-// results leave the CTA: a row's bits depend on its own sequence only.
+// A work item is 256 query rows of a sequence and a q head: two tiles of 128
+// rows share the K/V ring that a TMA warp fills.  Both products run on tcgen05:
+// S = Q K^T (128 x 128 x D) into tensor memory, P (bf16) back into tensor memory
+// over S, O += P V with P read from there and V N-major as it lies.  Two
+// softmax threads own a row, 64 scores each from their tensor memory lane, and
+// exchange its maximum through shared memory: with one thread a row the chain
+// from a tile's scores to its P, not the tensor cores, set the pace (tensor
+// pipe 51% busy, issue slots 29%).  While one tile's softmax runs, the tensor
+// cores work for the other.  O stays in tensor memory and is rescaled only when
+// a row's maximum grows by more than 2^8 over the one its exponentials refer to
+// (the sum and O use the same reference, so nothing is lost; P is at most 2^8).
+// P is rounded to bf16 (relative 2^-8) since the tensor cores take it so;
+// scores, maxima, sums and O are fp32.  No partial results leave the CTA: a
+// row's bits depend on its own sequence only.
+//
+// The grid has a CTA per work item, but a running CTA takes over the items of
+// those that have not started (cluster launch control), so barriers and tensor
+// memory are set up once per SM and the next item's Q, K and V are on their way
+// while the last one's output is written.  A warp looks items up two ahead.
 #include "../../include/gocr.h"
 #include "attn_packed.cuh"
 
@@ -22,13 +29,14 @@ using namespace gocr::packed;
 
 namespace {
 
-constexpr int QT = 256;        // query rows of a CTA
-// Two softmax groups of four warps, and a group with the TMA and the MMA warp.
-// A softmax thread holds a row's 128 scores: its group takes 208 registers a
-// thread of the 168 x 384 that the block is launched with, the third 88.
-constexpr int THREADS = 384;
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
-static_assert(2 * SOFTMAX_REGS + OTHER_REGS <= 3 * 168, "registers of the block at launch");
+constexpr int QT = 256;        // query rows of a work item
+// Sixteen softmax warps (two tiles x two column halves x four lane quarters),
+// then the TMA, MMA, work and tail warps.  The softmax groups take 104
+// registers a thread of the 96 x 640 that the block is launched with, the last
+// group 64.
+constexpr int SW = 16, THREADS = (SW + 4) * 32;
+constexpr int SOFTMAX_REGS = 104, OTHER_REGS = 64;
+static_assert(4 * SOFTMAX_REGS + OTHER_REGS <= 5 * 96, "registers of the block at launch");
 constexpr float GROW = 8.f;    // log2 of the growth of a row's maximum that rescales O
 
 static __device__ int g_error;  // DevErr of a wait that gave up
@@ -45,10 +53,58 @@ template <int D> struct Fwd {
   static constexpr int SLOTS = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TILE_BYTES<D>;
-  static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE_BYTES<D>;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static constexpr int OFF_MAX = OFF_KV + SLOTS * TILE_BYTES<D>;  // float [2 turns][2 tiles][2 halves][128]
+  static constexpr int OFF_SUM = OFF_MAX + 2 * 2 * 2 * 128 * 4;   // float [2 tiles][2 halves][128]
+  static constexpr int OFF_WORK = OFF_SUM + 2 * 2 * 128 * 4;      // int4 [2], and the launch control's answer
+  static constexpr int OFF_BAR = OFF_WORK + 64;
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t O_COL = 256;  // S0, S1 at 0, 128; O0, O1 behind them
 };
+
+// One work item, as every warp sees it.
+struct Item {
+  Block blk;
+  int head;
+  int n0, n1, n;  // key blocks of the two tiles: up to the diagonal, and within the sequence
+  int tail;       // rows of the last key block within the sequence, if < 128
+  __device__ explicit Item(int4 w) : blk{w.x, w.y, w.z}, head(w.w) {
+    n0 = blk.at / 128 + 1;
+    n1 = blk.len - blk.at > 128 ? n0 + 1 : 0;
+    n = n1 ? n1 : n0;
+    tail = blk.len - (n - 1) * 128;
+  }
+};
+
+// The warp's next item from the ring of two; false past the last one.
+__device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full, uint64_t* work_free, int i, int4& w,
+                                          bool& ok) {
+  const int s = i & 1;
+  if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(work_full + s, (i >> 1) & 1)))) return false;
+  w = work[s];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(work_free + s);
+  return w.y > 0;
+}
+
+// The index of a CTA of this launch that now will not start, or -1; one thread.
+__device__ __forceinline__ int take_cta(void* answer, uint64_t* bar, int turn, bool& ok) {
+  const uint32_t at = tc::smem_u32(answer);
+  tc::fence_proxy_async_smem();
+  tc::mbar_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(at), "r"(tc::smem_u32(bar)) : "memory");
+  if (!(ok = tc::mbar_wait_ns(bar, turn & 1))) return -1;
+  uint32_t yes, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(yes), "=r"(x) : "r"(at) : "memory");
+  return yes ? (int)x : -1;
+}
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -59,234 +115,315 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + F::OFF_BAR);
-  uint64_t* full = q_full + 1;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* full = q_empty + 1;
   uint64_t* empty = full + SLOTS;
   uint64_t* s_full = empty + SLOTS;  // [2]
   uint64_t* p_full = s_full + 2;     // [2]
   uint64_t* o_full = p_full + 2;     // [2]
-  uint64_t* v_tail = o_full + 2;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(v_tail + 1);
+  // ragged V tiles, one barrier a slot: a slot's next load waits for this one's
+  // use, so no barrier is ever two phases ahead of the warp that waits on it
+  uint64_t* tail_go = o_full + 2;      // [SLOTS] the load has been issued
+  uint64_t* v_tail = tail_go + SLOTS;  // [SLOTS] the rows behind the sequence are zero
+  uint64_t* work_full = v_tail + SLOTS;  // [2]
+  uint64_t* work_free = work_full + 2;  // [2]
+  uint64_t* taken = work_free + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(taken + 1);
+  int4* work = reinterpret_cast<int4*>(sm + F::OFF_WORK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  const int head = blockIdx.x % a.Hq;
-  const Block blk = find_block<true>(a.cu, a.n_seq, a.T, QT, blockIdx.x / a.Hq);  // each warp for itself
-  if (blk.len == 0) return;
-  const int kvh = head / (a.Hq / a.Hkv);
-  // key blocks of the two tiles: up to the diagonal, and within the sequence
-  const int left = blk.len - blk.at;
-  const int n0 = blk.at / 128 + 1;
-  const int n1 = left > 128 ? n0 + 1 : 0;
-  const int n = n1 ? n1 : n0;
-  const int tail = blk.len - (n - 1) * 128;  // rows of the last key block within the sequence, if < 128
 
   if (tid == 0) {
     tc::mbar_init(q_full, 1);
+    tc::mbar_init(q_empty, 1);
     for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(full + s, 1);
       tc::mbar_init(empty + s, 1);
+      tc::mbar_init(tail_go + s, 1);
+      tc::mbar_init(v_tail + s, 1);
     }
     for (int j = 0; j < 2; ++j) {
       tc::mbar_init(s_full + j, 1);
-      tc::mbar_init(p_full + j, 4);
+      tc::mbar_init(p_full + j, SW / 2);
       tc::mbar_init(o_full + j, 1);
+      tc::mbar_init(work_full + j, 1);
+      tc::mbar_init(work_free + j, SW + 3);
     }
-    tc::mbar_init(v_tail, 1);
+    tc::mbar_init(taken, 1);
     tc::fence_mbar_init();
   }
   __syncwarp();
-  if (warp == 9) tc::tmem_alloc(holder, 512);
+  if (warp == SW + 1) tc::tmem_alloc(holder, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *holder;
   bool ok = true;
+  int4 w;
 
-  if (warp >= 8) {
+  if (warp >= SW) {
     fewer_registers<OTHER_REGS>();
-    if (warp == 8) {
-    // K(0), V(0), K(1), V(1), ... through the ring
-    if (lane == 0) {
-      tc::mbar_expect_tx(q_full, (n1 ? 2 : 1) * TILE_BYTES<D>);
-      load_tile<D>(sm + F::OFF_Q, &mq, head, blk.row0 + blk.at, q_full);
-      if (n1) load_tile<D>(sm + F::OFF_Q + TILE_BYTES<D>, &mq, head, blk.row0 + blk.at + 128, q_full);
+    if (warp == SW) {
+      // K(0), V(0), K(1), V(1), ... through the ring, Q behind the item's K(0)
       int slot = 0, ph = 0;
-      for (int i = 0; i < 2 * n; ++i) {
-        if (!(ok = tc::mbar_wait_ns(empty + slot, ph ^ 1))) break;
-        tc::mbar_expect_tx(full + slot, TILE_BYTES<D>);
-        load_tile<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, i & 1 ? &mv : &mk, kvh, blk.row0 + (i >> 1) * 128, full + slot);
-        if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+      for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
+        const Item t(w);
+        if (lane == 0) {
+          const int kvh = t.head / (a.Hq / a.Hkv);
+          for (int x = 0; x < 2 * t.n; ++x) {
+            if (!(ok = tc::mbar_wait_ns(empty + slot, ph ^ 1))) break;
+            tc::mbar_expect_tx(full + slot, TILE_BYTES<D>);
+            load_tile<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, x & 1 ? &mv : &mk, kvh, t.blk.row0 + (x >> 1) * 128, full + slot);
+            if (x == 2 * t.n - 1 && t.tail < 128) tc::mbar_arrive(tail_go + slot);
+            if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+            if (x == 0) {
+              if (!(ok = tc::mbar_wait_ns(q_empty, (i & 1) ^ 1))) break;
+              tc::mbar_expect_tx(q_full, (t.n1 ? 2 : 1) * TILE_BYTES<D>);
+              load_tile<D>(sm + F::OFF_Q, &mq, t.head, t.blk.row0 + t.blk.at, q_full);
+              if (t.n1) load_tile<D>(sm + F::OFF_Q + TILE_BYTES<D>, &mq, t.head, t.blk.row0 + t.blk.at + 128, q_full);
+            }
+          }
+        }
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok && tail < 128) {  // the last V tile: nothing behind the sequence
-      const int i = 2 * n - 1, slot = i % SLOTS;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(full + slot, (i / SLOTS) & 1));
-      zero_rows<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, tail);
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(v_tail);
-    }
-    } else if (warp == 9) {
-    if (lane == 0) {
+    } else if (warp == SW + 1) {
       constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
       constexpr uint32_t idesc_o = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
       const uint32_t q = tc::smem_u32(sm + F::OFF_Q), kv = tc::smem_u32(sm + F::OFF_KV);
-      auto tile_of = [&](int i) { return kv + (i % SLOTS) * TILE_BYTES<D>; };
-      auto wait_full = [&](int i) {
-        const bool w = tc::mbar_wait_ns(full + i % SLOTS, (i / SLOTS) & 1);
-        tc::fence_after_sync();
-        return w;
-      };
-      auto scores = [&](int j, int it) {
-        const uint32_t k = tile_of(2 * it);
+      int ring = 0;              // ring position of the item's K(0)
+      unsigned tails = 0;        // parity of each slot's ragged tiles so far
+      int turn[2] = {0, 0};      // blocks of the two tiles so far
+      for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
+        const Item t(w);
+        if (lane == 0) {
+          auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
+          auto wait = [&](uint64_t* bar, int ph) {
+            const bool r = tc::mbar_wait_ns(bar, ph & 1);
+            tc::fence_after_sync();
+            return r;
+          };
+          auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
+          auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
+          auto scores = [&](int j, int it) {
+            const uint32_t k = tile_of(2 * it);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_bf16(tmem + j * 128, desc_k(q + j * TILE_BYTES<D>, ks), desc_k(k, ks), idesc_s, ks > 0 ? 1u : 0u);
-        tc::mma_commit(s_full + j);
-      };
-      ok = tc::mbar_wait_ns(q_full, 0) && wait_full(0);
-      if (ok) {
-        scores(0, 0);
-        if (n1) scores(1, 0);
-        tc::mma_commit(empty);
-      }
-      for (int it = 0; it < n && ok; ++it) {
-        if (!(ok = wait_full(2 * it + 1))) break;
-        if (it == n - 1 && tail < 128) {
-          if (!(ok = tc::mbar_wait_ns(v_tail, 0))) break;
-          tc::fence_after_sync();
-        }
-        const uint32_t v = tile_of(2 * it + 1);
-        const bool more = it + 1 < n;
-        bool have_k = false;
+            for (int ks = 0; ks < D / 16; ++ks)
+              tc::mma_bf16(tmem + j * 128, desc_k(q + j * TILE_BYTES<D>, ks), desc_k(k, ks), idesc_s, ks > 0 ? 1u : 0u);
+            tc::mma_commit(s_full + j);
+          };
+          ok = wait(q_full, i) && wait_full(0);
+          if (ok) {
+            // over P of the last item, whose products were issued before
+            scores(0, 0);
+            if (t.n1) scores(1, 0);
+            release(0);
+            if (t.n == 1) tc::mma_commit(q_empty);
+          }
+          for (int it = 0; it < t.n && ok; ++it) {
+            if (!(ok = wait_full(2 * it + 1))) break;
+            if (it == t.n - 1 && t.tail < 128) {
+              const int slot = (ring + 2 * it + 1) % SLOTS;
+              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+              tails ^= 1u << slot;
+            }
+            const uint32_t v = tile_of(2 * it + 1);
+            bool have_k = false;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int nj = j ? n1 : n0;
-          if (it >= nj) continue;
-          if (!(ok = tc::mbar_wait_ns(p_full + j, it & 1))) break;
-          tc::fence_after_sync();
+            for (int j = 0; j < 2; ++j) {
+              const int nj = j ? t.n1 : t.n0;
+              if (it >= nj) continue;
+              if (!(ok = wait(p_full + j, turn[j] + it))) break;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            tc::mma_bf16_ta(tmem + F::O_COL + j * D, tmem + j * 128 + ks * 8, desc_n(v, ks), idesc_o,
-                            it > 0 || ks > 0 ? 1u : 0u);
-          if (it + 1 < nj) {
-            if (!have_k && !(ok = wait_full(2 * it + 2))) break;
-            have_k = true;
-            scores(j, it + 1);
-          } else {
-            tc::mma_commit(o_full + j);
+              for (int ks = 0; ks < 8; ++ks)
+                tc::mma_bf16_ta(tmem + F::O_COL + j * D, tmem + j * 128 + packed_col<64>(ks), desc_n(v, ks), idesc_o,
+                                it > 0 || ks > 0 ? 1u : 0u);
+              if (it + 1 < nj) {
+                if (!have_k && !(ok = wait_full(2 * it + 2))) break;
+                have_k = true;
+                scores(j, it + 1);
+              } else {
+                tc::mma_commit(o_full + j);
+              }
+            }
+            if (!ok) break;
+            release(2 * it + 1);
+            if (it + 1 < t.n) release(2 * it + 2);
+            if (it + 2 == t.n) tc::mma_commit(q_empty);  // after the item's last scores
           }
         }
-        if (!ok) break;
-        tc::mma_commit(empty + (2 * it + 1) % SLOTS);
-        if (more) tc::mma_commit(empty + (2 * it + 2) % SLOTS);
+        ring += 2 * t.n;
+        turn[0] += t.n0;
+        turn[1] += t.n1;
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
-    }
+    } else if (warp == SW + 2) {
+      // the items: this CTA's own, then those of CTAs that have not started
+      int id = blockIdx.x, takes = 0;
+      auto take = [&] {
+        int x = -1;
+        if (lane == 0) x = take_cta(work + 2, taken, takes, ok);
+        ++takes;
+        id = __shfl_sync(0xffffffffu, x, 0);
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      for (int i = 0; ok; ++i) {
+        const int s = i & 1;
+        Block blk{0, 0, 0};
+        while (id >= 0) {
+          blk = find_block<true>(a.cu, a.n_seq, a.T, QT, id / a.Hq);
+          if (blk.len) break;
+          take();
+        }
+        const bool more = id >= 0;
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(work_free + s, ((i >> 1) & 1) ^ 1)))) break;
+        if (lane == 0) {
+          work[s] = make_int4(blk.row0, more ? blk.len : 0, blk.at, more ? id % a.Hq : 0);
+          tc::mbar_arrive(work_full + s);
+        }
+        if (!more) break;
+        take();
+      }
+    } else {
+      // ragged items: nothing behind the sequence in the last V tile
+      int ring = 0;
+      unsigned tails = 0;
+      for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
+        const Item t(w);
+        if (t.tail < 128) {
+          const int x = ring + 2 * t.n - 1, slot = x % SLOTS;
+          // the slot's barrier is in this load's phase only once it has been issued
+          ok = tc::mbar_wait_ns(tail_go + slot, (tails >> slot) & 1) && tc::mbar_wait_ns(full + slot, (x / SLOTS) & 1);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tails ^= 1u << slot;
+          zero_rows<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, t.tail);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(v_tail + slot);
+        }
+        ring += 2 * t.n;
+      }
     }
   } else {
     more_registers<SOFTMAX_REGS>();
-    const int j = warp >> 2;
-    const int nj = j ? n1 : n0;
-    const int row = blk.at + j * 128 + (warp & 3) * 32 + lane;  // within the sequence
+    const int j = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;  // tile, column half, row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + j * 128 + lanes, to = tmem + F::O_COL + j * D + lanes;
+    const uint32_t ts = tmem + j * 128 + half * 64 + lanes, to = tmem + F::O_COL + j * D + half * (D / 2) + lanes;
+    float* maxima = reinterpret_cast<float*>(sm + F::OFF_MAX) + j * 256 + r;  // [turn parity * 512 + half * 128]
+    float* sums = reinterpret_cast<float*>(sm + F::OFF_SUM) + j * 256 + r;
     const float sl2 = a.scale * LOG2E;
-    float ref = 0.f, ref2 = 0.f, l = 0.f;  // the exponentials' reference, also times sl2; their sum
-    for (int it = 0; it < nj; ++it) {
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(s_full + j, it & 1)))) break;
-      tc::fence_after_sync();
-      uint32_t u[128];
+    int turn = 0, outs = 0;
+    // the row's other thread is in the same place of the warp of the other half
+    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + j * 4 + (warp & 3)) : "memory"); };
+    for (int i = 0; ok && next_item(work, work_full, work_free, i, w, ok); ++i) {
+      const Item t(w);
+      const int nj = j ? t.n1 : t.n0;
+      if (!nj) continue;
+      const int row = t.blk.at + j * 128 + r;  // within the sequence
+      float ref = 0.f, ref2 = 0.f, l = 0.f;    // the exponentials' reference, also times sl2; their sum
+      for (int it = 0; it < nj; ++it, ++turn) {
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(s_full + j, turn & 1)))) break;
+        tc::fence_after_sync();
+        uint32_t u[64];
+        tc::tmem_ld32_nowait(ts, u);
+        tc::tmem_ld32_nowait(ts + 32, u + 32);
+        tc::tmem_wait_ld();
+        if (it + 1 == nj) {  // the diagonal block; it holds the end of the sequence, too
+          const int see = min(row, t.blk.len - 1) - it * 128 - half * 64;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(ts + c * 32, u + c * 32);
-      tc::tmem_wait_ld();
-      if (it + 1 == nj) {  // the diagonal block; it holds the end of the sequence, too
-        const int see = min(row, blk.len - 1) - it * 128;
+          for (int x = 0; x < 64; ++x)
+            if (x > see) u[x] = 0xff800000u;  // -infinity
+        }
+        float m4[4];
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i > see) u[i] = 0xff800000u;  // -infinity
-      }
-      float m4[4];
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 4]));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 4]));
+        for (int x = 8; x < 64; x += 8)
 #pragma unroll
-      for (int i = 8; i < 128; i += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(u[i + e])), __uint_as_float(u[i + e + 4]));
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      if (it == 0) {
-        ref = mx == -INFINITY ? 0.f : mx;
-        ref2 = ref * sl2;
-      } else {
-        const bool grow = (mx - ref) * sl2 > GROW;
-        if (__any_sync(0xffffffffu, grow)) {
-          // S(it) was issued after P V(it - 1): O is complete
-          const float to_new = grow ? mx : ref;
-          const float f = ex2(ref2 - to_new * sl2);
-          ref = to_new;
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(u[x + e])), __uint_as_float(u[x + e + 4]));
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        float* at = maxima + (turn & 1) * 512;
+        at[half * 128] = mx;
+        meet();
+        mx = fmaxf(mx, at[(half ^ 1) * 128]);
+        if (it == 0) {
+          ref = mx == -INFINITY ? 0.f : mx;
           ref2 = ref * sl2;
-          l *= f;
+        } else {
+          const bool grow = (mx - ref) * sl2 > GROW;
+          if (__any_sync(0xffffffffu, grow)) {
+            // S(it) was issued after P V(it - 1): O is complete
+            const float to_new = grow ? mx : ref;
+            const float f = ex2(ref2 - to_new * sl2);
+            ref = to_new;
+            ref2 = ref * sl2;
+            l *= f;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t w[32];
-            tc::tmem_ld32_nowait(to + c, w);
-            tc::tmem_wait_ld();
+            for (int c = 0; c < D / 2; c += 16) {
+              float v[16];
+              tc::tmem_ld16(to + c, v);
+              uint32_t x[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-            tc::tmem_st32(to + c, w);
+              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(v[e] * f);
+              tc::tmem_st16(to + c, x);
+            }
           }
         }
-      }
-      const F2 scale2 = f2(sl2, sl2), ref22 = f2(-ref2, -ref2);
-      F2 s4[4] = {f2(l, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+        const F2 scale2 = f2(sl2, sl2), ref22 = f2(-ref2, -ref2);
+        F2 s2[2] = {f2(l, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        float x, y;
-        split(fma2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), scale2, ref22), x, y);
-        x = ex2(x);
-        y = ex2(y);
-        s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], f2(x, y));
-        u[i / 2] = pack2(x, y);
+        for (int x = 0; x < 64; x += 2) {
+          float p, q;
+          split(fma2(f2(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), scale2, ref22), p, q);
+          p = ex2(p);
+          q = ex2(q);
+          s2[(x >> 1) & 1] = add2(s2[(x >> 1) & 1], f2(p, q));
+          u[x / 2] = pack2(p, q);
+        }
+        tc::tmem_st32(ts, u);
+        {
+          float p, q;
+          split(add2(s2[0], s2[1]), p, q);
+          l = p + q;
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + j);
       }
-      {
-        float x, y;
-        split(add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])), x, y);
-        l = x + y;
-      }
-      tc::tmem_st32(ts, u);
-      tc::tmem_st32(ts + 32, u + 32);
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full + j);
-    }
-    if (nj && ok) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(o_full + j, 0));
+      if (!ok) break;
+      sums[half * 128] = l;
+      meet();
+      l = sums[0] + sums[128];
+      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(o_full + j, outs & 1)))) break;
+      ++outs;
       tc::fence_after_sync();
       const float inv = 1.f / l;
-      const size_t t = (size_t)blk.row0 + row;
-      bf16* dst = a.o + (t * a.Hq + head) * D;
+      const size_t tok = (size_t)t.blk.row0 + row;
+      bf16* dst = a.o + (tok * a.Hq + t.head) * D + half * (D / 2);
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t w[32];
-        tc::tmem_ld32_nowait(to + c, w);
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t x[32];
+        tc::tmem_ld32_nowait(to + c, x);
         tc::tmem_wait_ld();
-        if (ok && row < blk.len)
+        if (row < t.blk.len)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              h[e] = pack2(__uint_as_float(w[g * 8 + 2 * e]) * inv, __uint_as_float(w[g * 8 + 2 * e + 1]) * inv);
+              h[e] = pack2(__uint_as_float(x[g * 8 + 2 * e]) * inv, __uint_as_float(x[g * 8 + 2 * e + 1]) * inv);
             *reinterpret_cast<uint4*>(dst + c + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
           }
       }
-      if (ok && row < blk.len) a.lse[(size_t)head * a.T + t] = (ref2 + log2f(l)) * LN2;
+      if (row < t.blk.len && half == 0) a.lse[(size_t)t.head * a.T + tok] = (ref2 + log2f(l)) * LN2;
+      tc::fence_before_sync();  // O has been read before the next item's P V, which waits for its P
     }
+    // a warp that gave up does not keep its partner in meet()
+    if (!ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + j * 4 + (warp & 3)) : "memory");
   }
   if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == SW + 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }

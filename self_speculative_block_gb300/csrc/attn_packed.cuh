@@ -134,6 +134,14 @@ __device__ __forceinline__ uint64_t desc_n(uint32_t tile, int ks) {
   return tc::sdesc_sw128_mn(tile + ks * 2048, BOX_BYTES);
 }
 
+// A block's 128 scores of a row are shared by 128 / W threads of W columns
+// each.  A thread writes its W values in bf16 over the first half of its own
+// columns, so nobody overwrites scores that another has yet to read; step ks
+// of the product over them (16 values, 8 packed columns) then starts here:
+template <int W> __device__ __forceinline__ uint32_t packed_col(int ks) {
+  return (ks * 16 / W) * W + (ks * 16 % W) / 2;
+}
+
 // 3-D TMA map over [T, heads, D] bf16 rows `ld` elements apart: boxes of 64
 // columns x 1 head x 128 rows.
 inline bool map_rows(CUtensorMap* m, const void* p, int T, int heads, int D, long long ld) {

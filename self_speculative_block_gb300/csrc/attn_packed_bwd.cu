@@ -40,6 +40,8 @@ constexpr int SMEM = BAR_OFF + 256 + 1024;
 
 // Barrier of the elementwise warps.
 __device__ __forceinline__ void elementwise_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// A warp that gave up does not keep the others in it.
+__device__ __forceinline__ void elementwise_leave() { asm volatile("bar.arrive 1, 256;" ::: "memory"); }
 
 static __device__ int g_error;  // DevErr of a wait that gave up
 
@@ -89,12 +91,6 @@ __device__ __forceinline__ void store32(uint32_t taddr, float f, bf16* dst, bool
       *reinterpret_cast<uint4*>(dst + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
-
-// 64 packed values (32 columns) of an elementwise thread back to tensor memory.
-// The two column halves of a block keep to their own columns, [0, 32) and
-// [64, 96), so neither overwrites scores that the other has yet to read; step
-// ks of the product (16 of the 128 columns, 8 packed) then starts here:
-__device__ __forceinline__ uint32_t packed_col(int ks) { return (ks >> 2) * 64 + (ks & 3) * 8; }
 
 // ---------------------------------------------------------------- dk, dv
 
@@ -233,7 +229,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       auto add = [&](uint32_t dst, uint32_t src, uint32_t y, bool first) {  // dst += src y over 128 rows
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16_ta(tmem + dst, tmem + src + packed_col(ks), desc_n(y, ks), idesc_g, !first || ks > 0 ? 1u : 0u);
+          tc::mma_bf16_ta(tmem + dst, tmem + src + packed_col<64>(ks), desc_n(y, ks), idesc_g, !first || ks > 0 ? 1u : 0u);
       };
       ok = wait(kv_full, 0) && wait(q_full, 0);
       if (ok) {
@@ -348,7 +344,9 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(ds_full);
     }
-    if (ok) {
+    if (!ok) {
+      elementwise_leave();
+    } else {
       ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(done, 0));
       tc::fence_after_sync();
       const bool in = ok && key < blk.len;
@@ -493,7 +491,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
         if (it + 1 == n && tail < 128 && !(ok = wait(k_tail, 0))) break;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16_ta(tmem + DQ, tmem + st * 128 + packed_col(ks), desc_n(k + ks0 * G::TILE, ks), idesc_g,
+          tc::mma_bf16_ta(tmem + DQ, tmem + st * 128 + packed_col<64>(ks), desc_n(k + ks0 * G::TILE, ks), idesc_g,
                           it > 0 || ks > 0 ? 1u : 0u);
         tc::mma_commit(k_empty + ks0);
       }
@@ -560,7 +558,9 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(ds_full + st);
     }
-    if (ok) {
+    if (!ok) {
+      elementwise_leave();
+    } else {
       ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(done, 0));
       tc::fence_after_sync();
       const uint32_t tq = tmem + lanes + DQ + half * (D / 2);

@@ -190,21 +190,21 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   Tile t;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int st = 0, ph = 0;
-      for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
-        // few rows: the odd CTA has none; what its part of A then holds only
-        // reaches accumulator rows that nobody reads
-        const bool with_a = KIND == PROD || a.a_rows == RM || rank == 0;
-        const uint32_t bytes = 2 * (t.half ? BOX : B_BYTES) + (KIND == PROD || a.a_rows == RM ? 2 * A_BYTES : a_bytes);
-        const int m = t.m0 + rank * RM, n = t.n0 + rank * (t.half ? 64 : RN);
-        for (int k = 0; k < t.ks; ++k) {
-          if (!(ok = tc::mbar_wait_ns(empty + st, ph ^ 1))) break;
-          uint8_t* sa = sm + st * stage_bytes;
-          uint8_t* sb = sa + a_bytes;
-          const int kk = (t.k0 + k) * TK;
+    int st = 0, ph = 0;
+    for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
+      // few rows: the odd CTA has none; what its part of A then holds only
+      // reaches accumulator rows that nobody reads
+      const bool with_a = KIND == PROD || a.a_rows == RM || rank == 0;
+      const uint32_t bytes = 2 * (t.half ? BOX : B_BYTES) + (KIND == PROD || a.a_rows == RM ? 2 * A_BYTES : a_bytes);
+      const int m = t.m0 + rank * RM, n = t.n0 + rank * (t.half ? 64 : RN);
+      for (int k = 0; k < t.ks; ++k) {
+        if (!(ok = tc::mbar_wait_warp(empty + st, ph ^ 1))) break;
+        uint8_t* sa = sm + st * stage_bytes;
+        uint8_t* sb = sa + a_bytes;
+        const int kk = (t.k0 + k) * TK;
+        const uint32_t bar = tc::mapa(tc::smem_u32(full + st), 0);
+        if (tc::elect_one()) {
           if (rank == 0) tc::mbar_expect_tx(full + st, bytes);
-          const uint32_t bar = tc::mapa(tc::smem_u32(full + st), 0);
           if (KIND != PROD) {
             if (with_a) tc::tma_load_2d_pair(sa, &maps.a0, kk, m, bar);
             tc::tma_load_2d_pair(sb, &maps.b0, kk, a.v0 + n, bar);
@@ -220,23 +220,24 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             tc::tma_load_2d_pair(sb, mb, n, row, bar);
             if (!t.half) tc::tma_load_2d_pair(sb + BOX, mb, n + 64, row, bar);
           }
-          if (++st == a.stages) { st = 0; ph ^= 1; }
         }
+        __syncwarp();
+        if (++st == a.stages) { st = 0; ph ^= 1; }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      int st = 0, ph = 0, acc = 0, aph = 0;
-      for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
-        if (!(ok = tc::mbar_wait_ns(acc_free + acc, aph ^ 1))) break;
+    int st = 0, ph = 0, acc = 0, aph = 0;
+    for (int i = 0; rank == 0 && ok && tile_of<KIND>(a, pair, i, t); ++i) {
+      if (!(ok = tc::mbar_wait_warp(acc_free + acc, aph ^ 1))) break;
+      tc::fence_after_sync();
+      const uint32_t d = tmem + acc * TN;
+      uint32_t idesc = tc::idesc_bf16(TM, t.half ? RN : TN);
+      if (KIND == PROD) idesc |= tc::IDESC_B_MN | (t.prod ? tc::IDESC_A_MN : 0u);
+      for (int k = 0; k < t.ks; ++k) {
+        if (!(ok = tc::mbar_wait_warp(full + st, ph))) break;
         tc::fence_after_sync();
-        const uint32_t d = tmem + acc * TN;
-        uint32_t idesc = tc::idesc_bf16(TM, t.half ? RN : TN);
-        if (KIND == PROD) idesc |= tc::IDESC_B_MN | (t.prod ? tc::IDESC_A_MN : 0u);
-        for (int k = 0; k < t.ks; ++k) {
-          if (!(ok = tc::mbar_wait_ns(full + st, ph))) break;
-          tc::fence_after_sync();
-          const uint32_t sa = tc::smem_u32(sm + st * stage_bytes), sb = sa + a_bytes;
+        const uint32_t sa = tc::smem_u32(sm + st * stage_bytes), sb = sa + a_bytes;
+        if (tc::elect_one()) {
 #pragma unroll
           for (int j = 0; j < TK / 16; ++j) {
             const uint64_t ad = KIND == PROD && t.prod ? tc::sdesc_sw128_mn(sa + j * 2048, BOX) : tc::sdesc_sw128(sa + j * 32);
@@ -244,21 +245,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             tc::mma_bf16_pair(d, ad, bd, idesc, k > 0 || j > 0 ? 1u : 0u);
           }
           tc::mma_commit_pair(empty + st);
-          if (++st == a.stages) { st = 0; ph ^= 1; }
+          if (k + 1 == t.ks) tc::mma_commit_pair(acc_full + acc);
         }
-        if (!ok) break;
-        tc::mma_commit_pair(acc_full + acc);
-        acc ^= 1;
-        if (acc == 0) aph ^= 1;
+        __syncwarp();
+        if (++st == a.stages) { st = 0; ph ^= 1; }
       }
+      acc ^= 1;
+      if (acc == 0) aph ^= 1;
     }
   } else {
     const int q = warp & 3;  // the tensor memory lanes this warp may read: 32 q ..
     uint8_t* box = sm + OFF_STORE + q * 2 * STORE_BYTES;
     int acc = 0, aph = 0, buf = 0;
     for (int i = 0; tile_of<KIND>(a, pair, i, t); ++i) {
-      // one verdict a warp: its lanes leave the loop together
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(acc_full + acc, aph)))) break;
+      if (!(ok = tc::mbar_wait_warp(acc_full + acc, aph))) break;
       tc::fence_after_sync();
       const uint32_t src = tmem + acc * TN + ((uint32_t)(q * 32) << 16);
       const int row0 = t.m0 + rank * RM + q * 32;  // the warp's first row

@@ -49,6 +49,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// One lane of a converged warp, the same one each time.  MMAs and copies take
+// their descriptors from uniform registers: issued under elect_one() by a warp
+// that runs its loop as a whole, they get them directly, while a branch on the
+// lane number makes the compiler move every operand for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Wait bounded in time (WAIT_NS): false when it ran out.  For kernels whose
 // roles hand work to one another: each role that gives up ends its loop, and
 // the roles that wait on it end theirs within the same bound.
@@ -64,6 +74,11 @@ __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity) {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   } while (t - t0 < WAIT_NS);
   return false;
+}
+
+// The same for a warp, which gets one verdict.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_ns(bar, parity));
 }
 
 // 2-D tiled TMA load global -> shared, completion counted on `bar`.
@@ -301,6 +316,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
         "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
