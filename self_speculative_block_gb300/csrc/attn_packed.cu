@@ -20,7 +20,8 @@
 // The grid has a CTA per work item, but a running CTA takes over the items of
 // those that have not started (cluster launch control), so barriers and tensor
 // memory are set up once per SM and the next item's Q, K and V are on their way
-// while the last one's output is written.  A warp looks items up two ahead.
+// while the last one's output is written.  A warp takes the next item when the
+// last loads of this one have been issued.
 #include "../../include/gocr.h"
 #include "attn_packed.cuh"
 
@@ -79,7 +80,7 @@ struct Item {
 __device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full, uint64_t* work_free, int i, int4& w,
                                           bool& ok) {
   const int s = i & 1;
-  if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(work_full + s, (i >> 1) & 1)))) return false;
+  if (!(ok = tc::mbar_wait_warp(work_full + s, (i >> 1) & 1))) return false;
   w = work[s];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) tc::mbar_arrive(work_free + s);
@@ -128,7 +129,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* work_full = v_tail + SLOTS;  // [2]
   uint64_t* work_free = work_full + 2;  // [2]
   uint64_t* taken = work_free + 2;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(taken + 1);
+  uint64_t* ask = taken + 1;            // the item's loads are on their way
+  uint32_t* holder = reinterpret_cast<uint32_t*>(ask + 1);
   int4* work = reinterpret_cast<int4*>(sm + F::OFF_WORK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::mbar_init(work_free + j, SW + 3);
     }
     tc::mbar_init(taken, 1);
+    tc::mbar_init(ask, 1);
     tc::fence_mbar_init();
   }
   __syncwarp();
@@ -167,93 +170,95 @@ __global__ void __launch_bounds__(THREADS, 1)
       int slot = 0, ph = 0;
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
-        if (lane == 0) {
-          const int kvh = t.head / (a.Hq / a.Hkv);
-          for (int x = 0; x < 2 * t.n; ++x) {
-            if (!(ok = tc::mbar_wait_ns(empty + slot, ph ^ 1))) break;
+        const int kvh = t.head / (a.Hq / a.Hkv);
+        for (int x = 0; x < 2 * t.n; ++x) {
+          if (!(ok = tc::mbar_wait_warp(empty + slot, ph ^ 1))) break;
+          if (tc::elect_one()) {
             tc::mbar_expect_tx(full + slot, TILE_BYTES<D>);
             load_tile<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, x & 1 ? &mv : &mk, kvh, t.blk.row0 + (x >> 1) * 128, full + slot);
             if (x == 2 * t.n - 1 && t.tail < 128) tc::mbar_arrive(tail_go + slot);
-            if (++slot == SLOTS) { slot = 0; ph ^= 1; }
-            if (x == 0) {
-              if (!(ok = tc::mbar_wait_ns(q_empty, (i & 1) ^ 1))) break;
+          }
+          __syncwarp();
+          if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+          if (x == 0) {
+            if (!(ok = tc::mbar_wait_warp(q_empty, (i & 1) ^ 1))) break;
+            if (tc::elect_one()) {
               tc::mbar_expect_tx(q_full, (t.n1 ? 2 : 1) * TILE_BYTES<D>);
               load_tile<D>(sm + F::OFF_Q, &mq, t.head, t.blk.row0 + t.blk.at, q_full);
               if (t.n1) load_tile<D>(sm + F::OFF_Q + TILE_BYTES<D>, &mq, t.head, t.blk.row0 + t.blk.at + 128, q_full);
             }
+            __syncwarp();
           }
         }
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!ok) break;
+        if (lane == 0) tc::mbar_arrive(ask);
       }
     } else if (warp == SW + 1) {
-      constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
-      constexpr uint32_t idesc_o = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
       const uint32_t q = tc::smem_u32(sm + F::OFF_Q), kv = tc::smem_u32(sm + F::OFF_KV);
       int ring = 0;              // ring position of the item's K(0)
       unsigned tails = 0;        // parity of each slot's ragged tiles so far
       int turn[2] = {0, 0};      // blocks of the two tiles so far
+      auto wait = [&](uint64_t* bar, int ph) {
+        const bool r = tc::mbar_wait_warp(bar, ph & 1);
+        tc::fence_after_sync();
+        return r;
+      };
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
-        if (lane == 0) {
-          auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
-          auto wait = [&](uint64_t* bar, int ph) {
-            const bool r = tc::mbar_wait_ns(bar, ph & 1);
-            tc::fence_after_sync();
-            return r;
-          };
-          auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
-          auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
-          auto scores = [&](int j, int it) {
-            const uint32_t k = tile_of(2 * it);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc::mma_bf16(tmem + j * 128, desc_k(q + j * TILE_BYTES<D>, ks), desc_k(k, ks), idesc_s, ks > 0 ? 1u : 0u);
-            tc::mma_commit(s_full + j);
-          };
-          ok = wait(q_full, i) && wait_full(0);
-          if (ok) {
-            // over P of the last item, whose products were issued before
-            scores(0, 0);
-            if (t.n1) scores(1, 0);
-            release(0);
-            if (t.n == 1) tc::mma_commit(q_empty);
+        auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
+        auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
+        auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
+        if (!(ok = wait(q_full, i) && wait_full(0))) break;
+        if (tc::elect_one()) {
+          // over P of the last item, whose products were issued before
+          mma_rows<D>(tmem, q, tile_of(0));
+          tc::mma_commit(s_full);
+          if (t.n1) {
+            mma_rows<D>(tmem + 128, q + TILE_BYTES<D>, tile_of(0));
+            tc::mma_commit(s_full + 1);
           }
-          for (int it = 0; it < t.n && ok; ++it) {
-            if (!(ok = wait_full(2 * it + 1))) break;
-            if (it == t.n - 1 && t.tail < 128) {
-              const int slot = (ring + 2 * it + 1) % SLOTS;
-              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
-              tails ^= 1u << slot;
-            }
-            const uint32_t v = tile_of(2 * it + 1);
-            bool have_k = false;
+          release(0);
+          if (t.n == 1) tc::mma_commit(q_empty);
+        }
+        __syncwarp();
+        for (int it = 0; it < t.n; ++it) {
+          if (!(ok = wait_full(2 * it + 1))) break;
+          if (it == t.n - 1 && t.tail < 128) {
+            const int slot = (ring + 2 * it + 1) % SLOTS;
+            if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+            tails ^= 1u << slot;
+          }
+          const uint32_t v = tile_of(2 * it + 1), k = tile_of(2 * it + 2);
+          bool have_k = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int nj = j ? t.n1 : t.n0;
-              if (it >= nj) continue;
-              if (!(ok = wait(p_full + j, turn[j] + it))) break;
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc::mma_bf16_ta(tmem + F::O_COL + j * D, tmem + j * 128 + packed_col<64>(ks), desc_n(v, ks), idesc_o,
-                                it > 0 || ks > 0 ? 1u : 0u);
+          for (int j = 0; j < 2; ++j) {
+            const int nj = j ? t.n1 : t.n0;
+            if (it >= nj) continue;
+            if (!(ok = wait(p_full + j, turn[j] + it))) break;
+            if (it + 1 < nj && !have_k && !(have_k = ok = wait_full(2 * it + 2))) break;
+            if (tc::elect_one()) {
+              mma_add<D, 64>(tmem + F::O_COL + j * D, tmem + j * 128, v, it == 0);
               if (it + 1 < nj) {
-                if (!have_k && !(ok = wait_full(2 * it + 2))) break;
-                have_k = true;
-                scores(j, it + 1);
+                mma_rows<D>(tmem + j * 128, q + j * TILE_BYTES<D>, k);
+                tc::mma_commit(s_full + j);
               } else {
                 tc::mma_commit(o_full + j);
               }
             }
-            if (!ok) break;
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (tc::elect_one()) {
             release(2 * it + 1);
             if (it + 1 < t.n) release(2 * it + 2);
             if (it + 2 == t.n) tc::mma_commit(q_empty);  // after the item's last scores
           }
+          __syncwarp();
         }
+        if (!ok) break;
         ring += 2 * t.n;
         turn[0] += t.n0;
         turn[1] += t.n1;
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
     } else if (warp == SW + 2) {
       // the items: this CTA's own, then those of CTAs that have not started
@@ -274,12 +279,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           take();
         }
         const bool more = id >= 0;
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(work_free + s, ((i >> 1) & 1) ^ 1)))) break;
+        if (!(ok = tc::mbar_wait_warp(work_free + s, ((i >> 1) & 1) ^ 1))) break;
         if (lane == 0) {
           work[s] = make_int4(blk.row0, more ? blk.len : 0, blk.at, more ? id % a.Hq : 0);
           tc::mbar_arrive(work_full + s);
         }
         if (!more) break;
+        // no earlier: an item in hand here is one that no idle SM can take
+        if (!(ok = tc::mbar_wait_warp(ask, i & 1))) break;
         take();
       }
     } else {
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row = t.blk.at + j * 128 + r;  // within the sequence
       float ref = 0.f, ref2 = 0.f, l = 0.f;    // the exponentials' reference, also times sl2; their sum
       for (int it = 0; it < nj; ++it, ++turn) {
-        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(s_full + j, turn & 1)))) break;
+        if (!(ok = tc::mbar_wait_warp(s_full + j, turn & 1))) break;
         tc::fence_after_sync();
         uint32_t u[64];
         tc::tmem_ld32_nowait(ts, u);
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       sums[half * 128] = l;
       meet();
       l = sums[0] + sums[128];
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(o_full + j, outs & 1)))) break;
+      if (!(ok = tc::mbar_wait_warp(o_full + j, outs & 1))) break;
       ++outs;
       tc::fence_after_sync();
       const float inv = 1.f / l;

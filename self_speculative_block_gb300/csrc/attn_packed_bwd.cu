@@ -184,14 +184,15 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       const bool ragged = at + 128 > blk.len;
       uint8_t* q = sm + G::OFF_Q + st * G::TILE;
       uint8_t* d_o = sm + G::OFF_DO + st * G::TILE;
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(q_empty + st, ph ^ 1)))) break;
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(do_empty + st, ph ^ 1)))) break;
-      if (lane == 0) {
+      if (!(ok = tc::mbar_wait_warp(q_empty + st, ph ^ 1))) break;
+      if (!(ok = tc::mbar_wait_warp(do_empty + st, ph ^ 1))) break;
+      if (tc::elect_one()) {
         tc::mbar_expect_tx(q_full + st, G::TILE);
         load_tile<D>(q, &mq, head, blk.row0 + at, q_full + st);
         tc::mbar_expect_tx(do_full + st, G::TILE);
         load_tile<D>(d_o, &mdo, head, blk.row0 + at, do_full + st);
       }
+      __syncwarp();
       // the stage is free: dK of its last block, after every read of its rows, has completed
       float* lse = rows + st * 256;
       for (int i = lane; i < 128; i += 32) {
@@ -201,7 +202,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
         lse[128 + i] = in ? a.delta[src] : 0.f;
       }
       if (ragged) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(q_full + st, ph) && tc::mbar_wait_ns(do_full + st, ph));
+        ok = tc::mbar_wait_warp(q_full + st, ph) && tc::mbar_wait_warp(do_full + st, ph);
         if (!ok) break;
         zero_rows<D>(q, tail);
         zero_rows<D>(d_o, tail);
@@ -211,49 +212,57 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       if (lane == 0) tc::mbar_arrive(row_full + st);
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
-      constexpr uint32_t idesc_g = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
-      const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
-      const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
-      auto wait = [&](uint64_t* bar, int ph) {
-        const bool w = tc::mbar_wait_ns(bar, ph);
-        tc::fence_after_sync();
-        return w;
-      };
-      auto block = [&](uint32_t dst, uint32_t x, uint32_t y, uint64_t* bar) {  // dst = x y^T over D
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) tc::mma_bf16(tmem + dst, desc_k(x, ks), desc_k(y, ks), idesc_s, ks > 0 ? 1u : 0u);
-        tc::mma_commit(bar);
-      };
-      auto add = [&](uint32_t dst, uint32_t src, uint32_t y, bool first) {  // dst += src y over 128 rows
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16_ta(tmem + dst, tmem + src + packed_col<64>(ks), desc_n(y, ks), idesc_g, !first || ks > 0 ? 1u : 0u);
-      };
-      ok = wait(kv_full, 0) && wait(q_full, 0);
-      if (ok) {
-        block(0, k, q, s_full);
-        if ((ok = wait(do_full, 0))) block(DP, v, d_o, dp_full);
-      }
-      for (int it = 0; it < n && ok; ++it) {
-        const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
-        if (!(ok = wait(p_full, it & 1))) break;
-        add(DV, 0, d_o + st * G::TILE, it == 0);
+    const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
+    const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
+    auto wait = [&](uint64_t* bar, int ph) {
+      const bool w = tc::mbar_wait_warp(bar, ph);
+      tc::fence_after_sync();
+      return w;
+    };
+    ok = wait(kv_full, 0) && wait(q_full, 0);
+    if (ok && tc::elect_one()) {
+      mma_rows<D>(tmem, k, q);
+      tc::mma_commit(s_full);
+    }
+    __syncwarp();
+    ok = ok && wait(do_full, 0);
+    if (ok && tc::elect_one()) {
+      mma_rows<D>(tmem + DP, v, d_o);
+      tc::mma_commit(dp_full);
+    }
+    __syncwarp();
+    for (int it = 0; it < n && ok; ++it) {
+      const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
+      const bool more = it + 1 < n;
+      if (!(ok = wait(p_full, it & 1))) break;
+      if (tc::elect_one()) {
+        mma_add<D, 64>(tmem + DV, tmem, d_o + st * G::TILE, it == 0);
         tc::mma_commit(do_empty + st);
-        if (it + 1 < n) {
-          if (!(ok = wait(q_full + nx, nph))) break;
-          block(0, k, q + nx * G::TILE, s_full);
-        }
-        if (!(ok = wait(ds_full, it & 1))) break;
-        add(DK, DP, q + st * G::TILE, it == 0);
-        tc::mma_commit(q_empty + st);
-        if (it + 1 < n) {
-          if (!(ok = wait(do_full + nx, nph))) break;
-          block(DP, v, d_o + nx * G::TILE, dp_full);
-        }
       }
-      if (ok) tc::mma_commit(done);
+      __syncwarp();
+      if (more) {
+        if (!(ok = wait(q_full + nx, nph))) break;
+        if (tc::elect_one()) {
+          mma_rows<D>(tmem, k, q + nx * G::TILE);
+          tc::mma_commit(s_full);
+        }
+        __syncwarp();
+      }
+      if (!(ok = wait(ds_full, it & 1))) break;
+      if (tc::elect_one()) {
+        mma_add<D, 64>(tmem + DK, tmem + DP, q + st * G::TILE, it == 0);
+        tc::mma_commit(q_empty + st);
+        if (!more) tc::mma_commit(done);
+      }
+      __syncwarp();
+      if (more) {
+        if (!(ok = wait(do_full + nx, nph))) break;
+        if (tc::elect_one()) {
+          mma_rows<D>(tmem + DP, v, d_o + nx * G::TILE);
+          tc::mma_commit(dp_full);
+        }
+        __syncwarp();
+      }
     }
   } else {
     const int half = warp >> 2;
@@ -299,7 +308,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(p_full);
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(dp_full, it & 1)))) break;
+      if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
       tc::fence_after_sync();
       {
         uint32_t u[64];
@@ -347,7 +356,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
     if (!ok) {
       elementwise_leave();
     } else {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(done, 0));
+      ok = tc::mbar_wait_warp(done, 0);
       tc::fence_after_sync();
       const bool in = ok && key < blk.len;
       const size_t at = ((size_t)(blk.row0 + key) * a.Hkv + kvh) * D + half * (D / 2);
@@ -429,73 +438,82 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   bool ok = true;
 
   if (warp == 8) {
-    if (lane == 0) {
+    if (tc::elect_one()) {
       tc::mbar_expect_tx(q_full, 2 * G::TILE);
       load_tile<D>(sm + G::OFF_Q, &mq, head, blk.row0 + blk.at, q_full);
       load_tile<D>(sm + G::OFF_DO, &mdo, head, blk.row0 + blk.at, q_full);
-      for (int it = 0; it < n; ++it) {
-        const int st = it & 1, ph = (it >> 1) & 1;
-        const int ks = it % 3;
-        if (!(ok = tc::mbar_wait_ns(k_empty + ks, (it / 3 & 1) ^ 1))) break;
+    }
+    __syncwarp();
+    for (int it = 0; it < n; ++it) {
+      const int st = it & 1, ph = (it >> 1) & 1, ks = it % 3;
+      if (!(ok = tc::mbar_wait_warp(k_empty + ks, (it / 3 & 1) ^ 1))) break;
+      if (tc::elect_one()) {
         tc::mbar_expect_tx(k_full + ks, G::TILE);
         load_tile<D>(sm + G::OFF_K + ks * G::TILE, &mk, kvh, blk.row0 + it * 128, k_full + ks);
-        if (!(ok = tc::mbar_wait_ns(v_empty + st, ph ^ 1))) break;
+      }
+      __syncwarp();
+      if (!(ok = tc::mbar_wait_warp(v_empty + st, ph ^ 1))) break;
+      if (tc::elect_one()) {
         tc::mbar_expect_tx(v_full + st, G::TILE);
         load_tile<D>(sm + G::OFF_V + st * G::TILE, &mv, kvh, blk.row0 + it * 128, v_full + st);
       }
+      __syncwarp();
     }
-    ok = __all_sync(0xffffffffu, ok);
     if (ok && tail < 128) {  // nothing behind the sequence in dQ += dS K
       const int ks = (n - 1) % 3;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(k_full + ks, (n - 1) / 3 & 1));
+      ok = tc::mbar_wait_warp(k_full + ks, (n - 1) / 3 & 1);
       zero_rows<D>(sm + G::OFF_K + ks * G::TILE, tail);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(k_tail);
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128);
-      constexpr uint32_t idesc_g = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
-      const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
-      const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
-      auto wait = [&](uint64_t* bar, int ph) {
-        const bool w = tc::mbar_wait_ns(bar, ph);
-        tc::fence_after_sync();
-        return w;
-      };
-      auto block = [&](uint32_t dst, uint32_t x, uint32_t y, uint64_t* bar) {
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) tc::mma_bf16(tmem + dst, desc_k(x, ks), desc_k(y, ks), idesc_s, ks > 0 ? 1u : 0u);
-        tc::mma_commit(bar);
-      };
-      ok = wait(q_full, 0) && wait(k_full, 0);
-      if (ok) {
-        block(0, q, k, s_full);
-        if ((ok = wait(v_full, 0))) {
-          block(DP, d_o, v, dp_full);
-          tc::mma_commit(v_empty);
+    const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
+    const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
+    auto wait = [&](uint64_t* bar, int ph) {
+      const bool w = tc::mbar_wait_warp(bar, ph);
+      tc::fence_after_sync();
+      return w;
+    };
+    ok = wait(q_full, 0) && wait(k_full, 0);
+    if (ok && tc::elect_one()) {
+      mma_rows<D>(tmem, q, k);
+      tc::mma_commit(s_full);
+    }
+    __syncwarp();
+    ok = ok && wait(v_full, 0);
+    if (ok && tc::elect_one()) {
+      mma_rows<D>(tmem + DP, d_o, v);
+      tc::mma_commit(dp_full);
+      tc::mma_commit(v_empty);
+    }
+    __syncwarp();
+    for (int it = 0; it < n && ok; ++it) {
+      const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1, ks0 = it % 3, ks1 = (it + 1) % 3;
+      if (it + 1 < n) {
+        // the other score buffer: its dS was consumed by dQ(it - 1), issued before
+        if (!(ok = wait(k_full + ks1, (it + 1) / 3 & 1))) break;
+        if (tc::elect_one()) {
+          mma_rows<D>(tmem + nx * 128, q, k + ks1 * G::TILE);
+          tc::mma_commit(s_full + nx);
         }
-      }
-      for (int it = 0; it < n && ok; ++it) {
-        const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1, ks0 = it % 3, ks1 = (it + 1) % 3;
-        if (it + 1 < n) {
-          // the other score buffer: its dS was consumed by dQ(it - 1), issued before
-          if (!(ok = wait(k_full + ks1, (it + 1) / 3 & 1))) break;
-          block(nx * 128, q, k + ks1 * G::TILE, s_full + nx);
-          if (!(ok = wait(v_full + nx, nph) && wait(dp_free, it & 1))) break;
-          block(DP, d_o, v + nx * G::TILE, dp_full);
+        __syncwarp();
+        if (!(ok = wait(v_full + nx, nph) && wait(dp_free, it & 1))) break;
+        if (tc::elect_one()) {
+          mma_rows<D>(tmem + DP, d_o, v + nx * G::TILE);
+          tc::mma_commit(dp_full);
           tc::mma_commit(v_empty + nx);
         }
-        if (!(ok = wait(ds_full + st, (it >> 1) & 1))) break;
-        if (it + 1 == n && tail < 128 && !(ok = wait(k_tail, 0))) break;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16_ta(tmem + DQ, tmem + st * 128 + packed_col<64>(ks), desc_n(k + ks0 * G::TILE, ks), idesc_g,
-                          it > 0 || ks > 0 ? 1u : 0u);
-        tc::mma_commit(k_empty + ks0);
+        __syncwarp();
       }
-      if (ok) tc::mma_commit(done);
+      if (!(ok = wait(ds_full + st, (it >> 1) & 1))) break;
+      if (it + 1 == n && tail < 128 && !(ok = wait(k_tail, 0))) break;
+      if (tc::elect_one()) {
+        mma_add<D, 64>(tmem + DQ, tmem + st * 128, k + ks0 * G::TILE, it == 0);
+        tc::mma_commit(k_empty + ks0);
+        if (it + 1 == n) tc::mma_commit(done);
+      }
+      __syncwarp();
     }
   } else {
     const int half = warp >> 2;
@@ -510,7 +528,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     for (int it = 0; it < n; ++it) {
       const int st = it & 1;
       const uint32_t ts = tmem + lanes + st * 128 + half * 64;
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(s_full + st, (it >> 1) & 1)))) break;
+      if (!(ok = tc::mbar_wait_warp(s_full + st, (it >> 1) & 1))) break;
       tc::fence_after_sync();
       float p[64];
       {
@@ -521,7 +539,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
 #pragma unroll
         for (int i = 0; i < 64; ++i) p[i] = ex2(fmaf(__uint_as_float(u[i]), sl2, -lse));
       }
-      if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(dp_full, it & 1)))) break;
+      if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
       tc::fence_after_sync();
       {
         uint32_t u[64];
@@ -561,7 +579,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     if (!ok) {
       elementwise_leave();
     } else {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_ns(done, 0));
+      ok = tc::mbar_wait_warp(done, 0);
       tc::fence_after_sync();
       const uint32_t tq = tmem + lanes + DQ + half * (D / 2);
 #pragma unroll

@@ -238,12 +238,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         tc::fence_after_sync();
         const uint32_t sa = tc::smem_u32(sm + st * stage_bytes), sb = sa + a_bytes;
         if (tc::elect_one()) {
+          // a step of 16 along K: 32 bytes of a K-major tile, 16 rows of an M- or N-major one
+          const bool a_mn = KIND == PROD && t.prod;
+          const uint64_t ad = a_mn ? tc::sdesc_sw128_mn(sa, BOX) : tc::sdesc_sw128(sa);
+          const uint64_t bd = KIND == PROD ? tc::sdesc_sw128_mn(sb, BOX) : tc::sdesc_sw128(sb);
+          const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (KIND == PROD ? 2048 : 32) >> 4;
 #pragma unroll
-          for (int j = 0; j < TK / 16; ++j) {
-            const uint64_t ad = KIND == PROD && t.prod ? tc::sdesc_sw128_mn(sa + j * 2048, BOX) : tc::sdesc_sw128(sa + j * 32);
-            const uint64_t bd = KIND == PROD ? tc::sdesc_sw128_mn(sb + j * 2048, BOX) : tc::sdesc_sw128(sb + j * 32);
-            tc::mma_bf16_pair(d, ad, bd, idesc, k > 0 || j > 0 ? 1u : 0u);
-          }
+          for (int j = 0; j < TK / 16; ++j) tc::mma_bf16_pair(d, ad + j * a_step, bd + j * b_step, idesc, k > 0 || j > 0 ? 1u : 0u);
           tc::mma_commit_pair(empty + st);
           if (k + 1 == t.ks) tc::mma_commit_pair(acc_full + acc);
         }
