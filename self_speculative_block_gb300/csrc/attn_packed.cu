@@ -13,6 +13,9 @@
 // cores work for the other.  O stays in tensor memory and is rescaled only when
 // a row's maximum grows by more than 2^8 over the one its exponentials refer to
 // (the sum and O use the same reference, so nothing is lost; P is at most 2^8).
+// Each tile has an MMA warp of its own: an MMA of 128 x 128 x 16 lasts 64
+// cycles and few fit the queue, so a single warp's waits between its batches
+// left the tensor cores idle a third of the time.
 // P is rounded to bf16 (relative 2^-8) since the tensor cores take it so;
 // scores, maxima, sums and O are fp32.  No partial results leave the CTA: a
 // row's bits depend on its own sequence only.
@@ -32,7 +35,7 @@ namespace {
 
 constexpr int QT = 256;        // query rows of a work item
 // Sixteen softmax warps (two tiles x two column halves x four lane quarters),
-// then the TMA, MMA, work and tail warps.  The softmax groups take 104
+// then the TMA warp, an MMA warp a tile and the work warp.  The softmax groups take 104
 // registers a thread of the 96 x 640 that the block is launched with, the last
 // group 64.
 constexpr int SW = 16, THREADS = (SW + 4) * 32;
@@ -87,14 +90,19 @@ __device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full,
   return w.y > 0;
 }
 
-// The index of a CTA of this launch that now will not start, or -1; one thread.
-__device__ __forceinline__ int take_cta(void* answer, uint64_t* bar, int turn, bool& ok) {
-  const uint32_t at = tc::smem_u32(answer);
-  tc::fence_proxy_async_smem();
-  tc::mbar_expect_tx(bar, 16);
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
-               ::"r"(at), "r"(tc::smem_u32(bar)) : "memory");
-  if (!(ok = tc::mbar_wait_ns(bar, turn & 1))) return -1;
+// Asks for a CTA of this launch that has not started, and its index if it now
+// will not start, else -1 (then no further ask is allowed).  One warp.
+__device__ __forceinline__ void ask_cta(void* answer, uint64_t* bar) {
+  if ((threadIdx.x & 31) == 0) {
+    tc::fence_proxy_async_smem();
+    tc::mbar_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(tc::smem_u32(answer)), "r"(tc::smem_u32(bar)) : "memory");
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ int taken_cta(const void* answer, uint64_t* bar, int turn, bool& ok) {
+  if (!(ok = tc::mbar_wait_warp(bar, turn & 1))) return -1;
   uint32_t yes, x;
   asm volatile(
       "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
@@ -103,7 +111,8 @@ __device__ __forceinline__ int take_cta(void* answer, uint64_t* bar, int turn, b
       "selp.u32 %0, 1, 0, p;\n\t"
       "mov.u32 %1, 0;\n\t"
       "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(yes), "=r"(x) : "r"(at) : "memory");
+      : "=r"(yes), "=r"(x) : "r"(tc::smem_u32(answer)) : "memory");
+  __syncwarp();
   return yes ? (int)x : -1;
 }
 
@@ -124,23 +133,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* o_full = p_full + 2;     // [2]
   // ragged V tiles, one barrier a slot: a slot's next load waits for this one's
   // use, so no barrier is ever two phases ahead of the warp that waits on it
-  uint64_t* tail_go = o_full + 2;      // [SLOTS] the load has been issued
-  uint64_t* v_tail = tail_go + SLOTS;  // [SLOTS] the rows behind the sequence are zero
+  uint64_t* v_tail = o_full + 2;         // [SLOTS] the rows behind the sequence are zero
   uint64_t* work_full = v_tail + SLOTS;  // [2]
   uint64_t* work_free = work_full + 2;  // [2]
   uint64_t* taken = work_free + 2;
-  uint64_t* ask = taken + 1;            // the item's loads are on their way
-  uint32_t* holder = reinterpret_cast<uint32_t*>(ask + 1);
+  uint64_t* issued = taken + 1;            // the item's loads are on their way
+  uint32_t* holder = reinterpret_cast<uint32_t*>(issued + 1);
   int4* work = reinterpret_cast<int4*>(sm + F::OFF_WORK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     tc::mbar_init(q_full, 1);
-    tc::mbar_init(q_empty, 1);
+    tc::mbar_init(q_empty, 2);
     for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(full + s, 1);
-      tc::mbar_init(empty + s, 1);
-      tc::mbar_init(tail_go + s, 1);
+      tc::mbar_init(empty + s, 2);
       tc::mbar_init(v_tail + s, 1);
     }
     for (int j = 0; j < 2; ++j) {
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::mbar_init(work_free + j, SW + 3);
     }
     tc::mbar_init(taken, 1);
-    tc::mbar_init(ask, 1);
+    tc::mbar_init(issued, 1);
     tc::fence_mbar_init();
   }
   __syncwarp();
@@ -176,7 +183,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (tc::elect_one()) {
             tc::mbar_expect_tx(full + slot, TILE_BYTES<D>);
             load_tile<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, x & 1 ? &mv : &mk, kvh, t.blk.row0 + (x >> 1) * 128, full + slot);
-            if (x == 2 * t.n - 1 && t.tail < 128) tc::mbar_arrive(tail_go + slot);
           }
           __syncwarp();
           if (++slot == SLOTS) { slot = 0; ph ^= 1; }
@@ -191,13 +197,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (!ok) break;
-        if (lane == 0) tc::mbar_arrive(ask);
+        if (lane == 0) tc::mbar_arrive(issued);
       }
-    } else if (warp == SW + 1) {
-      const uint32_t q = tc::smem_u32(sm + F::OFF_Q), kv = tc::smem_u32(sm + F::OFF_KV);
-      int ring = 0;              // ring position of the item's K(0)
-      unsigned tails = 0;        // parity of each slot's ragged tiles so far
-      int turn[2] = {0, 0};      // blocks of the two tiles so far
+    } else if (warp < SW + 3) {
+      const int j = warp - (SW + 1);  // the tile
+      const uint32_t q = tc::smem_u32(sm + F::OFF_Q + j * TILE_BYTES<D>), kv = tc::smem_u32(sm + F::OFF_KV);
+      int ring = 0;        // ring position of the item's K(0)
+      unsigned tails = 0;  // parity of each slot's ragged tiles so far
+      int turn = 0;        // blocks of the tile so far
       auto wait = [&](uint64_t* bar, int ph) {
         const bool r = tc::mbar_wait_warp(bar, ph & 1);
         tc::fence_after_sync();
@@ -205,108 +212,86 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
+        const int nj = j ? t.n1 : t.n0;
         auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
         auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
+        // both MMA warps give a K/V tile back, whether they used it or not
+        // (but not before it is there: the barrier is in an older phase)
         auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
         if (!(ok = wait(q_full, i) && wait_full(0))) break;
         if (tc::elect_one()) {
-          // over P of the last item, whose products were issued before
-          mma_rows<D>(tmem, q, tile_of(0));
-          tc::mma_commit(s_full);
-          if (t.n1) {
-            mma_rows<D>(tmem + 128, q + TILE_BYTES<D>, tile_of(0));
-            tc::mma_commit(s_full + 1);
+          if (nj) {
+            // over P of the last item, whose product was issued before
+            mma_rows<D>(tmem + j * 128, q, tile_of(0));
+            tc::mma_commit(s_full + j);
           }
           release(0);
-          if (t.n == 1) tc::mma_commit(q_empty);
+          if (nj < 2) tc::mma_commit(q_empty);
         }
         __syncwarp();
         for (int it = 0; it < t.n; ++it) {
+          const bool more = it + 1 < t.n;
           if (!(ok = wait_full(2 * it + 1))) break;
-          if (it == t.n - 1 && t.tail < 128) {
+          if (more && !(ok = wait_full(2 * it + 2))) break;
+          if (!more && t.tail < 128) {
             const int slot = (ring + 2 * it + 1) % SLOTS;
             if (!(ok = wait(v_tail + slot, tails >> slot))) break;
             tails ^= 1u << slot;
           }
-          const uint32_t v = tile_of(2 * it + 1), k = tile_of(2 * it + 2);
-          bool have_k = false;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int nj = j ? t.n1 : t.n0;
-            if (it >= nj) continue;
-            if (!(ok = wait(p_full + j, turn[j] + it))) break;
-            if (it + 1 < nj && !have_k && !(have_k = ok = wait_full(2 * it + 2))) break;
-            if (tc::elect_one()) {
-              mma_add<D, 64>(tmem + F::O_COL + j * D, tmem + j * 128, v, it == 0);
-              if (it + 1 < nj) {
-                mma_rows<D>(tmem + j * 128, q + j * TILE_BYTES<D>, k);
-                tc::mma_commit(s_full + j);
-              } else {
-                tc::mma_commit(o_full + j);
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
+          if (it < nj && !(ok = wait(p_full + j, turn + it))) break;
           if (tc::elect_one()) {
+            if (it < nj) mma_add<D, 64>(tmem + F::O_COL + j * D, tmem + j * 128, tile_of(2 * it + 1), it == 0);
             release(2 * it + 1);
-            if (it + 1 < t.n) release(2 * it + 2);
-            if (it + 2 == t.n) tc::mma_commit(q_empty);  // after the item's last scores
+            if (it + 1 < nj) {
+              mma_rows<D>(tmem + j * 128, q, tile_of(2 * it + 2));
+              tc::mma_commit(s_full + j);
+            } else if (it + 1 == nj) {
+              tc::mma_commit(o_full + j);
+            }
+            if (more) release(2 * it + 2);
+            if (it + 2 == nj) tc::mma_commit(q_empty);  // after the item's last scores
           }
           __syncwarp();
         }
         if (!ok) break;
         ring += 2 * t.n;
-        turn[0] += t.n0;
-        turn[1] += t.n1;
+        turn += nj;
       }
-    } else if (warp == SW + 2) {
-      // the items: this CTA's own, then those of CTAs that have not started
-      int id = blockIdx.x, takes = 0;
-      auto take = [&] {
-        int x = -1;
-        if (lane == 0) x = take_cta(work + 2, taken, takes, ok);
-        ++takes;
-        id = __shfl_sync(0xffffffffu, x, 0);
-        ok = __all_sync(0xffffffffu, ok);
-      };
+    } else {
+      // the items: this CTA's own, then those of CTAs that have not started;
+      // and the last V tile of a ragged item: nothing behind the sequence
+      int id = blockIdx.x, takes = 0, ring = 0;
       for (int i = 0; ok; ++i) {
         const int s = i & 1;
         Block blk{0, 0, 0};
-        while (id >= 0) {
+        while (id >= 0 && ok) {
           blk = find_block<true>(a.cu, a.n_seq, a.T, QT, id / a.Hq);
           if (blk.len) break;
-          take();
+          ask_cta(work + 2, taken);
+          id = taken_cta(work + 2, taken, takes++, ok);
         }
         const bool more = id >= 0;
-        if (!(ok = tc::mbar_wait_warp(work_free + s, ((i >> 1) & 1) ^ 1))) break;
+        if (!ok || !(ok = tc::mbar_wait_warp(work_free + s, ((i >> 1) & 1) ^ 1))) break;
+        w = make_int4(blk.row0, more ? blk.len : 0, blk.at, more ? id % a.Hq : 0);
         if (lane == 0) {
-          work[s] = make_int4(blk.row0, more ? blk.len : 0, blk.at, more ? id % a.Hq : 0);
+          work[s] = w;
           tc::mbar_arrive(work_full + s);
         }
         if (!more) break;
         // no earlier: an item in hand here is one that no idle SM can take
-        if (!(ok = tc::mbar_wait_warp(ask, i & 1))) break;
-        take();
-      }
-    } else {
-      // ragged items: nothing behind the sequence in the last V tile
-      int ring = 0;
-      unsigned tails = 0;
-      for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
+        if (!(ok = tc::mbar_wait_warp(issued, i & 1))) break;
+        ask_cta(work + 2, taken);
         const Item t(w);
         if (t.tail < 128) {
           const int x = ring + 2 * t.n - 1, slot = x % SLOTS;
-          // the slot's barrier is in this load's phase only once it has been issued
-          ok = tc::mbar_wait_ns(tail_go + slot, (tails >> slot) & 1) && tc::mbar_wait_ns(full + slot, (x / SLOTS) & 1);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tails ^= 1u << slot;
+          if (!(ok = tc::mbar_wait_warp(full + slot, (x / SLOTS) & 1))) break;
           zero_rows<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, t.tail);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(v_tail + slot);
         }
         ring += 2 * t.n;
+        id = taken_cta(work + 2, taken, takes++, ok);
       }
     }
   } else {
