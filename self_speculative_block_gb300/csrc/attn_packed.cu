@@ -3,22 +3,27 @@
 //   S_ij = c q_i . k_j (j <= i),  lse_i = log sum_j exp S_ij,  o_i = sum_j exp(S_ij - lse_i) v_j
 //
 // A work item is 256 query rows of a sequence and a q head: two tiles of 128
-// rows share the K/V ring that a TMA warp fills.  Both products run on tcgen05:
-// S = Q K^T (128 x 128 x D) into tensor memory, P (bf16) back into tensor memory
-// over S, O += P V with P read from there and V N-major as it lies.  Two
-// softmax threads own a row, 64 scores each from their tensor memory lane, and
-// exchange its maximum through shared memory: with one thread a row the chain
-// from a tile's scores to its P, not the tensor cores, set the pace (tensor
-// pipe 51% busy, issue slots 29%).  While one tile's softmax runs, the tensor
-// cores work for the other.  O stays in tensor memory and is rescaled only when
-// a row's maximum grows by more than 2^8 over the one its exponentials refer to
-// (the sum and O use the same reference, so nothing is lost; P is at most 2^8).
-// Each tile has an MMA warp of its own: an MMA of 128 x 128 x 16 lasts 64
-// cycles and few fit the queue, so a single warp's waits between its batches
-// left the tensor cores idle a third of the time.
-// P is rounded to bf16 (relative 2^-8) since the tensor cores take it so;
-// scores, maxima, sums and O are fp32.  No partial results leave the CTA: a
-// row's bits depend on its own sequence only.
+// rows share the K/V ring that a TMA warp fills.  Keys go by in blocks of 64.
+// Both products run on tcgen05: S = Q K^T (128 x 64 x D) into one of two
+// buffers a tile in tensor memory, P (bf16) back into tensor memory over S, O
+// += P V with P read from there and V N-major as it lies.  A softmax thread owns
+// a row: its 64 scores come from its own tensor memory lane, so the running
+// maximum and sum need no exchange.
+//
+// What bounds it: a 128 x 128 block takes 1,024 cycles of exponentials on the
+// special-function unit (16 a cycle and SM) and 1,024 of products, and the chain
+// S, softmax, P, O of a block is as long as both.  Two tiles alone left a third
+// of the cycles idle (3,250 for two blocks of 128 keys); with two S buffers a
+// tile, a tile's next scores are ready when its softmax is, at the price of
+// 64-column score products (49 instead of 32 cycles each: A is read again for
+// half the columns).
+//
+// O stays in tensor memory and is rescaled only when a row's maximum grows by
+// more than 2^8 over the one its exponentials refer to (the sum and O use the
+// same reference, so nothing is lost; P is at most 2^8).  P is rounded to bf16
+// (relative 2^-8) since the tensor cores take it so; scores, maxima, sums and O
+// are fp32.  No partial results leave the CTA: a row's bits depend on its own
+// sequence only.
 //
 // The grid has a CTA per work item, but a running CTA takes over the items of
 // those that have not started (cluster launch control), so barriers and tensor
@@ -34,13 +39,9 @@ using namespace gocr::packed;
 namespace {
 
 constexpr int QT = 256;        // query rows of a work item
-// Sixteen softmax warps (two tiles x two column halves x four lane quarters),
-// then the TMA warp, an MMA warp a tile and the work warp.  The softmax groups take 104
-// registers a thread of the 96 x 640 that the block is launched with, the last
-// group 64.
-constexpr int SW = 16, THREADS = (SW + 4) * 32;
-constexpr int SOFTMAX_REGS = 104, OTHER_REGS = 64;
-static_assert(4 * SOFTMAX_REGS + OTHER_REGS <= 5 * 96, "registers of the block at launch");
+// Eight softmax warps (two tiles x four lane quarters), then the TMA warp, an
+// MMA warp a tile and the work warp.
+constexpr int SW = 8, THREADS = (SW + 4) * 32;
 constexpr float GROW = 8.f;    // log2 of the growth of a row's maximum that rescales O
 
 static __device__ int g_error;  // DevErr of a wait that gave up
@@ -57,25 +58,28 @@ template <int D> struct Fwd {
   static constexpr int SLOTS = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TILE_BYTES<D>;
-  static constexpr int OFF_MAX = OFF_KV + SLOTS * TILE_BYTES<D>;  // float [2 turns][2 tiles][2 halves][128]
-  static constexpr int OFF_SUM = OFF_MAX + 2 * 2 * 2 * 128 * 4;   // float [2 tiles][2 halves][128]
-  static constexpr int OFF_WORK = OFF_SUM + 2 * 2 * 128 * 4;      // int4 [2], and the launch control's answer
+  static constexpr int OFF_WORK = OFF_KV + SLOTS * TILE_BYTES<D>;  // int4 [2], and the launch control's answer
   static constexpr int OFF_BAR = OFF_WORK + 64;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
-  static constexpr uint32_t O_COL = 256;  // S0, S1 at 0, 128; O0, O1 behind them
+  static constexpr uint32_t O_COL = 256;  // S [2 tiles][2 buffers] of 64 columns; O [2 tiles] of D behind them
 };
 
 // One work item, as every warp sees it.
 struct Item {
   Block blk;
   int head;
-  int n0, n1, n;  // key blocks of the two tiles: up to the diagonal, and within the sequence
-  int tail;       // rows of the last key block within the sequence, if < 128
+  int n0, n1, n;  // K/V tiles of the two query tiles: up to the diagonal, and within the sequence
+  int tail;       // rows of the last K/V tile within the sequence, if < 128
   __device__ explicit Item(int4 w) : blk{w.x, w.y, w.z}, head(w.w) {
     n0 = blk.at / 128 + 1;
     n1 = blk.len - blk.at > 128 ? n0 + 1 : 0;
     n = n1 ? n1 : n0;
     tail = blk.len - (n - 1) * 128;
+  }
+  // blocks of 64 keys of query tile j; the last K/V tile's second may lie behind the sequence
+  __device__ int blocks(int j) const {
+    const int nj = j ? n1 : n0;
+    return 2 * nj - (nj == n && tail <= 64);
   }
 };
 
@@ -85,7 +89,11 @@ __device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full,
   const int s = i & 1;
   if (!(ok = tc::mbar_wait_warp(work_full + s, (i >> 1) & 1))) return false;
   w = work[s];
-  __syncwarp();
+  // as uniform values, for the loops and operands that follow from them
+  w.x = __shfl_sync(0xffffffffu, w.x, 0);
+  w.y = __shfl_sync(0xffffffffu, w.y, 0);
+  w.z = __shfl_sync(0xffffffffu, w.z, 0);
+  w.w = __shfl_sync(0xffffffffu, w.w, 0);
   if ((threadIdx.x & 31) == 0) tc::mbar_arrive(work_free + s);
   return w.y > 0;
 }
@@ -103,7 +111,7 @@ __device__ __forceinline__ void ask_cta(void* answer, uint64_t* bar) {
 }
 __device__ __forceinline__ int taken_cta(const void* answer, uint64_t* bar, int turn, bool& ok) {
   if (!(ok = tc::mbar_wait_warp(bar, turn & 1))) return -1;
-  uint32_t yes, x;
+  uint32_t yes, x;  // every lane reads the answer; lane 0's counts
   asm volatile(
       "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
       "ld.shared.b128 h, [%2];\n\t"
@@ -112,8 +120,7 @@ __device__ __forceinline__ int taken_cta(const void* answer, uint64_t* bar, int 
       "mov.u32 %1, 0;\n\t"
       "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
       : "=r"(yes), "=r"(x) : "r"(tc::smem_u32(answer)) : "memory");
-  __syncwarp();
-  return yes ? (int)x : -1;
+  return __shfl_sync(0xffffffffu, yes ? (int)x : -1, 0);
 }
 
 template <int D>
@@ -128,9 +135,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* full = q_empty + 1;
   uint64_t* empty = full + SLOTS;
-  uint64_t* s_full = empty + SLOTS;  // [2]
-  uint64_t* p_full = s_full + 2;     // [2]
-  uint64_t* o_full = p_full + 2;     // [2]
+  uint64_t* s_full = empty + SLOTS;  // [2 tiles][2 buffers]
+  uint64_t* p_full = s_full + 4;     // [2 tiles][2 buffers]
+  uint64_t* o_full = p_full + 4;     // [2] a block's P V is complete
   // ragged V tiles, one barrier a slot: a slot's next load waits for this one's
   // use, so no barrier is ever two phases ahead of the warp that waits on it
   uint64_t* v_tail = o_full + 2;         // [SLOTS] the rows behind the sequence are zero
@@ -150,9 +157,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::mbar_init(empty + s, 2);
       tc::mbar_init(v_tail + s, 1);
     }
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
       tc::mbar_init(s_full + j, 1);
       tc::mbar_init(p_full + j, SW / 2);
+    }
+    for (int j = 0; j < 2; ++j) {
       tc::mbar_init(o_full + j, 1);
       tc::mbar_init(work_full + j, 1);
       tc::mbar_init(work_free + j, SW + 3);
@@ -166,12 +175,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *holder;
+  // all 512 columns, which start at 0: a constant keeps the MMAs' operands in uniform registers
+  constexpr uint32_t tmem = 0;
   bool ok = true;
   int4 w;
 
   if (warp >= SW) {
-    fewer_registers<OTHER_REGS>();
     if (warp == SW) {
       // K(0), V(0), K(1), V(1), ... through the ring, Q behind the item's K(0)
       int slot = 0, ph = 0;
@@ -202,9 +211,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp < SW + 3) {
       const int j = warp - (SW + 1);  // the tile
       const uint32_t q = tc::smem_u32(sm + F::OFF_Q + j * TILE_BYTES<D>), kv = tc::smem_u32(sm + F::OFF_KV);
-      int ring = 0;        // ring position of the item's K(0)
-      unsigned tails = 0;  // parity of each slot's ragged tiles so far
-      int turn = 0;        // blocks of the tile so far
+      const uint32_t s_col = tmem + j * 128, o_col = tmem + F::O_COL + j * D;
+      int ring = 0;           // ring position of the item's K(0)
+      unsigned tails = 0;     // parity of each slot's ragged tiles so far
+      int turn[2] = {0, 0};   // blocks of each buffer so far
       auto wait = [&](uint64_t* bar, int ph) {
         const bool r = tc::mbar_wait_warp(bar, ph & 1);
         tc::fence_after_sync();
@@ -212,50 +222,55 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
-        const int nj = j ? t.n1 : t.n0;
+        const int nb = t.blocks(j), most = max(t.blocks(0), t.blocks(1));
         auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
         auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
         // both MMA warps give a K/V tile back, whether they used it or not
-        // (but not before it is there: the barrier is in an older phase)
+        // (but not before it is there: its barrier is in an older phase)
         auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
+        auto scores = [&](int b) {
+          mma_rows<D>(s_col + (b & 1) * 64, q, tile_of(2 * (b >> 1)), b & 1);
+          tc::mma_commit(s_full + j * 2 + (b & 1));
+        };
+        // after the scores of block b: the K tile, and at last Q
+        auto release_k = [&](int b) {
+          if ((b & 1) || b + 1 == most) release(2 * (b >> 1));
+          if (b + 1 == most) tc::mma_commit(q_empty);
+        };
         if (!(ok = wait(q_full, i) && wait_full(0))) break;
         if (tc::elect_one()) {
-          if (nj) {
-            // over P of the last item, whose product was issued before
-            mma_rows<D>(tmem + j * 128, q, tile_of(0));
-            tc::mma_commit(s_full + j);
+          // over P of the last item, whose products were issued before
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (b < nb) scores(b);
+            if (b < most) release_k(b);
           }
-          release(0);
-          if (nj < 2) tc::mma_commit(q_empty);
         }
         __syncwarp();
-        for (int it = 0; it < t.n; ++it) {
-          const bool more = it + 1 < t.n;
-          if (!(ok = wait_full(2 * it + 1))) break;
-          if (more && !(ok = wait_full(2 * it + 2))) break;
-          if (!more && t.tail < 128) {
-            const int slot = (ring + 2 * it + 1) % SLOTS;
-            if (!(ok = wait(v_tail + slot, tails >> slot))) break;
-            tails ^= 1u << slot;
+        for (int b = 0; b < most; ++b) {
+          if (!(b & 1)) {
+            if (!(ok = wait_full(b + 1))) break;                  // V tile b / 2
+            if (b + 2 < most && !(ok = wait_full(b + 2))) break;  // K tile b / 2 + 1
+            if (b + 2 >= most && t.tail < 128) {
+              const int slot = (ring + b + 1) % SLOTS;
+              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+              tails ^= 1u << slot;
+            }
           }
-          if (it < nj && !(ok = wait(p_full + j, turn + it))) break;
+          if (b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
           if (tc::elect_one()) {
-            if (it < nj) mma_add<D, 64>(tmem + F::O_COL + j * D, tmem + j * 128, tile_of(2 * it + 1), it == 0);
-            release(2 * it + 1);
-            if (it + 1 < nj) {
-              mma_rows<D>(tmem + j * 128, q, tile_of(2 * it + 2));
-              tc::mma_commit(s_full + j);
-            } else if (it + 1 == nj) {
+            if (b < nb) {
+              mma_add<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * (b >> 1) + 1), b & 1, b == 0);
               tc::mma_commit(o_full + j);
             }
-            if (more) release(2 * it + 2);
-            if (it + 2 == nj) tc::mma_commit(q_empty);  // after the item's last scores
+            if (b + 2 < nb) scores(b + 2);
+            if ((b & 1) || b + 1 == most) release(2 * (b >> 1) + 1);
+            if (b + 2 < most) release_k(b + 2);
           }
           __syncwarp();
         }
         if (!ok) break;
         ring += 2 * t.n;
-        turn += nj;
       }
     } else {
       // the items: this CTA's own, then those of CTAs that have not started;
@@ -295,34 +310,31 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else {
-    more_registers<SOFTMAX_REGS>();
-    const int j = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;  // tile, column half, row of the tile
+    const int j = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + j * 128 + half * 64 + lanes, to = tmem + F::O_COL + j * D + half * (D / 2) + lanes;
-    float* maxima = reinterpret_cast<float*>(sm + F::OFF_MAX) + j * 256 + r;  // [turn parity * 512 + half * 128]
-    float* sums = reinterpret_cast<float*>(sm + F::OFF_SUM) + j * 256 + r;
+    const uint32_t to = tmem + F::O_COL + j * D + lanes;
     const float sl2 = a.scale * LOG2E;
-    int turn = 0, outs = 0;
-    // the row's other thread is in the same place of the warp of the other half
-    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + j * 4 + (warp & 3)) : "memory"); };
+    int turn[2] = {0, 0}, outs = 0;  // blocks of each buffer, of the tile so far
     for (int i = 0; ok && next_item(work, work_full, work_free, i, w, ok); ++i) {
       const Item t(w);
-      const int nj = j ? t.n1 : t.n0;
+      const int nj = j ? t.n1 : t.n0, nb = t.blocks(j);
       if (!nj) continue;
       const int row = t.blk.at + j * 128 + r;  // within the sequence
+      const int see = min(row, t.blk.len - 1); // the last key that the row sees
       float ref = 0.f, ref2 = 0.f, l = 0.f;    // the exponentials' reference, also times sl2; their sum
-      for (int it = 0; it < nj; ++it, ++turn) {
-        if (!(ok = tc::mbar_wait_warp(s_full + j, turn & 1))) break;
+      for (int b = 0; b < nb; ++b, ++outs) {
+        const uint32_t ts = tmem + j * 128 + (b & 1) * 64 + lanes;
+        if (!(ok = tc::mbar_wait_warp(s_full + j * 2 + (b & 1), (b & 1 ? turn[1]++ : turn[0]++) & 1))) break;
         tc::fence_after_sync();
         uint32_t u[64];
         tc::tmem_ld32_nowait(ts, u);
         tc::tmem_ld32_nowait(ts + 32, u + 32);
         tc::tmem_wait_ld();
-        if (it + 1 == nj) {  // the diagonal block; it holds the end of the sequence, too
-          const int see = min(row, t.blk.len - 1) - it * 128 - half * 64;
+        if (b >= 2 * nj - 2) {  // the diagonal's K/V tile; it holds the end of the sequence, too
+          const int last = see - b * 64;
 #pragma unroll
           for (int x = 0; x < 64; ++x)
-            if (x > see) u[x] = 0xff800000u;  // -infinity
+            if (x > last) u[x] = 0xff800000u;  // -infinity
         }
         float m4[4];
 #pragma unroll
@@ -331,68 +343,61 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int x = 8; x < 64; x += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(u[x + e])), __uint_as_float(u[x + e + 4]));
-        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        float* at = maxima + (turn & 1) * 512;
-        at[half * 128] = mx;
-        meet();
-        mx = fmaxf(mx, at[(half ^ 1) * 128]);
-        if (it == 0) {
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        if (b == 0) {
           ref = mx == -INFINITY ? 0.f : mx;
           ref2 = ref * sl2;
         } else {
           const bool grow = (mx - ref) * sl2 > GROW;
           if (__any_sync(0xffffffffu, grow)) {
-            // S(it) was issued after P V(it - 1): O is complete
+            if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;  // the last block's P V
+            tc::fence_after_sync();
             const float to_new = grow ? mx : ref;
             const float f = ex2(ref2 - to_new * sl2);
             ref = to_new;
             ref2 = ref * sl2;
             l *= f;
 #pragma unroll
-            for (int c = 0; c < D / 2; c += 16) {
-              float v[16];
-              tc::tmem_ld16(to + c, v);
-              uint32_t x[16];
+            for (int c = 0; c < D; c += 32) {
+              uint32_t x[32];
+              tc::tmem_ld32_nowait(to + c, x);
+              tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(v[e] * f);
-              tc::tmem_st16(to + c, x);
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+              tc::tmem_st32(to + c, x);
             }
           }
         }
         const F2 scale2 = f2(sl2, sl2), ref22 = f2(-ref2, -ref2);
-        F2 s2[2] = {f2(l, 0.f), f2(0.f, 0.f)};
+        F2 s4[4] = {f2(l, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-        for (int x = 0; x < 64; x += 2) {
+        for (int x = 0; x < 32; ++x) {
           float p, q;
-          split(fma2(f2(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), scale2, ref22), p, q);
+          split(fma2(f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), scale2, ref22), p, q);
           p = ex2(p);
           q = ex2(q);
-          s2[(x >> 1) & 1] = add2(s2[(x >> 1) & 1], f2(p, q));
-          u[x / 2] = pack2(p, q);
+          s4[x & 3] = add2(s4[x & 3], f2(p, q));
+          u[x] = pack2(p, q);
         }
         tc::tmem_st32(ts, u);
-        {
-          float p, q;
-          split(add2(s2[0], s2[1]), p, q);
-          l = p + q;
-        }
+        float p, q;
+        split(add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])), p, q);
+        l = p + q;
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + j);
+        if (lane == 0) tc::mbar_arrive(p_full + j * 2 + (b & 1));
       }
-      if (!ok) break;
-      sums[half * 128] = l;
-      meet();
-      l = sums[0] + sums[128];
-      if (!(ok = tc::mbar_wait_warp(o_full + j, outs & 1))) break;
-      ++outs;
+      // the last block's P V, after the one before it: the scores of a block vouch
+      // for the P V two blocks back, and a barrier tells only neighbouring phases apart
+      if (ok && nb > 1) ok = tc::mbar_wait_warp(o_full + j, (outs - 2) & 1);
+      if (!ok || !(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
       tc::fence_after_sync();
       const float inv = 1.f / l;
       const size_t tok = (size_t)t.blk.row0 + row;
-      bf16* dst = a.o + (tok * a.Hq + t.head) * D + half * (D / 2);
+      bf16* dst = a.o + (tok * a.Hq + t.head) * D;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
+      for (int c = 0; c < D; c += 32) {
         uint32_t x[32];
         tc::tmem_ld32_nowait(to + c, x);
         tc::tmem_wait_ld();
@@ -406,11 +411,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             *reinterpret_cast<uint4*>(dst + c + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
           }
       }
-      if (row < t.blk.len && half == 0) a.lse[(size_t)t.head * a.T + tok] = (ref2 + log2f(l)) * LN2;
+      if (row < t.blk.len) a.lse[(size_t)t.head * a.T + tok] = (ref2 + log2f(l)) * LN2;
       tc::fence_before_sync();  // O has been read before the next item's P V, which waits for its P
     }
-    // a warp that gave up does not keep its partner in meet()
-    if (!ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + j * 4 + (warp & 3)) : "memory");
   }
   if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
   tc::fence_before_sync();

@@ -48,10 +48,6 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   return r;
 }
 
-// Registers of a warpgroup's threads, out of those the block was launched with.
-template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -125,31 +121,27 @@ template <int D> __device__ __forceinline__ void zero_rows(uint8_t* tile, int n)
     for (int c = 0; c < D / 64; ++c) *reinterpret_cast<uint4*>(tile + c * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// Products of 128 x 128 tiles, issued by one elected lane.
-//   mma_rows   dst[128, 128] = X Y^T over D: both tiles K-major
-//   mma_add    dst[128, D] (+)= P Y over Y's 128 rows: P (bf16) from tensor
-//              memory, W columns of scores to a thread (packed_col); Y N-major
+// Products over tiles of 128 rows, issued by one elected lane.
+//   mma_rows   dst[128, N] = X Y^T over D: both tiles K-major; N = 64: rows 64
+//              half .. of Y's, N = 128: all of them
+//   mma_add    dst[128, D] (+)= P Y over rows 64 half .. of Y's, N-major: P
+//              (bf16, two a column) from tensor memory
 // first: dst is overwritten.
-template <int D> __device__ __forceinline__ void mma_rows(uint32_t dst, uint32_t x, uint32_t y) {
-  constexpr uint32_t idesc = tc::idesc_bf16(128, 128);
-  const uint64_t xd = tc::sdesc_sw128(x), yd = tc::sdesc_sw128(y);
+constexpr int HALF_ROWS = 64 * 128;  // bytes of 64 rows in a box
+template <int D, int N = 64> __device__ __forceinline__ void mma_rows(uint32_t dst, uint32_t x, uint32_t y, int half) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, N);
+  const uint64_t xd = tc::sdesc_sw128(x), yd = tc::sdesc_sw128(y + half * HALF_ROWS);
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
     const uint32_t step = ((ks >> 2) * BOX_BYTES + (ks & 3) * 32) >> 4;
     tc::mma_bf16(dst, xd + step, yd + step, idesc, ks > 0 ? 1u : 0u);
   }
 }
-// A block's 128 scores of a row are shared by 128 / W threads of W columns
-// each.  A thread writes its W values in bf16 over the first half of its own
-// columns, so nobody overwrites scores that another has yet to read; step ks
-// of the product over them (16 values, 8 packed columns) then starts here:
-template <int W> __host__ __device__ constexpr uint32_t packed_col(int ks) { return (ks * 16 / W) * W + (ks * 16 % W) / 2; }
-template <int D, int W> __device__ __forceinline__ void mma_add(uint32_t dst, uint32_t p, uint32_t y, bool first) {
+template <int D> __device__ __forceinline__ void mma_add(uint32_t dst, uint32_t p, uint32_t y, int half, bool first) {
   constexpr uint32_t idesc = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
-  const uint64_t yd = tc::sdesc_sw128_mn(y, BOX_BYTES);
+  const uint64_t yd = tc::sdesc_sw128_mn(y + half * HALF_ROWS, BOX_BYTES);
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
-    tc::mma_bf16_ta(dst, p + packed_col<W>(ks), yd + (ks * 2048 >> 4), idesc, !first || ks > 0 ? 1u : 0u);
+  for (int ks = 0; ks < 4; ++ks) tc::mma_bf16_ta(dst, p + ks * 8, yd + (ks * 2048 >> 4), idesc, !first || ks > 0 ? 1u : 0u);
 }
 
 // 3-D TMA map over [T, heads, D] bf16 rows `ld` elements apart: boxes of 64

@@ -17,9 +17,13 @@
 // relative 2^-8, as the tensor cores take them) go back to tensor memory over
 // the scores they came from and are the A operands of dV += P^T dO and dK +=
 // dS^T Q; dO and Q serve as they lie, K-major for S^T and dP^T and N-major
-// here.  A dq CTA has lanes of query rows and dQ += dS K.  Eight warps do the
-// elementwise work, two to a lane quarter with 64 columns each; it overlaps the
-// products: P^T with dK and dP^T, dS^T with dV and the next S^T.
+// here.  A dq CTA has lanes of query rows and dQ += dS K.  The elementwise work
+// of a block is two groups of four warps, 64 columns to a thread, each with
+// barriers of its own: the groups fall out of step, and one's exponentials and
+// stores run while the tensor cores work for the other (in step, as one group
+// of eight warps, a dk/dv block took 3,600 cycles, of which 2,048 were
+// products).  In return S^T and dP^T of a dk/dv CTA, and dP of a dq CTA, are
+// products of 64 columns, which take 49 cycles instead of 32.
 //
 // delta from o takes o's rounding to bf16 into every dS of the row.  That
 // matters where a row sees few keys (o is then large), so for the first 128
@@ -34,14 +38,16 @@ using namespace gocr::packed;
 namespace {
 
 constexpr int THREADS = 320;  // eight elementwise warps, a TMA and an MMA warp
-constexpr int EW = 8;         // elementwise warps
+constexpr int EW = 4;         // warps of an elementwise group
 constexpr int BAR_OFF = 7 * 128 * 128 * 2;  // behind seven tiles of D = 128
 constexpr int SMEM = BAR_OFF + 256 + 1024;
 
-// Barrier of the elementwise warps.
-__device__ __forceinline__ void elementwise_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// A warp that gave up does not keep the others in it.
-__device__ __forceinline__ void elementwise_leave() { asm volatile("bar.arrive 1, 256;" ::: "memory"); }
+// Barrier of the threads of an elementwise group, or of both.  A warp
+// that gives up leaves them, so that it keeps nobody.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory"); }
+__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void group_leave(int group) { asm volatile("bar.arrive %0, 128;" ::"r"(2 + group) : "memory"); }
+__device__ __forceinline__ void both_leave() { asm volatile("bar.arrive 1, 256;" ::: "memory"); }
 
 static __device__ int g_error;  // DevErr of a wait that gave up
 
@@ -99,7 +105,7 @@ template <int D> struct DkvGeo {
   static constexpr int OFF_K = 0, OFF_V = TILE;
   static constexpr int OFF_Q = 2 * TILE;    // [2]
   static constexpr int OFF_DO = 4 * TILE;   // [2]
-  static constexpr int OFF_ROW = 6 * TILE;  // float [2 stages][lse, delta][128]
+  static constexpr int OFF_ROW = 6 * TILE;  // float [2 stages][-lse log2 e, -delta][128]
   static constexpr int OFF_RED = OFF_ROW + 2 * 2 * 128 * 4;  // float [2 halves][4 warps][64]
   static_assert(OFF_RED + 2 * 4 * 64 * 4 <= BAR_OFF, "shared memory");
 };
@@ -132,11 +138,11 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
   uint64_t* do_full = q_empty + 2;   // [2]
   uint64_t* do_empty = do_full + 2;  // [2]
   uint64_t* row_full = do_empty + 2; // [2] lse and delta of the stage; ragged tiles zeroed
-  uint64_t* s_full = row_full + 2;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* dp_full = p_full + 1;
-  uint64_t* ds_full = dp_full + 1;
-  uint64_t* done = ds_full + 1;
+  uint64_t* s_full = row_full + 2;   // [2 groups]
+  uint64_t* p_full = s_full + 2;     // [2]
+  uint64_t* dp_full = p_full + 2;    // [2]
+  uint64_t* ds_full = dp_full + 2;   // [2]
+  uint64_t* done = ds_full + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -145,6 +151,8 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
   const int per = nqb - kb;         // query blocks of a head that see these keys
   const int n = group * per;
   const int tail = blk.len - (nqb - 1) * 128;  // rows of the last query block within the sequence
+  // group 1 has the second 64 rows of a query block, if the sequence has them
+  auto both = [&](int it) { return it % per + 1 < per || tail > 64; };
 
   if (tid == 0) {
     tc::mbar_init(kv_full, 1);
@@ -155,10 +163,12 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::mbar_init(do_empty + s, 1);
       tc::mbar_init(row_full + s, 1);
     }
-    tc::mbar_init(s_full, 1);
-    tc::mbar_init(p_full, EW);
-    tc::mbar_init(dp_full, 1);
-    tc::mbar_init(ds_full, EW);
+    for (int g = 0; g < 2; ++g) {
+      tc::mbar_init(s_full + g, 1);
+      tc::mbar_init(p_full + g, EW);
+      tc::mbar_init(dp_full + g, 1);
+      tc::mbar_init(ds_full + g, EW);
+    }
     tc::mbar_init(done, 1);
     tc::fence_mbar_init();
   }
@@ -167,7 +177,8 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *holder;
+  // all 512 columns, which start at 0: a constant keeps the MMAs' operands in uniform registers
+  constexpr uint32_t tmem = 0;
   tc::grid_dep_wait();  // delta
   constexpr uint32_t DP = 128, DV = 256, DK = 256 + D;  // S^T at 0
   bool ok = true;
@@ -198,8 +209,8 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       for (int i = lane; i < 128; i += 32) {
         const bool in = at + i < blk.len;
         const size_t src = (size_t)head * a.T + blk.row0 + at + i;
-        lse[i] = in ? a.lse[src] * LOG2E : 0.f;
-        lse[128 + i] = in ? a.delta[src] : 0.f;
+        lse[i] = in ? a.lse[src] * -LOG2E : 0.f;
+        lse[128 + i] = in ? -a.delta[src] : 0.f;
       }
       if (ragged) {
         ok = tc::mbar_wait_warp(q_full + st, ph) && tc::mbar_wait_warp(do_full + st, ph);
@@ -219,47 +230,53 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::fence_after_sync();
       return w;
     };
-    ok = wait(kv_full, 0) && wait(q_full, 0);
+    auto scores = [&](int g, int st) {
+      mma_rows<D>(tmem + g * 64, k, q + st * G::TILE, g);
+      tc::mma_commit(s_full + g);
+    };
+    auto products = [&](int g, int st) {
+      mma_rows<D>(tmem + DP + g * 64, v, d_o + st * G::TILE, g);
+      tc::mma_commit(dp_full + g);
+    };
+    ok = wait(kv_full, 0) && wait(q_full, 0) && wait(do_full, 0);
     if (ok && tc::elect_one()) {
-      mma_rows<D>(tmem, k, q);
-      tc::mma_commit(s_full);
+      scores(0, 0);
+      if (both(0)) scores(1, 0);
+      products(0, 0);
+      if (both(0)) products(1, 0);
     }
     __syncwarp();
-    ok = ok && wait(do_full, 0);
-    if (ok && tc::elect_one()) {
-      mma_rows<D>(tmem + DP, v, d_o);
-      tc::mma_commit(dp_full);
-    }
-    __syncwarp();
+    int turn[2] = {0, 0};  // blocks of the groups so far
     for (int it = 0; it < n && ok; ++it) {
       const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
-      const bool more = it + 1 < n;
-      if (!(ok = wait(p_full, it & 1))) break;
-      if (tc::elect_one()) {
-        mma_add<D, 64>(tmem + DV, tmem, d_o + st * G::TILE, it == 0);
-        tc::mma_commit(do_empty + st);
-      }
-      __syncwarp();
-      if (more) {
-        if (!(ok = wait(q_full + nx, nph))) break;
+      const bool more = it + 1 < n, two = both(it), next_two = more && both(it + 1);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g == 0 || two) {
+          if (!(ok = wait(p_full + g, turn[g] & 1))) break;
+          if (tc::elect_one()) mma_add<D>(tmem + DV, tmem + g * 64, d_o + st * G::TILE, g, it == 0 && g == 0);
+          __syncwarp();
+        }
+        if (g == 0 && more && !(ok = wait(q_full + nx, nph))) break;
         if (tc::elect_one()) {
-          mma_rows<D>(tmem, k, q + nx * G::TILE);
-          tc::mma_commit(s_full);
+          if (g == 1) tc::mma_commit(do_empty + st);
+          if (g == 0 ? more : next_two) scores(g, nx);
         }
         __syncwarp();
       }
-      if (!(ok = wait(ds_full, it & 1))) break;
-      if (tc::elect_one()) {
-        mma_add<D, 64>(tmem + DK, tmem + DP, q + st * G::TILE, it == 0);
-        tc::mma_commit(q_empty + st);
-        if (!more) tc::mma_commit(done);
-      }
-      __syncwarp();
-      if (more) {
-        if (!(ok = wait(do_full + nx, nph))) break;
+      if (!ok) break;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g == 0 || two) {
+          if (!(ok = wait(ds_full + g, turn[g]++ & 1))) break;
+          if (tc::elect_one()) mma_add<D>(tmem + DK, tmem + DP + g * 64, q + st * G::TILE, g, it == 0 && g == 0);
+          __syncwarp();
+        }
+        if (g == 0 && more && !(ok = wait(do_full + nx, nph))) break;
         if (tc::elect_one()) {
-          mma_rows<D>(tmem + DP, v, d_o + nx * G::TILE);
-          tc::mma_commit(dp_full);
+          if (g == 1) tc::mma_commit(q_empty + st);
+          if (g == 0 ? more : next_two) products(g, nx);
+          if (g == 1 && !more) tc::mma_commit(done);
         }
         __syncwarp();
       }
@@ -269,13 +286,15 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int key = blk.at + (warp & 3) * 32 + lane;  // within the sequence
     const uint32_t ts = tmem + lanes + half * 64, tp = ts + DP;
-    const float sl2 = a.scale * LOG2E;
+    const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E);
+    int turn = 0;  // blocks of the group so far
     for (int it = 0; it < n; ++it) {
+      if (half && !both(it)) continue;
       const int st = it & 1;
       const int at = (kb + it % per) * 128 + half * 64;  // first query row of this thread's columns
       const float4* lse = reinterpret_cast<const float4*>(rows + st * 256 + half * 64);
       const float4* del = lse + 32;
-      ok = tc::mbar_wait_ns(row_full + st, (it >> 1) & 1) && tc::mbar_wait_ns(s_full, it & 1);
+      ok = tc::mbar_wait_ns(row_full + st, (it >> 1) & 1) && tc::mbar_wait_ns(s_full + half, turn & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::fence_after_sync();
       // query column i is visible from `lo` on (causal) and below `hi` (the end of the sequence)
@@ -289,11 +308,14 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
         tc::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
-          const float4 r = lse[i / 4];
-          p[i] = ex2(fmaf(__uint_as_float(u[i]), sl2, -r.x));
-          p[i + 1] = ex2(fmaf(__uint_as_float(u[i + 1]), sl2, -r.y));
-          p[i + 2] = ex2(fmaf(__uint_as_float(u[i + 2]), sl2, -r.z));
-          p[i + 3] = ex2(fmaf(__uint_as_float(u[i + 3]), sl2, -r.w));
+          const float4 r = lse[i / 4];  // -lse, in units of log2
+          float x, y;
+          split(fma2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), scale2, f2(r.x, r.y)), x, y);
+          p[i] = ex2(x);
+          p[i + 1] = ex2(y);
+          split(fma2(f2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), scale2, f2(r.z, r.w)), x, y);
+          p[i + 2] = ex2(x);
+          p[i + 3] = ex2(y);
         }
         if (cut)
 #pragma unroll
@@ -307,8 +329,8 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full);
-      if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
+      if (lane == 0) tc::mbar_arrive(p_full + half);
+      if (!(ok = tc::mbar_wait_warp(dp_full + half, turn++ & 1))) break;
       tc::fence_after_sync();
       {
         uint32_t u[64];
@@ -323,21 +345,24 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
             for (int i = 0; i < 32; ++i) x[i] = c + i < lo || c + i >= hi ? 0.f : p[c + i] * __uint_as_float(u[c + i]);
             red[(half * 4 + (warp & 3)) * 64 + c + lane] = lane_sums(x);
           }
-          elementwise_sync();
-          if ((warp & 3) < 2) {
-            const int c = (warp & 3) * 32 + lane;
-            const float* r = red + half * 256 + c;
-            rows[st * 256 + 128 + half * 64 + c] = (r[0] + r[64]) + (r[128] + r[192]);
-          }
-          elementwise_sync();
-        }
+          group_sync(half);
+          const float4* r4 = reinterpret_cast<const float4*>(red + half * 256);
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 r = del[i / 4];
-          p[i] *= __uint_as_float(u[i]) - r.x;
-          p[i + 1] *= __uint_as_float(u[i + 1]) - r.y;
-          p[i + 2] *= __uint_as_float(u[i + 2]) - r.z;
-          p[i + 3] *= __uint_as_float(u[i + 3]) - r.w;
+          for (int i = 0; i < 64; i += 4) {
+            const float4 a0 = r4[i / 4], a1 = r4[16 + i / 4], a2 = r4[32 + i / 4], a3 = r4[48 + i / 4];
+            p[i] *= __uint_as_float(u[i]) - ((a0.x + a1.x) + (a2.x + a3.x));
+            p[i + 1] *= __uint_as_float(u[i + 1]) - ((a0.y + a1.y) + (a2.y + a3.y));
+            p[i + 2] *= __uint_as_float(u[i + 2]) - ((a0.z + a1.z) + (a2.z + a3.z));
+            p[i + 3] *= __uint_as_float(u[i + 3]) - ((a0.w + a1.w) + (a2.w + a3.w));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 r = del[i / 4];  // -delta
+            split(mul2(f2(p[i], p[i + 1]), add2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f2(r.x, r.y))), p[i], p[i + 1]);
+            split(mul2(f2(p[i + 2], p[i + 3]), add2(f2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), f2(r.z, r.w))),
+                  p[i + 2], p[i + 3]);
+          }
         }
         if (cut)
 #pragma unroll
@@ -351,10 +376,10 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(ds_full);
+      if (lane == 0) tc::mbar_arrive(ds_full + half);
     }
     if (!ok) {
-      elementwise_leave();
+      group_leave(half);
     } else {
       ok = tc::mbar_wait_warp(done, 0);
       tc::fence_after_sync();
@@ -397,9 +422,9 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   uint64_t* v_empty = v_full + 2;   // [2]
   uint64_t* k_tail = v_empty + 2;
   uint64_t* s_full = k_tail + 1;    // [2]
-  uint64_t* dp_full = s_full + 2;
-  uint64_t* dp_free = dp_full + 1;
-  uint64_t* ds_full = dp_free + 1;  // [2]
+  uint64_t* dp_full = s_full + 2;   // [2 groups]
+  uint64_t* dp_free = dp_full + 2;  // [2]
+  uint64_t* ds_full = dp_free + 2;  // [2]
   uint64_t* done = ds_full + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ float row_sum[2][128];  // the first block's delta, by column half
@@ -408,6 +433,8 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   const int kvh = head / (a.Hq / a.Hkv);
   const int n = blk.at / 128 + 1;
   const int tail = blk.len - blk.at;  // rows of the last key block within the sequence, if < 128
+  // group 1 has the second 64 keys of a block, if the sequence has them
+  auto both = [&](int it) { return it + 1 < n || tail > 64; };
 
   if (tid == 0) {
     tc::mbar_init(q_full, 1);
@@ -419,11 +446,11 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::mbar_init(v_full + s, 1);
       tc::mbar_init(v_empty + s, 1);
       tc::mbar_init(s_full + s, 1);
+      tc::mbar_init(dp_full + s, 1);
+      tc::mbar_init(dp_free + s, EW);
       tc::mbar_init(ds_full + s, EW);
     }
     tc::mbar_init(k_tail, 1);
-    tc::mbar_init(dp_full, 1);
-    tc::mbar_init(dp_free, EW);
     tc::mbar_init(done, 1);
     tc::fence_mbar_init();
   }
@@ -432,7 +459,8 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *holder;
+  // all 512 columns, which start at 0: a constant keeps the MMAs' operands in uniform registers
+  constexpr uint32_t tmem = 0;
   tc::grid_dep_wait();  // delta
   constexpr uint32_t DP = 256, DQ = 384;  // S at 0 and 128
   bool ok = true;
@@ -475,43 +503,55 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::fence_after_sync();
       return w;
     };
+    auto products = [&](int g, int st) {
+      mma_rows<D>(tmem + DP + g * 64, d_o, v + st * G::TILE, g);
+      tc::mma_commit(dp_full + g);
+    };
     ok = wait(q_full, 0) && wait(k_full, 0);
     if (ok && tc::elect_one()) {
-      mma_rows<D>(tmem, q, k);
+      mma_rows<D, 128>(tmem, q, k, 0);
       tc::mma_commit(s_full);
     }
     __syncwarp();
     ok = ok && wait(v_full, 0);
     if (ok && tc::elect_one()) {
-      mma_rows<D>(tmem + DP, d_o, v);
-      tc::mma_commit(dp_full);
+      products(0, 0);
+      if (both(0)) products(1, 0);
       tc::mma_commit(v_empty);
     }
     __syncwarp();
     for (int it = 0; it < n && ok; ++it) {
       const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1, ks0 = it % 3, ks1 = (it + 1) % 3;
-      if (it + 1 < n) {
+      const bool more = it + 1 < n, two = both(it), next_two = more && both(it + 1);
+      if (more) {
         // the other score buffer: its dS was consumed by dQ(it - 1), issued before
         if (!(ok = wait(k_full + ks1, (it + 1) / 3 & 1))) break;
         if (tc::elect_one()) {
-          mma_rows<D>(tmem + nx * 128, q, k + ks1 * G::TILE);
+          mma_rows<D, 128>(tmem + nx * 128, q, k + ks1 * G::TILE, 0);
           tc::mma_commit(s_full + nx);
         }
         __syncwarp();
-        if (!(ok = wait(v_full + nx, nph) && wait(dp_free, it & 1))) break;
-        if (tc::elect_one()) {
-          mma_rows<D>(tmem + DP, d_o, v + nx * G::TILE);
-          tc::mma_commit(dp_full);
-          tc::mma_commit(v_empty + nx);
+        if (!(ok = wait(v_full + nx, nph))) break;
+      } else if (tail < 128 && !(ok = wait(k_tail, 0))) {
+        break;
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g == 1 && !two) continue;  // the last block
+        if (g == 0 ? more : next_two) {
+          if (!(ok = wait(dp_free + g, it & 1))) break;
+          if (tc::elect_one()) products(g, nx);
+          __syncwarp();
         }
+        if (!(ok = wait(ds_full + g, it & 1))) break;
+        if (tc::elect_one()) mma_add<D>(tmem + DQ, tmem + st * 128 + g * 64, k + ks0 * G::TILE, g, it == 0 && g == 0);
         __syncwarp();
       }
-      if (!(ok = wait(ds_full + st, (it >> 1) & 1))) break;
-      if (it + 1 == n && tail < 128 && !(ok = wait(k_tail, 0))) break;
+      if (!ok) break;
       if (tc::elect_one()) {
-        mma_add<D, 64>(tmem + DQ, tmem + st * 128, k + ks0 * G::TILE, it == 0);
+        if (more) tc::mma_commit(v_empty + nx);
         tc::mma_commit(k_empty + ks0);
-        if (it + 1 == n) tc::mma_commit(done);
+        if (!more) tc::mma_commit(done);
       }
       __syncwarp();
     }
@@ -521,11 +561,12 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     const int row = blk.at + (warp & 3) * 32 + lane;  // within the sequence
     const bool in = row < blk.len;
     const size_t t = (size_t)blk.row0 + row;
-    const float lse = in ? a.lse[(size_t)head * a.T + t] * LOG2E : 0.f;
-    float del = in ? a.delta[(size_t)head * a.T + t] : 0.f;
-    const float sl2 = a.scale * LOG2E;
+    const float lse = in ? a.lse[(size_t)head * a.T + t] * -LOG2E : 0.f;
+    float del = in ? -a.delta[(size_t)head * a.T + t] : 0.f;
+    const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), lse2 = f2(lse, lse);
     const uint32_t tp = tmem + lanes + DP + half * 64;
     for (int it = 0; it < n; ++it) {
+      if (half && !both(it)) break;  // the last block
       const int st = it & 1;
       const uint32_t ts = tmem + lanes + st * 128 + half * 64;
       if (!(ok = tc::mbar_wait_warp(s_full + st, (it >> 1) & 1))) break;
@@ -537,9 +578,14 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
         tc::tmem_ld32_nowait(ts + 32, u + 32);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) p[i] = ex2(fmaf(__uint_as_float(u[i]), sl2, -lse));
+        for (int i = 0; i < 64; i += 2) {
+          float x, y;
+          split(fma2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), scale2, lse2), x, y);
+          p[i] = ex2(x);
+          p[i + 1] = ex2(y);
+        }
       }
-      if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
+      if (!(ok = tc::mbar_wait_warp(dp_full + half, it & 1))) break;
       tc::fence_after_sync();
       {
         uint32_t u[64];
@@ -548,7 +594,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(dp_free);
+        if (lane == 0) tc::mbar_arrive(dp_free + half);
         // the diagonal block holds the end of the sequence, too: it lies past every row
         const int see = it + 1 == n ? min(row, blk.len - 1) - it * 128 - half * 64 : 64;
         if (n == 1) {  // all the keys that the row sees
@@ -556,12 +602,16 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (i <= see) x = fmaf(p[i], __uint_as_float(u[i]), x);
-          row_sum[half][(warp & 3) * 32 + lane] = x;
-          elementwise_sync();
-          del = row_sum[0][(warp & 3) * 32 + lane] + row_sum[1][(warp & 3) * 32 + lane];
+          if (both(0)) {
+            row_sum[half][(warp & 3) * 32 + lane] = x;
+            both_sync();
+            x = row_sum[0][(warp & 3) * 32 + lane] + row_sum[1][(warp & 3) * 32 + lane];
+          }
+          del = -x;
         }
 #pragma unroll
-        for (int i = 0; i < 64; ++i) p[i] *= __uint_as_float(u[i]) - del;
+        for (int i = 0; i < 64; i += 2)
+          split(mul2(f2(p[i], p[i + 1]), add2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f2(del, del))), p[i], p[i + 1]);
         if (it + 1 == n)
 #pragma unroll
           for (int i = 0; i < 64; ++i)
@@ -574,10 +624,10 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(ds_full + st);
+      if (lane == 0) tc::mbar_arrive(ds_full + half);
     }
     if (!ok) {
-      elementwise_leave();
+      both_leave();
     } else {
       ok = tc::mbar_wait_warp(done, 0);
       tc::fence_after_sync();
