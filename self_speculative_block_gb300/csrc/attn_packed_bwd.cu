@@ -37,7 +37,10 @@ using namespace gocr::packed;
 
 namespace {
 
-constexpr int THREADS = 320;  // eight elementwise warps, a TMA and an MMA warp
+// Eight elementwise warps, a TMA warp, and two MMA warps: a warp's waits cost
+// 100 cycles and more behind its own queue of MMAs, which then run dry unless
+// the other warp has some.
+constexpr int THREADS = 352;
 constexpr int EW = 4;         // warps of an elementwise group
 constexpr int BAR_OFF = 7 * 128 * 128 * 2;  // behind seven tiles of D = 128
 constexpr int SMEM = BAR_OFF + 256 + 1024;
@@ -158,9 +161,9 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
     tc::mbar_init(kv_full, 1);
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(q_full + s, 1);
-      tc::mbar_init(q_empty + s, 1);
+      tc::mbar_init(q_empty + s, 2);   // both MMA warps read Q and dO
       tc::mbar_init(do_full + s, 1);
-      tc::mbar_init(do_empty + s, 1);
+      tc::mbar_init(do_empty + s, 2);
       tc::mbar_init(row_full + s, 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -169,7 +172,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::mbar_init(dp_full + g, 1);
       tc::mbar_init(ds_full + g, EW);
     }
-    tc::mbar_init(done, 1);
+    tc::mbar_init(done, 2);
     tc::fence_mbar_init();
   }
   __syncwarp();
@@ -222,61 +225,49 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(row_full + st);
     }
-  } else if (warp == 9) {
-    const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
-    const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
+  } else if (warp >= 9) {
+    // warp 9: S^T and dV, warp 10: dP^T and dK
+    const bool ds = warp == 10;
+    const uint32_t kv = tc::smem_u32(sm + (ds ? G::OFF_V : G::OFF_K));    // A of the 64-column products
+    const uint32_t bx = tc::smem_u32(sm + (ds ? G::OFF_DO : G::OFF_Q));   // their B
+    const uint32_t by = tc::smem_u32(sm + (ds ? G::OFF_Q : G::OFF_DO));   // B of the sums
+    uint64_t* bx_full = ds ? do_full : q_full;
+    uint64_t* by_full = ds ? q_full : do_full;
+    uint64_t* bx_empty = ds ? do_empty : q_empty;
+    uint64_t* by_empty = ds ? q_empty : do_empty;
+    uint64_t* out_full = ds ? dp_full : s_full;
+    uint64_t* in_full = ds ? ds_full : p_full;
+    const uint32_t blocks = ds ? DP : 0, sum = ds ? DK : DV;
     auto wait = [&](uint64_t* bar, int ph) {
       const bool w = tc::mbar_wait_warp(bar, ph);
       tc::fence_after_sync();
       return w;
     };
-    auto scores = [&](int g, int st) {
-      mma_rows<D>(tmem + g * 64, k, q + st * G::TILE, g);
-      tc::mma_commit(s_full + g);
+    auto product = [&](int g, int st) {
+      mma_rows<D>(tmem + blocks + g * 64, kv, bx + st * G::TILE, g);
+      tc::mma_commit(out_full + g);
     };
-    auto products = [&](int g, int st) {
-      mma_rows<D>(tmem + DP + g * 64, v, d_o + st * G::TILE, g);
-      tc::mma_commit(dp_full + g);
-    };
-    ok = wait(kv_full, 0) && wait(q_full, 0) && wait(do_full, 0);
+    ok = wait(kv_full, 0) && wait(bx_full, 0);
     if (ok && tc::elect_one()) {
-      scores(0, 0);
-      if (both(0)) scores(1, 0);
-      products(0, 0);
-      if (both(0)) products(1, 0);
+      product(0, 0);
+      if (both(0)) product(1, 0);
+      tc::mma_commit(bx_empty);
     }
     __syncwarp();
     int turn[2] = {0, 0};  // blocks of the groups so far
     for (int it = 0; it < n && ok; ++it) {
-      const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
+      const int st = it & 1, ph = (it >> 1) & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
       const bool more = it + 1 < n, two = both(it), next_two = more && both(it + 1);
+      if (!(ok = wait(by_full + st, ph))) break;
+      if (more && !(ok = wait(bx_full + nx, nph))) break;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        if (g == 0 || two) {
-          if (!(ok = wait(p_full + g, turn[g] & 1))) break;
-          if (tc::elect_one()) mma_add<D>(tmem + DV, tmem + g * 64, d_o + st * G::TILE, g, it == 0 && g == 0);
-          __syncwarp();
-        }
-        if (g == 0 && more && !(ok = wait(q_full + nx, nph))) break;
+        if ((g == 0 || two) && !(ok = wait(in_full + g, turn[g]++ & 1))) break;
         if (tc::elect_one()) {
-          if (g == 1) tc::mma_commit(do_empty + st);
-          if (g == 0 ? more : next_two) scores(g, nx);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g == 0 || two) {
-          if (!(ok = wait(ds_full + g, turn[g]++ & 1))) break;
-          if (tc::elect_one()) mma_add<D>(tmem + DK, tmem + DP + g * 64, q + st * G::TILE, g, it == 0 && g == 0);
-          __syncwarp();
-        }
-        if (g == 0 && more && !(ok = wait(do_full + nx, nph))) break;
-        if (tc::elect_one()) {
-          if (g == 1) tc::mma_commit(q_empty + st);
-          if (g == 0 ? more : next_two) products(g, nx);
-          if (g == 1 && !more) tc::mma_commit(done);
+          if (g == 0 || two) mma_add<D>(tmem + sum, tmem + blocks + g * 64, by + st * G::TILE, g, it == 0 && g == 0);
+          if (g == 1) tc::mma_commit(by_empty + st);
+          if (g == 0 ? more : next_two) product(g, nx);
+          if (g == 1) tc::mma_commit(more ? bx_empty + nx : done);
         }
         __syncwarp();
       }
@@ -424,8 +415,10 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   uint64_t* s_full = k_tail + 1;    // [2]
   uint64_t* dp_full = s_full + 2;   // [2 groups]
   uint64_t* dp_free = dp_full + 2;  // [2]
-  uint64_t* ds_full = dp_free + 2;  // [2]
-  uint64_t* done = ds_full + 2;
+  // [2 groups][2 score buffers]: a group may finish a block and the next one while
+  // the other group holds up the warp that waits for both, but not a third
+  uint64_t* ds_full = dp_free + 2;
+  uint64_t* done = ds_full + 4;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ float row_sum[2][128];  // the first block's delta, by column half
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -449,6 +442,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::mbar_init(dp_full + s, 1);
       tc::mbar_init(dp_free + s, EW);
       tc::mbar_init(ds_full + s, EW);
+      tc::mbar_init(ds_full + 2 + s, EW);
     }
     tc::mbar_init(k_tail, 1);
     tc::mbar_init(done, 1);
@@ -495,7 +489,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(k_tail);
     }
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
     const uint32_t q = tc::smem_u32(sm + G::OFF_Q), d_o = tc::smem_u32(sm + G::OFF_DO);
     const uint32_t k = tc::smem_u32(sm + G::OFF_K), v = tc::smem_u32(sm + G::OFF_V);
     auto wait = [&](uint64_t* bar, int ph) {
@@ -503,57 +497,57 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::fence_after_sync();
       return w;
     };
-    auto products = [&](int g, int st) {
-      mma_rows<D>(tmem + DP + g * 64, d_o, v + st * G::TILE, g);
-      tc::mma_commit(dp_full + g);
-    };
-    ok = wait(q_full, 0) && wait(k_full, 0);
-    if (ok && tc::elect_one()) {
-      mma_rows<D, 128>(tmem, q, k, 0);
-      tc::mma_commit(s_full);
-    }
-    __syncwarp();
-    ok = ok && wait(v_full, 0);
-    if (ok && tc::elect_one()) {
-      products(0, 0);
-      if (both(0)) products(1, 0);
-      tc::mma_commit(v_empty);
-    }
-    __syncwarp();
-    for (int it = 0; it < n && ok; ++it) {
-      const int st = it & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1, ks0 = it % 3, ks1 = (it + 1) % 3;
-      const bool more = it + 1 < n, two = both(it), next_two = more && both(it + 1);
-      if (more) {
-        // the other score buffer: its dS was consumed by dQ(it - 1), issued before
-        if (!(ok = wait(k_full + ks1, (it + 1) / 3 & 1))) break;
-        if (tc::elect_one()) {
-          mma_rows<D, 128>(tmem + nx * 128, q, k + ks1 * G::TILE, 0);
-          tc::mma_commit(s_full + nx);
-        }
-        __syncwarp();
-        if (!(ok = wait(v_full + nx, nph))) break;
-      } else if (tail < 128 && !(ok = wait(k_tail, 0))) {
-        break;
-      }
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g == 1 && !two) continue;  // the last block
-        if (g == 0 ? more : next_two) {
-          if (!(ok = wait(dp_free + g, it & 1))) break;
-          if (tc::elect_one()) products(g, nx);
-          __syncwarp();
-        }
-        if (!(ok = wait(ds_full + g, it & 1))) break;
-        if (tc::elect_one()) mma_add<D>(tmem + DQ, tmem + st * 128 + g * 64, k + ks0 * G::TILE, g, it == 0 && g == 0);
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (tc::elect_one()) {
-        if (more) tc::mma_commit(v_empty + nx);
-        tc::mma_commit(k_empty + ks0);
-        if (!more) tc::mma_commit(done);
+    ok = wait(q_full, 0);
+    if (warp == 9) {  // S and dQ
+      ok = ok && wait(k_full, 0);
+      if (ok && tc::elect_one()) {
+        mma_rows<D, 128>(tmem, q, k, 0);
+        tc::mma_commit(s_full);
       }
       __syncwarp();
+      for (int it = 0; it < n && ok; ++it) {
+        const int st = it & 1, nx = (it + 1) & 1, ks0 = it % 3, ks1 = (it + 1) % 3;
+        const bool more = it + 1 < n;
+        if (more) {
+          // the other score buffer: its dS was consumed by dQ(it - 1), issued before
+          if (!(ok = wait(k_full + ks1, (it + 1) / 3 & 1))) break;
+          if (tc::elect_one()) {
+            mma_rows<D, 128>(tmem + nx * 128, q, k + ks1 * G::TILE, 0);
+            tc::mma_commit(s_full + nx);
+          }
+          __syncwarp();
+        } else if (tail < 128 && !(ok = wait(k_tail, 0))) {
+          break;
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const bool has = g == 0 || both(it);
+          if (has && !(ok = wait(ds_full + 2 * g + st, (it >> 1) & 1))) break;
+          if (tc::elect_one()) {
+            if (has) mma_add<D>(tmem + DQ, tmem + st * 128 + g * 64, k + ks0 * G::TILE, g, it == 0 && g == 0);
+            if (g == 1) tc::mma_commit(more ? k_empty + ks0 : done);
+          }
+          __syncwarp();
+        }
+      }
+    } else {  // dP
+      for (int it = 0; it < n && ok; ++it) {
+        const int st = it & 1;
+        if (!(ok = wait(v_full + st, (it >> 1) & 1))) break;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const bool has = g == 0 || both(it);
+          if (has && it > 0 && !(ok = wait(dp_free + g, (it - 1) & 1))) break;
+          if (tc::elect_one()) {
+            if (has) {
+              mma_rows<D>(tmem + DP + g * 64, d_o, v + st * G::TILE, g);
+              tc::mma_commit(dp_full + g);
+            }
+            if (g == 1) tc::mma_commit(v_empty + st);
+          }
+          __syncwarp();
+        }
+      }
     }
   } else {
     const int half = warp >> 2;
@@ -624,7 +618,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(ds_full + half);
+      if (lane == 0) tc::mbar_arrive(ds_full + 2 * half + st);
     }
     if (!ok) {
       both_leave();
