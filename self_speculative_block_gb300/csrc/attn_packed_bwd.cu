@@ -17,13 +17,9 @@
 // relative 2^-8, as the tensor cores take them) go back to tensor memory over
 // the scores they came from and are the A operands of dV += P^T dO and dK +=
 // dS^T Q; dO and Q serve as they lie, K-major for S^T and dP^T and N-major
-// here.  A dq CTA has lanes of query rows and dQ += dS K.  The elementwise work
-// of a block is two groups of four warps, 64 columns to a thread, each with
-// barriers of its own: the groups fall out of step, and one's exponentials and
-// stores run while the tensor cores work for the other (in step, as one group
-// of eight warps, a dk/dv block took 3,600 cycles, of which 2,048 were
-// products).  In return S^T and dP^T of a dk/dv CTA, and dP of a dq CTA, are
-// products of 64 columns, which take 49 cycles instead of 32.
+// here.  A dq CTA has lanes of query rows and dQ += dS K.  Two groups of four
+// warps do the elementwise work, 64 columns of a block to a thread; it overlaps
+// the products: P^T with dK and dP^T, dS^T with dV and the next S^T.
 //
 // delta from o takes o's rounding to bf16 into every dS of the row.  That
 // matters where a row sees few keys (o is then large), so for the first 128
@@ -141,10 +137,10 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
   uint64_t* do_full = q_empty + 2;   // [2]
   uint64_t* do_empty = do_full + 2;  // [2]
   uint64_t* row_full = do_empty + 2; // [2] lse and delta of the stage; ragged tiles zeroed
-  uint64_t* s_full = row_full + 2;   // [2 groups]
-  uint64_t* p_full = s_full + 2;     // [2]
-  uint64_t* dp_full = p_full + 2;    // [2]
-  uint64_t* ds_full = dp_full + 2;   // [2]
+  uint64_t* s_full = row_full + 2;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_full = dp_full + 1;    // [2 groups]
+  uint64_t* ds_full = p_full + 2;    // [2]
   uint64_t* done = ds_full + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -166,10 +162,10 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::mbar_init(do_empty + s, 2);
       tc::mbar_init(row_full + s, 1);
     }
+    tc::mbar_init(s_full, 1);
+    tc::mbar_init(dp_full, 1);
     for (int g = 0; g < 2; ++g) {
-      tc::mbar_init(s_full + g, 1);
       tc::mbar_init(p_full + g, EW);
-      tc::mbar_init(dp_full + g, 1);
       tc::mbar_init(ds_full + g, EW);
     }
     tc::mbar_init(done, 2);
@@ -228,7 +224,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
   } else if (warp >= 9) {
     // warp 9: S^T and dV, warp 10: dP^T and dK
     const bool ds = warp == 10;
-    const uint32_t kv = tc::smem_u32(sm + (ds ? G::OFF_V : G::OFF_K));    // A of the 64-column products
+    const uint32_t kv = tc::smem_u32(sm + (ds ? G::OFF_V : G::OFF_K));    // A of the blocks
     const uint32_t bx = tc::smem_u32(sm + (ds ? G::OFF_DO : G::OFF_Q));   // their B
     const uint32_t by = tc::smem_u32(sm + (ds ? G::OFF_Q : G::OFF_DO));   // B of the sums
     uint64_t* bx_full = ds ? do_full : q_full;
@@ -243,34 +239,34 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::fence_after_sync();
       return w;
     };
-    auto product = [&](int g, int st) {
-      mma_rows<D>(tmem + blocks + g * 64, kv, bx + st * G::TILE, g);
-      tc::mma_commit(out_full + g);
+    auto product = [&](int st, bool two) {
+      if (two) mma_rows<D, 128>(tmem + blocks, kv, bx + st * G::TILE, 0);
+      else mma_rows<D, 64>(tmem + blocks, kv, bx + st * G::TILE, 0);
+      tc::mma_commit(out_full);
     };
     ok = wait(kv_full, 0) && wait(bx_full, 0);
     if (ok && tc::elect_one()) {
-      product(0, 0);
-      if (both(0)) product(1, 0);
+      product(0, both(0));
       tc::mma_commit(bx_empty);
     }
     __syncwarp();
     int turn[2] = {0, 0};  // blocks of the groups so far
     for (int it = 0; it < n && ok; ++it) {
       const int st = it & 1, ph = (it >> 1) & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
-      const bool more = it + 1 < n, two = both(it), next_two = more && both(it + 1);
+      const bool more = it + 1 < n, two = both(it);
       if (!(ok = wait(by_full + st, ph))) break;
       if (more && !(ok = wait(bx_full + nx, nph))) break;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if ((g == 0 || two) && !(ok = wait(in_full + g, turn[g]++ & 1))) break;
-        if (tc::elect_one()) {
-          if (g == 0 || two) mma_add<D>(tmem + sum, tmem + blocks + g * 64, by + st * G::TILE, g, it == 0 && g == 0);
-          if (g == 1) tc::mma_commit(by_empty + st);
-          if (g == 0 ? more : next_two) product(g, nx);
-          if (g == 1) tc::mma_commit(more ? bx_empty + nx : done);
-        }
-        __syncwarp();
+      if (!(ok = wait(in_full, turn[0]++ & 1))) break;
+      if (tc::elect_one()) mma_add<D>(tmem + sum, tmem + blocks, by + st * G::TILE, 0, it == 0);
+      __syncwarp();
+      if (two && !(ok = wait(in_full + 1, turn[1]++ & 1))) break;
+      if (tc::elect_one()) {
+        if (two) mma_add<D>(tmem + sum, tmem + blocks + 64, by + st * G::TILE, 1, false);
+        tc::mma_commit(by_empty + st);
+        if (more) product(nx, both(it + 1));
+        tc::mma_commit(more ? bx_empty + nx : done);
       }
+      __syncwarp();
     }
   } else {
     const int half = warp >> 2;
@@ -278,14 +274,16 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
     const int key = blk.at + (warp & 3) * 32 + lane;  // within the sequence
     const uint32_t ts = tmem + lanes + half * 64, tp = ts + DP;
     const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E);
-    int turn = 0;  // blocks of the group so far
     for (int it = 0; it < n; ++it) {
-      if (half && !both(it)) continue;
+      if (half && !both(it)) {  // nothing to do, but the barriers' phases go by
+        if (!(ok = tc::mbar_wait_warp(s_full, it & 1) && tc::mbar_wait_warp(dp_full, it & 1))) break;
+        continue;
+      }
       const int st = it & 1;
       const int at = (kb + it % per) * 128 + half * 64;  // first query row of this thread's columns
       const float4* lse = reinterpret_cast<const float4*>(rows + st * 256 + half * 64);
       const float4* del = lse + 32;
-      ok = tc::mbar_wait_ns(row_full + st, (it >> 1) & 1) && tc::mbar_wait_ns(s_full + half, turn & 1);
+      ok = tc::mbar_wait_ns(row_full + st, (it >> 1) & 1) && tc::mbar_wait_ns(s_full, it & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::fence_after_sync();
       // query column i is visible from `lo` on (causal) and below `hi` (the end of the sequence)
@@ -321,7 +319,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(p_full + half);
-      if (!(ok = tc::mbar_wait_warp(dp_full + half, turn++ & 1))) break;
+      if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
       tc::fence_after_sync();
       {
         uint32_t u[64];
@@ -413,11 +411,11 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   uint64_t* v_empty = v_full + 2;   // [2]
   uint64_t* k_tail = v_empty + 2;
   uint64_t* s_full = k_tail + 1;    // [2]
-  uint64_t* dp_full = s_full + 2;   // [2 groups]
-  uint64_t* dp_free = dp_full + 2;  // [2]
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* dp_free = dp_full + 1;  // both groups
   // [2 groups][2 score buffers]: a group may finish a block and the next one while
   // the other group holds up the warp that waits for both, but not a third
-  uint64_t* ds_full = dp_free + 2;
+  uint64_t* ds_full = dp_free + 1;
   uint64_t* done = ds_full + 4;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ float row_sum[2][128];  // the first block's delta, by column half
@@ -439,12 +437,12 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       tc::mbar_init(v_full + s, 1);
       tc::mbar_init(v_empty + s, 1);
       tc::mbar_init(s_full + s, 1);
-      tc::mbar_init(dp_full + s, 1);
-      tc::mbar_init(dp_free + s, EW);
       tc::mbar_init(ds_full + s, EW);
       tc::mbar_init(ds_full + 2 + s, EW);
     }
     tc::mbar_init(k_tail, 1);
+    tc::mbar_init(dp_full, 1);
+    tc::mbar_init(dp_free, 2 * EW);
     tc::mbar_init(done, 1);
     tc::fence_mbar_init();
   }
@@ -534,19 +532,14 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       for (int it = 0; it < n && ok; ++it) {
         const int st = it & 1;
         if (!(ok = wait(v_full + st, (it >> 1) & 1))) break;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const bool has = g == 0 || both(it);
-          if (has && it > 0 && !(ok = wait(dp_free + g, (it - 1) & 1))) break;
-          if (tc::elect_one()) {
-            if (has) {
-              mma_rows<D>(tmem + DP + g * 64, d_o, v + st * G::TILE, g);
-              tc::mma_commit(dp_full + g);
-            }
-            if (g == 1) tc::mma_commit(v_empty + st);
-          }
-          __syncwarp();
+        if (it > 0 && !(ok = wait(dp_free, (it - 1) & 1))) break;
+        if (tc::elect_one()) {
+          if (both(it)) mma_rows<D, 128>(tmem + DP, d_o, v + st * G::TILE, 0);
+          else mma_rows<D, 64>(tmem + DP, d_o, v + st * G::TILE, 0);
+          tc::mma_commit(dp_full);
+          tc::mma_commit(v_empty + st);
         }
+        __syncwarp();
       }
     }
   } else {
@@ -579,7 +572,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
           p[i + 1] = ex2(y);
         }
       }
-      if (!(ok = tc::mbar_wait_warp(dp_full + half, it & 1))) break;
+      if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
       tc::fence_after_sync();
       {
         uint32_t u[64];
@@ -588,7 +581,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(dp_free + half);
+        if (lane == 0) tc::mbar_arrive(dp_free);
         // the diagonal block holds the end of the sequence, too: it lies past every row
         const int see = it + 1 == n ? min(row, blk.len - 1) - it * 128 - half * 64 : 64;
         if (n == 1) {  // all the keys that the row sees
