@@ -138,9 +138,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* s_full = empty + SLOTS;  // [2 tiles][2 buffers]
   uint64_t* p_full = s_full + 4;     // [2 tiles][2 buffers]
   uint64_t* o_full = p_full + 4;     // [2] a block's P V is complete
+  uint64_t* o_done = o_full + 2;     // [2] the item's last one is
   // ragged V tiles, one barrier a slot: a slot's next load waits for this one's
   // use, so no barrier is ever two phases ahead of the warp that waits on it
-  uint64_t* v_tail = o_full + 2;         // [SLOTS] the rows behind the sequence are zero
+  uint64_t* v_tail = o_done + 2;         // [SLOTS] the rows behind the sequence are zero
   uint64_t* work_full = v_tail + SLOTS;  // [2]
   uint64_t* work_free = work_full + 2;  // [2]
   uint64_t* taken = work_free + 2;
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int j = 0; j < 2; ++j) {
       tc::mbar_init(o_full + j, 1);
+      tc::mbar_init(o_done + j, 1);
       tc::mbar_init(work_full + j, 1);
       tc::mbar_init(work_free + j, SW + 3);
     }
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (b < nb) {
               mma_add<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * (b >> 1) + 1), b & 1, b == 0);
               tc::mma_commit(o_full + j);
+              if (b + 1 == nb) tc::mma_commit(o_done + j);
             }
             if (b + 2 < nb) scores(b + 2);
             if ((b & 1) || b + 1 == most) release(2 * (b >> 1) + 1);
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tmem + F::O_COL + j * D + lanes;
     const float sl2 = a.scale * LOG2E;
-    int turn[2] = {0, 0}, outs = 0;  // blocks of each buffer, of the tile so far
+    int turn[2] = {0, 0}, outs = 0, done = 0;  // blocks of each buffer, of the tile, and items so far
     for (int i = 0; ok && next_item(work, work_full, work_free, i, w, ok); ++i) {
       const Item t(w);
       const int nj = j ? t.n1 : t.n0, nb = t.blocks(j);
@@ -350,7 +353,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           const bool grow = (mx - ref) * sl2 > GROW;
           if (__any_sync(0xffffffffu, grow)) {
-            if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;  // the last block's P V
+            // the last block's P V; these scores vouch for the one before it, and
+            // the next one waits for this block's P, so the parity is unambiguous
+            if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
             tc::fence_after_sync();
             const float to_new = grow ? mx : ref;
             const float f = ex2(ref2 - to_new * sl2);
@@ -388,10 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + j * 2 + (b & 1));
       }
-      // the last block's P V, after the one before it: the scores of a block vouch
-      // for the P V two blocks back, and a barrier tells only neighbouring phases apart
-      if (ok && nb > 1) ok = tc::mbar_wait_warp(o_full + j, (outs - 2) & 1);
-      if (!ok || !(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
+      if (!ok || !(ok = tc::mbar_wait_warp(o_done + j, done++ & 1))) break;
       tc::fence_after_sync();
       const float inv = 1.f / l;
       const size_t tok = (size_t)t.blk.row0 + row;

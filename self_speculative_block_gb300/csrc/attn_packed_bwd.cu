@@ -22,9 +22,8 @@
 // the products: P^T with dK and dP^T, dS^T with dV and the next S^T.
 //
 // delta from o takes o's rounding to bf16 into every dS of the row.  That
-// matters where a row sees few keys (o is then large), so for the first 128
-// rows of a sequence, whose keys are one block, both kinds of CTA take delta_i
-// = sum_j P_ij dP_ij in fp32 instead.
+// matters where a row sees few keys (o is then large), so for the first 32 rows
+// of a sequence delta is sum_j P_ij dP_ij instead, in fp32.
 #include "../../include/gocr.h"
 #include "attn_packed.cuh"
 
@@ -38,15 +37,13 @@ namespace {
 // the other warp has some.
 constexpr int THREADS = 352;
 constexpr int EW = 4;         // warps of an elementwise group
-constexpr int BAR_OFF = 7 * 128 * 128 * 2;  // behind seven tiles of D = 128
-constexpr int SMEM = BAR_OFF + 256 + 1024;
-
-// Barrier of the threads of an elementwise group, or of both.  A warp
-// that gives up leaves them, so that it keeps nobody.
-__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory"); }
-__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void group_leave(int group) { asm volatile("bar.arrive %0, 128;" ::"r"(2 + group) : "memory"); }
-__device__ __forceinline__ void both_leave() { asm volatile("bar.arrive 1, 256;" ::: "memory"); }
+// Seven tiles of D = 128 (dynamic shared memory starts at a multiple of 1,024,
+// checked in the kernel: there is no room for slack), -lse and -delta of two
+// query blocks, barriers.
+constexpr int ROW_OFF = 7 * 128 * 128 * 2;
+constexpr int BAR_OFF = ROW_OFF + 2 * 2 * 128 * 4;
+constexpr int SMEM = BAR_OFF + 256;
+static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 
 static __device__ int g_error;  // DevErr of a wait that gave up
 
@@ -59,27 +56,81 @@ struct BwdArgs {
   float scale;
 };
 
-// delta[h][t] = sum_d do o: D / 8 lanes per (t, h)
-template <int D>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const bf16* o, const bf16* d_o, float* delta, int T, int Hq) {
-  constexpr int L = D / 8;
-  if (threadIdx.x == 0) tc::grid_dep_launch();
-  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) / L;
-  const int l = threadIdx.x % L;
-  const bool in = i < (long long)T * Hq;
-  float s = 0.f;
-  if (in) {
-    const uint4 x = *reinterpret_cast<const uint4*>(o + i * D + l * 8), y = *reinterpret_cast<const uint4*>(d_o + i * D + l * 8);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+constexpr int FEW = 32;  // rows of a delta CTA; of a sequence's start with delta from P and dP
+
+struct DeltaArgs {
+  const bf16* q; const bf16* k; const bf16* v; const bf16* o; const bf16* d_o;
+  long long ldq, ldk, ldv;
+  const int* cu;
+  const float* lse;
+  float* delta;
+  int n_seq, T, Hq, Hkv;
+  float scale;
+};
+
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-      s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
-    }
+  for (int e = 0; e < 4; ++e) {
+    s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+    s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
   }
+  return s;
+}
+
+// delta of 32 rows of a sequence and a q head.  Bound by reading o and do, D / 8
+// lanes to a row; the sequence's first CTA holds its rows of q, k, v and do in
+// shared memory and its lanes are keys.
+template <int D>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
+  constexpr int L = D / 8, LD = L + 1;  // 16-byte pieces of a row; row pitch in shared memory
+  __shared__ uint4 t[4][FEW][LD];       // q, k, do, v
+  const Block blk = find_block<false>(a.cu, a.n_seq, a.T, FEW, blockIdx.x);
+  if (threadIdx.x == 0) tc::grid_dep_launch();
+  if (!blk.len) return;
+  const int head = blockIdx.y, n = min(FEW, blk.len - blk.at);
+  const size_t row0 = (size_t)blk.row0 + blk.at;
+  float* out = a.delta + (size_t)head * a.T + row0;
+  if (blk.at > 0) {
+    const int l = threadIdx.x % L;
 #pragma unroll
-  for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (in && l == 0) delta[(i % Hq) * T + i / Hq] = s;
+    for (int r0 = 0; r0 < FEW; r0 += 256 / L) {
+      const int r = r0 + threadIdx.x / L;
+      float s = 0.f;
+      if (r < n) {
+        const size_t at = ((row0 + r) * a.Hq + head) * L + l;
+        s = dot8(reinterpret_cast<const uint4*>(a.o)[at], reinterpret_cast<const uint4*>(a.d_o)[at], 0.f);
+      }
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (r < n && l == 0) out[r] = s;
+    }
+    return;
+  }
+  const int kvh = head / (a.Hq / a.Hkv);
+  for (int i = threadIdx.x; i < FEW * L; i += 256) {
+    const int r = i / L, l = i % L;
+    const size_t row = row0 + r;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    t[0][r][l] = r < n ? reinterpret_cast<const uint4*>(a.q + row * a.ldq + head * D)[l] : z;
+    t[1][r][l] = r < n ? reinterpret_cast<const uint4*>(a.k + row * a.ldk + kvh * D)[l] : z;
+    t[2][r][l] = r < n ? reinterpret_cast<const uint4*>(a.d_o)[(row * a.Hq + head) * L + l] : z;
+    t[3][r][l] = r < n ? reinterpret_cast<const uint4*>(a.v + row * a.ldv + kvh * D)[l] : z;
+  }
+  __syncthreads();
+  const int key = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < n; r += 8) {
+    float s = 0.f, dp = 0.f;
+#pragma unroll 4
+    for (int l = 0; l < L; ++l) {
+      s = dot8(t[0][r][l], t[1][key][l], s);
+      dp = dot8(t[2][r][l], t[3][key][l], dp);
+    }
+    float x = key <= r ? ex2((s * a.scale - a.lse[(size_t)head * a.T + row0 + r]) * LOG2E) * dp : 0.f;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    if (key == 0) out[r] = x;
+  }
 }
 
 // The 32 columns of an accumulator row, times f, as bf16 to dst (16-byte aligned).
@@ -102,42 +153,23 @@ __device__ __forceinline__ void store32(uint32_t taddr, float f, bf16* dst, bool
 template <int D> struct DkvGeo {
   static constexpr int TILE = TILE_BYTES<D>;
   static constexpr int OFF_K = 0, OFF_V = TILE;
-  static constexpr int OFF_Q = 2 * TILE;    // [2]
-  static constexpr int OFF_DO = 4 * TILE;   // [2]
-  static constexpr int OFF_ROW = 6 * TILE;  // float [2 stages][-lse log2 e, -delta][128]
-  static constexpr int OFF_RED = OFF_ROW + 2 * 2 * 128 * 4;  // float [2 halves][4 warps][64]
-  static_assert(OFF_RED + 2 * 4 * 64 * 4 <= BAR_OFF, "shared memory");
+  static constexpr int OFF_Q = 2 * TILE;    // [3]: S^T(it + 1) runs while dK(it - 1) still needs its Q
+  static constexpr int OFF_DO = 5 * TILE;   // [2]
 };
-
-// Sums over the warp's lanes of 32 values: lane l gets that of value l.  Each
-// step hands half of the values that are left to the lane that keeps them.
-__device__ __forceinline__ float lane_sums(float* x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float give = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  }
-  return x[0];
-}
 
 template <int D>
 __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                         const CUtensorMap& mdo, const BwdArgs& a, const Block& blk, int kvh) {
   using G = DkvGeo<D>;
-  float* rows = reinterpret_cast<float*>(sm + G::OFF_ROW);
-  float* red = reinterpret_cast<float*>(sm + G::OFF_RED);
+  float* rows = reinterpret_cast<float*>(sm + ROW_OFF);  // [2 stages][-lse log2 e, -delta][128]
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(sm + BAR_OFF);
-  uint64_t* q_full = kv_full + 1;    // [2]
-  uint64_t* q_empty = q_full + 2;    // [2]
-  uint64_t* do_full = q_empty + 2;   // [2]
+  uint64_t* q_full = kv_full + 1;    // [3]
+  uint64_t* q_empty = q_full + 3;    // [3]
+  uint64_t* do_full = q_empty + 3;   // [2]
   uint64_t* do_empty = do_full + 2;  // [2]
   uint64_t* row_full = do_empty + 2; // [2] lse and delta of the stage; ragged tiles zeroed
-  uint64_t* s_full = row_full + 2;
+  uint64_t* row_free = row_full + 2; // [2] their readers are done
+  uint64_t* s_full = row_free + 2;
   uint64_t* dp_full = s_full + 1;
   uint64_t* p_full = dp_full + 1;    // [2 groups]
   uint64_t* ds_full = p_full + 2;    // [2]
@@ -155,12 +187,15 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
 
   if (tid == 0) {
     tc::mbar_init(kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 3; ++s) {
       tc::mbar_init(q_full + s, 1);
       tc::mbar_init(q_empty + s, 2);   // both MMA warps read Q and dO
+    }
+    for (int s = 0; s < 2; ++s) {
       tc::mbar_init(do_full + s, 1);
       tc::mbar_init(do_empty + s, 2);
       tc::mbar_init(row_full + s, 1);
+      tc::mbar_init(row_free + s, 2 * EW);
     }
     tc::mbar_init(s_full, 1);
     tc::mbar_init(dp_full, 1);
@@ -192,18 +227,23 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       const int st = it & 1, ph = (it >> 1) & 1;
       const int head = kvh * group + it / per, at = (kb + it % per) * 128;
       const bool ragged = at + 128 > blk.len;
-      uint8_t* q = sm + G::OFF_Q + st * G::TILE;
+      const int qs = it % 3, qp = it / 3 & 1;
+      uint8_t* q = sm + G::OFF_Q + qs * G::TILE;
       uint8_t* d_o = sm + G::OFF_DO + st * G::TILE;
-      if (!(ok = tc::mbar_wait_warp(q_empty + st, ph ^ 1))) break;
+      if (!(ok = tc::mbar_wait_warp(q_empty + qs, qp ^ 1))) break;
+      if (tc::elect_one()) {
+        tc::mbar_expect_tx(q_full + qs, G::TILE);
+        load_tile<D>(q, &mq, head, blk.row0 + at, q_full + qs);
+      }
+      __syncwarp();
       if (!(ok = tc::mbar_wait_warp(do_empty + st, ph ^ 1))) break;
       if (tc::elect_one()) {
-        tc::mbar_expect_tx(q_full + st, G::TILE);
-        load_tile<D>(q, &mq, head, blk.row0 + at, q_full + st);
         tc::mbar_expect_tx(do_full + st, G::TILE);
         load_tile<D>(d_o, &mdo, head, blk.row0 + at, do_full + st);
       }
       __syncwarp();
-      // the stage is free: dK of its last block, after every read of its rows, has completed
+      // the stage's rows were last read for the block two back
+      if (it > 1 && !(ok = tc::mbar_wait_warp(row_free + st, ph ^ 1))) break;
       float* lse = rows + st * 256;
       for (int i = lane; i < 128; i += 32) {
         const bool in = at + i < blk.len;
@@ -212,7 +252,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
         lse[128 + i] = in ? -a.delta[src] : 0.f;
       }
       if (ragged) {
-        ok = tc::mbar_wait_warp(q_full + st, ph) && tc::mbar_wait_warp(do_full + st, ph);
+        ok = tc::mbar_wait_warp(q_full + qs, qp) && tc::mbar_wait_warp(do_full + st, ph);
         if (!ok) break;
         zero_rows<D>(q, tail);
         zero_rows<D>(d_o, tail);
@@ -233,6 +273,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
     uint64_t* by_empty = ds ? q_empty : do_empty;
     uint64_t* out_full = ds ? dp_full : s_full;
     uint64_t* in_full = ds ? ds_full : p_full;
+    const int bx_n = ds ? 2 : 3, by_n = ds ? 3 : 2;  // stages
     const uint32_t blocks = ds ? DP : 0, sum = ds ? DK : DV;
     auto wait = [&](uint64_t* bar, int ph) {
       const bool w = tc::mbar_wait_warp(bar, ph);
@@ -250,23 +291,24 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       tc::mma_commit(bx_empty);
     }
     __syncwarp();
-    int turn[2] = {0, 0};  // blocks of the groups so far
+    int x = 0, xp = 0, y = 0, yp = 0;  // stage and phase of the block's B of both kinds
     for (int it = 0; it < n && ok; ++it) {
-      const int st = it & 1, ph = (it >> 1) & 1, nx = (it + 1) & 1, nph = ((it + 1) >> 1) & 1;
       const bool more = it + 1 < n, two = both(it);
-      if (!(ok = wait(by_full + st, ph))) break;
-      if (more && !(ok = wait(bx_full + nx, nph))) break;
-      if (!(ok = wait(in_full, turn[0]++ & 1))) break;
-      if (tc::elect_one()) mma_add<D>(tmem + sum, tmem + blocks, by + st * G::TILE, 0, it == 0);
+      if (!(ok = wait(by_full + y, yp))) break;
+      if (++x == bx_n) { x = 0; xp ^= 1; }  // of the next block
+      if (more && !(ok = wait(bx_full + x, xp))) break;
+      if (!(ok = wait(in_full, it & 1))) break;
+      if (tc::elect_one()) mma_add<D>(tmem + sum, tmem + blocks, by + y * G::TILE, 0, it == 0);
       __syncwarp();
-      if (two && !(ok = wait(in_full + 1, turn[1]++ & 1))) break;
+      if (!(ok = wait(in_full + 1, it & 1))) break;
       if (tc::elect_one()) {
-        if (two) mma_add<D>(tmem + sum, tmem + blocks + 64, by + st * G::TILE, 1, false);
-        tc::mma_commit(by_empty + st);
-        if (more) product(nx, both(it + 1));
-        tc::mma_commit(more ? bx_empty + nx : done);
+        if (two) mma_add<D>(tmem + sum, tmem + blocks + 64, by + y * G::TILE, 1, false);
+        tc::mma_commit(by_empty + y);
+        if (more) product(x, both(it + 1));
+        tc::mma_commit(more ? bx_empty + x : done);
       }
       __syncwarp();
+      if (++y == by_n) { y = 0; yp ^= 1; }
     }
   } else {
     const int half = warp >> 2;
@@ -275,8 +317,15 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
     const uint32_t ts = tmem + lanes + half * 64, tp = ts + DP;
     const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E);
     for (int it = 0; it < n; ++it) {
-      if (half && !both(it)) {  // nothing to do, but the barriers' phases go by
-        if (!(ok = tc::mbar_wait_warp(s_full, it & 1) && tc::mbar_wait_warp(dp_full, it & 1))) break;
+      if (half && !both(it)) {
+        // nothing to do, but in step: a barrier tells only neighbouring phases apart
+        if (!(ok = tc::mbar_wait_warp(s_full, it & 1))) break;
+        if (lane == 0) tc::mbar_arrive(p_full + 1);
+        if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;
+        if (lane == 0) {
+          tc::mbar_arrive(ds_full + 1);
+          tc::mbar_arrive(row_free + (it & 1));
+        }
         continue;
       }
       const int st = it & 1;
@@ -326,32 +375,12 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
         tc::tmem_ld32_nowait(tp, u);
         tc::tmem_ld32_nowait(tp + 32, u + 32);
         tc::tmem_wait_ld();
-        if (at - half * 64 == 0) {  // the first query block: these keys are all that its rows see
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = c + i < lo || c + i >= hi ? 0.f : p[c + i] * __uint_as_float(u[c + i]);
-            red[(half * 4 + (warp & 3)) * 64 + c + lane] = lane_sums(x);
-          }
-          group_sync(half);
-          const float4* r4 = reinterpret_cast<const float4*>(red + half * 256);
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const float4 a0 = r4[i / 4], a1 = r4[16 + i / 4], a2 = r4[32 + i / 4], a3 = r4[48 + i / 4];
-            p[i] *= __uint_as_float(u[i]) - ((a0.x + a1.x) + (a2.x + a3.x));
-            p[i + 1] *= __uint_as_float(u[i + 1]) - ((a0.y + a1.y) + (a2.y + a3.y));
-            p[i + 2] *= __uint_as_float(u[i + 2]) - ((a0.z + a1.z) + (a2.z + a3.z));
-            p[i + 3] *= __uint_as_float(u[i + 3]) - ((a0.w + a1.w) + (a2.w + a3.w));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const float4 r = del[i / 4];  // -delta
-            split(mul2(f2(p[i], p[i + 1]), add2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f2(r.x, r.y))), p[i], p[i + 1]);
-            split(mul2(f2(p[i + 2], p[i + 3]), add2(f2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), f2(r.z, r.w))),
-                  p[i + 2], p[i + 3]);
-          }
+        for (int i = 0; i < 64; i += 4) {
+          const float4 r = del[i / 4];  // -delta
+          split(mul2(f2(p[i], p[i + 1]), add2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f2(r.x, r.y))), p[i], p[i + 1]);
+          split(mul2(f2(p[i + 2], p[i + 3]), add2(f2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), f2(r.z, r.w))), p[i + 2],
+                p[i + 3]);
         }
         if (cut)
 #pragma unroll
@@ -365,11 +394,12 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(ds_full + half);
+      if (lane == 0) {
+        tc::mbar_arrive(ds_full + half);
+        tc::mbar_arrive(row_free + st);
+      }
     }
-    if (!ok) {
-      group_leave(half);
-    } else {
+    if (ok) {
       ok = tc::mbar_wait_warp(done, 0);
       tc::fence_after_sync();
       const bool in = ok && key < blk.len;
@@ -418,7 +448,6 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   uint64_t* ds_full = dp_free + 1;
   uint64_t* done = ds_full + 4;
   uint32_t* holder = reinterpret_cast<uint32_t*>(done + 1);
-  __shared__ float row_sum[2][128];  // the first block's delta, by column half
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int kvh = head / (a.Hq / a.Hkv);
@@ -549,7 +578,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     const bool in = row < blk.len;
     const size_t t = (size_t)blk.row0 + row;
     const float lse = in ? a.lse[(size_t)head * a.T + t] * -LOG2E : 0.f;
-    float del = in ? -a.delta[(size_t)head * a.T + t] : 0.f;
+    const float del = in ? -a.delta[(size_t)head * a.T + t] : 0.f;
     const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), lse2 = f2(lse, lse);
     const uint32_t tp = tmem + lanes + DP + half * 64;
     for (int it = 0; it < n; ++it) {
@@ -584,18 +613,6 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
         if (lane == 0) tc::mbar_arrive(dp_free);
         // the diagonal block holds the end of the sequence, too: it lies past every row
         const int see = it + 1 == n ? min(row, blk.len - 1) - it * 128 - half * 64 : 64;
-        if (n == 1) {  // all the keys that the row sees
-          float x = 0.f;
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i <= see) x = fmaf(p[i], __uint_as_float(u[i]), x);
-          if (both(0)) {
-            row_sum[half][(warp & 3) * 32 + lane] = x;
-            both_sync();
-            x = row_sum[0][(warp & 3) * 32 + lane] + row_sum[1][(warp & 3) * 32 + lane];
-          }
-          del = -x;
-        }
 #pragma unroll
         for (int i = 0; i < 64; i += 2)
           split(mul2(f2(p[i], p[i + 1]), add2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f2(del, del))), p[i], p[i + 1]);
@@ -613,9 +630,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(ds_full + 2 * half + st);
     }
-    if (!ok) {
-      both_leave();
-    } else {
+    if (ok) {
       ok = tc::mbar_wait_warp(done, 0);
       tc::fence_after_sync();
       const uint32_t tq = tmem + lanes + DQ + half * (D / 2);
@@ -637,8 +652,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     attn_packed_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                            const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                            const BwdArgs a, int n_dkv) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (tc::smem_u32(sm) & 1023u) {  // every thread sees the same
+    if (threadIdx.x == 0) atomicCAS(&g_error, 0, (int)DERR_CAPACITY);
+    tc::grid_dep_wait();
+    return;
+  }
   int b = blockIdx.x;
   if (b < n_dkv) {
     const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, b / a.Hkv);
@@ -653,11 +672,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int D>
-int backward(const CUtensorMap* m, const BwdArgs& a, const bf16* o, const bf16* d_o, float* delta, cudaStream_t s) {
+int backward(const CUtensorMap* m, const BwdArgs& a, const DeltaArgs& da, cudaStream_t s) {
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_packed_bwd_kernel<D>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
-  const long long threads = (long long)a.T * a.Hq * (D / 8);
-  launch_k(attn_delta_kernel<D>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, false, o, d_o, delta, a.T, a.Hq);
+  launch_k(attn_delta_kernel<D>, dim3((unsigned)max_blocks(a.n_seq, a.T, FEW), a.Hq), dim3(256), 0, s, false, da);
   if (int rc = op_launched("attention_packed delta")) return rc;
   const long long blocks = max_blocks(a.n_seq, a.T, 128);
   launch_k(attn_packed_bwd_kernel<D>, dim3((unsigned)(blocks * (a.Hkv + a.Hq))), dim3(THREADS), SMEM, s, true, m[0], m[1],
@@ -704,8 +722,9 @@ int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void
     return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
   float* delta = (float*)workspace;
   const BwdArgs a{cu_seqlens, lse, delta, (bf16*)dq, (bf16*)dk, (bf16*)dv, n_seq, T, Hq, Hkv, scale};
-  return d == 128 ? backward<128>(m, a, (const bf16*)o, (const bf16*)d_o, delta, s)
-                  : backward<64>(m, a, (const bf16*)o, (const bf16*)d_o, delta, s);
+  const DeltaArgs da{(const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)o, (const bf16*)d_o, ldq, ldk, ldv,
+                     cu_seqlens, lse, delta, n_seq, T, Hq, Hkv, scale};
+  return d == 128 ? backward<128>(m, a, da, s) : backward<64>(m, a, da, s);
 }
 
 }  // extern "C"
