@@ -447,7 +447,7 @@ cudaError_t take_attn_packed_error(int* out) {
 int attn_packed_check(int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk, long long ldv,
                       float scale) {
   if (n_seq < 0 || n_seq > (1 << 20) || T < 0 || T > (1 << 24) || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq > 1024 ||
-      (d != 64 && d != 128) || max_blocks(n_seq, T, 128) * (Hq + Hkv) > 0x7fffffffLL)
+      (d != 64 && d != 128) || ((long long)n_seq + T) * (Hq + Hkv) > 0x7fffffffLL)
     return op_fail(GOCR_EINVAL, "bad shape: %d sequences, T=%d Hq=%d Hkv=%d d=%d", n_seq, T, Hq, Hkv, d);
   const long long most = 1ll << 32;  // row pitch: 2^33 bytes, within a TMA stride
   if (ldq < (long long)Hq * d || ldk < (long long)Hkv * d || ldv < (long long)Hkv * d || (ldq | ldk | ldv) % 8 ||

@@ -47,23 +47,23 @@ static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 
 static __device__ int g_error;  // DevErr of a wait that gave up
 
+constexpr int FEW = 32;  // rows at the start of a sequence with delta from P and dP
+
 struct BwdArgs {
   const int* cu;
   const float* lse;
-  const float* delta;
+  const float* delta; const float* first;  // first: of the first FEW rows of a sequence
   bf16* dq; bf16* dk; bf16* dv;
   int n_seq, T, Hq, Hkv;
   float scale;
 };
-
-constexpr int FEW = 32;  // rows of a delta CTA; of a sequence's start with delta from P and dP
 
 struct DeltaArgs {
   const bf16* q; const bf16* k; const bf16* v; const bf16* o; const bf16* d_o;
   long long ldq, ldk, ldv;
   const int* cu;
   const float* lse;
-  float* delta;
+  float* delta; float* first;
   int n_seq, T, Hq, Hkv;
   float scale;
 };
@@ -78,35 +78,31 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
   return s;
 }
 
-// delta of 32 rows of a sequence and a q head.  Bound by reading o and do, D / 8
-// lanes to a row; the sequence's first CTA holds its rows of q, k, v and do in
-// shared memory and its lanes are keys.
+// delta, two kinds of CTA.  The first n_seq x Hq take the first 32 rows of a
+// sequence for a q head, with its rows of q, k, v and do in shared memory and
+// lanes of keys; the others take o and do as they lie (of every row, which
+// costs less than finding out which they are), D / 8 lanes to a (row, head).
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
   constexpr int L = D / 8, LD = L + 1;  // 16-byte pieces of a row; row pitch in shared memory
   __shared__ uint4 t[4][FEW][LD];       // q, k, do, v
-  const Block blk = find_block<false>(a.cu, a.n_seq, a.T, FEW, blockIdx.x);
   if (threadIdx.x == 0) tc::grid_dep_launch();
-  if (!blk.len) return;
-  const int head = blockIdx.y, n = min(FEW, blk.len - blk.at);
-  const size_t row0 = (size_t)blk.row0 + blk.at;
-  float* out = a.delta + (size_t)head * a.T + row0;
-  if (blk.at > 0) {
-    const int l = threadIdx.x % L;
+  const int firsts = a.n_seq * a.Hq;
+  if ((int)blockIdx.x >= firsts) {
+    const long long i = (long long)(blockIdx.x - firsts) * 256 + threadIdx.x;  // of a piece of o
+    const bool in = i < (long long)a.T * a.Hq * L;
+    float s = in ? dot8(reinterpret_cast<const uint4*>(a.o)[i], reinterpret_cast<const uint4*>(a.d_o)[i], 0.f) : 0.f;
 #pragma unroll
-    for (int r0 = 0; r0 < FEW; r0 += 256 / L) {
-      const int r = r0 + threadIdx.x / L;
-      float s = 0.f;
-      if (r < n) {
-        const size_t at = ((row0 + r) * a.Hq + head) * L + l;
-        s = dot8(reinterpret_cast<const uint4*>(a.o)[at], reinterpret_cast<const uint4*>(a.d_o)[at], 0.f);
-      }
-#pragma unroll
-      for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (r < n && l == 0) out[r] = s;
-    }
+    for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    const int r = (int)(i / L);
+    if (in && i % L == 0) a.delta[(size_t)(r % a.Hq) * a.T + r / a.Hq] = s;
     return;
   }
+  const int head = blockIdx.x % a.Hq, seq = blockIdx.x / a.Hq;
+  const int lo = min(max(a.cu[seq], 0), a.T), n = min(FEW, min(a.cu[seq + 1], a.T) - lo);
+  if (n <= 0) return;
+  const size_t row0 = lo;
+  float* out = a.first + (size_t)head * a.T + row0;
   const int kvh = head / (a.Hq / a.Hkv);
   for (int i = threadIdx.x; i < FEW * L; i += 256) {
     const int r = i / L, l = i % L;
@@ -249,7 +245,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
         const bool in = at + i < blk.len;
         const size_t src = (size_t)head * a.T + blk.row0 + at + i;
         lse[i] = in ? a.lse[src] * -LOG2E : 0.f;
-        lse[128 + i] = in ? -a.delta[src] : 0.f;
+        lse[128 + i] = in ? -(at + i < FEW ? a.first : a.delta)[src] : 0.f;
       }
       if (ragged) {
         ok = tc::mbar_wait_warp(q_full + qs, qp) && tc::mbar_wait_warp(do_full + st, ph);
@@ -578,7 +574,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     const bool in = row < blk.len;
     const size_t t = (size_t)blk.row0 + row;
     const float lse = in ? a.lse[(size_t)head * a.T + t] * -LOG2E : 0.f;
-    const float del = in ? -a.delta[(size_t)head * a.T + t] : 0.f;
+    const float del = in ? -(row < FEW ? a.first : a.delta)[(size_t)head * a.T + t] : 0.f;
     const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), lse2 = f2(lse, lse);
     const uint32_t tp = tmem + lanes + DP + half * 64;
     for (int it = 0; it < n; ++it) {
@@ -675,7 +671,8 @@ template <int D>
 int backward(const CUtensorMap* m, const BwdArgs& a, const DeltaArgs& da, cudaStream_t s) {
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_packed_bwd_kernel<D>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
-  launch_k(attn_delta_kernel<D>, dim3((unsigned)max_blocks(a.n_seq, a.T, FEW), a.Hq), dim3(256), 0, s, false, da);
+  const long long firsts = (long long)a.n_seq * a.Hq, threads = (long long)a.T * a.Hq * (D / 8);
+  launch_k(attn_delta_kernel<D>, dim3((unsigned)(firsts + (threads + 255) / 256)), dim3(256), 0, s, false, da);
   if (int rc = op_launched("attention_packed delta")) return rc;
   const long long blocks = max_blocks(a.n_seq, a.T, 128);
   launch_k(attn_packed_bwd_kernel<D>, dim3((unsigned)(blocks * (a.Hkv + a.Hq))), dim3(THREADS), SMEM, s, true, m[0], m[1],
@@ -698,7 +695,7 @@ extern "C" {
 
 size_t gocr_op_attention_packed_backward_workspace(int T, int Hq) {
   if (T < 0 || Hq < 1) return 0;
-  return (((size_t)T * Hq * 4 + 255) & ~(size_t)255) + 256;
+  return (size_t)T * Hq * 8 + 256;
 }
 
 int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void* k, const void* v, const void* o,
@@ -721,9 +718,10 @@ int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void
       !map_rows(&m[3], d_o, T, Hq, d, (long long)Hq * d))
     return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
   float* delta = (float*)workspace;
-  const BwdArgs a{cu_seqlens, lse, delta, (bf16*)dq, (bf16*)dk, (bf16*)dv, n_seq, T, Hq, Hkv, scale};
+  float* first = delta + (size_t)T * Hq;
+  const BwdArgs a{cu_seqlens, lse, delta, first, (bf16*)dq, (bf16*)dk, (bf16*)dv, n_seq, T, Hq, Hkv, scale};
   const DeltaArgs da{(const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)o, (const bf16*)d_o, ldq, ldk, ldv,
-                     cu_seqlens, lse, delta, n_seq, T, Hq, Hkv, scale};
+                     cu_seqlens, lse, delta, first, n_seq, T, Hq, Hkv, scale};
   return d == 128 ? backward<128>(m, a, da, s) : backward<64>(m, a, da, s);
 }
 
