@@ -241,3 +241,54 @@ def test_attention_packed_in_a_graph_and_on_a_stream(g):
         fresh = _run(g, q, k, v, do, cu)
         assert all(torch.equal(out[n], fresh[n]) for n in out), cut
     g.op_status()
+
+
+def test_attention_packed_rows_before_the_first_sequence(g):
+    """cu_seqlens may start behind row 0: the rows before it belong to no sequence either."""
+    lens, lead, Hq, Hkv, d = [70, 200], 33, 2, 1, 64
+    q, k, v, do, cu = _case(lens, Hq, Hkv, d, seed=13, pad=lead)
+    T = sum(lens) + lead
+    roll = lambda t: torch.cat([torch.full_like(t[:lead], math.nan), t[:T - lead]])
+    want = _run(g, q[:T - lead], k[:T - lead], v[:T - lead], do[:T - lead].contiguous(), cu)
+    q2, k2, v2, do2 = (roll(t) for t in (q, k, v, do))
+    o = torch.full_like(do2, 5.0)
+    lse = torch.full((Hq, T), 5.0, device="cuda")
+    g.op_attention_packed(q2, k2, v2, cu + lead, o=o, lse=lse)
+    mark = lambda h: torch.full((T, h, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    dq, dk, dv = g.op_attention_packed_backward(do2, q2, k2, v2, o, lse, cu + lead, dq=mark(Hq), dk=mark(Hkv), dv=mark(Hkv))
+    for name, got in dict(o=o, dq=dq, dk=dk, dv=dv).items():
+        assert (got[:lead] == 5.0).all() and torch.equal(got[lead:], want[name]), name
+    assert (lse[:, :lead] == 5.0).all() and torch.equal(lse[:, lead:], want["lse"])
+
+
+def test_attention_packed_many_mixes_repeat(g):
+    """Random mixes of short and long sequences, back to back: equal bits on every call and no wait given up."""
+    import random
+    rng = random.Random(3)
+    for i in range(24):
+        lens = [rng.choice([0, 1, 3, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 300, 500]) for _ in range(rng.randint(1, 40))]
+        if not sum(lens):
+            continue
+        Hkv = rng.randint(1, 4)
+        q, k, v, do, cu = _case(lens, Hkv * rng.randint(1, 3), Hkv, rng.choice([64, 128]), seed=100 + i)
+        first = _run(g, q, k, v, do, cu)
+        for _ in range(5):
+            again = _run(g, q, k, v, do, cu)
+            assert all(torch.equal(again[n], first[n]) for n in first), lens
+        g.op_status()
+
+
+def test_attention_packed_on_two_streams_at_once(g):
+    q, k, v, do, cu = _case([500, 300, 65], 6, 2, 128, seed=14)
+    q2, k2, v2, do2, cu2 = _case([64] * 20, 4, 4, 64, seed=15)
+    want, want2 = _run(g, q, k, v, do, cu), _run(g, q2, k2, v2, do2, cu2)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(s):
+            a = _run(g, q, k, v, do, cu)
+        with torch.cuda.stream(t):
+            b = _run(g, q2, k2, v2, do2, cu2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[n], want[n]) for n in want) and all(torch.equal(b[n], want2[n]) for n in want2)
+    g.op_status()
