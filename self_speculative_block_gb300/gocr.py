@@ -482,14 +482,15 @@ def op_attention(q, kc, vc, lim, dtype: int, lo2=None, hi2=None):
 
 def _want(name: str, t, shape: tuple, dtype, device):
     """Check one operand: a contiguous CUDA tensor of this shape, dtype and device."""
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other operands are on {device}")
+    raise ValueError(f"{name} is on {t.device}, the other operands are on {device}")
 
 
 def _lead(name: str, t, dims: int, *dtypes):
@@ -500,28 +501,20 @@ def _lead(name: str, t, dims: int, *dtypes):
         raise ValueError(f"{name} must be a tensor of {dims} dimensions, got {list(t.shape)}")
 
 
-class _On:
-    """The device's current stream; makes the device current where another one is."""
+def _on_cuda(device) -> None:
+    if device.type != "cuda":
+        raise ValueError(f"the operands must be CUDA tensors, got {device}")
 
-    __slots__ = ("index", "other")
 
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError(f"the operands must be CUDA tensors, got {device}")
-        self.index = device.index
-
-    def __enter__(self):
-        torch = _torch()
-        self.other = None
-        if torch.cuda.current_device() != self.index:
-            self.other = torch.cuda.device(self.index)
-            self.other.__enter__()
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
-        return raw(self.index) if raw is not None else torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
+def _launch(device, fn, *args) -> None:
+    """Call a C entry on the device's current stream, with the device current."""
+    torch = _torch()
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+    _check(fn(*args, raw(index) if raw is not None else torch.cuda.current_stream().cuda_stream))
 
 
 def _workspace(ws, need: int, device):
@@ -543,10 +536,10 @@ def op_embed(ids, embed, mask_embed=None, scale: float = 1.0):
     _want("ids", ids, (T,), torch.int32, dev)
     if mask_embed is not None:
         _want("mask_embed", mask_embed, (H,), embed.dtype, dev)
-    with _On(dev) as stream:
-        y = torch.empty((T, H), dtype=embed.dtype, device=dev)
-        _check(load().gocr_op_embed(_dt(embed), embed.data_ptr(), mask_embed.data_ptr() if mask_embed is not None else None,
-                                    ids.data_ptr(), y.data_ptr(), T, H, V, scale, stream))
+    _on_cuda(dev)
+    y = torch.empty((T, H), dtype=embed.dtype, device=dev)
+    _launch(dev, load().gocr_op_embed, _dt(embed), embed.data_ptr(), mask_embed.data_ptr() if mask_embed is not None
+            else None, ids.data_ptr(), y.data_ptr(), T, H, V, scale)
     return y
 
 
@@ -559,13 +552,12 @@ def op_embed_backward(dy, ids, vocab: int, scale: float = 1.0, mask: bool = Fals
     dev, (T, H) = dy.device, dy.shape
     _want("dy", dy, (T, H), dy.dtype, dev)
     _want("ids", ids, (T,), torch.int32, dev)
-    with _On(dev) as stream:
-        d_embed = torch.empty((vocab, H), dtype=dy.dtype, device=dev)
-        d_mask = torch.empty((H,), dtype=dy.dtype, device=dev) if mask else None
-        ws = _workspace(workspace, lib.gocr_op_embed_backward_workspace(T, H), dev)
-        _check(lib.gocr_op_embed_backward(_dt(dy), dy.data_ptr(), ids.data_ptr(), d_embed.data_ptr(),
-                                          d_mask.data_ptr() if mask else None, T, H, vocab, scale, ws.data_ptr(),
-                                          ws.numel(), stream))
+    _on_cuda(dev)
+    d_embed = torch.empty((vocab, H), dtype=dy.dtype, device=dev)
+    d_mask = torch.empty((H,), dtype=dy.dtype, device=dev) if mask else None
+    ws = _workspace(workspace, lib.gocr_op_embed_backward_workspace(T, H), dev)
+    _launch(dev, lib.gocr_op_embed_backward, _dt(dy), dy.data_ptr(), ids.data_ptr(), d_embed.data_ptr(),
+            d_mask.data_ptr() if mask else None, T, H, vocab, scale, ws.data_ptr(), ws.numel())
     return d_embed, d_mask
 
 
@@ -574,13 +566,14 @@ def _rows(name: str, t, T, heads, d, device):
     torch = _torch()
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{T}, {'*' if heads is None else heads}, {d}], got {list(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
-        raise ValueError(f"the heads of a row of {name} must be contiguous, got strides {t.stride()}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [{T}, {'*' if heads is None else heads}, {d}], got {list(shape)}")
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != d):
+        raise ValueError(f"the heads of a row of {name} must be contiguous, got strides {stride}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, q is on {device}")
-    return t.stride(0) if T > 1 else t.shape[1] * d
+    return stride[0] if T > 1 else shape[1] * d
 
 
 def _packed_args(q, k, v, cu_seqlens, scale):
@@ -606,17 +599,17 @@ def op_attention_packed(q, k, v, cu_seqlens, scale=None, o=None, lse=None):
     not written."""
     torch = _torch()
     dev, T, Hq, Hkv, d, sizes = _packed_args(q, k, v, cu_seqlens, scale)
-    with _On(dev) as stream:
-        if o is None:
-            o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _want("o", o, (T, Hq, d), torch.bfloat16, dev)
-        if lse is None:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
-        else:
-            _want("lse", lse, (Hq, T), torch.float32, dev)
-        _check(load().gocr_op_attention_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                               cu_seqlens.data_ptr(), *sizes, stream))
+    _on_cuda(dev)
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _want("o", o, (T, Hq, d), torch.bfloat16, dev)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _want("lse", lse, (Hq, T), torch.float32, dev)
+    _launch(dev, load().gocr_op_attention_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), cu_seqlens.data_ptr(), *sizes)
     return o, lse
 
 
@@ -631,18 +624,18 @@ def op_attention_packed_backward(do, q, k, v, o, lse, cu_seqlens, scale=None, wo
     _want("do", do, (T, Hq, d), torch.bfloat16, dev)
     _want("o", o, (T, Hq, d), torch.bfloat16, dev)
     _want("lse", lse, (Hq, T), torch.float32, dev)
-    with _On(dev) as stream:
-        out = []
-        for name, t, heads in (("dq", dq, Hq), ("dk", dk, Hkv), ("dv", dv, Hkv)):
-            if t is None:
-                t = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev)
-            else:
-                _want(name, t, (T, heads, d), torch.bfloat16, dev)
-            out.append(t)
-        ws = _workspace(workspace, lib.gocr_op_attention_packed_backward_workspace(T, Hq), dev)
-        _check(lib.gocr_op_attention_packed_backward(
-            do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(),
-            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), *sizes, ws.data_ptr(), ws.numel(), stream))
+    _on_cuda(dev)
+    out = []
+    for name, t, heads in (("dq", dq, Hq), ("dk", dk, Hkv), ("dv", dv, Hkv)):
+        if t is None:
+            t = torch.empty((T, heads, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _want(name, t, (T, heads, d), torch.bfloat16, dev)
+        out.append(t)
+    ws = _workspace(workspace, lib.gocr_op_attention_packed_backward_workspace(T, Hq), dev)
+    _launch(dev, lib.gocr_op_attention_packed_backward, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+            out[2].data_ptr(), *sizes, ws.data_ptr(), ws.numel())
     return tuple(out)
 
 
@@ -657,12 +650,12 @@ def op_linear_ce(x, w, labels, workspace=None):
     _want("x", x, (T, H), torch.bfloat16, dev)
     _want("w", w, (V, H), torch.bfloat16, dev)
     _want("labels", labels, (T,), torch.int32, dev)
-    with _On(dev) as stream:
-        loss = torch.empty((T,), dtype=torch.float32, device=dev)
-        lse = torch.empty((T,), dtype=torch.float32, device=dev)
-        ws = _workspace(workspace, lib.gocr_op_linear_ce_workspace(T, V), dev)
-        _check(lib.gocr_op_linear_ce(x.data_ptr(), w.data_ptr(), labels.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-                                     T, V, H, ws.data_ptr(), ws.numel(), stream))
+    _on_cuda(dev)
+    loss = torch.empty((T,), dtype=torch.float32, device=dev)
+    lse = torch.empty((T,), dtype=torch.float32, device=dev)
+    ws = _workspace(workspace, lib.gocr_op_linear_ce_workspace(T, V), dev)
+    _launch(dev, lib.gocr_op_linear_ce, x.data_ptr(), w.data_ptr(), labels.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+            T, V, H, ws.data_ptr(), ws.numel())
     return loss, lse
 
 
@@ -678,12 +671,11 @@ def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None):
     _want("labels", labels, (T,), torch.int32, dev)
     _want("dloss", dloss, (T,), torch.float32, dev)
     _want("lse", lse, (T,), torch.float32, dev)
-    with _On(dev) as stream:
-        dx, dw = torch.empty_like(x), torch.empty_like(w)
-        ws = _workspace(workspace, lib.gocr_op_linear_ce_backward_workspace(T, V, H), dev)
-        _check(lib.gocr_op_linear_ce_backward(dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
-                                              lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(),
-                                              ws.numel(), stream))
+    _on_cuda(dev)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = _workspace(workspace, lib.gocr_op_linear_ce_backward_workspace(T, V, H), dev)
+    _launch(dev, lib.gocr_op_linear_ce_backward, dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
+            lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(), ws.numel())
     return dx, dw
 
 
