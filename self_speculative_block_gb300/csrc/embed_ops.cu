@@ -4,28 +4,35 @@
 //   dE_v = s * sum of dy_t over id_t = v;  d[M] likewise
 //
 // Both are bound by memory: the forward call reads the distinct rows and
-// writes T rows, the backward call reads T rows of dy and writes the dense
-// V x H gradient, which is most of its bytes.  The sum of a row runs over the
+// writes T rows (10,240 rows of 1,536 bf16: 9.3 us, 5.5 TB/s), the backward
+// call reads T rows of dy and writes the dense V x H gradient, which is most of
+// its bytes.  The sum of a row runs over the
 // token's positions in increasing order, in fixed pieces, in fp32 and without
 // atomics, so the gradient's bits are the same on every call.
 //
-// Backward, three launches:
-//   sort  a cluster of SORT_CTAS CTAs sorts the positions by token (stable
+// Backward, three launches (times: 10,240 positions, a third [M], 65,536 x 1,536
+// bf16):
+//   sort  a cluster of SORT_CTAS CTAs sorts the positions by token: a stable
 //         radix sort, digits of at most 9 bits, counts exchanged over
-//         distributed shared memory), while the other CTAs of the launch write
-//         the zeros of the whole gradient by bulk copies: the sort's latency
-//         hides behind the launch's V x H writes;
-//   sum   a CTA takes PIECE sorted positions.  A run of equal tokens is summed
-//         and written by the piece in which it begins, unless it is longer
-//         than LONG: each piece then leaves an fp32 partial row of it;
+//         distributed shared memory.  17 us of latencies on 8 SMs, so the next
+//         launch starts beside it;
+//   sum   the launch's first CTAs write the zeros of the rows that no position
+//         names, by bulk copies, and wait for nothing.  The others wait for the
+//         sort; then a CTA takes PIECE sorted positions.  A run of equal tokens
+//         is summed and written by the piece in which it begins, unless it is
+//         longer than LONG: each piece then leaves an fp32 partial row of it.
+//         37 us for 232 MB, 6.2 TB/s;
 //   join  one CTA per (long run, 128 columns) adds up the partial rows, eight
-//         warps a share each.
+//         warps a share each: 12 us, one dependent read after the other.
+// With the zeros in the sort's launch the sum came after both: 72 us the two
+// directions together, 67 now.  Half the zeros beside the join: no gain.
 // A frequent token ([M] above all) is one long run, so no CTA ever walks more
 // than PIECE + LONG rows of dy.
 #include "../../include/gocr.h"
 #include "kernels.cuh"
 #include "tc.cuh"
 
+#include <algorithm>
 #include <cooperative_groups.h>
 
 using namespace gocr;
@@ -40,6 +47,7 @@ constexpr int MAX_DIGITS = 512;
 constexpr int PIECE = 16;
 constexpr int LONG = 16;
 constexpr int FILL_BYTES = 16384;  // one bulk copy of zeros
+constexpr int FILL_ROWS = 32768;   // most table rows of a CTA that writes zeros
 
 // 16 bytes of a row in fp32
 template <typename T> struct Vec;
@@ -113,39 +121,14 @@ struct SortArgs {
   int* key[2];   // [T] sorted keys; the last pass's output is key[1]
   int* pos[2];   // [T] positions in that order
   int T, V, mask, passes, digit_bits;
-  void* d_embed; size_t embed_bytes;  // zeroed by the launch's other CTAs (multiples of 16 bytes)
-  void* d_mask; size_t mask_bytes;
-  int* n_long;                        // zeroed: the long runs that the sum kernel lists
+  int* n_long;   // zeroed: the long runs that the sum kernel lists
 };
 
-// n bytes of zeros (a multiple of 16) at d, by the CTAs of the launch past the sort's.
-__device__ __forceinline__ void fill_zero(uint8_t* d, size_t n, const uint8_t* zeros) {
-  const size_t step = (size_t)(gridDim.x - SORT_CTAS) * FILL_BYTES;
-  for (size_t i = (size_t)(blockIdx.x - SORT_CTAS) * FILL_BYTES; i < n; i += step) {
-    const uint32_t b = (uint32_t)(n - i < FILL_BYTES ? n - i : FILL_BYTES);
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d + i), "r"(tc::smem_u32(zeros)), "r"(b)
-                 : "memory");
-  }
-}
-
 __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(SortArgs a) {
-  __shared__ __align__(16) int cnt[SORT_WARPS][MAX_DIGITS];  // keys of (warp, digit), then the warp's next place
+  __shared__ int cnt[SORT_WARPS][MAX_DIGITS];  // keys of (warp, digit), then the warp's next place
   __shared__ int cta_cnt[MAX_DIGITS];
   __shared__ int scan[MAX_DIGITS];
-  static_assert(sizeof(cnt) >= FILL_BYTES, "the zeros' source");
-  if (blockIdx.x >= SORT_CTAS) {  // whole clusters
-    uint4* z = reinterpret_cast<uint4*>(&cnt[0][0]);
-    for (int i = threadIdx.x; i < FILL_BYTES / 16; i += SORT_THREADS) z[i] = make_uint4(0, 0, 0, 0);
-    tc::fence_proxy_async_smem();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      fill_zero(reinterpret_cast<uint8_t*>(a.d_embed), a.embed_bytes, reinterpret_cast<const uint8_t*>(z));
-      if (a.d_mask) fill_zero(reinterpret_cast<uint8_t*>(a.d_mask), a.mask_bytes, reinterpret_cast<const uint8_t*>(z));
-      tc::bulk_commit();
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
-    return;
-  }
+  if (threadIdx.x == 0) tc::grid_dep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_long = 0;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
@@ -232,6 +215,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(SortArgs a) {
 
 struct SumArgs {
   const void* dy;
+  const int* ids;
   const int* key;
   const int* pos;
   void* d_embed;
@@ -241,11 +225,71 @@ struct SumArgs {
   int* run;      // [n_long] the pieces in which a long run begins
   int T, H, V;
   float scale;
+  int fill, fill_rows;  // the sum launch's CTAs that write zeros, table rows of each
+  int pieces;
 };
 
 template <typename T>
 __device__ __forceinline__ T* grad_row(const SumArgs& a, int key) {
   return key < a.V ? reinterpret_cast<T*>(a.d_embed) + (size_t)key * a.H : reinterpret_cast<T*>(a.d_mask);
+}
+
+// n bytes of zeros (a multiple of 16) at d.
+__device__ __forceinline__ void fill_zero(uint8_t* d, size_t n, uint32_t zeros) {
+  for (size_t i = 0; i < n; i += FILL_BYTES) {
+    const uint32_t b = (uint32_t)(n - i < FILL_BYTES ? n - i : FILL_BYTES);
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d + i), "r"(zeros), "r"(b) : "memory");
+  }
+}
+
+// Zeros for the rows of the table's share blockIdx.x that no position names, and with
+// share 0 for the [M] row if none names it.  Nothing here waits for the sort: the CTA
+// notes the named rows of its share from the positions' tokens themselves.
+template <typename T>
+__device__ __forceinline__ void fill_unnamed(const SumArgs& a) {
+  __shared__ __align__(16) uint4 zeros[FILL_BYTES / 16];
+  __shared__ unsigned named[FILL_ROWS / 32];
+  __shared__ int mask_named;
+  const int row0 = blockIdx.x * a.fill_rows, rows = min(a.fill_rows, a.V - row0);
+  for (int i = threadIdx.x; i < FILL_BYTES / 16; i += blockDim.x) zeros[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) named[i] = 0;
+  if (threadIdx.x == 0) mask_named = 0;
+  tc::fence_proxy_async_smem();
+  __syncthreads();
+  auto note = [&](int id) {
+    const unsigned r = (unsigned)id - (unsigned)row0;
+    if (r < (unsigned)rows) atomicOr(&named[r >> 5], 1u << (r & 31));
+    if (id == TOK_MASK) mask_named = 1;
+  };
+  // four tokens a load, between the first 16-byte boundary and the last
+  const int head = min(a.T, (int)((16 - ((uintptr_t)a.ids & 15)) & 15) / 4), quads = (a.T - head) / 4;
+  const int4* q = reinterpret_cast<const int4*>(a.ids + head);
+#pragma unroll 8
+  for (int i = threadIdx.x; i < quads; i += blockDim.x) {
+    const int4 v = q[i];
+    note(v.x);
+    note(v.y);
+    note(v.z);
+    note(v.w);
+  }
+  for (int i = threadIdx.x; i < a.T - 4 * quads; i += blockDim.x) note(a.ids[i < head ? i : 4 * quads + i]);
+  __syncthreads();
+  const size_t row_bytes = (size_t)a.H * sizeof(T);
+  const uint32_t z = tc::smem_u32(zeros);
+  uint8_t* d = reinterpret_cast<uint8_t*>(a.d_embed) + (size_t)row0 * row_bytes;
+  for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) {
+    unsigned left = ~named[i];
+    if (rows - 32 * i < 32) left &= (1u << (rows - 32 * i)) - 1u;
+    while (left) {  // a run of unnamed rows
+      const int at = __ffs(left) - 1, len = __ffs(~(left >> at)) ? __ffs(~(left >> at)) - 1 : 32;
+      fill_zero(d + (size_t)(32 * i + at) * row_bytes, len * row_bytes, z);
+      left &= len < 32 ? ~(((1u << len) - 1u) << at) : 0u;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.d_mask && !mask_named)
+    fill_zero(reinterpret_cast<uint8_t*>(a.d_mask), row_bytes, z);
+  tc::bulk_commit();
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Rows of dy fetched at a time by a thread.
@@ -259,9 +303,11 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   __shared__ int poss[PIECE + LONG];        // of positions b ..
   __shared__ int edge[4];  // the runs of the piece's first and last position: first position, and past the last
   if (threadIdx.x == 0) tc::grid_dep_launch();
+  if (blockIdx.x < a.fill) return fill_unnamed<T>(a);
+  const int piece = (blockIdx.x - a.fill) % a.pieces, part = (blockIdx.x - a.fill) / a.pieces;
   if (threadIdx.x < 4) edge[threadIdx.x] = threadIdx.x & 1 ? PIECE + LONG + 1 : -LONG;
   tc::grid_dep_wait();
-  const int b = blockIdx.x * PIECE, n = min(PIECE, a.T - b);
+  const int b = piece * PIECE, n = min(PIECE, a.T - b);
   for (int i = threadIdx.x; i < WIN + 1; i += blockDim.x) {
     const int at = b - LONG + i;
     keys[i] = at >= 0 && at < a.T ? a.key[at] : -1;
@@ -292,9 +338,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   int end = n;  // the last run that begins here is summed to its end, unless it is long
   if (first < n && edge[3] > n) {
     if (edge[3] - edge[2] <= LONG) end = edge[3];
-    else if (blockIdx.y == 0 && threadIdx.x == 0 && k0[n - 1] <= a.V) a.run[atomicAdd(a.n_long, 1)] = blockIdx.x;
+    else if (part == 0 && threadIdx.x == 0 && k0[n - 1] <= a.V) a.run[atomicAdd(a.n_long, 1)] = piece;
   }
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
+  const int c = (part * blockDim.x + threadIdx.x) * N;
   if (c >= a.H) return;
   const T* dy = reinterpret_cast<const T*>(a.dy) + c;
   float acc[N];
@@ -319,7 +365,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
       if (goes_on && i + 1 < end) continue;
       const bool comes_in = in && i < n && k == k0[-1];
       if (comes_in || goes_on) {
-        float* p = a.part + ((size_t)blockIdx.x * 2 + (comes_in ? 0 : 1)) * a.H + c;
+        float* p = a.part + ((size_t)piece * 2 + (comes_in ? 0 : 1)) * a.H + c;
 #pragma unroll
         for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
       } else {
@@ -341,7 +387,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a) {
   __shared__ int s_last;
   tc::grid_dep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pieces = (a.T + PIECE - 1) / PIECE, n = *a.n_long;
+  const int pieces = a.pieces, n = *a.n_long;
   const int c = blockIdx.y * 128 + lane * 4;
   for (int r = blockIdx.x; r < n; r += gridDim.x) {
     const int first = a.run[r];
@@ -397,32 +443,35 @@ int check_shape(int dtype, int T, int H, int V) {
 }
 
 template <typename T>
-int embed_backward(const SortArgs& so, const SumArgs& su, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  // the clusters past the first write zeros, two CTAs per SM at most
-  const size_t fill = (so.embed_bytes + FILL_BYTES - 1) / FILL_BYTES;
-  const size_t most = 2 * SM_COUNT - SORT_CTAS;
-  const unsigned ctas = (unsigned)(fill < most ? fill : most);
-  cfg.gridDim = dim3(SORT_CTAS + (ctas + SORT_CTAS - 1) / SORT_CTAS * SORT_CTAS);
-  cfg.blockDim = dim3(SORT_THREADS);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = SORT_CTAS;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, embed_sort_kernel, so);
-  if (int rc = op_launched("embedding sort")) return rc;
-  if (!su.T) return GOCR_OK;
-  const unsigned pieces = (unsigned)((su.T + PIECE - 1) / PIECE);
+int embed_backward(const SortArgs& so, SumArgs su, cudaStream_t s) {
+  if (su.T) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(SORT_CTAS);
+    cfg.blockDim = dim3(SORT_THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = SORT_CTAS;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, embed_sort_kernel, so);
+    if (int rc = op_launched("embedding sort")) return rc;
+  }
+  // two CTAs per SM write the zeros, fewer for a small table, more for one
+  // whose shares would be longer than FILL_ROWS
+  const size_t bytes = (size_t)su.V * su.H * sizeof(T);
+  const int want = (int)std::min<size_t>((bytes + FILL_BYTES - 1) / FILL_BYTES, 2 * SM_COUNT);
+  su.fill_rows = std::min(FILL_ROWS, (su.V + want - 1) / want);
+  su.fill = (su.V + su.fill_rows - 1) / su.fill_rows;
+  su.pieces = (su.T + PIECE - 1) / PIECE;
   const int vecs = su.H / Vec<T>::N;
-  const int th = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
-  launch_k(embed_sum_kernel<T>, dim3(pieces, (vecs + th - 1) / th), dim3(th), 0, s, true, su);
+  const int th = std::max(128, std::min(256, (vecs + 31) / 32 * 32));
+  const unsigned parts = (unsigned)((vecs + th - 1) / th);
+  launch_k(embed_sum_kernel<T>, dim3(su.fill + su.pieces * parts), dim3(th), 0, s, su.T > 0, su);
   if (int rc = op_launched("embedding sum")) return rc;
   if (su.T > LONG) {
-    const unsigned runs = (unsigned)(su.T / LONG < 64 ? su.T / LONG : 64);
-    launch_k(embed_join_kernel<T>, dim3(runs, (su.H + 127) / 128), dim3(256), 0, s, true, su);
+    launch_k(embed_join_kernel<T>, dim3(std::min(su.T / LONG, 64), (su.H + 127) / 128), dim3(256), 0, s, true, su);
     return op_launched("embedding join");
   }
   return GOCR_OK;
@@ -464,7 +513,6 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
   if (workspace_bytes < gocr_op_embed_backward_workspace(T, H)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
-  const size_t es = dtype == GOCR_DTYPE_BF16 ? 2 : 4;
   SortArgs so{};
   char* ws = (char*)workspace;
   const size_t arr = up256((size_t)T * 4);
@@ -478,12 +526,10 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
   while ((1ll << bits) < (long long)V + 2) ++bits;
   so.passes = (bits + 8) / 9;
   so.digit_bits = (bits + so.passes - 1) / so.passes;
-  so.d_embed = d_embed; so.embed_bytes = (size_t)V * H * es;
-  so.d_mask = d_mask; so.mask_bytes = (size_t)H * es;
   float* part = (float*)(ws + 4 * arr);
   int* n_long = (int*)(part + (size_t)((T + PIECE - 1) / PIECE) * 2 * H);
   so.n_long = n_long;
-  SumArgs su{dy, so.key[1], so.pos[1], d_embed, d_mask, part, n_long, n_long + 1, T, H, V, scale};
+  SumArgs su{dy, ids, so.key[1], so.pos[1], d_embed, d_mask, part, n_long, n_long + 1, T, H, V, scale, 0, 0, 0};
   return dtype == GOCR_DTYPE_BF16 ? embed_backward<bf16>(so, su, s) : embed_backward<float>(so, su, s);
 }
 
