@@ -101,13 +101,13 @@ struct Args {
 struct Tile {
   int prod;             // PROD: 0 dx, 1 dw
   int m0, n0, k0, ks;   // first row, column, K step; K steps
-  int half;             // 128 columns of B instead of 256
+  int cols;             // columns of B: 256, or fewer
   int row_out, add;     // dx: first row in the slabs; add to them
 };
 
 // The pair's i-th tile; false past the last one.
 template <int KIND> __device__ __forceinline__ bool tile_of(const Args& a, int pair, int i, Tile& t) {
-  t.prod = 0; t.k0 = 0; t.row_out = 0; t.half = 0; t.add = 0;
+  t.prod = 0; t.k0 = 0; t.row_out = 0; t.add = 0;
   if (KIND != PROD) {
     // rows fastest: the pairs of a wave share a few tiles of w
     const int x = pair + i * PAIRS;
@@ -115,7 +115,7 @@ template <int KIND> __device__ __forceinline__ bool tile_of(const Args& a, int p
     t.m0 = (x % a.m_tiles) * TM;
     t.n0 = (x / a.m_tiles) * a.tn;
     t.ks = (a.H + TK - 1) / TK;
-    t.half = a.tn == RN;
+    t.cols = a.tn;
     return true;
   }
   const Deal& d = a.deal;
@@ -140,7 +140,7 @@ template <int KIND> __device__ __forceinline__ bool tile_of(const Args& a, int p
     t.n0 = (x % a.n_tiles) * TN;
     t.ks = (a.T + TK - 1) / TK;
   }
-  t.half = a.H - t.n0 <= RN;
+  t.cols = a.H - t.n0 <= RN ? RN : TN;
   return true;
 }
 
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
   const int a_bytes = a.a_rows * 128;
-  const int stage_bytes = a_bytes + (KIND != PROD && a.tn == RN ? BOX : B_BYTES);
+  const int stage_bytes = a_bytes + (KIND != PROD ? a.tn / 2 * 128 : B_BYTES);
 
   if (tid == 0) {
     tc::grid_dep_launch();
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
       // few rows: the odd CTA has none; what its part of A then holds only
       // reaches accumulator rows that nobody reads
       const bool with_a = KIND == PROD || a.a_rows == RM || rank == 0;
-      const uint32_t bytes = 2 * (t.half ? BOX : B_BYTES) + (KIND == PROD || a.a_rows == RM ? 2 * A_BYTES : a_bytes);
-      const int m = t.m0 + rank * RM, n = t.n0 + rank * (t.half ? 64 : RN);
+      const uint32_t bytes = t.cols * 128 + (KIND == PROD || a.a_rows == RM ? 2 * A_BYTES : a_bytes);
+      const int m = t.m0 + rank * RM, n = t.n0 + rank * (t.cols / 2);
       for (int k = 0; k < t.ks; ++k) {
         if (!(ok = tc::mbar_wait_warp(empty + st, ph ^ 1))) break;
         uint8_t* sa = sm + st * stage_bytes;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             const CUtensorMap* mb = t.prod ? &maps.b1 : &maps.b0;
             const int row = t.prod ? kk : a.v0 + kk;
             tc::tma_load_2d_pair(sb, mb, n, row, bar);
-            if (!t.half) tc::tma_load_2d_pair(sb + BOX, mb, n + 64, row, bar);
+            if (t.cols > RN) tc::tma_load_2d_pair(sb + BOX, mb, n + 64, row, bar);
           }
         }
         __syncwarp();
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
       if (!(ok = tc::mbar_wait_warp(acc_free + acc, aph ^ 1))) break;
       tc::fence_after_sync();
       const uint32_t d = tmem + acc * TN;
-      uint32_t idesc = tc::idesc_bf16(TM, t.half ? RN : TN);
+      uint32_t idesc = tc::idesc_bf16(TM, t.cols);
       if (KIND == PROD) idesc |= tc::IDESC_B_MN | (t.prod ? tc::IDESC_A_MN : 0u);
       for (int k = 0; k < t.ks; ++k) {
         if (!(ok = tc::mbar_wait_warp(full + st, ph))) break;
@@ -583,17 +583,25 @@ int check_shape(int T, int V, int H) {
   return GOCR_OK;
 }
 
-// Columns of a tile of the z products: 128 where tiles of 256 would leave half
-// the pairs without one (193 rows x 8,191 x 512: 66 -> 53 us with the gradient),
-// else 256.  An MMA of 128 columns takes nearly the time of one of 256: 33 rows
-// x 65,536 x 1,536 took 57 us with tiles of 128, 43 with 256.
-int z_columns(int T, int vc) { return 2LL * cdiv(T, TM) * cdiv(vc, TN) <= PAIRS ? RN : TN; }
+// Columns of a tile of the z products, a multiple of `step`: as many as 256
+// would take rounds of the pairs, but no more than fill them (33 rows x 65,536 x
+// 1,536: 256 tiles of 256 columns are four rounds of 76 pairs, the last a third
+// full; with 224 all four are full).  At least 128: an MMA of 128 columns takes
+// nearly the time of one of 256.
+int z_columns(int T, int vc, int step) {
+  const int m = cdiv(T < 1 ? 1 : T, TM);
+  const long long rounds = ((long long)m * cdiv(vc, TN) + PAIRS - 1) / PAIRS;
+  const int n = (int)(rounds * PAIRS / m);  // tiles a row of tiles may have
+  const int c = cdiv(cdiv(vc, n), step) * step;
+  return c < RN ? RN : c;
+}
+constexpr int STATS_STEP = 32, GRAD_STEP = 64;  // columns that an epilogue step takes
 
 // Few rows: only those that there are are staged, so that the ring holds more
 // of w, whose reading bounds the call.
 void set_ring(Args& a, bool z) {
   a.a_rows = z && a.T < RM ? cdiv(a.T, 8) * 8 : RM;
-  const int stage = a.a_rows * 128 + (z && a.tn == RN ? BOX : B_BYTES);
+  const int stage = a.a_rows * 128 + (z ? a.tn / 2 * 128 : B_BYTES);
   const int n = RING / stage;
   a.stages = n < MAX_STAGES ? n : MAX_STAGES;
 }
@@ -635,7 +643,7 @@ extern "C" {
 
 size_t gocr_op_linear_ce_workspace(int T, int V) {
   if (T < 0 || V < 1) return 0;
-  return up256((size_t)T * cdiv(V, z_columns(T, V)) * 8) + 256;
+  return up256((size_t)T * cdiv(V, z_columns(T, V, STATS_STEP)) * 8) + 256;
 }
 
 int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,
@@ -651,7 +659,7 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
   Args a{};
   a.T = T; a.H = H; a.V = V;
   a.labels = labels;
-  a.tn = z_columns(T, V);
+  a.tn = z_columns(T, V, STATS_STEP);
   set_ring(a, true);
   a.m_tiles = cdiv(T, TM); a.n_tiles = cdiv(V, a.tn);
   a.tiles = a.m_tiles * a.n_tiles;
@@ -689,7 +697,7 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
   Args common{};
   common.T = T; common.H = H; common.V = V;
   common.labels = labels; common.lse = lse; common.dloss = dloss;
-  common.tn = z_columns(T, p.piece);
+  common.tn = z_columns(T, p.piece, GRAD_STEP);
   set_ring(common, true);
   if (!map2(&z.a0, x, T, H, H, common.a_rows) || !map2(&z.b0, w, V, H, H, common.tn / 2) || !map2(&pr.b0, w, V, H, H, 64) ||
       !map2(&pr.b1, x, T, H, H, 64) || !map2(&pr.out1, dw, V, H, H, 32))

@@ -176,6 +176,12 @@ def test_linear_ce_and_gradient(g, T, V, H):
     g.op_status()
 
 
+@pytest.mark.parametrize("T,V,H", [(33, 19457, 64), (40, 25001, 72), (200, 30001, 136), (600, 7000, 264)])
+def test_linear_ce_vocabularies_of_a_round_and_a_bit(g, T, V, H):
+    """Vocabularies just past what one round of full tiles covers: narrower tiles, of 160 to 256 columns."""
+    test_linear_ce_and_gradient(g, T, V, H)
+
+
 def test_linear_ce_in_several_pieces(g):
     """More columns than one piece of the vocabulary holds, and a ragged last piece."""
     T, V, H = 5000, 12 * 1024 + 77, 128
