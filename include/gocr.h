@@ -367,14 +367,15 @@ int gocr_three_stream_ranges(int P, int N, int B, int32_t* lim, int32_t* lo2, in
 /* y[T, H] = scale * row(ids[t]), rounded once to dtype: row(id) is embed[id]
  * for 0 <= id < V, mask_embed for id = -1 (the [M] row; zero when mask_embed
  * is NULL), and zero for every other id (padding).  embed [V, H], mask_embed
- * [H] and y in dtype, ids int32[T] (device).  H % 8 == 0. */
+ * [H] and y in dtype, ids int32[T] (device).  H % 8 == 0, H <= 2^20, T and
+ * V <= 2^28. */
 int gocr_op_embed(int dtype, const void* embed, const void* mask_embed, const int32_t* ids, void* y, int T, int H,
                   int V, float scale, void* stream);
 
 /* Gradient of gocr_op_embed: d_embed[V, H] (dense: rows of tokens that do not
  * occur are zero) and d_mask[H] (NULL: not wanted) from dy[T, H], all in
- * dtype.  Positions are sorted by token; a row's sum runs over its positions
- * in increasing order in pieces of 16, in fp32, and is rounded once. */
+ * dtype.  Positions are sorted by token; a row's sum is in fp32, in an order
+ * that follows from ids alone, and is rounded once. */
 size_t gocr_op_embed_backward_workspace(int T, int H);
 int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* d_embed, void* d_mask, int T, int H,
                            int V, float scale, void* workspace, size_t workspace_bytes, void* stream);
@@ -387,10 +388,11 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
  * rows ldq elements apart, k and v [T, Hkv, d] with rows ldk and ldv apart (so
  * the three may be column ranges of one fused projection; pitches % 8 == 0);
  * o [T, Hq, d] bf16 and lse [Hq, T] fp32 dense.  d 64 or 128, Hq % Hkv == 0,
- * scale > 0.  Rows that belong to no sequence are not read into any result,
- * whatever they hold, and their o and lse are left as they were; nothing of
- * one sequence reaches another, non-finite values included.  Within a
- * sequence, a non-finite v or do may reach the other rows of its block of 128. */
+ * scale > 0, Hq <= 1024, n_seq <= 2^20, T <= 2^24.  Rows that belong to no
+ * sequence are not read into any result, whatever they hold, and their o and
+ * lse are left as they were; nothing of one sequence reaches another,
+ * non-finite values included.  Within a sequence, a non-finite v or do may
+ * reach the other rows of its block of 128. */
 int gocr_op_attention_packed(const void* q, const void* k, const void* v, void* o, float* lse,
                              const int32_t* cu_seqlens, int n_seq, int T, int Hq, int Hkv, int d, long long ldq,
                              long long ldk, long long ldv, float scale, void* stream);
@@ -410,7 +412,7 @@ int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void
  * in bf16 (fp32 sums), lse[t] = log sum_v exp z[t, v], loss[t] = lse[t] -
  * z[t, labels[t]].  A label outside 0..V-1 marks a row without a target: its
  * loss is zero (lse is written all the same).  The logits are not stored.  H %
- * 8 == 0, any V. */
+ * 8 == 0, H <= 2^15, T and V <= 2^22. */
 size_t gocr_op_linear_ce_workspace(int T, int V);
 int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,
                       int H, void* workspace, size_t workspace_bytes, void* stream);

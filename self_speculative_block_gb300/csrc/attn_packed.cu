@@ -10,13 +10,20 @@
 // a row: its 64 scores come from its own tensor memory lane, so the running
 // maximum and sum need no exchange.
 //
-// What bounds it: a 128 x 128 block takes 1,024 cycles of exponentials on the
-// special-function unit (16 a cycle and SM) and 1,024 of products, and the chain
-// S, softmax, P, O of a block is as long as both.  Two tiles alone left a third
-// of the cycles idle (3,250 for two blocks of 128 keys); with two S buffers a
-// tile, a tile's next scores are ready when its softmax is, at the price of
-// 64-column score products (49 instead of 32 cycles each: A is read again for
-// half the columns).
+// What bounds it: the products of a tile with 64 keys take 646 cycles of the
+// tensor pipe (score MMAs of 64 columns read A again for half the columns: 49
+// cycles instead of 32), its softmax 620 of four warps, and the chain scores,
+// softmax, P V is as long as both.  128 keys of both tiles pass in 3,270 cycles,
+// 2,586 of them products.  With one score buffer a tile and blocks of 128 keys
+// the tiles waited for one another; with two buffers a tile's next scores are
+// ready when its softmax is.  Each tile has an MMA warp, because a warp's wait
+// on a barrier costs 100 cycles and more behind its own queue of MMAs, a time
+// that the other warp's MMAs fill.  12 heads of 128: one sequence of 8,192 in
+// 180 us (1.15 PFLOP/s), 16 prompts of 25 to 1,200 in 45, 18 regions of 1 to 140
+// in 17, where a launch's fixed chain (sequence search, loads, one block, store)
+// is most of it.  Measured slower: part of the exponentials as polynomials on
+// the FMA pipe, P given over in halves, sixteen softmax warps (two threads a
+// row), one MMA warp, score MMAs of 128 columns with 208 registers a thread.
 //
 // O stays in tensor memory and is rescaled only when a row's maximum grows by
 // more than 2^8 over the one its exponentials refer to (the sum and O use the
