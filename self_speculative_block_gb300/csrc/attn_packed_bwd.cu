@@ -29,8 +29,7 @@
 // 95 to 1,203 take 111 us, 46 at the long one's rate; the rest goes to blocks on
 // the diagonal, ragged ones, and CTAs that start and finish.  Measured slower:
 // groups that run ahead of one another on products of 64 columns (541 to 667 us
-// for the long one), one MMA warp (541).  delta's pass reads o and do once, 13.5
-// us for 8,192 rows.
+// for the long one), one MMA warp (541).
 //
 // delta from o takes o's rounding to bf16 into every dS of the row.  That
 // matters where a row sees few keys (o is then large), so for the first 32 rows
@@ -58,6 +57,7 @@ static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 
 static __device__ int g_error;  // DevErr of a wait that gave up
 
+constexpr int FLAT = 4;  // 16-byte pieces of o and of do in flight a thread
 constexpr int FEW = 32;  // rows at the start of a sequence with delta from P and dP
 
 struct BwdArgs {
@@ -93,6 +93,8 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
 // sequence for a q head, with its rows of q, k, v and do in shared memory and
 // lanes of keys; the others take o and do as they lie (of every row, which
 // costs less than finding out which they are), D / 8 lanes to a (row, head).
+// 8,192 rows x 12 heads: 13 us, 101 MB half of which the forward call left in L2;
+// with 15 sequences 15 us, the first rows' chains beside it.
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
   constexpr int L = D / 8, LD = L + 1;  // 16-byte pieces of a row; row pitch in shared memory
@@ -100,13 +102,25 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
   if (threadIdx.x == 0) tc::grid_dep_launch();
   const int firsts = a.n_seq * a.Hq;
   if ((int)blockIdx.x >= firsts) {
-    const long long i = (long long)(blockIdx.x - firsts) * 256 + threadIdx.x;  // of a piece of o
-    const bool in = i < (long long)a.T * a.Hq * L;
-    float s = in ? dot8(reinterpret_cast<const uint4*>(a.o)[i], reinterpret_cast<const uint4*>(a.d_o)[i], 0.f) : 0.f;
+    const long long i0 = (long long)(blockIdx.x - firsts) * (256 * FLAT) + threadIdx.x;  // of a piece of o
+    const long long n = (long long)a.T * a.Hq * L;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    uint4 x[FLAT], y[FLAT];
 #pragma unroll
-    for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    const int r = (int)(i / L);
-    if (in && i % L == 0) a.delta[(size_t)(r % a.Hq) * a.T + r / a.Hq] = s;
+    for (int u = 0; u < FLAT; ++u) {
+      const long long i = i0 + u * 256;
+      x[u] = i < n ? reinterpret_cast<const uint4*>(a.o)[i] : z;
+      y[u] = i < n ? reinterpret_cast<const uint4*>(a.d_o)[i] : z;
+    }
+#pragma unroll
+    for (int u = 0; u < FLAT; ++u) {
+      const long long i = i0 + u * 256;
+      float s = dot8(x[u], y[u], 0.f);
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      const int r = (int)(i / L);
+      if (i < n && i % L == 0) a.delta[(size_t)(r % a.Hq) * a.T + r / a.Hq] = s;
+    }
     return;
   }
   const int head = blockIdx.x % a.Hq, seq = blockIdx.x / a.Hq;
@@ -220,7 +234,6 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
   tc::fence_after_sync();
   // all 512 columns, which start at 0: a constant keeps the MMAs' operands in uniform registers
   constexpr uint32_t tmem = 0;
-  tc::grid_dep_wait();  // delta
   constexpr uint32_t DP = 128, DV = 256, DK = 256 + D;  // S^T at 0
   bool ok = true;
 
@@ -251,6 +264,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       __syncwarp();
       // the stage's rows were last read for the block two back
       if (it > 1 && !(ok = tc::mbar_wait_warp(row_free + st, ph ^ 1))) break;
+      if (it == 0) tc::grid_dep_wait();  // for delta; nothing else here is that launch's
       float* lse = rows + st * 256;
       for (int i = lane; i < 128; i += 32) {
         const bool in = at + i < blk.len;
@@ -489,7 +503,6 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
   tc::fence_after_sync();
   // all 512 columns, which start at 0: a constant keeps the MMAs' operands in uniform registers
   constexpr uint32_t tmem = 0;
-  tc::grid_dep_wait();  // delta
   constexpr uint32_t DP = 256, DQ = 384;  // S at 0 and 128
   bool ok = true;
 
@@ -585,6 +598,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     const bool in = row < blk.len;
     const size_t t = (size_t)blk.row0 + row;
     const float lse = in ? a.lse[(size_t)head * a.T + t] * -LOG2E : 0.f;
+    tc::grid_dep_wait();  // for delta; nothing else here is that launch's
     const float del = in ? -(row < FEW ? a.first : a.delta)[(size_t)head * a.T + t] : 0.f;
     const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), lse2 = f2(lse, lse);
     const uint32_t tp = tmem + lanes + DP + half * 64;
@@ -683,7 +697,7 @@ int backward(const CUtensorMap* m, const BwdArgs& a, const DeltaArgs& da, cudaSt
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_packed_bwd_kernel<D>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
   const long long firsts = (long long)a.n_seq * a.Hq, threads = (long long)a.T * a.Hq * (D / 8);
-  launch_k(attn_delta_kernel<D>, dim3((unsigned)(firsts + (threads + 255) / 256)), dim3(256), 0, s, false, da);
+  launch_k(attn_delta_kernel<D>, dim3((unsigned)(firsts + (threads + 256 * FLAT - 1) / (256 * FLAT))), dim3(256), 0, s, false, da);
   if (int rc = op_launched("attention_packed delta")) return rc;
   const long long blocks = max_blocks(a.n_seq, a.T, 128);
   launch_k(attn_packed_bwd_kernel<D>, dim3((unsigned)(blocks * (a.Hkv + a.Hq))), dim3(THREADS), SMEM, s, true, m[0], m[1],
