@@ -34,6 +34,12 @@
         second-interval attention (attention_part_kernel then
         attention_merge_kernel each), the shapes bench.py times.
 
+    python -m self_speculative_block_gb300.profile_cases train_ops
+        The training and scoring operators with their gradients at the
+        0.5B-class decoder's sizes, twice each: the embedding of 10,240 tokens
+        (a third [M]), causal attention over 15 packed sequences and over one
+        of 8,192 rows, the cross entropy of 2,048 rows.
+
 All hold a few GB on the device.  The sweep's shapes and inputs are the ones
 bench.py times for its kernel roofline.
 """
@@ -157,6 +163,41 @@ def train_mask_case():
     torch.cuda.synchronize()
 
 
+def train_ops_case(repeat: int = 2):
+    import torch
+    from . import gocr
+    cfg, dev = synth.BASE, torch.device("cuda:0")
+    g = torch.Generator(device=dev)
+    g.manual_seed(0)
+
+    def bf16(*shape, scale=1.0):
+        return (scale * torch.randn(shape, generator=g, device=dev)).to(torch.bfloat16)
+
+    V, H = cfg.vocab, cfg.hidden
+    w = bf16(V, H, scale=0.02)
+    T = 10240
+    ids = torch.randint(0, V, (T,), generator=g, device=dev, dtype=torch.int32)
+    ids[torch.rand(T, generator=g, device=dev) < 0.33] = -1
+    mask, dy = bf16(H, scale=0.02), bf16(T, H)
+    for _ in range(repeat):
+        gocr.op_embed(ids, w, mask)
+        gocr.op_embed_backward(dy, ids, V, mask=True)
+    for lens in ([872, 345, 419, 1097, 601, 287, 95, 512, 873, 444, 1203, 730, 368, 146, 200], [8192]):
+        cu = torch.tensor([0, *lens], device=dev).cumsum(0).to(torch.int32)
+        q = bf16(sum(lens), cfg.n_q_heads, cfg.head_dim)
+        k, v = (bf16(sum(lens), cfg.n_kv_heads, cfg.head_dim) for _ in range(2))
+        do = torch.ones_like(q)
+        for _ in range(repeat):
+            o, lse = gocr.op_attention_packed(q, k, v, cu)
+            gocr.op_attention_packed_backward(do, q, k, v, o, lse, cu)
+    x, labels = bf16(2048, H), torch.randint(0, V, (2048,), generator=g, device=dev, dtype=torch.int32)
+    weight = torch.full((2048,), 1 / 2048, device=dev)
+    for _ in range(repeat):
+        _, lse = gocr.op_linear_ce(x, w, labels)
+        gocr.op_linear_ce_backward(weight, x, w, labels, lse)
+    gocr.op_status(dev)
+
+
 def draft_case(B: int = 32):
     from . import gocr
     cfg = synth.BASE
@@ -195,7 +236,9 @@ def batch_case():
 
 def main(argv):
     what = argv[1] if len(argv) > 1 else ""
-    if what == "draft":
+    if what == "train_ops":
+        train_ops_case()
+    elif what == "draft":
         draft_case(int(argv[2]) if len(argv) > 2 else 32)
     elif what == "sweep":
         sweep_case()
