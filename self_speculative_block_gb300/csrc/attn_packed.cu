@@ -286,11 +286,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the items: this CTA's own, then those of CTAs that have not started;
       // and the last V tile of a ragged item: nothing behind the sequence
       int id = blockIdx.x, takes = 0, ring = 0;
+      Cursor cursor;
       for (int i = 0; ok; ++i) {
         const int s = i & 1;
         Block blk{0, 0, 0};
         while (id >= 0 && ok) {
-          blk = find_block<true>(a.cu, a.n_seq, a.T, QT, id / a.Hq);
+          blk = find_block<true>(a.cu, a.n_seq, a.T, QT, id / a.Hq, cursor);
           if (blk.len) break;
           ask_cta(work + 2, taken);
           id = taken_cta(work + 2, taken, takes++, ok);

@@ -59,46 +59,68 @@ struct Block {
   int at;     // first row (within the sequence) of this block of `size` rows
 };
 
+// Where a search for a block may begin: a sequence, and the blocks before it.
+struct Cursor { int seq = 0, before = 0; };
+
 // The b-th block of `size` rows over all sequences, in a sequence's order or
 // its last block first (the order of falling work: the last query rows read
 // the most keys, the first keys are read by the most rows); one warp, all
 // lanes get the answer.  len = 0: there is no such block.  Whatever cu holds,
-// the rows stay within 0 .. T - 1.
+// the rows stay within 0 .. T - 1.  A lane takes 8 sequences at a time, whose
+// loads go out together, and a later search goes on where this one ended: with
+// 2,000 sequences of 64 a lane for each one and a fresh start took more time
+// than the attention.
 template <bool LAST_FIRST>
-__device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int size, int b) {
+__device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int size, int b, Cursor& from) {
+  constexpr int PER = 8;
   const int lane = threadIdx.x & 31;
   Block r{0, 0, 0};
-  int seen = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += 32) {
-    const int s = s0 + lane;
-    int lo = 0, len = 0;
-    if (s < n_seq) {
-      lo = min(max(cu[s], 0), T);
-      len = max(min(cu[s + 1], T) - lo, 0);
-    }
-    const int n = (len + size - 1) / size;
-    int inc = n;
+  if (b < from.before) from = Cursor{};
+  while (from.seq < n_seq) {
+    const int s = from.seq + lane * PER;
+    int c[PER + 1], sum = 0;
+#pragma unroll
+    for (int i = 0; i <= PER; ++i) c[i] = min(max(cu[min(s + i, n_seq)], 0), T);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += (max(c[i + 1] - c[i], 0) + size - 1) / size;
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, seen + inc > b);
+    const unsigned past = __ballot_sync(0xffffffffu, from.before + inc > b);
     if (past) {
+      int at = b - (from.before + inc - sum);  // among this lane's blocks
+      bool open = true;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int len = max(c[i + 1] - c[i], 0), n = (len + size - 1) / size;
+        if (open && at < n) {
+          r.row0 = c[i];
+          r.len = len;
+          r.at = (LAST_FIRST ? n - 1 - at : at) * size;
+          open = false;
+        }
+        at -= n;
+      }
       const int src = __ffs(past) - 1;
-      const int i = b - (seen + inc - n);
-      r.row0 = __shfl_sync(0xffffffffu, lo, src);
-      r.len = __shfl_sync(0xffffffffu, len, src);
-      r.at = __shfl_sync(0xffffffffu, (LAST_FIRST ? n - 1 - i : i) * size, src);
+      r.row0 = __shfl_sync(0xffffffffu, r.row0, src);
+      r.len = __shfl_sync(0xffffffffu, r.len, src);
+      r.at = __shfl_sync(0xffffffffu, r.at, src);
       return r;
     }
-    seen += __shfl_sync(0xffffffffu, inc, 31);
+    from.before += __shfl_sync(0xffffffffu, inc, 31);
+    from.seq += 32 * PER;
   }
   return r;
 }
 
 // Most blocks of `size` rows that n_seq sequences of T rows in all can have.
-inline long long max_blocks(int n_seq, int T, int size) { return (long long)n_seq + T / size; }
+inline long long max_blocks(int n_seq, int T, int size) {
+  const int m = n_seq < T ? n_seq : T;  // sequences that are not empty
+  return (long long)m + (T - m) / size;
+}
 
 // A tile of 128 rows x D bf16 in shared memory: D / 64 boxes of 128 rows x 128
 // bytes, swizzled, as TMA writes them.

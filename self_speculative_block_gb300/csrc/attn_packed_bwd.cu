@@ -680,13 +680,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
   int b = blockIdx.x;
+  Cursor cursor;
   if (b < n_dkv) {
-    const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, b / a.Hkv);
+    const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, b / a.Hkv, cursor);
     if (blk.len) dkv_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hkv);
     else tc::grid_dep_wait();
   } else {
     b -= n_dkv;
-    const Block blk = find_block<true>(a.cu, a.n_seq, a.T, 128, b / a.Hq);
+    const Block blk = find_block<true>(a.cu, a.n_seq, a.T, 128, b / a.Hq, cursor);
     if (blk.len) dq_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hq);
     else tc::grid_dep_wait();
   }

@@ -292,3 +292,13 @@ def test_attention_packed_on_two_streams_at_once(g):
         torch.cuda.synchronize()
         assert all(torch.equal(a[n], want[n]) for n in want) and all(torch.equal(b[n], want2[n]) for n in want2)
     g.op_status()
+
+
+def test_attention_packed_many_sequences(g):
+    """More sequences than one step of the search for a block takes, empty ones among them."""
+    lens = [(i * 7) % 23 if i % 5 else 0 for i in range(1300)] + [300, 0, 129, 0]
+    q, k, v, do, cu = _case(lens, 2, 1, 64, seed=8)
+    val, tol = _ref(q, k, v, do, lens, 0.125)
+    for name, got in _run(g, q, k, v, do, cu).items():
+        _close(name, got, val, tol)
+    g.op_status()
