@@ -66,13 +66,12 @@ struct Cursor { int seq = 0, before = 0; };
 // its last block first (the order of falling work: the last query rows read
 // the most keys, the first keys are read by the most rows); one warp, all
 // lanes get the answer.  len = 0: there is no such block.  Whatever cu holds,
-// the rows stay within 0 .. T - 1.  A lane takes 8 sequences at a time, whose
+// the rows stay within 0 .. T - 1.  A lane takes PER sequences at a time, whose
 // loads go out together, and a later search goes on where this one ended: with
 // 2,000 sequences of 64 a lane for each one and a fresh start took more time
-// than the attention.
-template <bool LAST_FIRST>
+// than the attention (PER = 8 and going on: 2,400 -> 513 us).
+template <bool LAST_FIRST, int PER>
 __device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int size, int b, Cursor& from) {
-  constexpr int PER = 8;
   const int lane = threadIdx.x & 31;
   Block r{0, 0, 0};
   if (b < from.before) from = Cursor{};

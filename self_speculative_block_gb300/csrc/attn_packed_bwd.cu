@@ -37,6 +37,8 @@
 #include "../../include/gocr.h"
 #include "attn_packed.cuh"
 
+#include <type_traits>
+
 using namespace gocr;
 using namespace gocr::packed;
 
@@ -680,14 +682,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
   int b = blockIdx.x;
-  Cursor cursor;
+  // up to 32 sequences, one a lane: one load's latency, without the eight's arithmetic behind it
+  auto find = [&](auto last_first, int block) {
+    Cursor cursor;
+    return a.n_seq <= 32 ? find_block<last_first.value, 1>(a.cu, a.n_seq, a.T, 128, block, cursor)
+                         : find_block<last_first.value, 8>(a.cu, a.n_seq, a.T, 128, block, cursor);
+  };
   if (b < n_dkv) {
-    const Block blk = find_block<false>(a.cu, a.n_seq, a.T, 128, b / a.Hkv, cursor);
+    const Block blk = find(std::false_type{}, b / a.Hkv);
     if (blk.len) dkv_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hkv);
     else tc::grid_dep_wait();
   } else {
     b -= n_dkv;
-    const Block blk = find_block<true>(a.cu, a.n_seq, a.T, 128, b / a.Hq, cursor);
+    const Block blk = find(std::true_type{}, b / a.Hq);
     if (blk.len) dq_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hq);
     else tc::grid_dep_wait();
   }
