@@ -359,7 +359,8 @@ int gocr_three_stream_ranges(int P, int N, int B, int32_t* lim, int32_t* lo2, in
  * stream of the current device (GOCR_EINVAL otherwise); operands aligned to 16
  * bytes; nothing is allocated, kept between calls or synchronised, so a call
  * can be captured into a graph; a workspace need not be cleared and belongs to
- * one call at a time.  The same inputs give the same bits.  Outputs must not
+ * one call at a time (for calls of several shapes: the largest of their sizes,
+ * which need not be that of the largest shape).  The same inputs give the same bits.  Outputs must not
  * overlap inputs.  Zero rows (T = 0) are allowed: gradients of weights are
  * then zero.  Errors: GOCR_EINVAL (null pointer, shape, alignment, stream),
  * GOCR_ECAPACITY (workspace), GOCR_ECUDA (launch). */

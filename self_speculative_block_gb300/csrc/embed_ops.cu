@@ -44,8 +44,12 @@ constexpr int SORT_CTAS = 8;
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int MAX_DIGITS = 512;
-constexpr int PIECE = 16;
+// Sorted positions of a sum CTA.  Few positions want many CTAs; of many, pieces
+// of 128 leave an eighth of the partial rows, which one CTA per 128 columns of a
+// run joins (262,144 positions, 30 % [M], of 65,536 x 1,536: 519 -> 373 us).
+constexpr int PIECE_FEW = 16, PIECE_MANY = 128, MANY = 1 << 15;
 constexpr int LONG = 16;
+inline int piece_of(int T) { return T > MANY ? PIECE_MANY : PIECE_FEW; }
 constexpr int FILL_BYTES = 16384;  // one bulk copy of zeros
 constexpr int FILL_ROWS = 32768;   // most table rows of a CTA that writes zeros
 
@@ -295,7 +299,7 @@ __device__ __forceinline__ void fill_unnamed(const SumArgs& a) {
 // Rows of dy fetched at a time by a thread.
 constexpr int BATCH = 8;
 
-template <typename T>
+template <typename T, int PIECE>
 __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int WIN = LONG + PIECE + LONG;  // positions b - LONG .. b + PIECE + LONG - 1
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(SumArgs a) {
 
 // The long runs: warp w adds the w-th eighth of a run's partial rows, four
 // columns a lane, and warp 0 the eight sums.
-template <typename T>
+template <typename T, int PIECE>
 __global__ void __launch_bounds__(256) embed_join_kernel(SumArgs a) {
   __shared__ float4 sums[8][32];
   __shared__ int s_last;
@@ -442,7 +446,7 @@ int check_shape(int dtype, int T, int H, int V) {
   return GOCR_OK;
 }
 
-template <typename T>
+template <typename T, int PIECE>
 int embed_backward(const SortArgs& so, SumArgs su, cudaStream_t s) {
   if (su.T) {
     cudaLaunchConfig_t cfg{};
@@ -468,10 +472,10 @@ int embed_backward(const SortArgs& so, SumArgs su, cudaStream_t s) {
   const int vecs = su.H / Vec<T>::N;
   const int th = std::max(128, std::min(256, (vecs + 31) / 32 * 32));
   const unsigned parts = (unsigned)((vecs + th - 1) / th);
-  launch_k(embed_sum_kernel<T>, dim3(su.fill + su.pieces * parts), dim3(th), 0, s, su.T > 0, su);
+  launch_k(embed_sum_kernel<T, PIECE>, dim3(su.fill + su.pieces * parts), dim3(th), 0, s, su.T > 0, su);
   if (int rc = op_launched("embedding sum")) return rc;
   if (su.T > LONG) {
-    launch_k(embed_join_kernel<T>, dim3(std::min(su.T / LONG, 64), (su.H + 127) / 128), dim3(256), 0, s, true, su);
+    launch_k(embed_join_kernel<T, PIECE>, dim3(std::min(su.T / LONG, 64), (su.H + 127) / 128), dim3(256), 0, s, true, su);
     return op_launched("embedding join");
   }
   return GOCR_OK;
@@ -500,7 +504,8 @@ int gocr_op_embed(int dtype, const void* embed, const void* mask_embed, const in
 
 size_t gocr_op_embed_backward_workspace(int T, int H) {
   if (T < 0 || H < 1) return 0;
-  const size_t pieces = (size_t)(T + PIECE - 1) / PIECE;
+  size_t pieces = ((size_t)T + piece_of(T) - 1) / piece_of(T);
+  if (T > MANY) pieces = std::max<size_t>(pieces, MANY / PIECE_FEW);  // enough for fewer positions, too
   return sort_bytes(T) + pieces * 2 * H * 4 + up256(pieces * 4 + 4) + 256;
 }
 
@@ -527,10 +532,12 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
   so.passes = (bits + 8) / 9;
   so.digit_bits = (bits + so.passes - 1) / so.passes;
   float* part = (float*)(ws + 4 * arr);
-  int* n_long = (int*)(part + (size_t)((T + PIECE - 1) / PIECE) * 2 * H);
+  int* n_long = (int*)(part + (size_t)((T + piece_of(T) - 1) / piece_of(T)) * 2 * H);
   so.n_long = n_long;
   SumArgs su{dy, ids, so.key[1], so.pos[1], d_embed, d_mask, part, n_long, n_long + 1, T, H, V, scale, 0, 0, 0};
-  return dtype == GOCR_DTYPE_BF16 ? embed_backward<bf16>(so, su, s) : embed_backward<float>(so, su, s);
+  if (piece_of(T) == PIECE_MANY)
+    return dtype == GOCR_DTYPE_BF16 ? embed_backward<bf16, PIECE_MANY>(so, su, s) : embed_backward<float, PIECE_MANY>(so, su, s);
+  return dtype == GOCR_DTYPE_BF16 ? embed_backward<bf16, PIECE_FEW>(so, su, s) : embed_backward<float, PIECE_FEW>(so, su, s);
 }
 
 }  // extern "C"

@@ -654,7 +654,7 @@ extern "C" {
 
 size_t gocr_op_linear_ce_workspace(int T, int V) {
   if (T < 0 || V < 1) return 0;
-  return up256((size_t)T * cdiv(V, z_columns(T, V, STATS_STEP)) * 8) + 256;
+  return up256((size_t)T * cdiv(V, RN) * 8) + 256;  // for the narrowest tiles: enough for fewer rows, too
 }
 
 int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,

@@ -54,6 +54,30 @@ def test_embed_gradient_of_token_arrays_that_begin_anywhere(g, T, offset):
     assert torch.equal(dE, ref[:V]) and torch.equal(dm, ref[V])
 
 
+@pytest.mark.parametrize("T", [32768, 32769, 32768 + 128, 100_003])
+@pytest.mark.parametrize("V,kind", [(1, "even"), (300, "even"), (2500, "even"), (50_000, "even"), (4000, "often"),
+                                    (97, "runs")])
+def test_embed_gradient_of_many_tokens(g, T, V, kind):
+    """Runs of every length against pieces of every length; integer gradients, so that every sum is exact."""
+    H = 24
+    r = _gen(T + V)
+    u = torch.rand(T, generator=r, device="cuda")
+    if kind == "runs":  # token v occurs 8 v + 1 times or so, which puts runs' ends everywhere in the pieces
+        ids = torch.repeat_interleave(torch.arange(V, device="cuda"), torch.arange(V, device="cuda") * 8 + 1)
+        ids = ids[torch.randint(0, len(ids), (T,), generator=r, device="cuda")].to(torch.int32)
+    else:
+        ids = (torch.exp(u * math.log(V)) - 1 if kind == "often" else u * V).long().clamp(0, V - 1).to(torch.int32)
+    ids[torch.rand(T, generator=r, device="cuda") < 0.2] = -1
+    ids[torch.rand(T, generator=r, device="cuda") < 0.05] = V + 3
+    dy = torch.randint(-3, 4, (T, H), generator=r, device="cuda").float()
+    dE = torch.full((V, H), math.nan, device="cuda")
+    dm = torch.full((H,), math.nan, device="cuda")
+    _grad_into(g, dy, ids, dE, dm)
+    at = torch.where(ids < 0, V, torch.where(ids < V, ids, V + 1)).long()
+    ref = torch.zeros((V + 2, H), device="cuda").index_add(0, at, dy)
+    assert torch.equal(dE, ref[:V]) and torch.equal(dm, ref[V])
+
+
 @pytest.mark.parametrize("V,H", [(10_000_123, 8), (32768 * 304 + 1, 8), (31, 8), (33, 4096)])
 def test_embed_gradient_writes_every_row(g, V, H):
     """Tables with more rows than the usual CTAs' shares hold, and with fewer rows than bits in a word."""

@@ -145,3 +145,17 @@ def test_attention_packed_wrapper_checks_rows():
         gocr.op_attention_packed(q.float(), q, q, cu)
     with pytest.raises(ValueError, match="CUDA"):
         gocr.op_attention_packed(q, q, q, cu)
+
+
+def test_workspaces_serve_fewer_rows(lib):
+    """A workspace for the most rows of a program serves its shorter calls."""
+    rows = [1, 2, 33, 128, 129, 256, 257, 300, 4096, 32768, 32769, 40000, 262144, 262145, 1 << 20]
+    for H in (8, 256, 1536):
+        sizes = [lib.gocr_op_embed_backward_workspace(T, H) for T in rows]
+        assert sizes == sorted(sizes)
+    for V in (1, 8191, 30000, 65536):
+        sizes = [lib.gocr_op_linear_ce_workspace(T, V) for T in rows]
+        assert sizes == sorted(sizes)
+    for Hq in (1, 12):
+        sizes = [lib.gocr_op_attention_packed_backward_workspace(T, Hq) for T in rows]
+        assert sizes == sorted(sizes)
