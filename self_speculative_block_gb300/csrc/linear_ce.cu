@@ -654,7 +654,10 @@ extern "C" {
 
 size_t gocr_op_linear_ce_workspace(int T, int V) {
   if (T < 0 || V < 1) return 0;
-  return up256((size_t)T * cdiv(V, RN) * 8) + 256;  // for the narrowest tiles: enough for fewer rows, too
+  // a bound that grows with T (T x tiles need not): tiles have RN columns at
+  // least, and there are at most PAIRS / (row tiles) more of them than of TN
+  const size_t narrow = (size_t)T * cdiv(V, RN), wide = (size_t)T * cdiv(V, TN) + TM * PAIRS;
+  return up256((narrow < wide ? narrow : wide) * 8) + 256;
 }
 
 int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int T, int V,
