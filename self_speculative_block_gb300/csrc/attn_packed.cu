@@ -19,7 +19,7 @@
 // ready when its softmax is.  Each tile has an MMA warp, because a warp's wait
 // on a barrier costs 100 cycles and more behind its own queue of MMAs, a time
 // that the other warp's MMAs fill.  12 heads of 128: one sequence of 8,192 in
-// 180 us (1.15 PFLOP/s), 16 prompts of 25 to 1,200 in 45, 18 regions of 1 to 140
+// 182 us (1.13 PFLOP/s), 16 prompts of 25 to 1,200 in 45, 18 regions of 1 to 140
 // in 17, where a launch's fixed chain (sequence search, loads, one block, store)
 // is most of it.  Measured slower: part of the exponentials as polynomials on
 // the FMA pipe, P given over in halves, sixteen softmax warps (two threads a
