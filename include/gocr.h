@@ -421,9 +421,11 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
 /* Gradient of sum_t dloss[t] loss[t]: dx[T, H] and dw[V, H] in bf16, from the
  * forward call's lse.  dloss[t] is the row's weight in the training loss (of a
  * clean or a corrupted stream's mean, say); rows without a target add nothing
- * (their dloss and lse are not read).  z is computed again in pieces of the
- * vocabulary; (softmax - one-hot) dloss is rounded to bf16 for the products,
- * whose sums are in fp32. */
+ * (their dloss and lse count for nothing, whatever they hold).  z is computed
+ * again in pieces of the vocabulary; (softmax - one-hot) dloss / u is rounded to
+ * bf16 for the products, whose sums are in fp32 and are multiplied by u: the
+ * mantissa of the first target's weight, so that the weight of a mean is not
+ * rounded. */
 size_t gocr_op_linear_ce_backward_workspace(int T, int V, int H);
 int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w, const int32_t* labels,
                                const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,

@@ -3,6 +3,7 @@
 //
 //   z_tv = x_t . w_v      lse_t = log sum_v exp z_tv      loss_t = lse_t - z_t,y(t)
 //   g_tv = (exp(z_tv - lse_t) - [v = y(t)]) dloss_t        dx = g W      dw = g^T x
+//   (g is kept without the mantissa of the rows' common weight: weight_unit)
 //
 // All of it is matrix products on tcgen05: 2 T V H operations forward, 6 T V H
 // backward (z again, dx, dw).  One persistent kernel shape serves the three
@@ -158,6 +159,35 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // Byte offset of 16-byte chunk c of row r in a 32-row swizzled box.
 __device__ __forceinline__ uint32_t box_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// The factor that g is without and its sums get back in fp32: the mantissa, in
+// [1, 2), of the first target's weight.  The rows of a mean have one weight, or
+// a few that are powers of two apart; with it in g, the bf16 rounding of nearly
+// every label's g would be the same relative error, up to 2^-8, and would not
+// average out of dx and dw.  One warp, all lanes get the answer.
+__device__ __forceinline__ float weight_unit(const float* dloss, const int* labels, int T, int V) {
+  constexpr int PER = 8;
+  const int lane = threadIdx.x & 31;
+  for (int t0 = 0; t0 < T; t0 += 32 * PER) {
+    float f[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int t = t0 + u * 32 + lane;
+      const float d = t < T ? fabsf(dloss[t]) : 0.f;  // beside the label, not after it
+      const int label = t < T ? labels[t] : -1;
+      f[u] = (unsigned)label < (unsigned)V ? d : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const unsigned some = __ballot_sync(0xffffffffu, f[u] >= 1.1754943508e-38f && f[u] <= 3.4028234664e38f);
+      if (some) {
+        const float first = __shfl_sync(0xffffffffu, f[u], __ffs(some) - 1);
+        return __uint_as_float((__float_as_uint(first) & 0x007fffffu) | 0x3f800000u);
+      }
+    }
+  }
+  return 1.f;
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -267,6 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
     const int q = warp & 3;  // the tensor memory lanes this warp may read: 32 q ..
     uint8_t* box = sm + OFF_STORE + q * 2 * STORE_BYTES;
     int acc = 0, aph = 0, buf = 0;
+    const float unit = KIND == STATS ? 1.f : weight_unit(a.dloss, a.labels, a.T, a.V);
     for (int i = 0; tile_of<KIND>(a, pair, i, t); ++i) {
       if (!(ok = tc::mbar_wait_warp(acc_full + acc, aph))) break;
       tc::fence_after_sync();
@@ -317,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         if (row < a.T) {
           label = a.labels[row];
           if ((unsigned)label < (unsigned)a.V) {
-            f = a.dloss[row];
+            f = a.dloss[row] / unit;
             ref = a.lse[row] * LOG2E;
           } else {
             label = -1;
@@ -387,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 p = __floats2bfloat162_rn(v[g * 8 + 2 * e], v[g * 8 + 2 * e + 1]);
+                  const __nv_bfloat162 p = __floats2bfloat162_rn(v[g * 8 + 2 * e] * unit, v[g * 8 + 2 * e + 1] * unit);
                   w[e] = *reinterpret_cast<const uint32_t*>(&p);
                 }
                 *reinterpret_cast<uint4*>(bx + box_at(lane, h * 4 + g)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -495,8 +526,10 @@ __global__ void __launch_bounds__(128) linear_ce_join_kernel(const float2* part,
 // dx = the sum of the tile's parts, in slab order: memory-bound, 13 us for 4,096
 // rows x 1,536.
 __global__ void __launch_bounds__(256) linear_ce_dx_kernel(const float* slabs, bf16* dx, int T, int H, int n_tiles,
-                                                           size_t slab, Deal last, Deal before) {
+                                                           size_t slab, Deal last, Deal before, const float* dloss,
+                                                           const int* labels, int V) {
   tc::grid_dep_wait();
+  const float unit = weight_unit(dloss, labels, T, V);
   const size_t n = (size_t)T * H / 8, step = (size_t)gridDim.x * 256;
   for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += step) {
     const int row = (int)(i * 8 / H), col = (int)(i * 8 % H);
@@ -510,8 +543,8 @@ __global__ void __launch_bounds__(256) linear_ce_dx_kernel(const float* slabs, b
       u.x += x.x; u.y += x.y; u.z += x.z; u.w += x.w;
       w.x += y.x; w.y += y.y; w.z += y.z; w.w += y.w;
     }
-    const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(u.x, u.y), __floats2bfloat162_rn(u.z, u.w),
-                                 __floats2bfloat162_rn(w.x, w.y), __floats2bfloat162_rn(w.z, w.w)};
+    const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(u.x * unit, u.y * unit), __floats2bfloat162_rn(u.z * unit, u.w * unit),
+                                 __floats2bfloat162_rn(w.x * unit, w.y * unit), __floats2bfloat162_rn(w.z * unit, w.w * unit)};
     reinterpret_cast<uint4*>(dx)[i] = *reinterpret_cast<const uint4*>(h);
   }
 }
@@ -743,7 +776,7 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
   const size_t vecs = (size_t)T * H / 8;
   const unsigned blocks = (unsigned)(vecs / 256 + 1 < 8u * SM_COUNT ? vecs / 256 + 1 : 8u * SM_COUNT);
   launch_k(linear_ce_dx_kernel, dim3(blocks), dim3(256), 0, s, true, (const float*)slabs, (bf16*)dx, T, H, cdiv(H, TN),
-           (size_t)p.slab_rows * H, p.last, p.full);
+           (size_t)p.slab_rows * H, p.last, p.full, dloss, labels, V);
   return op_launched("linear_ce dx");
 }
 

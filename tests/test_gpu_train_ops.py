@@ -302,3 +302,29 @@ def test_train_ops_workspace_may_hold_anything(g):
         want = g.op_embed_backward(dy, ids, 30, mask=True)
         got = g.op_embed_backward(dy, ids, 30, mask=True, workspace=ws(lib.gocr_op_embed_backward_workspace(100, 64)))
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T,first", [(1, 0), (40, 0), (600, 300)])
+def test_linear_ce_gradient_of_a_mean(g, T, first):
+    """All targets have one weight, which bf16 would round by 2^-8: that error must
+    not be in every gradient.  Rows before `first` have no target and a NaN weight."""
+    V, H = 5000, 128
+    x, w, _, _ = _ce_case(T, V, H, seed=T, ignored=0.0, lean=0.0)
+    labels = torch.randint(0, V, (T,), generator=_gen(T), device="cuda", dtype=torch.int32)
+    labels[:first] = -1
+    _, lse = g.op_linear_ce(x, w, labels)
+
+    def grads(weight):
+        dloss = torch.full((T,), weight, device="cuda")
+        dloss[:first] = math.nan
+        return [t.double() for t in g.op_linear_ce_backward(dloss, x, w, labels, lse)]
+    one = grads(1.0)
+    for weight in (1.0 + 2.0 ** -8 - 2.0 ** -20, -2.0 ** -9 * (1.0 + 2.0 ** -8 - 2.0 ** -20)):
+        for a, b in zip(grads(weight), one):
+            # each side rounds its sums once to bf16, by half a step at most
+            assert ((a - weight * b).abs() <= (2 * U[torch.bfloat16] + 4 * F32) * (weight * b).abs() + 1e-38).all()
+            # these errors are independent, of 2^-7 / sqrt(3) standard deviation at most: their mean over
+            # the values that count stays within six deviations
+            n = float(b.square().sum() ** 2 / (b ** 4).sum())
+            mean = float(((a - weight * b) * b).sum() / (weight * b.square().sum()))
+            assert abs(mean) <= 6 * 2.0 ** -7 / 3 ** 0.5 / n ** 0.5, (weight, mean, n)
