@@ -13,8 +13,9 @@
 // a ring of 64-deep stages full, one thread of the pair issues the MMAs into
 // one of two tensor memory accumulators, and four warps a CTA (one row a
 // thread) run the epilogue of the other:
-//   STATS  (z) the row's maximum and sum of exponentials over the tile's 256
-//          columns without the label's: 8 bytes per row and tile leave the SM.
+//   STATS  (z) the row's maximum and sum of exponentials over the tile's
+//          columns (256 or fewer) without the label's: 8 bytes per row and tile
+//          leave the SM.
 //          A second kernel joins them in tile order with the label's z, which
 //          it computes in fp32, and takes the loss as log(1 + exp(lse of the
 //          others - z of the label)): a confident row's small loss keeps its
@@ -34,7 +35,7 @@
 //
 // What bounds it: with many rows the tensor pipe, and with seconds of it the
 // card's power.  2,047 rows x 65,536 x 1,536 forward take 237 us (1.74 PFLOP/s,
-// the pipe busy 92 % of STATS); 4,096 rows with the gradient 2,035 us (1.62
+// the pipe busy 92 % of STATS); 4,096 rows with the gradient 2,055 us (1.61
 // PFLOP/s of the four products' operations, where cuBLAS sustains 1.73).  33
 // rows forward take 40 us, 35 of them reading w's 201 MB (5.8 TB/s) and 4 the
 // join.  193 rows x 8,191 x 512 with the gradient take 52 us, five launches of 7
