@@ -431,6 +431,15 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
                                const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* The same with the forward call's loss[T], too (NULL: without it).  The
+ * label's softmax - 1 is -(1 - exp(-loss)) then, with the loss's relative
+ * precision.  Without the loss it is the difference of z and lse, of which the
+ * rounding of both (about 1e-6 to 1e-5 for logits of tens) is left: rows whose
+ * loss is below 1e-3 want the loss. */
+int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, const void* w, const int32_t* labels,
+                                         const float* loss, const float* lse, void* dx, void* dw, int T, int V, int H,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream` and reports whether a kernel of these operators on the
  * current device gave up a wait since the last report (GOCR_EDEVICE; the
  * outputs of such a call are not valid). */

@@ -21,7 +21,10 @@
 //          others - z of the label)): a confident row's small loss keeps its
 //          precision, where lse - z would cancel;
 //   GRAD   (z) g in bf16, stored to the piece of the vocabulary in the
-//          workspace;
+//          workspace.  The label's exp(z - lse) - 1 is expm1(-loss) where the
+//          forward call's loss is given: of a confident row the difference of
+//          two rounded logits of tens has no right digit left (losses of
+//          1e-6 to 1e-5: dx off by 0.9 of its norm);
 //   PROD   dx += g W (fp32 slabs) and dw = g^T x (bf16) of the piece, both read
 //          g as it lies: rows for dx (K-major), columns for dw (M-major), W and
 //          x N-major, so nothing is transposed.
@@ -97,6 +100,7 @@ struct Args {
   int v0, vc;           // GRAD, PROD: the piece of the vocabulary
   const int* labels;
   const float* lse;
+  const float* loss;    // GRAD: the forward call's, or null
   const float* dloss;
   float2* part;         // STATS: [T][vocabulary tiles] (maximum, sum)
   int m_tiles, n_tiles; // STATS, GRAD; n_tiles also of PROD
@@ -300,11 +304,28 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
     int acc = 0, aph = 0, buf = 0;
     const float unit = KIND == STATS ? 1.f : weight_unit(a.dloss, a.labels, a.T, a.V);
     for (int i = 0; tile_of<KIND>(a, pair, i, t); ++i) {
+      const int row0 = t.m0 + rank * RM + q * 32;  // the warp's first row
+      const int row = row0 + lane;
+      // GRAD: the row's weight without the unit, its lse, and its label's g;
+      // before the wait, so that the loads cost nothing
+      int label = -1;
+      float f = 0.f, lse = 0.f, own = 0.f;
+      if (KIND == GRAD && row < a.T) {
+        const float d = a.dloss[row], e = a.lse[row], l = a.loss ? a.loss[row] : 0.f;
+        label = a.labels[row];
+        if ((unsigned)label < (unsigned)a.V) {
+          f = d / unit;
+          lse = e;
+          own = f * expm1f(-l);
+        } else {
+          label = -1;
+        }
+      }
+      const bool has = label >= 0;
+      const float ref = lse * LOG2E;
       if (!(ok = tc::mbar_wait_warp(acc_full + acc, aph))) break;
       tc::fence_after_sync();
       const uint32_t src = tmem + acc * TN + ((uint32_t)(q * 32) << 16);
-      const int row0 = t.m0 + rank * RM + q * 32;  // the warp's first row
-      const int row = row0 + lane;
       const uint32_t freed = tc::mapa(tc::smem_u32(acc_free + acc), 0);
       if (KIND == STATS) {
         const bool in = row < a.T;
@@ -344,19 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         if (lane == 0) tc::mbar_arrive_cluster(freed);
         if (in) a.part[(size_t)row * a.n_tiles + t.n0 / a.tn] = make_float2(m, s);
       } else if (KIND == GRAD) {
-        int label = -1;
-        float f = 0.f, ref = 0.f;
-        if (row < a.T) {
-          label = a.labels[row];
-          if ((unsigned)label < (unsigned)a.V) {
-            f = a.dloss[row] / unit;
-            ref = a.lse[row] * LOG2E;
-          } else {
-            label = -1;
-          }
-        }
         const int col0 = a.v0 + t.n0;
-        const bool has = label >= 0;
         for (int c = 0; c < a.tn; c += 64) {
           if (t.n0 + c >= a.vc) break;
           if (lane == 0) bulk_wait_read1();
@@ -368,12 +377,6 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
             tc::tmem_ld32(src + c + h * 32, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = has ? f * exp2f(fmaf(v[j], LOG2E, -ref)) : 0.f;
-            const unsigned at = (unsigned)(label - (col0 + c + h * 32));
-            if (__any_sync(0xffffffffu, has && at < 32u)) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (has && at == (unsigned)j) v[j] -= f;
-            }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint32_t w[4];
@@ -385,6 +388,19 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
               *reinterpret_cast<uint4*>(bx + box_at(lane, h * 4 + g)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+          const unsigned at = (unsigned)(label - (col0 + c));
+          if (!a.loss && __any_sync(0xffffffffu, at < 64u)) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // z again: seldom here, so nothing is kept for it
+              float z[32];
+              tc::tmem_ld32(src + c + h * 32, z);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (at == (unsigned)(h * 32 + j)) own = z[j] - lse;
+            }
+            own = f * expm1f(own > 0.f ? 0.f : own);  // the log of the label's share is not above 0
+          }
+          if (at < 64u) *reinterpret_cast<bf16*>(bx + box_at(lane, at >> 3) + (at & 7) * 2) = __float2bfloat16_rn(own);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -724,9 +740,9 @@ size_t gocr_op_linear_ce_backward_workspace(int T, int V, int H) {
   return backward_plan(T, V, H).bytes;
 }
 
-int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w, const int32_t* labels,
-                               const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,
-                               size_t workspace_bytes, void* stream) {
+int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, const void* w, const int32_t* labels,
+                                         const float* loss, const float* lse, void* dx, void* dw, int T, int V, int H,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
   if (int rc = check_shape(T, V, H)) return rc;
   if (!w || !dw || !workspace || (T && (!dloss || !x || !labels || !lse || !dx)))
     return op_fail(GOCR_EINVAL, "null pointer");
@@ -744,7 +760,7 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
   Maps z{}, pr{};
   Args common{};
   common.T = T; common.H = H; common.V = V;
-  common.labels = labels; common.lse = lse; common.dloss = dloss;
+  common.labels = labels; common.lse = lse; common.loss = loss; common.dloss = dloss;
   common.tn = z_columns(T, p.piece, GRAD_STEP);
   set_ring(common, true);
   if (!map2(&z.a0, x, T, H, H, common.a_rows) || !map2(&z.b0, w, V, H, H, common.tn / 2) || !map2(&pr.b0, w, V, H, H, 64) ||
@@ -779,6 +795,13 @@ int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w,
   launch_k(linear_ce_dx_kernel, dim3(blocks), dim3(256), 0, s, true, (const float*)slabs, (bf16*)dx, T, H, cdiv(H, TN),
            (size_t)p.slab_rows * H, p.last, p.full, dloss, labels, V);
   return op_launched("linear_ce dx");
+}
+
+int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w, const int32_t* labels,
+                               const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return gocr_op_linear_ce_backward_with_loss(dloss, x, w, labels, nullptr, lse, dx, dw, T, V, H, workspace,
+                                              workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -39,7 +39,7 @@ EXPORTS = ("gocr_create", "gocr_prefill", "gocr_decode", "gocr_decode_batch", "g
            "gocr_op_linear_static", "gocr_op_attention_ranges", "gocr_three_stream_ranges",
            "gocr_op_embed", "gocr_op_embed_backward_workspace", "gocr_op_embed_backward",
            "gocr_op_linear_ce_workspace", "gocr_op_linear_ce", "gocr_op_linear_ce_backward_workspace",
-           "gocr_op_linear_ce_backward", "gocr_op_attention_packed", "gocr_op_attention_packed_backward_workspace",
+           "gocr_op_linear_ce_backward", "gocr_op_linear_ce_backward_with_loss", "gocr_op_attention_packed", "gocr_op_attention_packed_backward_workspace",
            "gocr_op_attention_packed_backward", "gocr_op_status")
 
 
@@ -131,6 +131,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gocr_op_linear_ce": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
         "gocr_op_linear_ce_backward_workspace": (sz, [i32, i32, i32]),
         "gocr_op_linear_ce_backward": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
+        "gocr_op_linear_ce_backward_with_loss": (i32, [vp] * 8 + [i32, i32, i32, vp, sz, vp]),
         "gocr_op_attention_packed": (i32, [vp] * 6 + [i32] * 5 + [i64] * 3 + [f32, vp]),
         "gocr_op_attention_packed_backward_workspace": (sz, [i32, i32]),
         "gocr_op_attention_packed_backward": (i32, [vp] * 10 + [i32] * 5 + [i64] * 3 + [f32, vp, sz, vp]),
@@ -659,9 +660,11 @@ def op_linear_ce(x, w, labels, workspace=None):
     return loss, lse
 
 
-def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None):
+def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None, loss=None):
     """(dx [T, H], dw [V, H]) bf16: the gradient of sum(dloss * loss) of
-    op_linear_ce, from its lse; dloss fp32 [T] holds the rows' weights."""
+    op_linear_ce, from its lse; dloss fp32 [T] holds the rows' weights.  With
+    the forward call's loss, too, the gradient of rows whose loss is small
+    (below 1e-3) keeps its relative precision."""
     torch = _torch()
     lib = load()
     _lead("x", x, 2, torch.bfloat16)
@@ -671,11 +674,13 @@ def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None):
     _want("labels", labels, (T,), torch.int32, dev)
     _want("dloss", dloss, (T,), torch.float32, dev)
     _want("lse", lse, (T,), torch.float32, dev)
+    if loss is not None:
+        _want("loss", loss, (T,), torch.float32, dev)
     _on_cuda(dev)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     ws = _workspace(workspace, lib.gocr_op_linear_ce_backward_workspace(T, V, H), dev)
-    _launch(dev, lib.gocr_op_linear_ce_backward, dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
-            lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(), ws.numel())
+    _launch(dev, lib.gocr_op_linear_ce_backward_with_loss, dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
+            loss.data_ptr() if loss is not None else None, lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(), ws.numel())
     return dx, dw
 
 
