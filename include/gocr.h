@@ -423,9 +423,10 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
  * clean or a corrupted stream's mean, say); rows without a target add nothing
  * (their dloss and lse count for nothing, whatever they hold).  z is computed
  * again in pieces of the vocabulary; (softmax - one-hot) dloss / u is rounded to
- * bf16 for the products, whose sums are in fp32 and are multiplied by u: the
- * mantissa of the first target's weight, so that the weight of a mean is not
- * rounded. */
+ * bf16 for the products, whose sums are in fp32 and are multiplied by u.  u
+ * follows from the smallest and the largest mantissa among the targets' weights
+ * and is such that bf16 holds both nearly exactly in units of it: neither the
+ * weight of a mean nor those of two streams' means are a common rounding error. */
 size_t gocr_op_linear_ce_backward_workspace(int T, int V, int H);
 int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w, const int32_t* labels,
                                const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
             tc::fence_after_sync();
             const float to_new = grow ? mx : ref;
-            const float f = ex2(ref2 - to_new * sl2);
+            const float f = tc::ex2(ref2 - to_new * sl2);
             ref = to_new;
             ref2 = ref * sl2;
             l *= f;
@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int x = 0; x < 32; ++x) {
           float p, q;
           split(fma2(f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), scale2, ref22), p, q);
-          p = ex2(p);
-          q = ex2(q);
+          p = tc::ex2(p);
+          q = tc::ex2(q);
           s4[x & 3] = add2(s4[x & 3], f2(p, q));
           u[x] = pack2(p, q);
         }

@@ -16,14 +16,6 @@ namespace packed {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-// 2^x of the special-function unit (relative error 2^-22; subnormal results
-// become zero, which is below every rounding here).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 operations an instruction.
 struct F2 { unsigned long long v; };
 __device__ __forceinline__ F2 f2(float x, float y) {

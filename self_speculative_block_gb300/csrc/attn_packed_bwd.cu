@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
       s = dot8(t[0][r][l], t[1][key][l], s);
       dp = dot8(t[2][r][l], t[3][key][l], dp);
     }
-    float x = key <= r ? ex2((s * a.scale - a.lse[(size_t)head * a.T + row0 + r]) * LOG2E) * dp : 0.f;
+    float x = key <= r ? tc::ex2((s * a.scale - a.lse[(size_t)head * a.T + row0 + r]) * LOG2E) * dp : 0.f;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     if (key == 0) out[r] = x;
@@ -372,11 +372,11 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
           const float4 r = lse[i / 4];  // -lse, in units of log2
           float x, y;
           split(fma2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), scale2, f2(r.x, r.y)), x, y);
-          p[i] = ex2(x);
-          p[i + 1] = ex2(y);
+          p[i] = tc::ex2(x);
+          p[i + 1] = tc::ex2(y);
           split(fma2(f2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), scale2, f2(r.z, r.w)), x, y);
-          p[i + 2] = ex2(x);
-          p[i + 3] = ex2(y);
+          p[i + 2] = tc::ex2(x);
+          p[i + 3] = tc::ex2(y);
         }
         if (cut)
 #pragma unroll
@@ -620,8 +620,8 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
         for (int i = 0; i < 64; i += 2) {
           float x, y;
           split(fma2(f2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), scale2, lse2), x, y);
-          p[i] = ex2(x);
-          p[i + 1] = ex2(y);
+          p[i] = tc::ex2(x);
+          p[i + 1] = tc::ex2(y);
         }
       }
       if (!(ok = tc::mbar_wait_warp(dp_full, it & 1))) break;

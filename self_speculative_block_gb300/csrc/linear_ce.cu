@@ -3,7 +3,7 @@
 //
 //   z_tv = x_t . w_v      lse_t = log sum_v exp z_tv      loss_t = lse_t - z_t,y(t)
 //   g_tv = (exp(z_tv - lse_t) - [v = y(t)]) dloss_t        dx = g W      dw = g^T x
-//   (g is kept without the mantissa of the rows' common weight: weight_unit)
+//   (g is kept divided by a unit that the rows' weights share: weight_unit)
 //
 // All of it is matrix products on tcgen05: 2 T V H operations forward, 6 T V H
 // backward (z again, dx, dw).  One persistent kernel shape serves the three
@@ -63,8 +63,10 @@ constexpr int BOX = 64 * 128;            // one box of 64 rows x 64 columns
 constexpr int STORE_BYTES = 32 * 128;    // one epilogue box: 32 rows x 128 bytes
 constexpr int OFF_STORE = RING;
 constexpr int OFF_BAR = OFF_STORE + 4 * 2 * STORE_BYTES;
+constexpr int OFF_UNIT = OFF_BAR + 384;  // weight_unit's eight words, behind the barriers
 constexpr int SMEM = OFF_BAR + 512 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+static_assert((2 * MAX_STAGES + 4) * 8 + 4 <= OFF_UNIT - OFF_BAR, "room for the barriers");
 constexpr int THREADS = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -102,6 +104,7 @@ struct Args {
   const float* lse;
   const float* loss;    // GRAD: the forward call's, or null
   const float* dloss;
+  float* unit;          // GRAD of the first piece writes it (weight_unit), the later launches read it
   float2* part;         // STATS: [T][vocabulary tiles] (maximum, sum)
   int m_tiles, n_tiles; // STATS, GRAD; n_tiles also of PROD
   int tn;               // STATS, GRAD: columns of a tile
@@ -164,33 +167,65 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // Byte offset of 16-byte chunk c of row r in a 32-row swizzled box.
 __device__ __forceinline__ uint32_t box_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// The factor that g is without and its sums get back in fp32: the mantissa, in
-// [1, 2), of the first target's weight.  The rows of a mean have one weight, or
-// a few that are powers of two apart; with it in g, the bf16 rounding of nearly
-// every label's g would be the same relative error, up to 2^-8, and would not
-// average out of dx and dw.  One warp, all lanes get the answer.
-__device__ __forceinline__ float weight_unit(const float* dloss, const int* labels, int T, int V) {
+// The factor that g is divided by and its sums get back in fp32.  A stream's rows
+// have one weight in a mean, and the label's g is nearly all of it: rounded to
+// bf16 with the weight in it, that would be the same relative error of the whole
+// stream, up to 2^-8, which does not average out of dx and dw.  With the streams of a
+// joint loss there are two weights (powers of two aside).  So the unit is the one,
+// up to a power of two in [1, 2), in which the smallest mantissa among the targets'
+// weights is a / 128 with a whole number a, and of those a the one that brings the
+// largest mantissa nearest to 8 bits, too: means over 2,000 to 4,000 and 600 to
+// 2,000 rows keep a common error of 4e-5 on average instead of 1.6e-3.  One weight:
+// a = 128 and no error.  Further weights between the two are rounded as they come.
+// The 128 threads of the epilogue warps, while the first tile's products run; all
+// get the answer.
+__device__ __forceinline__ float weight_unit(const float* dloss, const int* labels, int T, int V, unsigned* tmp) {
   constexpr int PER = 8;
-  const int lane = threadIdx.x & 31;
-  for (int t0 = 0; t0 < T; t0 += 32 * PER) {
+  const int me = threadIdx.x - 64, lane = threadIdx.x & 31;
+  unsigned lo = 0x00800000u, hi = 0;  // mantissa bits
+  for (int t0 = 0; t0 < T; t0 += 128 * PER) {
     float f[PER];
+    int label[PER];
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      const int t = t0 + u * 32 + lane;
-      const float d = t < T ? fabsf(dloss[t]) : 0.f;  // beside the label, not after it
-      const int label = t < T ? labels[t] : -1;
-      f[u] = (unsigned)label < (unsigned)V ? d : 0.f;
+      const int t = t0 + u * 128 + me;
+      f[u] = t < T ? fabsf(dloss[t]) : 0.f;
+      label[u] = t < T ? labels[t] : -1;
     }
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const unsigned some = __ballot_sync(0xffffffffu, f[u] >= 1.1754943508e-38f && f[u] <= 3.4028234664e38f);
-      if (some) {
-        const float first = __shfl_sync(0xffffffffu, f[u], __ffs(some) - 1);
-        return __uint_as_float((__float_as_uint(first) & 0x007fffffu) | 0x3f800000u);
+    for (int u = 0; u < PER; ++u)
+      if ((unsigned)label[u] < (unsigned)V && f[u] >= 1.1754943508e-38f && f[u] <= 3.4028234664e38f) {
+        lo = min(lo, __float_as_uint(f[u]) & 0x007fffffu);
+        hi = max(hi, __float_as_uint(f[u]) & 0x007fffffu);
       }
-    }
   }
-  return 1.f;
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    tmp[me >> 5] = lo;
+    tmp[4 + (me >> 5)] = hi;
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  for (int w = 0; w < 4; ++w) {
+    lo = min(lo, tmp[w]);
+    hi = max(hi, tmp[4 + w]);
+  }
+  if (lo > hi) return 1.f;  // no target with a weight
+  const float m = __uint_as_float(lo | 0x3f800000u);
+  if (lo == hi) return m;
+  const float ratio = __uint_as_float(hi | 0x3f800000u) / m;  // 1 .. 2
+  unsigned least = 0xffffffffu;
+  int a = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int k = 128 + lane * 4 + i;
+    const float y = k * ratio, r = y < 256.f ? rintf(y) : 2.f * rintf(0.5f * y);
+    const unsigned e = __float_as_uint(fabsf(r - y) / y);
+    if (e < least) { least = e; a = k; }
+  }
+  const unsigned e = __reduce_min_sync(0xffffffffu, least);
+  a = (int)__reduce_min_sync(0xffffffffu, least == e ? (unsigned)a : 256u);
+  const float u = m * 128.f / a;
+  return u < 1.f ? 2.f * u : u;
 }
 
 template <int KIND>
@@ -302,7 +337,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
     const int q = warp & 3;  // the tensor memory lanes this warp may read: 32 q ..
     uint8_t* box = sm + OFF_STORE + q * 2 * STORE_BYTES;
     int acc = 0, aph = 0, buf = 0;
-    const float unit = KIND == STATS ? 1.f : weight_unit(a.dloss, a.labels, a.T, a.V);
+    float unit = 1.f;
+    if (KIND == GRAD && a.v0 == 0) {
+      unit = weight_unit(a.dloss, a.labels, a.T, a.V, reinterpret_cast<unsigned*>(sm + OFF_UNIT));
+      if (blockIdx.x == 0 && tid == 64) *a.unit = unit;
+    } else if (KIND != STATS) {
+      unit = *a.unit;
+    }
     for (int i = 0; tile_of<KIND>(a, pair, i, t); ++i) {
       const int row0 = t.m0 + rank * RM + q * 32;  // the warp's first row
       const int row = row0 + lane;
@@ -321,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           label = -1;
         }
       }
-      const bool has = label >= 0;
+      const uint32_t mask = label >= 0 ? 0xffffffffu : 0u;  // whatever z holds in a row without a target
       const float ref = lse * LOG2E;
       if (!(ok = tc::mbar_wait_warp(acc_full + acc, aph))) break;
       tc::fence_after_sync();
@@ -375,32 +416,32 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           for (int h = 0; h < 2; ++h) {
             float v[32];
             tc::tmem_ld32(src + c + h * 32, v);
+            // the epilogue is nearly as long as the products: with exp2f's care for
+            // subnormal results, and a select per element, a launch took 65 us, not 57
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = has ? f * exp2f(fmaf(v[j], LOG2E, -ref)) : 0.f;
+            for (int j = 0; j < 32; ++j) v[j] = f * tc::ex2(fmaf(v[j], LOG2E, -ref));
+            const unsigned at = (unsigned)(label - (col0 + c + h * 32));
+            if (__any_sync(0xffffffffu, at < 32u)) {
+              float g = own;
+              if (!a.loss) {  // the difference, but a share is not above one
+#pragma unroll
+                for (int j = 0; j < 32; ++j) g = at == (unsigned)j ? v[j] - f : g;
+                if ((__float_as_int(g) ^ __float_as_int(f)) >= 0 && g == g) g = 0.f;
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = at == (unsigned)j ? g : v[j];
+            }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const __nv_bfloat162 p = __floats2bfloat162_rn(v[g * 8 + 2 * e], v[g * 8 + 2 * e + 1]);
-                w[e] = *reinterpret_cast<const uint32_t*>(&p);
+                w[e] = *reinterpret_cast<const uint32_t*>(&p) & mask;
               }
               *reinterpret_cast<uint4*>(bx + box_at(lane, h * 4 + g)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          const unsigned at = (unsigned)(label - (col0 + c));
-          if (!a.loss && __any_sync(0xffffffffu, at < 64u)) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {  // z again: seldom here, so nothing is kept for it
-              float z[32];
-              tc::tmem_ld32(src + c + h * 32, z);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (at == (unsigned)(h * 32 + j)) own = z[j] - lse;
-            }
-            own = f * expm1f(own > 0.f ? 0.f : own);  // the log of the label's share is not above 0
-          }
-          if (at < 64u) *reinterpret_cast<bf16*>(bx + box_at(lane, at >> 3) + (at & 7) * 2) = __float2bfloat16_rn(own);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -543,10 +584,9 @@ __global__ void __launch_bounds__(128) linear_ce_join_kernel(const float2* part,
 // dx = the sum of the tile's parts, in slab order: memory-bound, 13 us for 4,096
 // rows x 1,536.
 __global__ void __launch_bounds__(256) linear_ce_dx_kernel(const float* slabs, bf16* dx, int T, int H, int n_tiles,
-                                                           size_t slab, Deal last, Deal before, const float* dloss,
-                                                           const int* labels, int V) {
+                                                           size_t slab, Deal last, Deal before, const float* unit_at) {
   tc::grid_dep_wait();
-  const float unit = weight_unit(dloss, labels, T, V);
+  const float unit = *unit_at;
   const size_t n = (size_t)T * H / 8, step = (size_t)gridDim.x * 256;
   for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += step) {
     const int row = (int)(i * 8 / H), col = (int)(i * 8 % H);
@@ -757,10 +797,11 @@ int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, cons
     return GOCR_OK;
   }
   float* slabs = (float*)((char*)workspace + p.off_slab);
+  float* unit = slabs + (size_t)p.slabs * p.slab_rows * H;
   Maps z{}, pr{};
   Args common{};
   common.T = T; common.H = H; common.V = V;
-  common.labels = labels; common.lse = lse; common.loss = loss; common.dloss = dloss;
+  common.labels = labels; common.lse = lse; common.loss = loss; common.dloss = dloss; common.unit = unit;
   common.tn = z_columns(T, p.piece, GRAD_STEP);
   set_ring(common, true);
   if (!map2(&z.a0, x, T, H, H, common.a_rows) || !map2(&z.b0, w, V, H, H, common.tn / 2) || !map2(&pr.b0, w, V, H, H, 64) ||
@@ -793,7 +834,7 @@ int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, cons
   const size_t vecs = (size_t)T * H / 8;
   const unsigned blocks = (unsigned)(vecs / 256 + 1 < 8u * SM_COUNT ? vecs / 256 + 1 : 8u * SM_COUNT);
   launch_k(linear_ce_dx_kernel, dim3(blocks), dim3(256), 0, s, true, (const float*)slabs, (bf16*)dx, T, H, cdiv(H, TN),
-           (size_t)p.slab_rows * H, p.last, p.full, dloss, labels, V);
+           (size_t)p.slab_rows * H, p.last, p.full, (const float*)common.unit);
   return op_launched("linear_ce dx");
 }
 

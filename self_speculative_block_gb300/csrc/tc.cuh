@@ -59,6 +59,14 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// 2^x of the special-function unit (relative error 2^-22; subnormal results
+// become zero, which is below every rounding here).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Wait bounded in time (WAIT_NS): false when it ran out.  For kernels whose
 // roles hand work to one another: each role that gives up ends its loop, and
 // the roles that wait on it end theirs within the same bound.

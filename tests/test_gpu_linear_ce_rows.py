@@ -1,5 +1,8 @@
 """Rows of the cross entropy's gradient that a tolerance over the whole softmax
-does not see: confident ones, whose gradient is as small as their loss."""
+does not see: confident ones, whose gradient is as small as their loss, and the
+streams of a joint loss, whose rows share a weight."""
+import math
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +101,60 @@ def test_linear_ce_gradient_with_and_without_loss_agree_on_unsure_rows(g):
     for p, q, mag in ((a[0], b[0], w[labels.clamp(min=0).long()].double().abs() * dloss[:, None]),):
         assert ((p.double() - q.double()).abs() <= 2 * U * mag + 2 * U * q.double().abs() + 1e-38).all()
     assert not b[0][labels < 0].any() and torch.isfinite(b[1]).all()
+
+
+def _off_8_bits(y):
+    """Relative distance of y to the nearest number of 8 significant bits."""
+    m, e = math.frexp(y)
+    return abs(round(m * 256) / 256 / m - 1)
+
+
+@pytest.mark.parametrize("n1,n2", [(2600, 1100), (3001, 777), (2048, 1999), (1, 1500)])
+def test_linear_ce_gradient_of_two_means(g, n1, n2):
+    """Two streams, each with a mean's weight: bf16 would round each weight by up to 2^-8, for
+    all of its stream's rows alike.  Targets of the two streams are of the two halves of the vocabulary."""
+    V, H, T = 5000, 128, n1 + n2
+    r = _gen(n1)
+    w = (H ** -0.5 * torch.randn((V, H), generator=r, device="cuda")).bfloat16()
+    x = torch.randn((T, H), generator=r, device="cuda").bfloat16()
+    second = torch.arange(T, device="cuda") >= n1
+    labels = torch.where(second, torch.randint(V // 2, V, (T,), generator=r, device="cuda"),
+                         torch.randint(0, V // 2, (T,), generator=r, device="cuda")).to(torch.int32)
+    _, lse = g.op_linear_ce(x, w, labels)
+    grads = lambda dloss: [t.double() for t in g.op_linear_ce_backward(dloss.float(), x, w, labels, lse)]
+    weight = [float(torch.tensor(0.5 / n)) for n in (n1, n2)]
+    lo, hi = sorted(math.frexp(a)[0] for a in weight)
+    # the best that two weights can be in units of a common one, and less than it would be without
+    best = min(_off_8_bits(a * hi / lo) for a in range(128, 256))
+    assert best < 2.0 ** -11
+    apart = [grads(~second), grads(second)]
+    both = grads(torch.where(second, weight[1], weight[0]))
+    for name, i, parts in (("dx", 0, (slice(0, n1), slice(n1, T))), ("dw", 1, (slice(0, V // 2), slice(V // 2, V)))):
+        want = weight[0] * apart[0][i] + weight[1] * apart[1][i]
+        for s in parts:
+            a, b = both[i][s], want[s]
+            # independent roundings, of 2^-7 / sqrt(3) standard deviation at most, over the values that
+            # count; and the label's 1 - p, which rounds to one on both sides but for the few rows with
+            # a p between 2^-9 and 2^-7, less than one in a hundred
+            n = float(b.square().sum() ** 2 / (b ** 4).sum())
+            mean = float(((a - b) * b).sum() / b.square().sum())
+            assert abs(mean) <= best + 2.0 ** -14 + 6 * 2.0 ** -7 / 3 ** 0.5 / n ** 0.5, (name, s, mean, best, n)
+
+
+def test_linear_ce_gradient_of_one_target_behind_many_rows(g):
+    """Only the last of many rows has a target; the others' weights and lse hold NaN."""
+    T, V, H = 5000, 700, 64
+    r = _gen(9)
+    w, x = torch.randn((V, H), generator=r, device="cuda").bfloat16(), torch.randn((T, H), generator=r, device="cuda").bfloat16()
+    labels = torch.full((T,), V, dtype=torch.int32, device="cuda")
+    labels[-1] = 5
+    dloss = torch.full((T,), math.nan, device="cuda")
+    dloss[-1] = 1.0 + 2.0 ** -8 - 2.0 ** -20
+    _, lse = g.op_linear_ce(x, w, labels)
+    lse[:-1] = math.nan
+    dx, dw = g.op_linear_ce_backward(dloss, x, w, labels, lse)
+    assert not dx[:-1].any()
+    one = g.op_linear_ce_backward(dloss[-1:], x[-1:].contiguous(), w, labels[-1:], lse[-1:])
+    # the sums of the two calls are cut into parts differently, in fp32, before the last rounding
+    for a, b in ((dx[-1:], one[0]), (dw, one[1])):
+        assert ((a.double() - b.double()).abs() <= (2 * U + 2.0 ** -12) * b.double().abs() + 2.0 ** -20).all()
