@@ -421,7 +421,7 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
 /* Gradient of sum_t dloss[t] loss[t]: dx[T, H] and dw[V, H] in bf16, from the
  * forward call's lse.  dloss[t] is the row's weight in the training loss (of a
  * clean or a corrupted stream's mean, say); rows without a target add nothing
- * (their dloss and lse count for nothing, whatever they hold).  z is computed
+ * (their dloss, lse and x count for nothing, whatever they hold).  z is computed
  * again in pieces of the vocabulary; (softmax - one-hot) dloss / u is rounded to
  * bf16 for the products, whose sums are in fp32 and are multiplied by u.  u
  * follows from the smallest and the largest mantissa among the targets' weights

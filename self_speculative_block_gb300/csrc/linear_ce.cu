@@ -76,7 +76,7 @@ static __device__ int g_error;  // DevErr of a wait that gave up
 
 struct Maps {
   CUtensorMap a0, b0;   // STATS, GRAD: x, w.  PROD: g (rows), w (N-major)
-  CUtensorMap a1, b1;   // PROD: g (columns), x (N-major)
+  CUtensorMap a1, b1;   // PROD: g (columns), x of the rows with a target (N-major)
   CUtensorMap out0;     // GRAD: g.  PROD: the dx slabs
   CUtensorMap out1;     // PROD: dw
 };
@@ -104,6 +104,8 @@ struct Args {
   const float* lse;
   const float* loss;    // GRAD: the forward call's, or null
   const float* dloss;
+  const uint4* x;       // GRAD of the first piece: x, and
+  uint4* x_targets;     // where copy_targets puts it
   float* unit;          // GRAD of the first piece writes it (weight_unit), the later launches read it
   float2* part;         // STATS: [T][vocabulary tiles] (maximum, sum)
   int m_tiles, n_tiles; // STATS, GRAD; n_tiles also of PROD
@@ -228,6 +230,40 @@ __device__ __forceinline__ float weight_unit(const float* dloss, const int* labe
   return u < 1.f ? 2.f * u : u;
 }
 
+// x with zeros in the rows without a target, for dw = g^T x: their g is zero, but
+// nobody need have written their x, and zero times NaN is NaN.  The MMA warps of
+// the odd CTAs, which have nothing else to do, while the first piece's g is made;
+// w of n warps, COPY vectors a lane in flight.
+__device__ __forceinline__ void copy_targets(const Args& a, int w, int n) {
+  constexpr int COPY = 16;
+  const int lane = threadIdx.x & 31, vecs = a.H / 8, parts = (vecs + 31) / 32;
+  const long long total = (long long)a.T * parts;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (long long i0 = (long long)w * COPY; i0 < total; i0 += (long long)n * COPY) {
+    const int row0 = (int)(i0 / parts), part0 = (int)(i0 % parts);
+    uint4 v[COPY];
+    int label[COPY];
+    int row = row0, part = part0;
+#pragma unroll
+    for (int u = 0; u < COPY; ++u) {
+      const int c = part * 32 + lane;
+      const bool in = row < a.T && c < vecs;
+      v[u] = in ? a.x[(size_t)row * vecs + c] : zero;
+      label[u] = in ? a.labels[row] : -1;
+      if (++part == parts) { part = 0; ++row; }
+    }
+    row = row0;
+    part = part0;
+#pragma unroll
+    for (int u = 0; u < COPY; ++u) {
+      const int c = part * 32 + lane;
+      if (row < a.T && c < vecs) a.x_targets[(size_t)row * vecs + c] = (unsigned)label[u] < (unsigned)a.V ? v[u] : zero;
+      if (++part == parts) { part = 0; ++row; }
+    }
+  }
+  asm volatile("fence.proxy.async;" ::: "memory");  // PROD reads it by TMA
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -304,9 +340,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
         if (++st == a.stages) { st = 0; ph ^= 1; }
       }
     }
+  } else if (warp == 1 && rank == 1) {
+    if (KIND == GRAD && a.v0 == 0) copy_targets(a, pair, gridDim.x / 2);
   } else if (warp == 1) {
     int st = 0, ph = 0, acc = 0, aph = 0;
-    for (int i = 0; rank == 0 && ok && tile_of<KIND>(a, pair, i, t); ++i) {
+    for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
       if (!(ok = tc::mbar_wait_warp(acc_free + acc, aph ^ 1))) break;
       tc::fence_after_sync();
       const uint32_t d = tmem + acc * TN;
@@ -629,7 +667,7 @@ constexpr int MAX_PARTS = 32;
 struct BackwardPlan {
   int piece, slabs, slab_rows;
   Deal full, last;         // of the pieces before the last (tiles = 0: none), of the last
-  size_t off_slab, bytes;
+  size_t off_slab, off_x, bytes;
 };
 
 Deal deal_of(int T, int vc, int H) {
@@ -674,7 +712,8 @@ BackwardPlan backward_plan(int T, int V, int H) {
   if (n > 1 && most_parts(p.full) > p.slabs) p.slabs = most_parts(p.full);
   p.slab_rows = cdiv(rows, TM) * TM;
   p.off_slab = up256((size_t)T * p.piece * 2);
-  p.bytes = p.off_slab + (size_t)p.slabs * p.slab_rows * H * 4 + 256;
+  p.off_x = p.off_slab + up256((size_t)p.slabs * p.slab_rows * H * 4);
+  p.bytes = p.off_x + up256((size_t)T * H * 2) + 256;  // the unit comes last
   return p;
 }
 
@@ -797,15 +836,17 @@ int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, cons
     return GOCR_OK;
   }
   float* slabs = (float*)((char*)workspace + p.off_slab);
-  float* unit = slabs + (size_t)p.slabs * p.slab_rows * H;
+  void* x_targets = (char*)workspace + p.off_x;
+  float* unit = (float*)((char*)workspace + p.bytes - 256);
   Maps z{}, pr{};
   Args common{};
   common.T = T; common.H = H; common.V = V;
   common.labels = labels; common.lse = lse; common.loss = loss; common.dloss = dloss; common.unit = unit;
+  common.x = (const uint4*)x; common.x_targets = (uint4*)x_targets;
   common.tn = z_columns(T, p.piece, GRAD_STEP);
   set_ring(common, true);
   if (!map2(&z.a0, x, T, H, H, common.a_rows) || !map2(&z.b0, w, V, H, H, common.tn / 2) || !map2(&pr.b0, w, V, H, H, 64) ||
-      !map2(&pr.b1, x, T, H, H, 64) || !map2(&pr.out1, dw, V, H, H, 32))
+      !map2(&pr.b1, x_targets, T, H, H, 64) || !map2(&pr.out1, dw, V, H, H, 32))
     return bad_map();
   {
     const unsigned long long dims[2] = {(unsigned long long)H, (unsigned long long)p.slabs * p.slab_rows},

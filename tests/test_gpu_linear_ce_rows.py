@@ -158,3 +158,26 @@ def test_linear_ce_gradient_of_one_target_behind_many_rows(g):
     # the sums of the two calls are cut into parts differently, in fp32, before the last rounding
     for a, b in ((dx[-1:], one[0]), (dw, one[1])):
         assert ((a.double() - b.double()).abs() <= (2 * U + 2.0 ** -12) * b.double().abs() + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("T,V,H", [(1, 300, 64), (70, 500, 72), (300, 9000, 1000), (5000, 12 * 1024 + 77, 128)])
+def test_linear_ce_rows_without_target_may_hold_anything(g, T, V, H):
+    """Padding rows, which nothing has written: their x reaches neither dx nor dw, nor do their loss, lse and weight."""
+    r = _gen(T + V)
+    w, x = (torch.randn(s, generator=r, device="cuda").bfloat16() for s in ((V, H), (T, H)))
+    labels = torch.randint(0, V, (T,), generator=r, device="cuda", dtype=torch.int32)
+    no = torch.rand(T, generator=r, device="cuda") < 0.4
+    no[T // 2] = True
+    labels[no] = torch.tensor([-1, V, -100, 2 ** 31 - 1], device="cuda", dtype=torch.int32)[torch.arange(int(no.sum()), device="cuda") % 4]
+    dloss = torch.rand(T, generator=r, device="cuda")
+    x[no] = 0.0
+    loss, lse = g.op_linear_ce(x, w, labels)
+    want = g.op_linear_ce_backward(dloss, x, w, labels, lse, loss=loss)
+    for junk in (math.nan, math.inf):
+        for t in (x, dloss, loss, lse):
+            t[no] = junk
+        dx, dw = g.op_linear_ce_backward(dloss, x, w, labels, lse, loss=loss)
+        assert not dx[no].any()
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    loss, lse = g.op_linear_ce(x, w, labels)
+    assert not loss[no].any() and torch.isfinite(lse[~no]).all()
