@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         if (b == 0) {
           ref = mx == -INFINITY ? 0.f : mx;
-          ref2 = ref * sl2;
+          ref2 = __fmul_rn(ref, sl2);
         } else {
           const bool grow = (mx - ref) * sl2 > GROW;
           if (__any_sync(0xffffffffu, grow)) {
@@ -366,10 +366,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             // the next one waits for this block's P, so the parity is unambiguous
             if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
             tc::fence_after_sync();
-            const float to_new = grow ? mx : ref;
-            const float f = tc::ex2(ref2 - to_new * sl2);
+            // a row whose reference stays, beside one whose grows (which may be of the
+            // next sequence), keeps its bits: the products are rounded by themselves,
+            // not in a fused multiply-add, so that its factor is 2^0
+            const float to_new = grow ? mx : ref, to_new2 = __fmul_rn(to_new, sl2);
+            const float f = tc::ex2(ref2 - to_new2);
             ref = to_new;
-            ref2 = ref * sl2;
+            ref2 = to_new2;
             l *= f;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
