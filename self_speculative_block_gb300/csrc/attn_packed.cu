@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int s = i & 1;
         Block blk{0, 0, 0};
         while (id >= 0 && ok) {
-          blk = a.n_seq <= 32 ? find_block<true, 1>(a.cu, a.n_seq, a.T, QT, id / a.Hq, cursor)
-                              : find_block<true, 8>(a.cu, a.n_seq, a.T, QT, id / a.Hq, cursor);
+          blk = a.n_seq <= 32 ? find_block<1>(a.cu, a.n_seq, a.T, QT, id / a.Hq, cursor)
+                              : find_block<8>(a.cu, a.n_seq, a.T, QT, id / a.Hq, cursor);
           if (blk.len) break;
           ask_cta(work + 2, taken);
           id = taken_cta(work + 2, taken, takes++, ok);

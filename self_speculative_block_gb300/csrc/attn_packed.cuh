@@ -54,15 +54,14 @@ struct Block {
 // Where a search for a block may begin: a sequence, and the blocks before it.
 struct Cursor { int seq = 0, before = 0; };
 
-// The b-th block of `size` rows over all sequences, in a sequence's order or
-// its last block first (the order of falling work: the last query rows read
-// the most keys, the first keys are read by the most rows); one warp, all
-// lanes get the answer.  len = 0: there is no such block.  Whatever cu holds,
+// The b-th block of `size` rows over all sequences, a sequence's last block
+// first (its rows read the most keys); one warp, all lanes get the answer.  len = 0: there is no such block.  Whatever cu holds,
 // the rows stay within 0 .. T - 1.  A lane takes PER sequences at a time, whose
 // loads go out together, and a later search goes on where this one ended: with
 // 2,000 sequences of 64 a lane for each one and a fresh start took more time
-// than the attention (PER = 8 and going on: 2,400 -> 513 us).
-template <bool LAST_FIRST, int PER>
+// than the attention (PER = 8 and going on: 2,400 -> 513 us).  A CTA that has one
+// block only cannot go on: the backward call's take theirs from a table.
+template <int PER>
 __device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int size, int b, Cursor& from) {
   const int lane = threadIdx.x & 31;
   Block r{0, 0, 0};
@@ -90,7 +89,7 @@ __device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int
         if (open && at < n) {
           r.row0 = c[i];
           r.len = len;
-          r.at = (LAST_FIRST ? n - 1 - at : at) * size;
+          r.at = (n - 1 - at) * size;
           open = false;
         }
         at -= n;
@@ -105,6 +104,43 @@ __device__ __forceinline__ Block find_block(const int* cu, int n_seq, int T, int
     from.seq += 32 * PER;
   }
   return r;
+}
+
+// The blocks of `size` rows of all sequences, in order, as (row0, len, at), and
+// len = 0 for what is left of `n` entries.  One CTA of 256 threads.
+__device__ __forceinline__ void block_table(const int* cu, int n_seq, int T, int size, int4* table, int n) {
+  constexpr int PER = 8;
+  __shared__ int sums[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int before = 0;  // blocks of the steps before
+  for (int s0 = 0; s0 < n_seq; s0 += 256 * PER) {
+    const int s = s0 + tid * PER;
+    int c[PER + 1], sum = 0;
+#pragma unroll
+    for (int i = 0; i <= PER; ++i) c[i] = min(max(cu[min(s + i, n_seq)], 0), T);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += (max(c[i + 1] - c[i], 0) + size - 1) / size;
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int at = before + inc - sum;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) at += sums[w];
+      before += sums[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int len = max(c[i + 1] - c[i], 0);
+      for (int r = 0; r < len && at < n; r += size) table[at++] = make_int4(c[i], len, r, 0);
+    }
+  }
+  for (int i = before + tid; i < n; i += 256) table[i] = make_int4(0, 0, 0, 0);
 }
 
 // Most blocks of `size` rows that n_seq sequences of T rows in all can have.

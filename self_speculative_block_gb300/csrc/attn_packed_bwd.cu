@@ -37,8 +37,6 @@
 #include "../../include/gocr.h"
 #include "attn_packed.cuh"
 
-#include <type_traits>
-
 using namespace gocr;
 using namespace gocr::packed;
 
@@ -67,6 +65,7 @@ struct BwdArgs {
   const float* lse;
   const float* delta; const float* first;  // first: of the first FEW rows of a sequence
   bf16* dq; bf16* dk; bf16* dv;
+  const int4* table;  // the blocks of 128 rows
   int n_seq, T, Hq, Hkv;
   float scale;
 };
@@ -77,6 +76,7 @@ struct DeltaArgs {
   const int* cu;
   const float* lse;
   float* delta; float* first;
+  int4* table; int blocks;  // the table of blocks and its entries
   int n_seq, T, Hq, Hkv;
   float scale;
 };
@@ -91,20 +91,22 @@ __device__ __forceinline__ float dot8(const uint4& x, const uint4& y, float s) {
   return s;
 }
 
-// delta, two kinds of CTA.  The first n_seq x Hq take the first 32 rows of a
-// sequence for a q head, with its rows of q, k, v and do in shared memory and
-// lanes of keys; the others take o and do as they lie (of every row, which
-// costs less than finding out which they are), D / 8 lanes to a (row, head).
-// 8,192 rows x 12 heads: 13 us, 101 MB half of which the forward call left in L2;
-// with 15 sequences 15 us, the first rows' chains beside it.
+// The table of blocks, by the first CTA, and delta, by two kinds of CTA.  n_seq x
+// Hq take the first 32 rows of a sequence for a q head, with its rows of q, k, v
+// and do in shared memory and lanes of keys; the others take o and do as they lie
+// (of every row, which costs less than finding out which they are), D / 8 lanes to
+// a (row, head).  8,192 rows x 12 heads: 13 us, 101 MB half of which the forward call
+// left in L2; with 15 sequences 15 us, the first rows' chains beside it.
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
   constexpr int L = D / 8, LD = L + 1;  // 16-byte pieces of a row; row pitch in shared memory
   __shared__ uint4 t[4][FEW][LD];       // q, k, do, v
   if (threadIdx.x == 0) tc::grid_dep_launch();
+  if (blockIdx.x == 0) return block_table(a.cu, a.n_seq, a.T, 128, a.table, a.blocks);
+  const int b = blockIdx.x - 1;
   const int firsts = a.n_seq * a.Hq;
-  if ((int)blockIdx.x >= firsts) {
-    const long long i0 = (long long)(blockIdx.x - firsts) * (256 * FLAT) + threadIdx.x;  // of a piece of o
+  if (b >= firsts) {
+    const long long i0 = (long long)(b - firsts) * (256 * FLAT) + threadIdx.x;  // of a piece of o
     const long long n = (long long)a.T * a.Hq * L;
     const uint4 z = make_uint4(0, 0, 0, 0);
     uint4 x[FLAT], y[FLAT];
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const DeltaArgs a) {
     }
     return;
   }
-  const int head = blockIdx.x % a.Hq, seq = blockIdx.x / a.Hq;
+  const int head = b % a.Hq, seq = b / a.Hq;
   const int lo = min(max(a.cu[seq], 0), a.T), n = min(FEW, min(a.cu[seq + 1], a.T) - lo);
   if (n <= 0) return;
   const size_t row0 = lo;
@@ -266,7 +268,6 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       __syncwarp();
       // the stage's rows were last read for the block two back
       if (it > 1 && !(ok = tc::mbar_wait_warp(row_free + st, ph ^ 1))) break;
-      if (it == 0) tc::grid_dep_wait();  // for delta; nothing else here is that launch's
       float* lse = rows + st * 256;
       for (int i = lane; i < 128; i += 32) {
         const bool in = at + i < blk.len;
@@ -600,7 +601,6 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
     const bool in = row < blk.len;
     const size_t t = (size_t)blk.row0 + row;
     const float lse = in ? a.lse[(size_t)head * a.T + t] * -LOG2E : 0.f;
-    tc::grid_dep_wait();  // for delta; nothing else here is that launch's
     const float del = in ? -(row < FEW ? a.first : a.delta)[(size_t)head * a.T + t] : 0.f;
     const F2 scale2 = f2(a.scale * LOG2E, a.scale * LOG2E), lse2 = f2(lse, lse);
     const uint32_t tp = tmem + lanes + DP + half * 64;
@@ -676,27 +676,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                            const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                            const BwdArgs a, int n_dkv) {
   extern __shared__ __align__(1024) uint8_t sm[];
+  tc::grid_dep_wait();
   if (tc::smem_u32(sm) & 1023u) {  // every thread sees the same
     if (threadIdx.x == 0) atomicCAS(&g_error, 0, (int)DERR_CAPACITY);
-    tc::grid_dep_wait();
     return;
   }
+  // The blocks come from a table: with a search from the first sequence on in every
+  // CTA, 40,000 sequences of 5 took 78 ms, with the table 8.2 (10,000: 6.4 and 2.0; 256
+  // of 64: 0.35 and 0.33; 15 long ones the same).  A dk/dv CTA takes the first keys first,
+  // which the most rows read, a dq CTA the last rows, which read the most keys.
   int b = blockIdx.x;
-  // up to 32 sequences, one a lane: one load's latency, without the eight's arithmetic behind it
-  auto find = [&](auto last_first, int block) {
-    Cursor cursor;
-    return a.n_seq <= 32 ? find_block<last_first.value, 1>(a.cu, a.n_seq, a.T, 128, block, cursor)
-                         : find_block<last_first.value, 8>(a.cu, a.n_seq, a.T, 128, block, cursor);
-  };
-  if (b < n_dkv) {
-    const Block blk = find(std::false_type{}, b / a.Hkv);
-    if (blk.len) dkv_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hkv);
-    else tc::grid_dep_wait();
+  const bool dkv = b < n_dkv;
+  if (!dkv) b -= n_dkv;
+  const int4 e = a.table[b / (dkv ? a.Hkv : a.Hq)];
+  Block blk{e.x, e.y, e.z};
+  if (!blk.len) return;
+  if (dkv) {
+    dkv_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hkv);
   } else {
-    b -= n_dkv;
-    const Block blk = find(std::true_type{}, b / a.Hq);
-    if (blk.len) dq_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hq);
-    else tc::grid_dep_wait();
+    blk.at = (blk.len - 1) / 128 * 128 - blk.at;
+    dq_cta<D>(sm, mq, mk, mv, mdo, a, blk, b % a.Hq);
   }
 }
 
@@ -705,9 +704,10 @@ int backward(const CUtensorMap* m, const BwdArgs& a, const DeltaArgs& da, cudaSt
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_packed_bwd_kernel<D>), SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
   const long long firsts = (long long)a.n_seq * a.Hq, threads = (long long)a.T * a.Hq * (D / 8);
-  launch_k(attn_delta_kernel<D>, dim3((unsigned)(firsts + (threads + 256 * FLAT - 1) / (256 * FLAT))), dim3(256), 0, s, false, da);
+  launch_k(attn_delta_kernel<D>, dim3((unsigned)(1 + firsts + (threads + 256 * FLAT - 1) / (256 * FLAT))), dim3(256), 0, s,
+           false, da);
   if (int rc = op_launched("attention_packed delta")) return rc;
-  const long long blocks = max_blocks(a.n_seq, a.T, 128);
+  const long long blocks = da.blocks;
   launch_k(attn_packed_bwd_kernel<D>, dim3((unsigned)(blocks * (a.Hkv + a.Hq))), dim3(THREADS), SMEM, s, true, m[0], m[1],
            m[2], m[3], a, (int)(blocks * a.Hkv));
   return op_launched("attention_packed backward");
@@ -724,11 +724,14 @@ cudaError_t take_attn_packed_bwd_error(int* out) {
 }
 }  // namespace gocr
 
+static size_t table_at(int T, int Hq) { return ((size_t)T * Hq * 8 + 255) & ~(size_t)255; }
+
 extern "C" {
 
 size_t gocr_op_attention_packed_backward_workspace(int T, int Hq) {
   if (T < 0 || Hq < 1) return 0;
-  return (size_t)T * Hq * 8 + 256;
+  // delta and that of the first rows, and the table: no more than T blocks have a row
+  return table_at(T, Hq) + (size_t)T * sizeof(int4) + 256;
 }
 
 int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void* k, const void* v, const void* o,
@@ -752,9 +755,10 @@ int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void
     return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
   float* delta = (float*)workspace;
   float* first = delta + (size_t)T * Hq;
-  const BwdArgs a{cu_seqlens, lse, delta, first, (bf16*)dq, (bf16*)dk, (bf16*)dv, n_seq, T, Hq, Hkv, scale};
+  int4* table = (int4*)((char*)workspace + table_at(T, Hq));
+  const BwdArgs a{cu_seqlens, lse, delta, first, (bf16*)dq, (bf16*)dk, (bf16*)dv, table, n_seq, T, Hq, Hkv, scale};
   const DeltaArgs da{(const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)o, (const bf16*)d_o, ldq, ldk, ldv,
-                     cu_seqlens, lse, delta, first, n_seq, T, Hq, Hkv, scale};
+                     cu_seqlens, lse, delta, first, table, (int)max_blocks(n_seq, T, 128), n_seq, T, Hq, Hkv, scale};
   return d == 128 ? backward<128>(m, a, da, s) : backward<64>(m, a, da, s);
 }
 
