@@ -441,10 +441,19 @@ int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, cons
                                          const float* loss, const float* lse, void* dx, void* dw, int T, int V, int H,
                                          void* workspace, size_t workspace_bytes, void* stream);
 
-/* Synchronises `stream` and reports whether a kernel of these operators on the
- * current device gave up a wait since the last report (GOCR_EDEVICE; the
- * outputs of such a call are not valid). */
+/* Waits for `stream` and reports whether a kernel of these operators on the
+ * current device gave up a wait (they do after two seconds) since the calling
+ * thread last asked, or, at its first question, since the library was loaded:
+ * GOCR_EDEVICE; the outputs of such a call are not valid, and no other call
+ * reports it.  The kernels count, and nothing is cleared, so threads take no
+ * report from one another; which stream's kernel it was is not recorded.
+ * GOCR_EINVAL while `stream` is being captured. */
 int gocr_op_status(void* stream);
+
+/* For tests of a program's handling of gocr_op_status: one warp that waits for
+ * something that does not come, gives up after so many microseconds (1 to
+ * 1,000,000) and reports it as the operators' kernels do. */
+int gocr_op_wait_probe(int microseconds, void* stream);
 
 /* ---- allocation-free GEMM ------------------------------------------------ */
 

@@ -51,7 +51,7 @@ constexpr int QT = 256;        // query rows of a work item
 constexpr int SW = 8, THREADS = (SW + 4) * 32;
 constexpr float GROW = 8.f;    // log2 of the growth of a row's maximum that rescales O
 
-static __device__ int g_error;  // DevErr of a wait that gave up
+static __device__ unsigned g_gave_up;  // threads whose wait gave up, ever
 
 struct FwdArgs {
   const int* cu;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::fence_before_sync();  // O has been read before the next item's P V, which waits for its P
     }
   }
-  if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
+  if (!ok) atomicAdd(&g_gave_up, 1u);
   tc::fence_before_sync();
   __syncthreads();
   if (warp == SW + 1) {
@@ -449,11 +449,8 @@ template <int D> int forward(const CUtensorMap* m, const FwdArgs& a, cudaStream_
 }  // namespace
 
 namespace gocr {
-cudaError_t take_attn_packed_error(int* out) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_error, sizeof(int));
-  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_error, &zero, sizeof(int));
-  return e;
+cudaError_t attn_packed_gave_up(unsigned* out, cudaStream_t s) {
+  return cudaMemcpyFromSymbolAsync(out, g_gave_up, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
 }
 
 int attn_packed_check(int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk, long long ldv,

@@ -55,7 +55,8 @@ constexpr int BAR_OFF = ROW_OFF + 2 * 2 * 128 * 4;
 constexpr int SMEM = BAR_OFF + 256;
 static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 
-static __device__ int g_error;  // DevErr of a wait that gave up
+static __device__ unsigned g_gave_up;  // threads whose wait gave up, ever
+static __device__ unsigned g_unaligned;  // CTAs whose shared memory did not begin at a multiple of 1,024
 
 constexpr int FLAT = 4;  // 16-byte pieces of o and of do in flight a thread
 constexpr int FEW = 32;  // rows at the start of a sequence with delta from P and dP
@@ -436,7 +437,7 @@ __device__ void dkv_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& m
       }
     }
   }
-  if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
+  if (!ok) atomicAdd(&g_gave_up, 1u);
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 9) {
@@ -661,7 +662,7 @@ __device__ void dq_cta(uint8_t* sm, const CUtensorMap& mq, const CUtensorMap& mk
       for (int c = 0; c < D / 2; c += 32) store32(tq + c, a.scale, a.dq + (t * a.Hq + head) * D + half * (D / 2) + c, ok && in);
     }
   }
-  if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
+  if (!ok) atomicAdd(&g_gave_up, 1u);
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 9) {
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ __align__(1024) uint8_t sm[];
   tc::grid_dep_wait();
   if (tc::smem_u32(sm) & 1023u) {  // every thread sees the same
-    if (threadIdx.x == 0) atomicCAS(&g_error, 0, (int)DERR_CAPACITY);
+    if (threadIdx.x == 0) atomicAdd(&g_unaligned, 1u);
     return;
   }
   // The blocks come from a table: with a search from the first sequence on in every
@@ -716,11 +717,11 @@ int backward(const CUtensorMap* m, const BwdArgs& a, const DeltaArgs& da, cudaSt
 }  // namespace
 
 namespace gocr {
-cudaError_t take_attn_packed_bwd_error(int* out) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_error, sizeof(int));
-  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_error, &zero, sizeof(int));
-  return e;
+cudaError_t attn_packed_bwd_gave_up(unsigned* out, cudaStream_t s) {
+  return cudaMemcpyFromSymbolAsync(out, g_gave_up, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+}
+cudaError_t attn_packed_bwd_unaligned(unsigned* out, cudaStream_t s) {
+  return cudaMemcpyFromSymbolAsync(out, g_unaligned, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
 }
 }  // namespace gocr
 

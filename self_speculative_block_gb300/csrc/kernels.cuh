@@ -265,11 +265,13 @@ void set_lib_error(const char* msg);
 int op_fail(int code, const char* fmt, ...);
 int op_stream_check(cudaStream_t s);
 int op_launched(const char* what);
-// Error word of the file's kernels with bounded waits (a DevErr; read and
-// cleared on an idle stream).
-cudaError_t take_linear_ce_error(int* out);
-cudaError_t take_attn_packed_error(int* out);
-cudaError_t take_attn_packed_bwd_error(int* out);
+// Copies of the counts that a file's kernels keep on the device, put on `s`: threads
+// whose wait gave up, CTAs that found their shared memory unaligned.  The counts
+// only grow, so a reader takes nothing from another one.
+cudaError_t linear_ce_gave_up(unsigned* out, cudaStream_t s);
+cudaError_t attn_packed_gave_up(unsigned* out, cudaStream_t s);
+cudaError_t attn_packed_bwd_gave_up(unsigned* out, cudaStream_t s);
+cudaError_t attn_packed_bwd_unaligned(unsigned* out, cudaStream_t s);
 // Argument checks that the packed attention calls share.
 int attn_packed_check(int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk, long long ldv,
                       float scale);

@@ -72,7 +72,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 enum Kind { STATS, GRAD, PROD };
 
-static __device__ int g_error;  // DevErr of a wait that gave up
+static __device__ unsigned g_gave_up;  // threads whose wait gave up, ever
 
 struct Maps {
   CUtensorMap a0, b0;   // STATS, GRAD: x, w.  PROD: g (rows), w (N-major)
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
     }
     if (lane == 0) bulk_wait_all();
   }
-  if (!ok) atomicCAS(&g_error, 0, (int)DERR_TIMEOUT);
+  if (!ok) atomicAdd(&g_gave_up, 1u);
   tc::fence_before_sync();
   __syncthreads();
   __syncwarp();
@@ -771,11 +771,8 @@ int bad_map() { return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected"); }
 }  // namespace
 
 namespace gocr {
-cudaError_t take_linear_ce_error(int* out) {
-  const int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_error, sizeof(int));
-  if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_error, &zero, sizeof(int));
-  return e;
+cudaError_t linear_ce_gave_up(unsigned* out, cudaStream_t s) {
+  return cudaMemcpyFromSymbolAsync(out, g_gave_up, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
 }
 }  // namespace gocr
 

@@ -2,6 +2,7 @@
 // own, and the status call of the kernels that report through device words.
 #include "../../include/gocr.h"
 #include "kernels.cuh"
+#include "tc.cuh"
 
 #include <cstdarg>
 #include <cstdio>
@@ -44,19 +45,69 @@ int op_launched(const char* what) {
 
 using namespace gocr;
 
+namespace {
+
+__device__ unsigned g_probe;  // as the operators' counts
+
+// A wait on a barrier that nothing arrives on.
+__global__ void wait_probe_kernel(unsigned long long limit) {
+  __shared__ uint64_t bar;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bar, 1);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  if (!tc::mbar_wait_ns(&bar, 0, limit) && threadIdx.x == 0) atomicAdd(&g_probe, 1u);
+}
+
+// What a thread has seen of a device's counts.
+constexpr int COUNTS = 5, DEVICES = 64;
+thread_local unsigned t_seen[DEVICES][COUNTS];
+
+bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cap) != cudaSuccess) {
+    cudaGetLastError();  // the legacy stream, while another one is being captured
+    return true;
+  }
+  return cap != cudaStreamCaptureStatusNone;
+}
+
+}  // namespace
+
 extern "C" int gocr_op_status(void* stream) {
-  if (int rc = op_stream_check((cudaStream_t)stream)) return rc;
-  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
-  int ce = 0, af = 0, ab = 0;
-  if (e == cudaSuccess) e = take_linear_ce_error(&ce);
-  if (e == cudaSuccess) e = take_attn_packed_error(&af);
-  if (e == cudaSuccess) e = take_attn_packed_bwd_error(&ab);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (capturing(s)) return op_fail(GOCR_EINVAL, "a stream that is being captured cannot be waited for");
+  if (int rc = op_stream_check(s)) return rc;
+  unsigned now[COUNTS] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = linear_ce_gave_up(now, s);
+  if (e == cudaSuccess) e = attn_packed_gave_up(now + 1, s);
+  if (e == cudaSuccess) e = attn_packed_bwd_gave_up(now + 2, s);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(now + 3, g_probe, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = attn_packed_bwd_unaligned(now + 4, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return op_fail(GOCR_ECUDA, "status read failed: %s", cudaGetErrorString(e));
   }
-  if (ce || af || ab)
-    return op_fail(GOCR_EDEVICE, "a wait inside a kernel of %s gave up",
-                   ce ? "linear_ce" : (af ? "attention_packed" : "attention_packed_backward"));
+  if (dev >= DEVICES) return op_fail(GOCR_ECUDA, "device %d: no more than %d are served", dev, DEVICES);
+  bool grown[COUNTS];
+  for (int i = 0; i < COUNTS; ++i) {
+    grown[i] = now[i] != t_seen[dev][i];
+    t_seen[dev][i] = now[i];
+  }
+  if (grown[4]) return op_fail(GOCR_EDEVICE, "a kernel of attention_packed_backward was given unaligned shared memory");
+  static const char* const who[4] = {"linear_ce", "attention_packed", "attention_packed_backward", "wait_probe"};
+  for (int i = 0; i < 4; ++i)
+    if (grown[i]) return op_fail(GOCR_EDEVICE, "a wait inside a kernel of %s gave up", who[i]);
   return GOCR_OK;
+}
+
+extern "C" int gocr_op_wait_probe(int microseconds, void* stream) {
+  if (microseconds < 1 || microseconds > 1000000) return op_fail(GOCR_EINVAL, "a wait of %d microseconds", microseconds);
+  if (int rc = op_stream_check((cudaStream_t)stream)) return rc;
+  wait_probe_kernel<<<1, 32, 0, (cudaStream_t)stream>>>(microseconds * 1000ull);
+  return op_launched("wait_probe");
 }

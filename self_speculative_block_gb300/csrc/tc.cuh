@@ -71,7 +71,7 @@ __device__ __forceinline__ float ex2(float x) {
 // roles hand work to one another: each role that gives up ends its loop, and
 // the roles that wait on it end theirs within the same bound.
 constexpr unsigned long long WAIT_NS = 2000000000ull;
-__device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity, unsigned long long limit = WAIT_NS) {
   for (int i = 0; i < 256; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   unsigned long long t0, t;
@@ -80,7 +80,7 @@ __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity) {
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  } while (t - t0 < WAIT_NS);
+  } while (t - t0 < limit);
   return false;
 }
 

@@ -40,7 +40,7 @@ EXPORTS = ("gocr_create", "gocr_prefill", "gocr_decode", "gocr_decode_batch", "g
            "gocr_op_embed", "gocr_op_embed_backward_workspace", "gocr_op_embed_backward",
            "gocr_op_linear_ce_workspace", "gocr_op_linear_ce", "gocr_op_linear_ce_backward_workspace",
            "gocr_op_linear_ce_backward", "gocr_op_linear_ce_backward_with_loss", "gocr_op_attention_packed", "gocr_op_attention_packed_backward_workspace",
-           "gocr_op_attention_packed_backward", "gocr_op_status")
+           "gocr_op_attention_packed_backward", "gocr_op_status", "gocr_op_wait_probe")
 
 
 class GocrError(RuntimeError):
@@ -136,6 +136,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gocr_op_attention_packed_backward_workspace": (sz, [i32, i32]),
         "gocr_op_attention_packed_backward": (i32, [vp] * 10 + [i32] * 5 + [i64] * 3 + [f32, vp, sz, vp]),
         "gocr_op_status": (i32, [vp]),
+        "gocr_op_wait_probe": (i32, [i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -686,7 +687,9 @@ def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None, loss=None):
 
 def op_status(device="cuda") -> None:
     """Wait for the device's current stream; raise when a kernel of these
-    operators gave up a wait since the last call."""
+    operators gave up a wait since this thread last asked.  The other calls do
+    not wait and do not ask: a program does, once a step or before it trusts
+    what it saves."""
     torch = _torch()
     with torch.cuda.device(device):
         _check(load().gocr_op_status(torch.cuda.current_stream().cuda_stream))

@@ -43,3 +43,8 @@ def test_linear_ce_backward_checks_loss():
         gocr.op_linear_ce_backward(f, b, b, i, f, loss=f.double())
     with pytest.raises(ValueError, match="loss must be"):
         gocr.op_linear_ce_backward(f, b, b, i, f, loss=f[:3])
+
+
+def test_wait_probe_refuses_long_waits(lib):
+    for us in (0, -1, 1_000_001):
+        assert lib.gocr_op_wait_probe(us, None) == EINVAL and "microseconds" in _message(lib)
