@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* work_free = work_full + 2;  // [2]
   uint64_t* taken = work_free + 2;
   uint64_t* issued = taken + 1;            // the item's loads are on their way
-  uint32_t* holder = reinterpret_cast<uint32_t*>(issued + 1);
+  uint64_t* drained = issued + 1;          // [2] an MMA warp's products, at its end
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drained + 2);
   int4* work = reinterpret_cast<int4*>(sm + F::OFF_WORK);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int j = 0; j < 2; ++j) {
       tc::mbar_init(o_full + j, 1);
       tc::mbar_init(o_done + j, 1);
+      tc::mbar_init(drained + j, 1);
       tc::mbar_init(work_full + j, 1);
       tc::mbar_init(work_free + j, SW + 3);
     }
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp >= SW) {
     if (warp == SW) {
       // K(0), V(0), K(1), V(1), ... through the ring, Q behind the item's K(0)
-      int slot = 0, ph = 0;
+      int slot = 0, ph = 0, loads = 0, q_loads = 0;
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
         const int kvh = t.head / (a.Hq / a.Hkv);
@@ -203,6 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             load_tile<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, x & 1 ? &mv : &mk, kvh, t.blk.row0 + (x >> 1) * 128, full + slot);
           }
           __syncwarp();
+          ++loads;
           if (++slot == SLOTS) { slot = 0; ph ^= 1; }
           if (x == 0) {
             if (!(ok = tc::mbar_wait_warp(q_empty, (i & 1) ^ 1))) break;
@@ -212,11 +215,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (t.n1) load_tile<D>(sm + F::OFF_Q + TILE_BYTES<D>, &mq, t.head, t.blk.row0 + t.blk.at + 128, q_full);
             }
             __syncwarp();
+            ++q_loads;
           }
         }
         if (!ok) break;
         if (lane == 0) tc::mbar_arrive(issued);
       }
+      ok = tc::ring_landed(full, SLOTS, loads) && tc::ring_landed(q_full, 1, q_loads) && ok;
     } else if (warp < SW + 3) {
       const int j = warp - (SW + 1);  // the tile
       const uint32_t q = tc::smem_u32(sm + F::OFF_Q + j * TILE_BYTES<D>), kv = tc::smem_u32(sm + F::OFF_KV);
@@ -282,10 +287,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         ring += 2 * t.n;
       }
+      ok = tc::mma_drain(drained + j) && ok;
     } else {
       // the items: this CTA's own, then those of CTAs that have not started;
       // and the last V tile of a ragged item: nothing behind the sequence
-      int id = blockIdx.x, takes = 0, ring = 0;
+      int id = blockIdx.x, asks = 0, takes = 0, ring = 0;
       Cursor cursor;
       for (int i = 0; ok; ++i) {
         const int s = i & 1;
@@ -295,6 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                               : find_block<8>(a.cu, a.n_seq, a.T, QT, id / a.Hq, cursor);
           if (blk.len) break;
           ask_cta(work + 2, taken);
+          ++asks;
           id = taken_cta(work + 2, taken, takes++, ok);
         }
         const bool more = id >= 0;
@@ -308,6 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // no earlier: an item in hand here is one that no idle SM can take
         if (!(ok = tc::mbar_wait_warp(issued, i & 1))) break;
         ask_cta(work + 2, taken);
+        ++asks;
         const Item t(w);
         if (t.tail < 128) {
           const int x = ring + 2 * t.n - 1, slot = x % SLOTS;
@@ -319,6 +327,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         ring += 2 * t.n;
         id = taken_cta(work + 2, taken, takes++, ok);
+      }
+      if (asks > takes) {  // gave up with a question under way
+        bool answered;
+        taken_cta(work + 2, taken, takes, answered);
       }
     }
   } else {

@@ -66,7 +66,7 @@ constexpr int OFF_BAR = OFF_STORE + 4 * 2 * STORE_BYTES;
 constexpr int OFF_UNIT = OFF_BAR + 384;  // weight_unit's eight words, behind the barriers
 constexpr int SMEM = OFF_BAR + 512 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
-static_assert((2 * MAX_STAGES + 4) * 8 + 4 <= OFF_UNIT - OFF_BAR, "room for the barriers");
+static_assert((2 * MAX_STAGES + 5) * 8 + 4 <= OFF_UNIT - OFF_BAR, "room for the barriers");
 constexpr int THREADS = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   uint64_t* empty = full + MAX_STAGES;  // each CTA's: the stage has been read
   uint64_t* acc_full = empty + MAX_STAGES;  // [2], each CTA's
   uint64_t* acc_free = acc_full + 2;    // [2], the even CTA's: the epilogue warps of both
-  uint32_t* holder = reinterpret_cast<uint32_t*>(acc_free + 2);
+  uint64_t* drained = acc_free + 2;     // each CTA's: the products, at the MMA warp's end
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drained + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
   const int a_bytes = a.a_rows * 128;
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
       tc::mbar_init(acc_full + b, 1);
       tc::mbar_init(acc_free + b, 8);
     }
+    tc::mbar_init(drained, 1);
     tc::fence_mbar_init();
   }
   __syncwarp();
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
   Tile t;
 
   if (warp == 0) {
-    int st = 0, ph = 0;
+    int st = 0, ph = 0, loads = 0;
     for (int i = 0; ok && tile_of<KIND>(a, pair, i, t); ++i) {
       // few rows: the odd CTA has none; what its part of A then holds only
       // reaches accumulator rows that nobody reads
@@ -337,9 +339,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
           }
         }
         __syncwarp();
+        ++loads;
         if (++st == a.stages) { st = 0; ph ^= 1; }
       }
     }
+    // the even CTA's barriers count both CTAs' loads, and the odd one does not leave before it
+    if (rank == 0) ok = tc::ring_landed(full, a.stages, loads) && ok;
   } else if (warp == 1 && rank == 1) {
     if (KIND == GRAD && a.v0 == 0) copy_targets(a, pair, gridDim.x / 2);
   } else if (warp == 1) {
@@ -371,6 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ce_kernel(const __grid_cons
       acc ^= 1;
       if (acc == 0) aph ^= 1;
     }
+    ok = tc::mma_drain_pair(drained) && ok;
   } else {
     const int q = warp & 3;  // the tensor memory lanes this warp may read: 32 q ..
     uint8_t* box = sm + OFF_STORE + q * 2 * STORE_BYTES;

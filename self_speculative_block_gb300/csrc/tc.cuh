@@ -70,7 +70,7 @@ __device__ __forceinline__ float ex2(float x) {
 // Wait bounded in time (WAIT_NS): false when it ran out.  For kernels whose
 // roles hand work to one another: each role that gives up ends its loop, and
 // the roles that wait on it end theirs within the same bound.
-constexpr unsigned long long WAIT_NS = 2000000000ull;
+constexpr unsigned long long WAIT_NS = 2000000000ull;  // longer by far than any copy or product under way
 __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity, unsigned long long limit = WAIT_NS) {
   for (int i = 0; i < 256; ++i)
     if (mbar_try_wait(bar, parity)) return true;
@@ -87,6 +87,17 @@ __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity, uns
 // The same for a warp, which gets one verdict.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait_ns(bar, parity));
+}
+
+// What a role does last, whether it finished or gave up: it waits, within the same
+// bound, for what it has under way.  A copy that lands, or a product that ends,
+// after its CTA has left would do so in the shared or tensor memory of the next.
+// ring_landed: the loads into a ring of `stages` barriers, of which `loads` were
+// issued; mma_drain, below: the issuing warp's products.
+__device__ __forceinline__ bool ring_landed(uint64_t* full, int stages, int loads) {
+  bool r = true;
+  for (int s = 0; r && s < stages && s < loads; ++s) r = mbar_wait_warp(full + s, ((loads - 1 - s) / stages) & 1);
+  return r;
 }
 
 // 2-D tiled TMA load global -> shared, completion counted on `bar`.
@@ -221,6 +232,13 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                ::"r"(smem_u32(bar)) : "memory");
 }
 
+// `bar` (one arrival, used for nothing else) completes when the products that this warp issued have.
+__device__ __forceinline__ bool mma_drain(uint64_t* bar) {
+  if (elect_one()) mma_commit(bar);
+  __syncwarp();
+  return mbar_wait_warp(bar, 0);
+}
+
 // ---- CTA pairs: two CTAs of a cluster on one 256-row tile --------------------
 //
 // The even CTA of the pair issues the MMAs; each CTA holds its 128 rows of A,
@@ -252,6 +270,13 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
       ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+
+// As mma_drain, for the issuing CTA of a pair.
+__device__ __forceinline__ bool mma_drain_pair(uint64_t* bar) {
+  if (elect_one()) mma_commit_pair(bar);
+  __syncwarp();
+  return mbar_wait_warp(bar, 0);
 }
 
 // Load into this CTA's shared memory, completion counted on a barrier of
