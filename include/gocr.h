@@ -389,11 +389,14 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
  * rows ldq elements apart, k and v [T, Hkv, d] with rows ldk and ldv apart (so
  * the three may be column ranges of one fused projection; pitches % 8 == 0);
  * o [T, Hq, d] bf16 and lse [Hq, T] fp32 dense.  d 64 or 128, Hq % Hkv == 0,
- * scale > 0, Hq <= 1024, n_seq <= 2^20, T <= 2^24.  Rows that belong to no
+ * 0 < scale <= 1e30, Hq <= 1024, n_seq <= 2^20, T <= 2^24, (n_seq + T) (Hq + Hkv)
+ * <= 2^31 - 1, pitches <= 2^32.  exp(scale q k^T - m), with m within 2^8 of the
+ * row's maximum so far, is rounded to bf16 for the product with v; scores,
+ * softmax statistics and sums are in fp32.  Rows that belong to no
  * sequence are not read into any result, whatever they hold, and their o and
  * lse are left as they were; nothing of one sequence reaches another,
- * non-finite values included.  Within a sequence, a non-finite v or do may
- * reach the other rows of its block of 128. */
+ * non-finite values included.  Within a sequence a non-finite v may reach the
+ * rows before it, too, that share its block of 128; a non-finite q or k does not. */
 int gocr_op_attention_packed(const void* q, const void* k, const void* v, void* o, float* lse,
                              const int32_t* cu_seqlens, int n_seq, int T, int Hq, int Hkv, int d, long long ldq,
                              long long ldk, long long ldv, float scale, void* stream);
@@ -401,7 +404,12 @@ int gocr_op_attention_packed(const void* q, const void* k, const void* v, void* 
 /* Gradient of gocr_op_attention_packed from d_o [T, Hq, d] and the forward
  * call's o and lse: dq [T, Hq, d], dk and dv [T, Hkv, d] bf16, dense (rows that
  * belong to no sequence are left as they were).  dk and dv sum over the q
- * heads of the group; all sums are in fp32, in a fixed order. */
+ * heads of the group; all sums are in fp32, in a fixed order.  P = exp(S - lse)
+ * and dS = P (do v^T - delta) are rounded to bf16 for the products with do, q and
+ * k.  delta = do . o takes o as it was rounded to bf16; for the first 32 rows of a
+ * sequence, which see few keys, it is summed from P and do v^T instead.  Within a
+ * sequence a non-finite q, k, v or do may reach all gradients of its block of
+ * 128 rows, beside those that depend on it. */
 size_t gocr_op_attention_packed_backward_workspace(int T, int Hq);
 int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void* k, const void* v, const void* o,
                                       const float* lse, const int32_t* cu_seqlens, void* dq, void* dk, void* dv,

@@ -468,8 +468,10 @@ cudaError_t attn_packed_gave_up(unsigned* out, cudaStream_t s) {
 int attn_packed_check(int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk, long long ldv,
                       float scale) {
   if (n_seq < 0 || n_seq > (1 << 20) || T < 0 || T > (1 << 24) || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq > 1024 ||
-      (d != 64 && d != 128) || ((long long)n_seq + T) * (Hq + Hkv) > 0x7fffffffLL)
+      (d != 64 && d != 128))
     return op_fail(GOCR_EINVAL, "bad shape: %d sequences, T=%d Hq=%d Hkv=%d d=%d", n_seq, T, Hq, Hkv, d);
+  if (((long long)n_seq + T) * (Hq + Hkv) > 0x7fffffffLL)  // CTAs of a launch
+    return op_fail(GOCR_EINVAL, "bad shape: (%d sequences + T=%d) x (Hq=%d + Hkv=%d) is above 2^31 - 1", n_seq, T, Hq, Hkv);
   const long long most = 1ll << 32;  // row pitch: 2^33 bytes, within a TMA stride
   if (ldq < (long long)Hq * d || ldk < (long long)Hkv * d || ldv < (long long)Hkv * d || (ldq | ldk | ldv) % 8 ||
       ldq > most || ldk > most || ldv > most)

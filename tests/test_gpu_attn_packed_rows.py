@@ -1,5 +1,5 @@
-"""Rows of the packed attention beside rows of other sequences: the same bits,
-whatever the neighbours' scores do."""
+"""Rows of the packed attention beside others: the same bits whatever the scores of a
+neighbouring sequence do, and where a non-finite row of the own sequence reaches."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +45,26 @@ def test_attention_packed_row_does_not_depend_on_growing_neighbours(g, d, scale,
                 *(torch.cat([a, b]) for a, b in zip((k, v, do), more)), cu, scale)
     for name, a in alone.items():
         assert torch.equal(both[name][:, :n] if name == "lse" else both[name][:n], a), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_packed_non_finite_row(g, d, what, bad):
+    """Rows before row 300 of one sequence do not see it: o and lse keep their bits (with a
+    non-finite v, those of the blocks of 128 before its own), dq of the blocks before, too."""
+    n, H, at = 500, 2, 300
+    r = torch.Generator(device="cuda").manual_seed(d)
+    t = {x: torch.randn((n, H, d), generator=r, device="cuda").bfloat16() for x in ("q", "k", "v", "do")}
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    clean = _run(g, t["q"], t["k"], t["v"], t["do"], cu, None)
+    t[what] = t[what].clone()
+    t[what][at, 1, 5] = bad
+    got = _run(g, t["q"], t["k"], t["v"], t["do"], cu, None)
+    block = at // 128 * 128
+    keep = block if what == "v" else at
+    assert torch.equal(got["o"][:keep], clean["o"][:keep]) and torch.equal(got["lse"][:, :keep], clean["lse"][:, :keep])
+    assert torch.equal(got["dq"][:block], clean["dq"][:block])
+    assert all(torch.equal(got[x][:, 0], clean[x][:, 0]) for x in ("o", "dq", "dk", "dv"))  # the other head
+    if what in ("q", "do"):  # row 300 is the only one that reads them: later blocks of keys are not its
+        assert all(torch.equal(got[x][block + 128:], clean[x][block + 128:]) for x in ("o", "dq", "dk", "dv"))

@@ -48,3 +48,58 @@ def test_linear_ce_backward_checks_loss():
 def test_wait_probe_refuses_long_waits(lib):
     for us in (0, -1, 1_000_001):
         assert lib.gocr_op_wait_probe(us, None) == EINVAL and "microseconds" in _message(lib)
+
+
+def _packed(lib, n=2, T=8, Hq=4, Hkv=2, d=64, ld=None, scale=0.125, ws=None):
+    """Both calls, refused at the latest for a pointer (the forward's o) or the workspace."""
+    ld = ld or (Hq * d, Hkv * d, Hkv * d)
+    sizes = (n, T, Hq, Hkv, d, *ld, scale)
+    a = lib.gocr_op_attention_packed(P, P, P, ODD, P, P, *sizes, None), _message(lib)
+    b = lib.gocr_op_attention_packed_backward(P, P, P, P, P, P, P, P, P, P, *sizes, P, 0, None), _message(lib)
+    return a, b
+
+
+def _passes(answers):
+    (a, am), (b, bm) = answers
+    return a == EINVAL and "aligned" in am and b == ECAPACITY and "workspace" in bm
+
+
+def _refused(answers, word):
+    return all(rc == EINVAL and word in m for rc, m in answers)
+
+
+def test_attention_packed_limits(lib):
+    """Each limit that the header states: its last value passes, the next one is refused."""
+    assert _passes(_packed(lib))
+    assert _passes(_packed(lib, n=1 << 20)) and _refused(_packed(lib, n=(1 << 20) + 1), "shape")
+    assert _passes(_packed(lib, T=1 << 24)) and _refused(_packed(lib, T=(1 << 24) + 1), "shape")
+    assert _passes(_packed(lib, Hq=1024, Hkv=1)) and _refused(_packed(lib, Hq=1025, Hkv=1), "shape")
+    # (n_seq + T) (Hq + Hkv) <= 2^31 - 1: 2^31 - 1 is prime, so the nearest products around it
+    T, heads = 1 << 24, 128
+    n = (2 ** 31 - 1) // heads - T
+    assert n < 0  # 2^24 rows of 127 + 1 heads are already above
+    assert _refused(_packed(lib, n=1, T=T, Hq=127, Hkv=1), "2^31")
+    T = (2 ** 31 - 1) // heads - 1
+    assert _passes(_packed(lib, n=1, T=T, Hq=127, Hkv=1)) and _refused(_packed(lib, n=2, T=T, Hq=127, Hkv=1), "2^31")
+    most = 1 << 32
+    for i in range(3):
+        ld = [256, 128, 128]
+        ld[i] = most
+        assert _passes(_packed(lib, ld=ld))
+        ld[i] = most + 8
+        assert _refused(_packed(lib, ld=ld), "pitch")
+    assert _passes(_packed(lib, scale=1e30)) and _refused(_packed(lib, scale=1.1e30), "scale")
+
+
+def test_embed_and_linear_ce_limits(lib):
+    def embed(T=4, H=64, V=100):
+        return lib.gocr_op_embed(1, ODD, P, P, P, T, H, V, 1.0, None), _message(lib)
+    for k, last, step in (("T", 1 << 28, 1), ("H", 1 << 20, 8), ("V", 1 << 28, 1)):
+        assert "aligned" in embed(**{k: last})[1], k
+        assert "shape" in embed(**{k: last + step})[1], k
+
+    def ce(T=4, V=100, H=64):
+        return lib.gocr_op_linear_ce(ODD, P, P, P, P, T, V, H, P, 0, None), _message(lib)
+    for k, last, step in (("T", 1 << 22, 1), ("H", 1 << 15, 8), ("V", 1 << 22, 1)):
+        assert "aligned" in ce(**{k: last})[1], k
+        assert "shape" in ce(**{k: last + step})[1], k
