@@ -103,3 +103,28 @@ def test_embed_and_linear_ce_limits(lib):
     for k, last, step in (("T", 1 << 22, 1), ("H", 1 << 15, 8), ("V", 1 << 22, 1)):
         assert "aligned" in ce(**{k: last})[1], k
         assert "shape" in ce(**{k: last + step})[1], k
+
+
+def test_wrappers_refuse_sizes_past_32_bits():
+    """The library takes 32-bit sizes; a longer one must not arrive as its remainder."""
+    torch = pytest.importorskip("torch")
+    from self_speculative_block_gb300 import gocr
+    bf16 = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="meta")
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="meta")
+    f32 = lambda *s: torch.empty(s, dtype=torch.float32, device="meta")
+    many = 2 ** 32 + 8
+    for call in (lambda: gocr.op_embed(i32(4), bf16(many, 8)),
+                 lambda: gocr.op_embed(i32(many), bf16(4, 8)),
+                 lambda: gocr.op_embed_backward(bf16(many, 8), i32(many), 10),
+                 lambda: gocr.op_embed_backward(bf16(4, 8), i32(4), many),
+                 lambda: gocr.op_embed_backward(bf16(4, 8), i32(4), -1),
+                 lambda: gocr.op_attention_packed(bf16(many, 1, 64), bf16(many, 1, 64), bf16(many, 1, 64), i32(2)),
+                 lambda: gocr.op_attention_packed(bf16(4, 1, 64), bf16(4, 1, 64), bf16(4, 1, 64), i32(many)),
+                 lambda: gocr.op_attention_packed_backward(bf16(many, 1, 64), bf16(many, 1, 64), bf16(many, 1, 64),
+                                                           bf16(many, 1, 64), bf16(many, 1, 64), f32(1, many), i32(2)),
+                 lambda: gocr.op_linear_ce(bf16(many, 8), bf16(4, 8), i32(many)),
+                 lambda: gocr.op_linear_ce(bf16(4, 8), bf16(many, 8), i32(4)),
+                 lambda: gocr.op_linear_ce_backward(f32(4), bf16(4, 8), bf16(many, 8), i32(4), f32(4))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
