@@ -479,7 +479,7 @@ def op_attention(q, kc, vc, lim, dtype: int, lo2=None, hi2=None):
 
 
 # ----------------------------------------------------------------------------
-# training and scoring operators
+# training and scoring operators (outside autograd: each has a call for its gradient)
 # ----------------------------------------------------------------------------
 
 def _want(name: str, t, shape: tuple, dtype, device):
@@ -503,11 +503,16 @@ def _lead(name: str, t, dims: int, *dtypes):
         raise ValueError(f"{name} must be a tensor of {dims} dimensions, got {list(t.shape)}")
 
 
-def _ready(device, sizes) -> None:
+def _ready(device, sizes, *operands) -> None:
     """The last checks before device work.  Sizes go to the library as 32-bit
-    numbers, which would be cut silently."""
+    numbers, which would be cut silently; the calls build no autograd graph, so an
+    operand that wants a gradient would lose it silently."""
     if max(sizes) > 0x7fffffff or min(sizes) < 0:
         raise ValueError(f"a size of {list(sizes)} is outside 0 .. 2^31 - 1")
+    for t in operands:
+        if t is not None and t.requires_grad and _torch().is_grad_enabled():
+            raise ValueError("an operand requires grad, but these calls are outside autograd: detach it, or call "
+                             "under torch.no_grad(), and use the _backward calls")
     if device.type != "cuda":
         raise ValueError(f"the operands must be CUDA tensors, got {device}")
 
@@ -542,7 +547,7 @@ def op_embed(ids, embed, mask_embed=None, scale: float = 1.0):
     _want("ids", ids, (T,), torch.int32, dev)
     if mask_embed is not None:
         _want("mask_embed", mask_embed, (H,), embed.dtype, dev)
-    _ready(dev, (T, H, V))
+    _ready(dev, (T, H, V), embed, mask_embed)
     y = torch.empty((T, H), dtype=embed.dtype, device=dev)
     _launch(dev, load().gocr_op_embed, _dt(embed), embed.data_ptr(), mask_embed.data_ptr() if mask_embed is not None
             else None, ids.data_ptr(), y.data_ptr(), T, H, V, scale)
@@ -558,7 +563,7 @@ def op_embed_backward(dy, ids, vocab: int, scale: float = 1.0, mask: bool = Fals
     dev, (T, H) = dy.device, dy.shape
     _want("dy", dy, (T, H), dy.dtype, dev)
     _want("ids", ids, (T,), torch.int32, dev)
-    _ready(dev, (T, H, vocab))
+    _ready(dev, (T, H, vocab), dy)
     d_embed = torch.empty((vocab, H), dtype=dy.dtype, device=dev)
     d_mask = torch.empty((H,), dtype=dy.dtype, device=dev) if mask else None
     ws = _workspace(workspace, lib.gocr_op_embed_backward_workspace(T, H), dev)
@@ -605,7 +610,7 @@ def op_attention_packed(q, k, v, cu_seqlens, scale=None, o=None, lse=None):
     not written."""
     torch = _torch()
     dev, T, Hq, Hkv, d, sizes = _packed_args(q, k, v, cu_seqlens, scale)
-    _ready(dev, sizes[:5])
+    _ready(dev, sizes[:5], q, k, v)
     if o is None:
         o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
     else:
@@ -630,7 +635,7 @@ def op_attention_packed_backward(do, q, k, v, o, lse, cu_seqlens, scale=None, wo
     _want("do", do, (T, Hq, d), torch.bfloat16, dev)
     _want("o", o, (T, Hq, d), torch.bfloat16, dev)
     _want("lse", lse, (Hq, T), torch.float32, dev)
-    _ready(dev, sizes[:5])
+    _ready(dev, sizes[:5], do, q, k, v, o, lse)
     out = []
     for name, t, heads in (("dq", dq, Hq), ("dk", dk, Hkv), ("dv", dv, Hkv)):
         if t is None:
@@ -656,7 +661,7 @@ def op_linear_ce(x, w, labels, workspace=None):
     _want("x", x, (T, H), torch.bfloat16, dev)
     _want("w", w, (V, H), torch.bfloat16, dev)
     _want("labels", labels, (T,), torch.int32, dev)
-    _ready(dev, (T, V, H))
+    _ready(dev, (T, V, H), x, w)
     loss = torch.empty((T,), dtype=torch.float32, device=dev)
     lse = torch.empty((T,), dtype=torch.float32, device=dev)
     ws = _workspace(workspace, lib.gocr_op_linear_ce_workspace(T, V), dev)
@@ -681,7 +686,7 @@ def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None, loss=None):
     _want("lse", lse, (T,), torch.float32, dev)
     if loss is not None:
         _want("loss", loss, (T,), torch.float32, dev)
-    _ready(dev, (T, V, H))
+    _ready(dev, (T, V, H), dloss, x, w, lse, loss)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     ws = _workspace(workspace, lib.gocr_op_linear_ce_backward_workspace(T, V, H), dev)
     _launch(dev, lib.gocr_op_linear_ce_backward_with_loss, dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),

@@ -128,3 +128,25 @@ def test_wrappers_refuse_sizes_past_32_bits():
         with pytest.raises(ValueError, match="2\\^31"):
             call()
 
+
+def test_wrappers_refuse_operands_that_want_a_gradient():
+    """The calls return tensors without a graph: a gradient must not be lost silently."""
+    torch = pytest.importorskip("torch")
+    from self_speculative_block_gb300 import gocr
+    i, f = torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+    b = torch.zeros(4, 64, dtype=torch.bfloat16)
+    q, lse, cu = torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(1, 4), torch.zeros(2, dtype=torch.int32)
+    calls = [(gocr.op_embed, (i, b), {}, (1,)),
+             (gocr.op_embed, (i, b, b[0].clone()), {}, (1, 2)),
+             (gocr.op_embed_backward, (b, i, 10), {}, (0,)),
+             (gocr.op_attention_packed, (q, q, q, cu), {}, (0, 1, 2)),
+             (gocr.op_attention_packed_backward, (q, q, q, q, q, lse, cu), {}, (0, 1, 2, 3, 4, 5)),
+             (gocr.op_linear_ce, (b, b, i), {}, (0, 1)),
+             (gocr.op_linear_ce_backward, (f, b, b, i, f), {}, (0, 1, 2, 4))]
+    for fn, args, kw, which in calls:
+        for k in which:
+            bad = [a.clone().requires_grad_() if j == k else a for j, a in enumerate(args)]
+            with pytest.raises(ValueError, match="outside autograd"):
+                fn(*bad, **kw)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # the next check
+                fn(*bad, **kw)
