@@ -356,14 +356,15 @@ int gocr_three_stream_ranges(int P, int N, int B, int32_t* lim, int32_t* lo2, in
  * The two ends of a decoder's training step and its attention over packed
  * sequences, forward (which also scores and prefills) and backward.  For all
  * of them: row-major arrays, device memory of the current device, `stream` a
- * stream of the current device (GOCR_EINVAL otherwise); operands aligned to 16
- * bytes; nothing is allocated, kept between calls or synchronised, so a call
+ * stream of the current device (GOCR_EINVAL otherwise); bf16 operands, the
+ * embedding's arrays and workspaces aligned to 16 bytes, other int32 and fp32
+ * arrays to 4; nothing is allocated, kept between calls or synchronised, so a call
  * can be captured into a graph; a workspace need not be cleared and belongs to
  * one call at a time (for calls of several shapes: the largest of their sizes,
- * which need not be that of the largest shape).  The same inputs give the same bits.  Outputs must not
- * overlap inputs.  Zero rows (T = 0) are allowed: gradients of weights are
- * then zero.  Errors: GOCR_EINVAL (null pointer, shape, alignment, stream),
- * GOCR_ECAPACITY (workspace), GOCR_ECUDA (launch). */
+ * which need not be that of the largest shape).  The same inputs give the same
+ * bits.  Outputs must not overlap inputs.  Zero rows (T = 0) are allowed:
+ * gradients of weights are then zero.  Errors: GOCR_EINVAL (null pointer, shape,
+ * alignment, stream), GOCR_ECAPACITY (workspace), GOCR_ECUDA (launch). */
 
 /* y[T, H] = scale * row(ids[t]), rounded once to dtype: row(id) is embed[id]
  * for 0 <= id < V, mask_embed for id = -1 (the [M] row; zero when mask_embed

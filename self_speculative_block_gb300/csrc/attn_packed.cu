@@ -487,6 +487,7 @@ extern "C" int gocr_op_attention_packed(const void* q, const void* k, const void
   if (int rc = attn_packed_check(n_seq, T, Hq, Hkv, d, ldq, ldk, ldv, scale)) return rc;
   if (!cu_seqlens || (T && (!q || !k || !v || !o || !lse))) return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o) & 15) return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if (((uintptr_t)lse | (uintptr_t)cu_seqlens) & 3) return op_fail(GOCR_EINVAL, "lse or cu_seqlens not 4-byte aligned");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
   if (!T || !n_seq) return GOCR_OK;

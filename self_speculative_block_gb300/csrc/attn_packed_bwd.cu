@@ -751,6 +751,7 @@ int gocr_op_attention_packed_backward(const void* d_o, const void* q, const void
   if (((uintptr_t)d_o | (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o | (uintptr_t)dq | (uintptr_t)dk |
        (uintptr_t)dv | (uintptr_t)workspace) & 15)
     return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if (((uintptr_t)lse | (uintptr_t)cu_seqlens) & 3) return op_fail(GOCR_EINVAL, "lse or cu_seqlens not 4-byte aligned");
   if (workspace_bytes < gocr_op_attention_packed_backward_workspace(T, Hq)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;

@@ -491,6 +491,7 @@ int gocr_op_embed(int dtype, const void* embed, const void* mask_embed, const in
   if (!embed || (T && (!ids || !y))) return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)embed | (uintptr_t)mask_embed | (uintptr_t)y) & 15)
     return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if ((uintptr_t)ids & 3) return op_fail(GOCR_EINVAL, "ids not 4-byte aligned");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
   if (!T) return GOCR_OK;
@@ -515,6 +516,7 @@ int gocr_op_embed_backward(int dtype, const void* dy, const int32_t* ids, void* 
   if (!d_embed || !workspace || (T && (!dy || !ids))) return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)dy | (uintptr_t)d_embed | (uintptr_t)d_mask | (uintptr_t)workspace) & 15)
     return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if ((uintptr_t)ids & 3) return op_fail(GOCR_EINVAL, "ids not 4-byte aligned");
   if (workspace_bytes < gocr_op_embed_backward_workspace(T, H)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;

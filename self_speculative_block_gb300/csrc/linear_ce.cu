@@ -797,6 +797,8 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
   if (int rc = check_shape(T, V, H)) return rc;
   if (!w || !workspace || (T && (!x || !labels || !loss || !lse))) return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)workspace) & 15) return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if (((uintptr_t)labels | (uintptr_t)loss | (uintptr_t)lse) & 3)
+    return op_fail(GOCR_EINVAL, "labels, loss or lse not 4-byte aligned");
   if (workspace_bytes < gocr_op_linear_ce_workspace(T, V)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
@@ -830,6 +832,8 @@ int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, cons
     return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)dx | (uintptr_t)dw | (uintptr_t)workspace) & 15)
     return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
+  if (((uintptr_t)dloss | (uintptr_t)labels | (uintptr_t)loss | (uintptr_t)lse) & 3)
+    return op_fail(GOCR_EINVAL, "dloss, labels, loss or lse not 4-byte aligned");
   const BackwardPlan p = backward_plan(T, V, H);
   if (workspace_bytes < p.bytes) return op_fail(GOCR_ECAPACITY, "workspace too small");
   cudaStream_t s = (cudaStream_t)stream;

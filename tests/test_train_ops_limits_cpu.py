@@ -7,6 +7,7 @@ import pytest
 EINVAL, ECAPACITY = -1, -2
 P = ctypes.c_void_p(256)      # never dereferenced: each call below is refused first
 ODD = ctypes.c_void_p(258)
+BIG = 1 << 60
 
 
 @pytest.fixture(scope="module")
@@ -150,3 +151,20 @@ def test_wrappers_refuse_operands_that_want_a_gradient():
                 fn(*bad, **kw)
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # the next check
                 fn(*bad, **kw)
+
+
+@pytest.mark.parametrize("at", [257, 258, 259])
+def test_arrays_of_words_are_aligned(lib, at):
+    """A word that straddles its boundary would fault on the device."""
+    W = ctypes.c_void_p(at)
+    sizes = (2, 8, 4, 2, 64, 256, 128, 128, 0.125)
+    for rc in (lib.gocr_op_embed(1, P, P, W, P, 4, 64, 100, 1.0, None),
+               lib.gocr_op_embed_backward(1, P, W, P, P, 4, 64, 100, 1.0, P, BIG, None),
+               lib.gocr_op_attention_packed(P, P, P, P, W, P, *sizes, None),
+               lib.gocr_op_attention_packed(P, P, P, P, P, W, *sizes, None),
+               lib.gocr_op_attention_packed_backward(P, P, P, P, P, W, P, P, P, P, *sizes, P, BIG, None),
+               lib.gocr_op_attention_packed_backward(P, P, P, P, P, P, W, P, P, P, *sizes, P, BIG, None),
+               *(lib.gocr_op_linear_ce(P, P, *(W if i == k else P for i in range(3)), 4, 100, 64, P, BIG, None) for k in range(3)),
+               *(lib.gocr_op_linear_ce_backward_with_loss(*(W if i == k else P for i in range(8)), 4, 100, 64, P, BIG, None)
+                 for k in (0, 3, 4, 5))):
+        assert rc == EINVAL and "4-byte" in _message(lib)
