@@ -434,8 +434,13 @@ int gocr_op_linear_ce(const void* x, const void* w, const int32_t* labels, float
  * again in pieces of the vocabulary; (softmax - one-hot) dloss / u is rounded to
  * bf16 for the products, whose sums are in fp32 and are multiplied by u.  u
  * follows from the smallest and the largest mantissa among the targets' weights
- * and is such that bf16 holds both nearly exactly in units of it: neither the
- * weight of a mean nor those of two streams' means are a common rounding error. */
+ * and is such that bf16 holds both nearly exactly in units of it: the weight of
+ * a mean is no common rounding error, those of two streams' means hardly ever
+ * one above 2^-10 (2^-9 at worst).  Weights between the two are rounded as they
+ * come, and a row's last bits depend on them. */
+/* Bytes: a piece of the softmax gradient (T times the larger of 4,096 columns and
+ * 2^25 / T, at most V, in bf16), the fp32 parts of dx and a copy of x; for short
+ * calls and small vocabularies more than the logits would take. */
 size_t gocr_op_linear_ce_backward_workspace(int T, int V, int H);
 int gocr_op_linear_ce_backward(const float* dloss, const void* x, const void* w, const int32_t* labels,
                                const float* lse, void* dx, void* dw, int T, int V, int H, void* workspace,

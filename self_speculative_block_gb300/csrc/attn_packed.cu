@@ -14,13 +14,16 @@
 // tensor pipe (score MMAs of 64 columns read A again for half the columns: 49
 // cycles instead of 32), its softmax 620 of four warps, and the chain scores,
 // softmax, P V is as long as both.  128 keys of both tiles pass in 3,270 cycles,
-// 2,586 of them products.  With one score buffer a tile and blocks of 128 keys
+// 2,586 of them products.  (The tensor pipe's counter takes such a score MMA for 32
+// cycles: by it 63 % of this loop is busy, and 47 % of a launch of one long sequence,
+// with its items' first and last blocks, the halves that the diagonal masks, and the
+// SMs without an item at the end.)  With one score buffer a tile and blocks of 128 keys
 // the tiles waited for one another; with two buffers a tile's next scores are
 // ready when its softmax is.  Each tile has an MMA warp, because a warp's wait
 // on a barrier costs 100 cycles and more behind its own queue of MMAs, a time
 // that the other warp's MMAs fill.  12 heads of 128: one sequence of 8,192 in
-// 182 us (1.13 PFLOP/s), 16 prompts of 25 to 1,200 in 45, 18 regions of 1 to 140
-// in 17, where a launch's fixed chain (sequence search, loads, one block, store)
+// 176 us (1.17 PFLOP/s), 16 prompts of 25 to 1,200 in 45 (heads of 64: 143 and 35),
+// 18 regions of 1 to 140 in 17, where a launch's fixed chain (sequence search, loads, one block, store)
 // is most of it.  Measured slower: part of the exponentials as polynomials on
 // the FMA pipe, P given over in halves, sixteen softmax warps (two threads a
 // row), one MMA warp, score MMAs of 128 columns with 208 registers a thread.

@@ -4,8 +4,8 @@
 //   dP_ij = do_i . v_j                   dS_ij = P_ij (dP_ij - delta_i)
 //   dv_j = sum_i P_ij do_i               dk_j = c sum_i dS_ij q_i      dq_i = c sum_j dS_ij k_j
 //
-// dk and dv also sum over the q heads of the group.  Two launches: delta, then
-// one of two kinds of CTA: for dk and dv one per (128 keys, k/v head), which
+// dk and dv also sum over the q heads of the group.  Two launches: delta with a
+// table of the blocks, then one of two kinds of CTA: for dk and dv one per (128 keys, k/v head), which
 // walks the q heads and the query blocks that see the keys; for dq one per (128
 // query rows, q head), which walks the keys.  S and dP are computed by both,
 // seven products of 128 x 128 x D a block pair instead of five; in return every
@@ -26,7 +26,7 @@
 // need, the tensor pipe busy 61 % of the time.  A block pair's chain (S, P, dS,
 // sums) is longer than its products, and there is room for one pair at a time
 // (dV, dK, S^T and dP^T fill all 512 columns of tensor memory).  15 sequences of
-// 95 to 1,203 take 111 us, 46 at the long one's rate; the rest goes to blocks on
+// 95 to 1,203 take 109 us (heads of 64: 441 us for the long one), 46 at the long one's rate; the rest goes to blocks on
 // the diagonal, ragged ones, and CTAs that start and finish.  Measured slower:
 // groups that run ahead of one another on products of 64 columns (541 to 667 us
 // for the long one), one MMA warp (541).

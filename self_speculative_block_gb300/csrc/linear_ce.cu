@@ -25,10 +25,12 @@
 //          forward call's loss is given: of a confident row the difference of
 //          two rounded logits of tens has no right digit left (losses of
 //          1e-6 to 1e-5: dx off by 0.9 of its norm);
-//   PROD   dx += g W (fp32 slabs) and dw = g^T x (bf16) of the piece, both read
+//   PROD   dx += g W (fp32 slabs) and dw = g^T x (bf16) of the piece, x from a
+//          copy that is zero in the rows without a target; both read
 //          g as it lies: rows for dx (K-major), columns for dw (M-major), W and
 //          x N-major, so nothing is transposed.
-// The vocabulary goes by in pieces whose g fits the workspace.  In PROD every
+// The vocabulary goes by in pieces of 64 MB of g, but of no fewer than 4,096
+// columns: of a small vocabulary all of g is there at once.  In PROD every
 // pair gets the same number of K steps: its share of the dw tiles, which are
 // not split, and a range of the dx tiles' steps, which may end inside a tile;
 // the parts of a tile go to slabs of their own that a last kernel adds up in
@@ -38,8 +40,8 @@
 //
 // What bounds it: with many rows the tensor pipe, and with seconds of it the
 // card's power.  2,047 rows x 65,536 x 1,536 forward take 237 us (1.74 PFLOP/s,
-// the pipe busy 92 % of STATS); 4,096 rows with the gradient 2,055 us (1.61
-// PFLOP/s of the four products' operations, where cuBLAS sustains 1.73).  33
+// the pipe busy 93 % of STATS); 4,096 rows with the gradient 2,012 to 2,070 us (1.59
+// to 1.64 PFLOP/s of the four products' operations, where cuBLAS sustains 1.73).  33
 // rows forward take 40 us, 35 of them reading w's 201 MB (5.8 TB/s) and 4 the
 // join.  193 rows x 8,191 x 512 with the gradient take 52 us, five launches of 7
 // to 18 us and the host's calls.
