@@ -90,3 +90,25 @@ def test_attention_packed_time_grows_with_the_sequences(g):
     few, many = time(10_000), time(40_000)
     for name, a, b in zip(("forward", "backward"), few, many):
         assert b < 7 * a, (name, a, b)
+
+
+def test_attention_packed_of_the_most_sequences(g):
+    """2^20 sequences of one row: o is v, lse the row's only score, dv the sum of the group's do, and
+    what is left of dS = P (dP - delta) is the difference of two fp32 sums of the same products."""
+    n, Hq, Hkv, d = 1 << 20, 2, 1, 64
+    q, k, v, do = _case(n, 1, Hq, Hkv, d, seed=2)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    o, lse = g.op_attention_packed(q, k, v, cu)
+    dq, dk, dv = g.op_attention_packed_backward(do, q, k, v, o, lse, cu)
+    g.op_status()
+    assert torch.equal(o, v.expand(n, Hq, d))
+    score = d ** -0.5 * (q.double() * k.double()).sum(2).T
+    # a sum of 64 products in steps of 16, times a scale that is a power of two, through a base 2 logarithm
+    err = (d / 16 + 16) * TC * d ** -0.5 * (q.double() * k.double()).abs().sum(2).T + 8 * TC * score.abs()
+    assert ((lse.double() - score).abs() <= err).all()
+    assert torch.equal(dv, do.float().sum(1, keepdim=True).bfloat16())
+    # P is 1 within the error of its exponent
+    mag = (do.double() * v.double()).abs().sum(2)
+    left = ((d / 16 + 16 + d) * TC * mag + 4 * (err.T + TC) * mag)[..., None] * d ** -0.5
+    assert (dq.double().abs() <= left * k.double().abs() * (1 + U) + 1e-38).all()
+    assert (dk.double().abs() <= (left * q.double().abs()).sum(1, keepdim=True) * (1 + U) + 1e-38).all()
