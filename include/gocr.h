@@ -455,6 +455,113 @@ int gocr_op_linear_ce_backward_with_loss(const float* dloss, const void* x, cons
                                          const float* loss, const float* lse, void* dx, void* dw, int T, int V, int H,
                                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- paged KV cache (device pointers) -----------------------------------
+ *
+ * Requests of any length share one pool of pages: the page step hands pages
+ * out and takes them back, the write puts a forward's rotated keys and its
+ * values into them, and the attention reads them.  One forward of a program
+ * that keeps its requests this way is gocr_op_page_step once and, in each
+ * layer, gocr_op_kv_write_paged and gocr_op_attention_paged.  The rules of the
+ * operators above (stream, alignment, errors, nothing kept, outputs apart from
+ * inputs) hold here, too.
+ *
+ * A request is a row of the block table [n_req, max_pages] (int32, device):
+ * position x of request r lies in page table[r, x / page_size], at offset x %
+ * page_size; its slot is page * page_size + offset.  page_size is 16, 32, 64,
+ * 128 or 256, n_pages * page_size <= 2^31 - 1, max_pages * page_size <= 2^24,
+ * n_req <= 4096.  A page belongs to one request. */
+
+/* One layer's cache, bf16: element (page, head, offset, c) of k at k + page *
+ * k_page + head * k_head + offset * k_token + c, and of v likewise; strides in
+ * elements, multiples of 8, no more than 2^32, and such that no two elements
+ * share a place (of a dimension of one entry the stride counts for nothing).
+ * Pages that hold a head's tokens together and pages that hold a token's heads
+ * together are both served, and pages of several layers or of k and v may be
+ * interleaved.  k and v 16-byte aligned. */
+typedef struct gocr_paged_kv {
+  void* k;
+  void* v;
+  int64_t k_page, k_head, k_token;
+  int64_t v_page, v_head, v_token;
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+} gocr_paged_kv;
+
+/* Block tables, row positions and slots of the next forward, from the
+ * requests' lengths.  Request r holds the pages of positions 0..held[r]-1; its
+ * rows of the forward are positions start[r]..end[r]-1, and afterwards it
+ * holds the pages of positions 0..end[r]-1: pages are taken where end needs
+ * more, and given back where it needs fewer.  So with p positions cached a
+ * draft window is (held, start, end) = (p, p, p+B+1), the verify window over it
+ * (p+B+1, p+1, p+B+2), its rollback to A accepted drafts (p+B+2, p+A+2,
+ * p+A+2), and the end of a request (held, 0, 0).
+ *
+ * free_pages[n_pages] is a stack, its lowest *n_free entries the free pages.
+ * The pages given back go onto it first, the first one (by request, then by
+ * position) on top; then pages are taken from the top, the first need first.
+ * Growth that is rolled back leaves the stack as it was, in order.  Pages go to
+ * requests in their order: from the first one on whose need, with the needs of
+ * those before it, is more than there is, requests that need pages are refused.
+ * Refused too are a request whose lengths do not satisfy 0 <= start <= held, start
+ * <= end and held, end <= max_pages * page_size (it has no rows), and one
+ * whose rows end behind row T.
+ *
+ * Outputs: table (in place: entries of pages taken; the others, those of pages
+ * given back among them, stay as they were), free_pages (in place, entries at
+ * and above *n_free), and
+ *   n_free_out[1]       the new *n_free;
+ *   held_out[n_req]     end, or held where refused: the next call's held;
+ *   kv_len[n_req]       end, or 0 where refused: gocr_op_attention_paged's;
+ *   cu_rows[n_req + 1]  request r's rows are cu_rows[r]..cu_rows[r+1]-1, <= T;
+ *   pos[T], slots[T]    of each row; -1 of refused requests' rows and of rows
+ *                       behind the last one.
+ * All int32, on the device; T <= 2^24.  Lengths, tables and stacks that contradict one
+ * another give meaningless pages, but no access outside the arrays. */
+int gocr_op_page_step(const int32_t* held, const int32_t* start, const int32_t* end, int n_req, int32_t* table,
+                      int max_pages, int page_size, int32_t* free_pages, int n_pages, const int32_t* n_free,
+                      int32_t* n_free_out, int32_t* held_out, int32_t* kv_len, int32_t* cu_rows, int32_t* pos,
+                      int32_t* slots, int T, void* stream);
+
+/* Rotary embedding of a forward's q and k rows and the write of k and v into
+ * the cache: for row t at position x = pos[t] and i < d / 2,
+ *   (y[i], y[i+d/2]) = (c u[i] - s u[i+d/2], c u[i+d/2] + s u[i]),
+ * c and s the cosine and sine of x theta^(-2i/d), for each head of q (into
+ * q_out[T, Hq, d], dense) and of k (into the cache at slots[t]); v is copied.
+ * The angle is exact to 2^-26 turns at any position, values are rounded once
+ * to bf16.  q, k and v bf16 with rows ldq, ldk and ldv elements apart, as in
+ * gocr_op_attention_packed; pos and slots int32[T] (device).  A row whose slot
+ * is outside 0..n_pages*page_size-1 is skipped: it is not read, and its q_out
+ * row is left as it was.  The slots of a call are distinct (of two rows with
+ * one slot, parts of either may be left).  Hq <= 1024, Hq % Hkv == 0, d 64 or
+ * 128, T <= 2^24, 1 <= theta <= 1e30. */
+int gocr_op_kv_write_paged(const void* q, const void* k, const void* v, const int32_t* pos, const int32_t* slots,
+                           void* q_out, const gocr_paged_kv* kv, int T, int Hq, long long ldq, long long ldk,
+                           long long ldv, float theta, void* stream);
+
+/* Attention of each request's new rows over its pages, the new rows' keys
+ * among them: request r's rows are q rows cu_rows[r]..cu_rows[r+1]-1 (device
+ * int32[n_req+1], non-decreasing, within 0..T), n of them; row i is at position
+ * p_i = kv_len[r] - n + i and reads keys 0..p_i: single tokens, verify windows,
+ * prompts prefilled whole or in chunks.  With kind GOCR_FWD_DRAFT the rows of a
+ * request are a draft window: its first row reads keys 0..p_0 and the others
+ * keys 0..kv_len[r]-1 (for GOCR_FWD_AR and GOCR_FWD_VERIFY: as above).  o[T, Hq, d]
+ * bf16 = softmax(scale q k^T) v and lse[Hq, T] fp32 = log of the row's sum of
+ * exponentials; o = 0 and lse = -infinity for a row without a key (p_i < 0).
+ * q [T, Hq, d] with rows ldq elements apart; q head h reads kv head h / (Hq /
+ * Hkv).  Rows that belong to no request are left as they were.  Keys behind
+ * kv_len, of other requests and of other pages reach nothing, whatever they
+ * hold; within a request a non-finite v may reach rows before it, too, that
+ * are of the same call.  kv_len above max_pages * page_size is taken for that;
+ * table entries outside 0..n_pages-1 read as pages of zeros.  Hq / Hkv <= 64, Hq <=
+ * 1024, d 64 or 128, T <= 2^24, pitch and scale as in gocr_op_attention_packed.
+ * Scores, softmax statistics, sums and the parts of a split key axis are in
+ * fp32; exp(scale q k^T - m), with m within 2^8 of the maximum so far, is
+ * rounded to bf16 for the product with v. */
+size_t gocr_op_attention_paged_workspace(int T, int Hq, int Hkv, int d);
+int gocr_op_attention_paged(const void* q, const gocr_paged_kv* kv, const int32_t* table, int max_pages,
+                            const int32_t* cu_rows, const int32_t* kv_len, int kind, void* o, float* lse, int n_req,
+                            int T, int Hq, long long ldq, float scale, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 /* Waits for `stream` and reports whether a kernel of these operators on the
  * current device gave up a wait (they do after two seconds) since the calling
  * thread last asked, or, at its first question, since the library was loaded:

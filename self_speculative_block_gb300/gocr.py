@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, List, Optional, Sequence
+from typing import Dict, List, NamedTuple, Optional, Sequence
 
 import numpy as np
 
@@ -40,7 +40,8 @@ EXPORTS = ("gocr_create", "gocr_prefill", "gocr_decode", "gocr_decode_batch", "g
            "gocr_op_embed", "gocr_op_embed_backward_workspace", "gocr_op_embed_backward",
            "gocr_op_linear_ce_workspace", "gocr_op_linear_ce", "gocr_op_linear_ce_backward_workspace",
            "gocr_op_linear_ce_backward", "gocr_op_linear_ce_backward_with_loss", "gocr_op_attention_packed", "gocr_op_attention_packed_backward_workspace",
-           "gocr_op_attention_packed_backward", "gocr_op_status", "gocr_op_wait_probe")
+           "gocr_op_attention_packed_backward", "gocr_op_page_step", "gocr_op_kv_write_paged",
+           "gocr_op_attention_paged_workspace", "gocr_op_attention_paged", "gocr_op_status", "gocr_op_wait_probe")
 
 
 class GocrError(RuntimeError):
@@ -76,6 +77,14 @@ class Stats(ctypes.Structure):
         d["accept_hist"] = list(self.accept_hist)
         d["tpf"] = self.committed / self.forwards if self.forwards else 0.0
         return d
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page", ctypes.c_int64), ("k_head", ctypes.c_int64), ("k_token", ctypes.c_int64),
+                ("v_page", ctypes.c_int64), ("v_head", ctypes.c_int64), ("v_token", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 class DecodeOpts(ctypes.Structure):
@@ -135,6 +144,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gocr_op_attention_packed": (i32, [vp] * 6 + [i32] * 5 + [i64] * 3 + [f32, vp]),
         "gocr_op_attention_packed_backward_workspace": (sz, [i32, i32]),
         "gocr_op_attention_packed_backward": (i32, [vp] * 10 + [i32] * 5 + [i64] * 3 + [f32, vp, sz, vp]),
+        "gocr_op_page_step": (i32, [vp] * 3 + [i32, vp, i32, i32, vp, i32] + [vp] * 7 + [i32, vp]),
+        "gocr_op_kv_write_paged": (i32, [vp] * 6 + [ctypes.POINTER(PagedKV), i32, i32, i64, i64, i64, f32, vp]),
+        "gocr_op_attention_paged_workspace": (sz, [i32] * 4),
+        "gocr_op_attention_paged": (i32, [vp, ctypes.POINTER(PagedKV), vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, i64,
+                                          f32, vp, sz, vp]),
         "gocr_op_status": (i32, [vp]),
         "gocr_op_wait_probe": (i32, [i32, vp]),
     }
@@ -692,6 +706,129 @@ def op_linear_ce_backward(dloss, x, w, labels, lse, workspace=None, loss=None):
     _launch(dev, lib.gocr_op_linear_ce_backward_with_loss, dloss.data_ptr(), x.data_ptr(), w.data_ptr(), labels.data_ptr(),
             loss.data_ptr() if loss is not None else None, lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, V, H, ws.data_ptr(), ws.numel())
     return dx, dw
+
+
+# ----------------------------------------------------------------------------
+# paged KV cache (serving: no gradients)
+# ----------------------------------------------------------------------------
+
+class PageStep(NamedTuple):
+    """What op_page_step returns: int32 tensors on the device."""
+    n_free: object   # [1] the stack's height after the step
+    held: object     # [n_req] the next step's held
+    kv_len: object   # [n_req] op_attention_paged's kv_len (0: refused)
+    cu_rows: object  # [n_req + 1] request r's rows are cu_rows[r] .. cu_rows[r + 1] - 1
+    pos: object      # [rows] position of each row, -1 of refused requests' and behind the last one
+    slots: object    # [rows] its slot in the cache, or -1
+
+
+def op_page_step(held, start, end, table, free_pages, n_free, page_size: int, rows: int) -> PageStep:
+    """Block table, positions and slots of the next forward, from the requests'
+    lengths (int32 [n_req] each, on the device): request r holds the pages of
+    held[r] positions, its rows are positions start[r] .. end[r] - 1, and
+    afterwards it holds the pages of end[r] positions, new ones taken from the
+    stack free_pages [n_pages] (n_free [1] of them free) or those behind given
+    back to it.  table [n_req, max_pages] and free_pages are updated in place;
+    rows is the number of rows that the forward is laid out for.  A request
+    whose pages or rows do not fit is refused: it keeps what it holds."""
+    torch = _torch()
+    _lead("table", table, 2, torch.int32)
+    dev, (R, width), n_pages = table.device, table.shape, free_pages.numel()
+    _want("table", table, (R, width), torch.int32, dev)
+    for name, t in (("held", held), ("start", start), ("end", end)):
+        _want(name, t, (R,), torch.int32, dev)
+    _want("free_pages", free_pages, (n_pages,), torch.int32, dev)
+    _want("n_free", n_free, (1,), torch.int32, dev)
+    _ready(dev, (R, width, page_size, n_pages, rows))
+    out = torch.empty((1 + 3 * R + 1 + 2 * rows,), dtype=torch.int32, device=dev).split((1, R, R, R + 1, rows, rows))
+    _launch(dev, load().gocr_op_page_step, held.data_ptr(), start.data_ptr(), end.data_ptr(), R, table.data_ptr(), width,
+            page_size, free_pages.data_ptr(), n_pages, n_free.data_ptr(), *[t.data_ptr() for t in out], rows)
+    return PageStep(*out)
+
+
+def _cache(k_cache, v_cache, device):
+    """Check the pages of a layer, [n_pages, Hkv, page_size, d] bf16 each, in any
+    order of the strides; returns (PagedKV, Hkv, d)."""
+    torch = _torch()
+    _lead("k_cache", k_cache, 4, torch.bfloat16)
+    _lead("v_cache", v_cache, 4, torch.bfloat16)
+    shape, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache must be {list(shape)}, got {list(v_cache.shape)}")
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the elements of a head must be contiguous in k_cache and v_cache")
+    if k_cache.device != device or v_cache.device != device:
+        raise ValueError(f"k_cache is on {k_cache.device}, v_cache on {v_cache.device}, q is on {device}")
+    n, heads, ps, d = shape
+    if max(n, heads, ps) > 0x7fffffff:
+        raise ValueError(f"a size of {list(shape)} is outside 0 .. 2^31 - 1")
+    return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), *ks[:3], *vs[:3], n, ps, heads, d), heads, d
+
+
+def op_kv_write_paged(q, k, v, pos, slots, k_cache, v_cache, theta: float = 10000.0, q_out=None):
+    """Rotary embedding of q [T, Hq, d] and k [T, Hkv, d] at positions pos (int32
+    [T]), and the write of k and v into slots (int32 [T], page * page_size +
+    offset, distinct) of k_cache and v_cache [n_pages, Hkv, page_size, d] bf16
+    (strides in any order).  Rows may be views of one fused projection.  Returns
+    the rotated q [T, Hq, d], written into q_out when given; rows whose slot is
+    outside the cache are skipped."""
+    torch = _torch()
+    _lead("q", q, 3, torch.bfloat16)
+    dev, (T, Hq, d) = q.device, q.shape
+    kv, Hkv, dk = _cache(k_cache, v_cache, dev)
+    if dk != d:
+        raise ValueError(f"the cache holds heads of {dk}, q has heads of {d}")
+    ld = (_rows("q", q, T, None, d, dev), _rows("k", k, T, Hkv, d, dev), _rows("v", v, T, Hkv, d, dev))
+    _want("pos", pos, (T,), torch.int32, dev)
+    _want("slots", slots, (T,), torch.int32, dev)
+    _ready(dev, (T, Hq), q, k, v, k_cache, v_cache)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _want("q_out", q_out, (T, Hq, d), torch.bfloat16, dev)
+    _launch(dev, load().gocr_op_kv_write_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(), pos.data_ptr(),
+            slots.data_ptr(), q_out.data_ptr(), ctypes.byref(kv), T, Hq, *ld, theta)
+    return q_out
+
+
+def op_attention_paged(q, k_cache, v_cache, table, cu_rows, kv_len, kind: int = FWD_VERIFY, scale=None, workspace=None,
+                       o=None, lse=None):
+    """Attention of each request's new rows over its pages: q [T, Hq, d] bf16
+    (rows may be views of one fused projection), k_cache and v_cache [n_pages,
+    Hkv, page_size, d] bf16 (strides in any order), table int32 [n_req,
+    max_pages], cu_rows int32 [n_req + 1] and kv_len int32 [n_req] (the new
+    rows' keys counted) on the device, as op_page_step gives them.  Row i of a
+    request's n is at position kv_len - n + i and reads the keys up to it;
+    kind=FWD_DRAFT: the rows behind the first read all kv_len keys.  Returns (o
+    [T, Hq, d] bf16, lse [Hq, T] fp32), written into o and lse when given; a row
+    without keys gets 0 and -inf, rows of no request are not written."""
+    torch = _torch()
+    lib = load()
+    _lead("q", q, 3, torch.bfloat16)
+    dev, (T, Hq, d) = q.device, q.shape
+    kv, Hkv, dk = _cache(k_cache, v_cache, dev)
+    if dk != d:
+        raise ValueError(f"the cache holds heads of {dk}, q has heads of {d}")
+    ldq = _rows("q", q, T, None, d, dev)
+    _lead("table", table, 2, torch.int32)
+    R, width = table.shape
+    _want("table", table, (R, width), torch.int32, dev)
+    _want("cu_rows", cu_rows, (R + 1,), torch.int32, dev)
+    _want("kv_len", kv_len, (R,), torch.int32, dev)
+    _ready(dev, (R, width, T, Hq), q, k_cache, v_cache)
+    if o is None:
+        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _want("o", o, (T, Hq, d), torch.bfloat16, dev)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _want("lse", lse, (Hq, T), torch.float32, dev)
+    ws = _workspace(workspace, lib.gocr_op_attention_paged_workspace(T, Hq, Hkv, d), dev)
+    _launch(dev, lib.gocr_op_attention_paged, q.data_ptr(), ctypes.byref(kv), table.data_ptr(), width,
+            cu_rows.data_ptr(), kv_len.data_ptr(), kind, o.data_ptr(), lse.data_ptr(), R, T, Hq, ldq,
+            d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+    return o, lse
 
 
 def op_status(device="cuda") -> None:
