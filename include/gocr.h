@@ -552,7 +552,8 @@ int gocr_op_kv_write_paged(const void* q, const void* k, const void* v, const in
  * hold; within a request a non-finite v may reach rows before it, too, that
  * are of the same call.  kv_len above max_pages * page_size is taken for that;
  * table entries outside 0..n_pages-1 read as pages of zeros.  Hq / Hkv <= 64, Hq <=
- * 1024, d 64 or 128, T <= 2^24, pitch and scale as in gocr_op_attention_packed.
+ * 1024, d 64 or 128, T <= 2^24, T Hq <= 2^31 - 1, pitch and scale as in
+ * gocr_op_attention_packed.
  * Scores, softmax statistics, sums and the parts of a split key axis are in
  * fp32; exp(scale q k^T - m), with m within 2^8 of the maximum so far, is
  * rounded to bf16 for the product with v. */

@@ -1,85 +1,703 @@
 // Attention of requests' new rows over a paged KV cache.
 //
-//   o_i = sum_j exp(c q_i . k_j - lse_i) v_j,  lse_i = log sum_j exp(c q_i . k_j),  j the keys that row i reads
+//   S_ij = c q_i . k_j,  lse_i = log sum_j exp S_ij,  o_i = sum_j exp(S_ij - lse_i) v_j,  j = 0 .. the last key row i reads
 //
-// A CTA owns a row and a q head, a warp every fourth key.
+// A unit of work is a request, a kv head and up to two tiles of query rows; a
+// tile holds 128 / G tokens with the G q heads that share the kv head, so a
+// window's rows read their keys once.  All units' key tiles (of 128 keys) lie on
+// one axis, which is cut into equal pieces, one a CTA: a single token's long
+// context spreads over the device, and chunks of prompts leave no last wave.  A
+// unit that a cut divides leaves its parts (O, maximum, sum, in fp32) in the workspace, and
+// a second launch joins them in order; the others are finished in place.
+//
+// Inside, a CTA runs as the packed-sequence kernel does: a TMA warp fills a ring
+// of K and V tiles (a box a page and 64 columns), an MMA warp a query tile
+// issues S = Q K^T (128 x 64 x D, two score buffers a tile in tensor memory) and
+// O += P V with P read from tensor memory, and a softmax thread owns a row.
+// Rows, tiles and keys that do not exist cost their products but no exponentials:
+// with one token a product of 128 rows takes less time than its keys do from HBM.
 #include "attn_packed.cuh"
 #include "paged.cuh"
 
 using namespace gocr;
+using namespace gocr::packed;
 using namespace gocr::paged;
 
 namespace {
 
+constexpr int KT = 128;        // keys of a tile
+constexpr int GRID = SM_COUNT; // pieces of the work; parts depend on it, so it is a constant
+// Eight softmax warps (two tiles x four lane quarters), then the TMA warp, an
+// MMA warp a tile and the work warp.
+constexpr int SW = 8, THREADS = (SW + 4) * 32;
+constexpr float GROW = 8.f;    // log2 of the growth of a row's maximum that rescales O
+
+static __device__ unsigned g_gave_up;  // threads whose wait gave up, ever
+
+// A unit that its CTA began and did not finish.
+struct Split {
+  long long after;  // where the next CTA's piece begins, within the unit
+  long long work, piece;
+  int row0, n, kv, tok0, head, weight;
+};
+
 struct PagedArgs {
-  const bf16* q;
-  gocr_paged_kv kv;
   const int *table, *cu, *kv_len;
   bf16* o;
   float* lse;
-  long long ldq;
-  int max_pages, n_req, T, Hq, G, draft, shift;
+  float4* part;   // [2 GRID][D / 4][rows]
+  float2* stat;   // [2 GRID][rows]: reference (times scale log2 e) and sum of the exponentials
+  Split* split;   // [GRID], n = 0: none
+  int max_pages, n_pages, n_req, T, Hq, Hkv, G, toks, draft, shift, rows;
   float scale;
 };
 
-template <int D> __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int r = -1, row0 = 0, n = 0;
-  for (int i = 0; i < a.n_req; ++i) {
-    const int c0 = min(max(a.cu[i], 0), a.T), c1 = min(max(a.cu[i + 1], 0), a.T);
-    if (t >= c0 && t < c1) {
-      r = i;
-      row0 = c0;
-      n = c1 - c0;
+template <int D> struct Lay {
+  static constexpr int SLOTS = D == 128 ? 4 : 8;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = 2 * TILE_BYTES<D>;
+  static constexpr int OFF_WORK = OFF_KV + SLOTS * TILE_BYTES<D>;  // int4 [2][3]
+  static constexpr int OFF_BAR = OFF_WORK + 96;
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t O_COL = 256;  // S [2 tiles][2 buffers] of 64 columns; O [2 tiles] of D behind them
+};
+
+struct Req {
+  int row0, n, kv;
+};
+__device__ __forceinline__ Req request(const PagedArgs& a, int r) {
+  const int c0 = min(max(a.cu[r], 0), a.T), c1 = min(max(a.cu[r + 1], 0), a.T);
+  return Req{c0, max(c1 - c0, 0), min(max(a.kv_len[r], 0), a.max_pages << a.shift)};
+}
+// The last key that token i reads; negative: none.
+__device__ __forceinline__ int last_key(const PagedArgs& a, const Req& q, int i) {
+  return a.draft && i > 0 ? q.kv - 1 : q.kv - q.n + i;
+}
+// Work of the two query tiles from token i on: key tiles, twice where both tiles
+// hold tokens.
+__device__ __forceinline__ int weight(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks ? 2 : 1; }
+__device__ __forceinline__ long long work_of(const PagedArgs& a, const Req& q, int i) {
+  if (i >= q.n) return 0;
+  const int last = last_key(a, q, min(i + 2 * a.toks, q.n) - 1);
+  return last < 0 ? 0 : (long long)(last / KT + 1) * weight(a, q, i);
+}
+// The key tiles of a unit that lie before its work x.
+__device__ __forceinline__ int tile_at(long long x, int weight) { return (int)((x + weight - 1) >> (weight - 1)); }
+
+// One work item, as every warp sees it.
+struct Item {
+  Req q;
+  int tok0, head, k0, k1, part, req;
+  __device__ Item(const int4* w)
+      : q{w[0].x, w[0].y, w[0].z}, tok0(w[0].w), head(w[1].x), k0(w[1].y), k1(w[1].z), part(w[1].w), req(w[2].x) {}
+  // tokens of query tile j
+  __device__ int tokens(const PagedArgs& a, int j) const { return min(max(q.n - tok0 - j * a.toks, 0), a.toks); }
+  // blocks of 64 keys of query tile j within the item
+  __device__ int blocks(const PagedArgs& a, int j) const {
+    const int n = tokens(a, j), last = last_key(a, q, tok0 + j * a.toks + n - 1);
+    return n == 0 || last < 0 ? 0 : max(min(2 * k1, last / 64 + 1) - 2 * k0, 0);
+  }
+  // keys of the item's last tile that exist
+  __device__ int tail() const { return min(q.kv - (k1 - 1) * KT, KT); }
+};
+
+// The warp's next item from the ring of two; false past the last one.
+__device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full, uint64_t* work_free, int i, int4* w,
+                                          bool& ok) {
+  const int s = i & 1;
+  if (!(ok = tc::mbar_wait_warp(work_full + s, (i >> 1) & 1))) return false;
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    w[e] = work[s * 3 + e];
+    // as uniform values, for the loops and operands that follow from them
+    w[e].x = __shfl_sync(0xffffffffu, w[e].x, 0);
+    w[e].y = __shfl_sync(0xffffffffu, w[e].y, 0);
+    w[e].z = __shfl_sync(0xffffffffu, w[e].z, 0);
+    w[e].w = __shfl_sync(0xffffffffu, w[e].w, 0);
+  }
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(work_free + s);
+  return w[0].y > 0;
+}
+
+// The pages of a request, 32 entries a warp in hand and the next 32 on their way.
+struct Pages {
+  const int* row;
+  int n, n_pages, at, cur, next;
+  __device__ int entry(int i) const {
+    const int p = i < n ? row[i] : 0;
+    return p >= 0 && p < n_pages ? p : n_pages;  // behind the last page TMA reads zeros
+  }
+  __device__ Pages(const PagedArgs& a, const Item& t)
+      : row(a.table + (size_t)t.req * a.max_pages), n((t.q.kv + (1 << a.shift) - 1) >> a.shift), n_pages(a.n_pages),
+        at((t.k0 * KT) >> a.shift) {
+    cur = entry(at + (threadIdx.x & 31));
+    next = entry(at + 32 + (threadIdx.x & 31));
+  }
+  // Page i, to all lanes; 32 is a multiple of a tile's pages, so a tile's entries
+  // (asked for twice, for K and for V) are in hand together.
+  __device__ int operator[](int i) {
+    if (i >= at + 32) {
+      at += 32;
+      cur = next;
+      next = entry(at + 32 + (threadIdx.x & 31));
+    }
+    return __shfl_sync(0xffffffffu, cur, i - at);
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedArgs a) {
+  using F = Lay<D>;
+  constexpr int SLOTS = F::SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long sums[SW + 4];
+  __shared__ long long start_at;  // this CTA's piece: where it begins within its first request,
+  __shared__ int start_req;       // and that request
+  uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + F::OFF_BAR);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* full = q_empty + 1;
+  uint64_t* empty = full + SLOTS;
+  uint64_t* s_full = empty + SLOTS;  // [2 tiles][2 buffers]
+  uint64_t* p_full = s_full + 4;     // [2 tiles][2 buffers]
+  uint64_t* o_full = p_full + 4;     // [2] a block's P V is complete
+  uint64_t* o_done = o_full + 2;     // [2] the item's last one is
+  // ragged V tiles, one barrier a slot: a slot's next load waits for this one's
+  // use, so no barrier is ever two phases ahead of the warp that waits on it
+  uint64_t* v_tail = o_done + 2;         // [SLOTS] the rows behind the request's keys are zero
+  uint64_t* work_full = v_tail + SLOTS;  // [2]
+  uint64_t* work_free = work_full + 2;   // [2]
+  uint64_t* issued = work_free + 2;      // [2] an item's loads are on their way
+  uint64_t* drained = issued + 2;        // [2] an MMA warp's products, at its end
+  uint32_t* holder = reinterpret_cast<uint32_t*>(drained + 2);
+  int4* work = reinterpret_cast<int4*>(sm + F::OFF_WORK);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  tc::grid_dep_launch();  // the join's CTAs start as SMs fall free, and wait for this grid's end
+  if (tid == 0) {
+    tc::mbar_init(q_full, 1);
+    tc::mbar_init(q_empty, 2);
+    for (int s = 0; s < SLOTS; ++s) {
+      tc::mbar_init(full + s, 1);
+      tc::mbar_init(empty + s, 2);
+      tc::mbar_init(v_tail + s, 1);
+    }
+    for (int j = 0; j < 4; ++j) {
+      tc::mbar_init(s_full + j, 1);
+      tc::mbar_init(p_full + j, SW / 2);
+    }
+    for (int j = 0; j < 2; ++j) {
+      tc::mbar_init(o_full + j, 1);
+      tc::mbar_init(o_done + j, 1);
+      tc::mbar_init(issued + j, 1);
+      tc::mbar_init(drained + j, 1);
+      tc::mbar_init(work_full + j, 1);
+      tc::mbar_init(work_free + j, SW + 3);
+    }
+    tc::fence_mbar_init();
+    start_req = a.n_req;
+  }
+
+  // All requests' work: its sum, and where this CTA's piece begins.
+  const int per = (a.n_req + THREADS - 1) / THREADS, r0 = min(tid * per, a.n_req), r1 = min(r0 + per, a.n_req);
+  long long mine = 0;
+  bool without = false;  // a request has rows without keys
+  for (int r = r0; r < r1; ++r) {
+    const Req q = request(a, r);
+    long long sum = 0;
+    for (int i = 0; i < q.n; i += 2 * a.toks) sum += work_of(a, q, i);
+    mine += sum * a.Hkv;
+    without |= q.n > q.kv;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncwarp();
+  if (warp == SW + 1) tc::tmem_alloc(holder, 512);
+  tc::fence_before_sync();
+  without = __syncthreads_or(without);
+  tc::fence_after_sync();
+  long long before = inc - mine, total = 0;
+  for (int w = 0; w < SW + 4; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  const long long piece = (total + GRID - 1) / GRID, x0 = piece * blockIdx.x, x1 = min(x0 + piece, total);
+  if (before <= x0 && x0 < before + mine) {
+    for (int r = r0; r < r1; ++r) {
+      const Req q = request(a, r);
+      long long sum = 0;
+      for (int i = 0; i < q.n; i += 2 * a.toks) sum += work_of(a, q, i);
+      sum *= a.Hkv;
+      if (x0 < before + sum) {
+        start_req = r;
+        start_at = x0 - before;
+        break;
+      }
+      before += sum;
     }
   }
-  if (r < 0) return;
-  const int kv = min(a.kv_len[r], a.max_pages << a.shift);
-  const int last = a.draft && t > row0 ? kv - 1 : kv - n + t - row0;
-  const long long kh = (h / a.G) * a.kv.k_head, vh = (h / a.G) * a.kv.v_head;
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(a.q[t * a.ldq + h * D + e * 32 + lane]) * a.scale;
-  for (int j = warp; j <= last; j += 4) {
-    const int page = a.table[(size_t)r * a.max_pages + (j >> a.shift)], off = j & ((1 << a.shift) - 1);
-    const bool there = page >= 0 && page < a.kv.n_pages;
-    const bf16* k = (const bf16*)a.kv.k + page * a.kv.k_page + kh + off * a.kv.k_token;
-    const bf16* v = (const bf16*)a.kv.v + page * a.kv.v_page + vh + off * a.kv.v_token;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += there ? q[e] * __bfloat162float(k[e * 32 + lane]) : 0.f;
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float to = fmaxf(m, s), f = m == to ? 1.f : __expf(m - to),
-                p = __expf(s - (to == -INFINITY ? 0.f : to));  // (NaN stays NaN)
-    m = to;
-    l = l * f + p;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + (there ? p * __bfloat162float(v[e * 32 + lane]) : 0.f);
+  if (without) {  // rows without keys, in requests with more rows than keys
+    for (int r = blockIdx.x; r < a.n_req; r += GRID) {
+      const Req q = request(a, r);
+      const int n = q.kv == 0 ? q.n : a.draft ? min(1, q.n - q.kv) : q.n - q.kv;
+      for (int i = tid; i < n * a.Hq; i += THREADS) {
+        const int t = q.row0 + i / a.Hq, h = i % a.Hq;
+        a.lse[(size_t)h * a.T + t] = -INFINITY;
+        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(a.o + ((size_t)t * a.Hq + h) * D + c) = make_uint4(0, 0, 0, 0);
+      }
+    }
   }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = o[e];
   __syncthreads();
-  const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float f[4], sum = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sm[w] == top ? 1.f : __expf(sm[w] - top);
-    sum += f[w] * sl[w];
+  // all 512 columns, which start at 0: a constant keeps the MMAs' operands in uniform registers
+  constexpr uint32_t tmem = 0;
+  bool ok = true;
+  int4 w[3];
+
+  if (warp >= SW) {
+    if (warp == SW) {
+      // K(0), V(0), K(1), V(1), ... through the ring, Q behind the item's K(0)
+      int slot = 0, ph = 0, loads = 0, q_loads = 0;
+      const int box = min(1 << a.shift, KT);  // keys of a page that a tile holds
+      for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
+        const Item t(w);
+        Pages pages(a, t);
+        const int n = t.k1 - t.k0;
+        for (int x = 0; x < 2 * n; ++x) {
+          if (!(ok = tc::mbar_wait_warp(empty + slot, ph ^ 1))) break;
+          const int key0 = (t.k0 + (x >> 1)) * KT, boxes = (min(t.q.kv - key0, KT) + box - 1) / box;
+          if (tc::elect_one()) tc::mbar_expect_tx(full + slot, boxes * box * D * 2);
+          __syncwarp();
+          uint8_t* dst = sm + F::OFF_KV + slot * TILE_BYTES<D>;
+          for (int b = 0; b < boxes; ++b) {
+            const int key = key0 + b * box, page = pages[key >> a.shift];
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tc::tma_load_4d(dst + c * BOX_BYTES + b * box * 128, x & 1 ? &mv : &mk, c * 64, key & ((1 << a.shift) - 1),
+                                t.head, page, full + slot);
+            }
+            __syncwarp();
+          }
+          ++loads;
+          if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+          if (x == 0) {
+            if (!(ok = tc::mbar_wait_warp(q_empty, (i & 1) ^ 1))) break;
+            const int tiles = t.tokens(a, 1) ? 2 : 1;
+            if (tc::elect_one()) {
+              tc::mbar_expect_tx(q_full, tiles * a.toks * a.G * D * 2);
+              for (int j = 0; j < tiles; ++j)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  tc::tma_load_3d(sm + F::OFF_Q + j * TILE_BYTES<D> + c * BOX_BYTES, &mq, c * 64, t.head * a.G,
+                                  t.q.row0 + t.tok0 + j * a.toks, q_full);
+            }
+            __syncwarp();
+            ++q_loads;
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) tc::mbar_arrive(issued + (i & 1));
+      }
+      ok = tc::ring_landed(full, SLOTS, loads) && tc::ring_landed(q_full, 1, q_loads) && ok;
+    } else if (warp < SW + 3) {
+      const int j = warp - (SW + 1);  // the tile
+      const uint32_t q = tc::smem_u32(sm + F::OFF_Q + j * TILE_BYTES<D>), kv = tc::smem_u32(sm + F::OFF_KV);
+      const uint32_t s_col = tmem + j * 128, o_col = tmem + F::O_COL + j * D;
+      int ring = 0;           // ring position of the item's K(0)
+      unsigned tails = 0;     // parity of each slot's ragged tiles so far
+      int turn[2] = {0, 0};   // blocks of each buffer so far
+      auto wait = [&](uint64_t* bar, int ph) {
+        const bool r = tc::mbar_wait_warp(bar, ph & 1);
+        tc::fence_after_sync();
+        return r;
+      };
+      for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
+        const Item t(w);
+        const int nb = t.blocks(a, j), most = max(t.blocks(a, 0), t.blocks(a, 1)), tail = t.tail();
+        auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
+        auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
+        // both MMA warps give a K/V tile back, whether they used it or not
+        // (but not before it is there: its barrier is in an older phase)
+        auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
+        auto scores = [&](int b) {
+          mma_rows<D>(s_col + (b & 1) * 64, q, tile_of(2 * (b >> 1)), b & 1);
+          tc::mma_commit(s_full + j * 2 + (b & 1));
+        };
+        // after the scores of block b: the K tile, and at last Q
+        auto release_k = [&](int b) {
+          if ((b & 1) || b + 1 == most) release(2 * (b >> 1));
+          if (b + 1 == most) tc::mma_commit(q_empty);
+        };
+        if (!(ok = wait(q_full, i) && wait_full(0))) break;
+        if (tc::elect_one()) {
+          // over P of the last item, whose products were issued before
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (b < nb) scores(b);
+            if (b < most) release_k(b);
+          }
+        }
+        __syncwarp();
+        for (int b = 0; b < most; ++b) {
+          if (!(b & 1)) {
+            if (!(ok = wait_full(b + 1))) break;                  // V tile b / 2
+            if (b + 2 < most && !(ok = wait_full(b + 2))) break;  // K tile b / 2 + 1
+            if (b + 2 >= most && tail < KT) {
+              const int slot = (ring + b + 1) % SLOTS;
+              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+              tails ^= 1u << slot;
+            }
+          }
+          if (b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
+          if (tc::elect_one()) {
+            if (b < nb) {
+              mma_add<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * (b >> 1) + 1), b & 1, b == 0);
+              tc::mma_commit(o_full + j);
+              if (b + 1 == nb) tc::mma_commit(o_done + j);
+            }
+            if (b + 2 < nb) scores(b + 2);
+            if ((b & 1) || b + 1 == most) release(2 * (b >> 1) + 1);
+            if (b + 2 < most) release_k(b + 2);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        ring += 2 * (t.k1 - t.k0);
+      }
+      ok = tc::mma_drain(drained + j) && ok;
+    } else {
+      // The piece's items; and the last V tile of a ragged item: nothing behind the request's keys.
+      int r = min(start_req, a.n_req - 1), h = 0, i = 0, items = 0, ring = 0;
+      long long at = 0, left = start_req < a.n_req ? x1 - x0 : 0;  // within the unit; of the piece
+      Req q = request(a, r);
+      Split split{};
+      if (left > 0) {
+        long long sum = 0;  // of one head
+        for (int b = 0; b < q.n; b += 64 * a.toks) {
+          long long v = work_of(a, q, b + lane * 2 * a.toks);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          sum += v;
+        }
+        h = (int)(start_at / max(sum, 1ll));
+        at = start_at % max(sum, 1ll);
+        for (bool found = false; !found && i < q.n;) {
+          const long long v = work_of(a, q, i + lane * 2 * a.toks);
+          long long upto = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, upto > at);
+          found = past != 0;
+          const int l = found ? __ffs(past) - 1 : 31;
+          at -= __shfl_sync(0xffffffffu, found ? upto - v : upto, l);
+          i += (found ? l : 32) * 2 * a.toks;
+        }
+      }
+      auto advance = [&] {  // to the next unit
+        at = 0;
+        i += 2 * a.toks;
+        if (i < q.n) return;
+        i = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        if (left > 0 && ++r < a.n_req) q = request(a, r);
+        else left = 0;
+      };
+      int tail = KT, tail_at = 0;  // of the item before
+      while (ok) {
+        int k0 = 0, k1 = 0, part = -1;
+        while (left > 0) {  // the next unit's piece; a cut may leave no whole tile of it
+          const long long all = work_of(a, q, i);
+          if (at < all) {
+            const int wt = weight(a, q, i), tiles = (int)(all >> (wt - 1));
+            const long long end = min(at + left, all);
+            k0 = tile_at(at, wt);
+            k1 = tile_at(end, wt);
+            part = k0 == 0 && k1 == tiles ? -1 : 2 * (int)blockIdx.x + (k0 == 0);
+            if (k0 == 0 && k1 < tiles) split = Split{end, all, piece, q.row0, q.n, q.kv, i, h, wt};
+            left -= end - at;
+            if (k0 < k1) break;
+          }
+          advance();
+        }
+        const int s = items & 1;
+        if (!(ok = tc::mbar_wait_warp(work_free + s, ((items >> 1) & 1) ^ 1))) break;
+        if (lane == 0) {
+          work[s * 3] = make_int4(q.row0, k0 < k1 ? q.n : 0, q.kv, i);
+          work[s * 3 + 1] = make_int4(h, k0, k1, part);
+          work[s * 3 + 2] = make_int4(r, 0, 0, 0);
+          tc::mbar_arrive(work_full + s);
+        }
+        ++items;
+        // The item before, whose tail the next one's loads need not wait for.  Once its
+        // loads are issued the slot's barrier is in their phase or the one before;
+        // of the barriers that say so, two in turn, none is asked two phases late.
+        if (items > 1 && !(ok = tc::mbar_wait_warp(issued + (items & 1), ((items - 2) >> 1) & 1))) break;
+        if (tail < KT) {
+          const int slot = tail_at % SLOTS;
+          if (!(ok = tc::mbar_wait_warp(full + slot, (tail_at / SLOTS) & 1))) break;
+          zero_rows<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, tail);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(v_tail + slot);
+        }
+        if (k0 >= k1) break;
+        ring += 2 * (k1 - k0);
+        tail = min(q.kv - (k1 - 1) * KT, KT);
+        tail_at = ring - 1;
+        advance();
+      }
+      if (lane == 0) a.split[blockIdx.x] = split;
+    }
+  } else {
+    const int j = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t to = tmem + F::O_COL + j * D + lanes;
+    const float sl2 = a.scale * LOG2E;
+    const int tok_of = r / a.G, head_of = r % a.G;
+    int turn[2] = {0, 0}, outs = 0, done = 0;  // blocks of each buffer, of the tile, and items so far
+    for (int i = 0; ok && next_item(work, work_full, work_free, i, w, ok); ++i) {
+      const Item t(w);
+      const int n = t.tokens(a, j), nb = t.blocks(a, j), row = j * a.toks * a.G + r;
+      const bool mine = tok_of < n, any = (warp & 3) * 32 < n * a.G;  // the thread's row, the warp's
+      if (!nb) {
+        if (t.part >= 0 && mine) a.stat[(size_t)t.part * a.rows + row] = make_float2(0.f, 0.f);
+        continue;
+      }
+      const int first = t.tok0 + j * a.toks, tok = first + tok_of;
+      const int see = last_key(a, t.q, tok), least = last_key(a, t.q, first);
+      float ref = 0.f, ref2 = 0.f, l = 0.f;    // the exponentials' reference, also times sl2; their sum
+      for (int b = 0; b < nb; ++b, ++outs) {
+        const uint32_t ts = tmem + j * 128 + (b & 1) * 64 + lanes;
+        if (!(ok = tc::mbar_wait_warp(s_full + j * 2 + (b & 1), (b & 1 ? turn[1]++ : turn[0]++) & 1))) break;
+        tc::fence_after_sync();
+        if (any) {
+          uint32_t u[64];
+          tc::tmem_ld32_nowait(ts, u);
+          tc::tmem_ld32_nowait(ts + 32, u + 32);
+          tc::tmem_wait_ld();
+          const int key0 = (2 * t.k0 + b) * 64;
+          if (key0 + 63 > least) {  // some row does not read all of these keys
+            const int last = see - key0;
+#pragma unroll
+            for (int x = 0; x < 64; ++x)
+              if (x > last) u[x] = 0xff800000u;  // -infinity
+          }
+          float m4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 4]));
+#pragma unroll
+          for (int x = 8; x < 64; x += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(u[x + e])), __uint_as_float(u[x + e + 4]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          if (b == 0) {
+            ref = mx == -INFINITY ? 0.f : mx;
+            ref2 = __fmul_rn(ref, sl2);
+          } else {
+            const bool grow = mine && (mx - ref) * sl2 > GROW;
+            if (__any_sync(0xffffffffu, grow)) {
+              // the last block's P V; these scores vouch for the one before it, and
+              // the next one waits for this block's P, so the parity is unambiguous
+              if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
+              tc::fence_after_sync();
+              // a row whose reference stays, beside one whose grows (which may be of the
+              // next request), keeps its bits: the products are rounded by themselves,
+              // not in a fused multiply-add, so that its factor is 2^0
+              const float to_new = grow ? mx : ref, to_new2 = __fmul_rn(to_new, sl2);
+              const float f = tc::ex2(ref2 - to_new2);
+              ref = to_new;
+              ref2 = to_new2;
+              l *= f;
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t x[32];
+                tc::tmem_ld32_nowait(to + c, x);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                tc::tmem_st32(to + c, x);
+              }
+            }
+          }
+          const F2 scale2 = f2(sl2, sl2), ref22 = f2(-ref2, -ref2);
+          F2 s4[4] = {f2(l, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            float p, q;
+            split(fma2(f2(__uint_as_float(u[2 * x]), __uint_as_float(u[2 * x + 1])), scale2, ref22), p, q);
+            p = tc::ex2(p);
+            q = tc::ex2(q);
+            s4[x & 3] = add2(s4[x & 3], f2(p, q));
+            u[x] = pack2(p, q);
+          }
+          tc::tmem_st32(ts, u);
+          float p, q;
+          split(add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])), p, q);
+          l = p + q;
+          tc::tmem_wait_st();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + j * 2 + (b & 1));
+      }
+      if (!ok || !(ok = tc::mbar_wait_warp(o_done + j, done++ & 1))) break;
+      tc::fence_after_sync();
+      if (!any) continue;
+      if (t.part >= 0) {
+        float4* dst = a.part + (size_t)t.part * (D / 4) * a.rows + row;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t x[32];
+          tc::tmem_ld32_nowait(to + c, x);
+          tc::tmem_wait_ld();
+          if (mine)
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              dst[(size_t)(c / 4 + g) * a.rows] = make_float4(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1]),
+                                                              __uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3]));
+        }
+        if (mine) a.stat[(size_t)t.part * a.rows + row] = make_float2(ref2, l);
+      } else {
+        const float inv = 1.f / l;
+        const size_t at = (size_t)t.q.row0 + tok, head = t.head * a.G + head_of;
+        const bool out = mine && see >= 0;
+        bf16* dst = a.o + (at * a.Hq + head) * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t x[32];
+          tc::tmem_ld32_nowait(to + c, x);
+          tc::tmem_wait_ld();
+          if (out)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                h[e] = pack2(__uint_as_float(x[g * 8 + 2 * e]) * inv, __uint_as_float(x[g * 8 + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + c + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+        }
+        if (out) a.lse[head * a.T + at] = (ref2 + log2f(l)) * LN2;
+      }
+      tc::fence_before_sync();  // O has been read before the next item's P V, which waits for its P
+    }
   }
-  for (int c = threadIdx.x; c < D; c += 128) {
-    float x = 0.f;
-    for (int w = 0; w < 4; ++w) x += f[w] * so[w][c];
-    a.o[((size_t)t * a.Hq + h) * D + c] = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+  if (!ok) atomicAdd(&g_gave_up, 1u);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == SW + 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0) a.lse[(size_t)h * a.T + t] = sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+// The parts of the unit that CTA blockIdx.x of the attention began and did not
+// finish: its own, then the first one of each CTA behind it.  A thread takes eight
+// columns of a row.
+template <int D> __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
+  tc::grid_dep_wait();
+  const Split s = a.split[blockIdx.x];
+  if (!s.n) return;
+  const int rows = min(s.n - s.tok0, 2 * a.toks) * a.G, id = blockIdx.y * 256 + threadIdx.x, row = id % rows, c8 = id / rows;
+  if (c8 >= D / 8) return;
+  const Req q{s.row0, s.n, s.kv};
+  const int tok = s.tok0 + row / a.G;
+  if (last_key(a, q, tok) < 0) return;
+  // calls f with each part that holds a tile
+  auto parts = [&](auto f) {
+    f(2 * (int)blockIdx.x + 1);
+    long long at = s.after;
+    for (int c = blockIdx.x + 1; at < s.work && c < GRID; ++c) {
+      const long long end = min(at + s.piece, s.work);
+      if (tile_at(at, s.weight) < tile_at(end, s.weight)) f(2 * c);
+      at = end;
+    }
+  };
+  float top = -INFINITY, sum = 0.f, acc[8] = {};
+  parts([&](int p) {
+    const float2 st = a.stat[(size_t)p * a.rows + row];
+    if (st.y != 0.f) top = fmaxf(top, st.x);
+  });
+  parts([&](int p) {
+    const float2 st = a.stat[(size_t)p * a.rows + row];
+    if (st.y == 0.f) return;  // none of the part's keys is the row's
+    const float f = tc::ex2(st.x - top);
+    const float4* src = a.part + ((size_t)p * (D / 4) + 2 * c8) * a.rows + row;
+    const float4 x = src[0], y = src[a.rows];
+    sum += f * st.y;
+    acc[0] += f * x.x; acc[1] += f * x.y; acc[2] += f * x.z; acc[3] += f * x.w;
+    acc[4] += f * y.x; acc[5] += f * y.y; acc[6] += f * y.z; acc[7] += f * y.w;
+  });
+  const float inv = 1.f / sum;
+  const size_t at = (size_t)s.row0 + tok, head = s.head * a.G + row % a.G;
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  *reinterpret_cast<uint4*>(a.o + (at * a.Hq + head) * D + c8 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (c8 == 0) a.lse[head * a.T + at] = (top + log2f(sum)) * LN2;
+}
+
+// Rows of a part: two tiles of tokens, or all there are.
+inline int part_rows(int T, int G) {
+  const int toks = 2 * (128 / G);
+  return (toks < T ? toks : T > 0 ? T : 1) * G;
+}
+inline size_t part_bytes(int rows, int d) { return ((size_t)2 * GRID * rows * d * 4 + 255) / 256 * 256; }
+inline size_t stat_bytes(int rows) { return ((size_t)2 * GRID * rows * 8 + 255) / 256 * 256; }
+
+template <int D> int attend(const CUtensorMap* m, const PagedArgs& a, cudaStream_t s) {
+  using F = Lay<D>;
+  if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_paged_kernel<D>), F::SMEM))
+    return op_fail(GOCR_ECUDA, "kernel configuration rejected");
+  attn_paged_kernel<D><<<GRID, THREADS, F::SMEM, s>>>(m[0], m[1], m[2], a);
+  if (int rc = op_launched("attention_paged")) return rc;
+  if (launch_k(attn_paged_join_kernel<D>, dim3(GRID, (a.rows * (D / 8) + 255) / 256), dim3(256), 0, s, true, a) != cudaSuccess)
+    return op_launched("attention_paged's join");
+  return GOCR_OK;
+}
+
+// TMA map over the pages of a cache: boxes of 64 columns x the keys of a page
+// that a tile holds.
+bool map_pages(CUtensorMap* m, const void* p, const gocr_paged_kv& kv, const int64_t* st) {
+  const unsigned long long dims[4] = {(unsigned long long)kv.head_dim, (unsigned long long)kv.page_size,
+                                      (unsigned long long)kv.n_kv_heads, (unsigned long long)kv.n_pages};
+  const unsigned long long strides[3] = {(unsigned long long)st[2] * 2, (unsigned long long)st[1] * 2,
+                                         (unsigned long long)st[0] * 2};
+  const unsigned box[4] = {64, (unsigned)(kv.page_size < KT ? kv.page_size : KT), 1, 1};
+  return encode_tmap(m, p, false, 4, dims, strides, box);
+}
+
+// The same over q: boxes of 64 columns x the G heads of a kv head x the tokens of a tile.
+bool map_queries(CUtensorMap* m, const void* p, int T, int Hq, int G, int D, long long ld) {
+  const unsigned long long dims[3] = {(unsigned long long)D, (unsigned long long)Hq, (unsigned long long)T};
+  const unsigned long long st[2] = {(unsigned long long)D * 2, (unsigned long long)ld * 2};
+  const unsigned box[3] = {64, (unsigned)G, (unsigned)(128 / G)};
+  return encode_tmap(m, p, false, 3, dims, st, box);
 }
 
 }  // namespace
 
+namespace gocr {
+cudaError_t attn_paged_gave_up(unsigned* out, cudaStream_t s) {
+  return cudaMemcpyFromSymbolAsync(out, g_gave_up, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+}
+}  // namespace gocr
+
 extern "C" size_t gocr_op_attention_paged_workspace(int T, int Hq, int Hkv, int d) {
-  if (T < 0 || Hq < 1 || Hkv < 1 || d < 1) return 0;
-  return 256;
+  if (T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 64 || d < 1) return 0;
+  const int rows = part_rows(T, Hq / Hkv);
+  return part_bytes(rows, d) + stat_bytes(rows) + GRID * sizeof(Split);
 }
 
 extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache, const int32_t* table, int max_pages,
@@ -91,7 +709,7 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
   const int Hkv = kv.n_kv_heads, d = kv.head_dim;
   if (int rc = table_check(n_req, max_pages, kv.page_size, kv.n_pages)) return rc;
   if (kind != GOCR_FWD_AR && kind != GOCR_FWD_DRAFT && kind != GOCR_FWD_VERIFY) return op_fail(GOCR_EINVAL, "bad kind %d", kind);
-  if (T < 0 || T > MAX_ROWS || Hq < 1 || Hq > 1024 || Hq % Hkv || Hq / Hkv > 64)
+  if (T < 0 || T > MAX_ROWS || Hq < 1 || Hq > 1024 || Hq % Hkv || Hq / Hkv > 64 || (long long)T * Hq > 0x7fffffffLL)
     return op_fail(GOCR_EINVAL, "bad shape: T=%d Hq=%d Hkv=%d", T, Hq, Hkv);
   if (!pitch_ok(ldq, Hq, d)) return op_fail(GOCR_EINVAL, "bad row pitch %lld", ldq);
   if (!(scale > 0.f) || scale > 1e30f) return op_fail(GOCR_EINVAL, "bad scale");
@@ -103,11 +721,15 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
   if (!T || !n_req) return GOCR_OK;
+  const int G = Hq / Hkv, rows = part_rows(T, G);
+  CUtensorMap m[3];
+  if (!map_queries(&m[0], q, T, Hq, G, d, ldq) || !map_pages(&m[1], kv.k, kv, &kv.k_page) || !map_pages(&m[2], kv.v, kv, &kv.v_page))
+    return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
   int shift = 4;
   while ((1 << shift) < kv.page_size) ++shift;
-  const PagedArgs a{(const bf16*)q, kv, table, cu_rows, kv_len, (bf16*)o, lse, ldq, max_pages, n_req, T, Hq, Hq / Hkv,
-                   kind == GOCR_FWD_DRAFT, shift, scale};
-  if (d == 128) attn_paged_kernel<128><<<dim3(T, Hq), 128, 0, s>>>(a);
-  else attn_paged_kernel<64><<<dim3(T, Hq), 128, 0, s>>>(a);
-  return op_launched("attention_paged");
+  uint8_t* ws = (uint8_t*)workspace;
+  const PagedArgs a{table, cu_rows, kv_len, (bf16*)o, lse, (float4*)ws, (float2*)(ws + part_bytes(rows, d)),
+                    (Split*)(ws + part_bytes(rows, d) + stat_bytes(rows)), max_pages, kv.n_pages, n_req, T, Hq, Hkv, G,
+                    128 / G, kind == GOCR_FWD_DRAFT, shift, rows, scale};
+  return d == 128 ? attend<128>(m, a, s) : attend<64>(m, a, s);
 }

@@ -272,6 +272,7 @@ cudaError_t linear_ce_gave_up(unsigned* out, cudaStream_t s);
 cudaError_t attn_packed_gave_up(unsigned* out, cudaStream_t s);
 cudaError_t attn_packed_bwd_gave_up(unsigned* out, cudaStream_t s);
 cudaError_t attn_packed_bwd_unaligned(unsigned* out, cudaStream_t s);
+cudaError_t attn_paged_gave_up(unsigned* out, cudaStream_t s);
 // Argument checks that the packed attention calls share.
 int attn_packed_check(int n_seq, int T, int Hq, int Hkv, int d, long long ldq, long long ldk, long long ldv,
                       float scale);

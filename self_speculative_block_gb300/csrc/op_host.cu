@@ -61,7 +61,7 @@ __global__ void wait_probe_kernel(unsigned long long limit) {
 }
 
 // What a thread has seen of a device's counts.
-constexpr int COUNTS = 5, DEVICES = 64;
+constexpr int COUNTS = 6, DEVICES = 64;
 thread_local unsigned t_seen[DEVICES][COUNTS];
 
 bool capturing(cudaStream_t s) {
@@ -87,6 +87,7 @@ extern "C" int gocr_op_status(void* stream) {
   if (e == cudaSuccess) e = attn_packed_bwd_gave_up(now + 2, s);
   if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(now + 3, g_probe, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = attn_packed_bwd_unaligned(now + 4, s);
+  if (e == cudaSuccess) e = attn_paged_gave_up(now + 5, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -102,6 +103,7 @@ extern "C" int gocr_op_status(void* stream) {
   static const char* const who[4] = {"linear_ce", "attention_packed", "attention_packed_backward", "wait_probe"};
   for (int i = 0; i < 4; ++i)
     if (grown[i]) return op_fail(GOCR_EDEVICE, "a wait inside a kernel of %s gave up", who[i]);
+  if (grown[5]) return op_fail(GOCR_EDEVICE, "a wait inside a kernel of attention_paged gave up");
   return GOCR_OK;
 }
 
