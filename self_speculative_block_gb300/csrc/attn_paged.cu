@@ -19,6 +19,8 @@
 #include "attn_packed.cuh"
 #include "paged.cuh"
 
+#include <numeric>
+
 using namespace gocr;
 using namespace gocr::packed;
 using namespace gocr::paged;
@@ -36,9 +38,9 @@ static __device__ unsigned g_gave_up;  // threads whose wait gave up, ever
 
 // A unit that its CTA began and did not finish.
 struct Split {
-  long long after;  // where the next CTA's piece begins, within the unit
-  long long work, piece;
-  int row0, n, kv, tok0, head, weight;
+  int after;  // where the next CTA's piece begins, within the unit
+  int work, piece;
+  int row0, n, kv, tok0, head, weight, pad[3];
 };
 
 struct PagedArgs {
@@ -49,8 +51,38 @@ struct PagedArgs {
   float2* stat;   // [2 GRID][rows]: reference (times scale log2 e) and sum of the exponentials
   Split* split;   // [GRID], n = 0: none
   int max_pages, n_pages, n_req, T, Hq, Hkv, G, toks, draft, shift, rows;
+  int k_page, k_head, k_units, v_page, v_head, v_units;  // page and head strides of the maps' last dimension, and its size
   float scale;
 };
+
+// A tile of K or V in shared memory: 16 groups of 8 keys, in each the D / 64
+// swizzled 8 x 128-byte atoms of its columns.  So a page's keys are whole groups, and one
+// TMA box brings all columns of a page.
+template <int D> constexpr int GROUP = 8 * D * 2;  // bytes of a group
+// dst[128, 64] = Q K^T over D: rows 64 half .. of K's tile; Q's as load_tile leaves it.
+template <int D> __device__ __forceinline__ void mma_scores(uint32_t dst, uint32_t q, uint32_t k, int half) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, 64);
+  const uint64_t qd = tc::sdesc_sw128(q), kd = tc::sdesc_sw128(k + half * 8 * GROUP<D>, GROUP<D>);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    tc::mma_bf16(dst, qd + (((ks >> 2) * BOX_BYTES + (ks & 3) * 32) >> 4), kd + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4),
+                 idesc, ks > 0 ? 1u : 0u);
+}
+// dst[128, D] (+)= P V over rows 64 half .. of V's tile, P from tensor memory.
+template <int D> __device__ __forceinline__ void mma_values(uint32_t dst, uint32_t p, uint32_t v, int half, bool first) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, D) | tc::IDESC_B_MN;
+  const uint64_t vd = tc::sdesc_sw128_mn(v + half * 8 * GROUP<D>, 1024, GROUP<D>);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    tc::mma_bf16_ta(dst, p + ks * 8, vd + (ks * 2 * GROUP<D> >> 4), idesc, !first || ks > 0 ? 1u : 0u);
+}
+// Keys n .. 127 of a tile become zero: they are nobody's and may hold anything.  One warp.
+template <int D> __device__ __forceinline__ void zero_keys(uint8_t* tile, int n) {
+  for (int i = n * 8 + (threadIdx.x & 31); i < KT * 8; i += 32)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      *reinterpret_cast<uint4*>(tile + (i >> 6) * GROUP<D> + c * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
+}
 
 template <int D> struct Lay {
   static constexpr int SLOTS = D == 128 ? 4 : 8;
@@ -76,13 +108,13 @@ __device__ __forceinline__ int last_key(const PagedArgs& a, const Req& q, int i)
 // Work of the two query tiles from token i on: key tiles, twice where both tiles
 // hold tokens.
 __device__ __forceinline__ int weight(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks ? 2 : 1; }
-__device__ __forceinline__ long long work_of(const PagedArgs& a, const Req& q, int i) {
+__device__ __forceinline__ int work_of(const PagedArgs& a, const Req& q, int i) {
   if (i >= q.n) return 0;
   const int last = last_key(a, q, min(i + 2 * a.toks, q.n) - 1);
-  return last < 0 ? 0 : (long long)(last / KT + 1) * weight(a, q, i);
+  return last < 0 ? 0 : (last / KT + 1) * weight(a, q, i);
 }
 // The key tiles of a unit that lie before its work x.
-__device__ __forceinline__ int tile_at(long long x, int weight) { return (int)((x + weight - 1) >> (weight - 1)); }
+__device__ __forceinline__ int tile_at(int x, int weight) { return (x + weight - 1) >> (weight - 1); }
 
 // One work item, as every warp sees it.
 struct Item {
@@ -92,10 +124,15 @@ struct Item {
       : q{w[0].x, w[0].y, w[0].z}, tok0(w[0].w), head(w[1].x), k0(w[1].y), k1(w[1].z), part(w[1].w), req(w[2].x) {}
   // tokens of query tile j
   __device__ int tokens(const PagedArgs& a, int j) const { return min(max(q.n - tok0 - j * a.toks, 0), a.toks); }
-  // blocks of 64 keys of query tile j within the item
+  // With one query tile, both softmax groups (each with its MMA warp) take it: group 0 the
+  // first 64 keys of each key tile, group 1 the others, and they join at the end.
+  __device__ bool one(const PagedArgs& a) const { return q.n - tok0 <= a.toks; }
+  // blocks of 64 keys of group j within the item
   __device__ int blocks(const PagedArgs& a, int j) const {
-    const int n = tokens(a, j), last = last_key(a, q, tok0 + j * a.toks + n - 1);
-    return n == 0 || last < 0 ? 0 : max(min(2 * k1, last / 64 + 1) - 2 * k0, 0);
+    const bool both = one(a);
+    const int end = min(q.n, tok0 + (both || j == 0 ? a.toks : 2 * a.toks)), last = last_key(a, q, end - 1);
+    const int all = last < 0 ? 0 : max(min(2 * k1, last / 64 + 1) - 2 * k0, 0);
+    return both ? (all + 1 - j) >> 1 : all;
   }
   // keys of the item's last tile that exist
   __device__ int tail() const { return min(q.kv - (k1 - 1) * KT, KT); }
@@ -123,25 +160,24 @@ __device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full,
 struct Pages {
   const int* row;
   int n, n_pages, at, cur, next;
-  __device__ int entry(int i) const {
-    const int p = i < n ? row[i] : 0;
-    return p >= 0 && p < n_pages ? p : n_pages;  // behind the last page TMA reads zeros
-  }
+  __device__ int entry(int i) const { return i < n ? row[i] : -1; }
   __device__ Pages(const PagedArgs& a, const Item& t)
       : row(a.table + (size_t)t.req * a.max_pages), n((t.q.kv + (1 << a.shift) - 1) >> a.shift), n_pages(a.n_pages),
         at((t.k0 * KT) >> a.shift) {
     cur = entry(at + (threadIdx.x & 31));
     next = entry(at + 32 + (threadIdx.x & 31));
   }
-  // Page i, to all lanes; 32 is a multiple of a tile's pages, so a tile's entries
-  // (asked for twice, for K and for V) are in hand together.
-  __device__ int operator[](int i) {
-    if (i >= at + 32) {
-      at += 32;
-      cur = next;
-      next = entry(at + 32 + (threadIdx.x & 31));
-    }
-    return __shfl_sync(0xffffffffu, cur, i - at);
+  // Before pages i .. of a tile are asked for (twice, for K and for V); 32 is a multiple of a tile's pages.
+  __device__ void reach(int i) {
+    if (i < at + 32) return;
+    at += 32;
+    cur = next;
+    next = entry(at + 32 + (threadIdx.x & 31));
+  }
+  // The last coordinate of page i in a map, to all lanes; behind the map's end TMA reads zeros.
+  __device__ int place(int i, int page, int head, int units) const {
+    const int p = __shfl_sync(0xffffffffu, cur, (i - at) & 31);
+    return p >= 0 && p < n_pages ? p * page + head : units;
   }
 };
 
@@ -152,9 +188,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   using F = Lay<D>;
   constexpr int SLOTS = F::SLOTS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long sums[SW + 4];
-  __shared__ long long start_at;  // this CTA's piece: where it begins within its first request,
-  __shared__ int start_req;       // and that request
+  __shared__ __align__(16) int sums[SW + 4];
+  __shared__ int start_at;                 // where this CTA's piece begins within its first request,
+  __shared__ int start_req, start_of[3];   // and that request
+  __shared__ float2 chain[2][128];         // of a tile whose keys both softmax groups share: reference and sum
   uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + F::OFF_BAR);
   uint64_t* q_empty = q_full + 1;
@@ -171,12 +208,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* work_free = work_full + 2;   // [2]
   uint64_t* issued = work_free + 2;      // [2] an item's loads are on their way
   uint64_t* drained = issued + 2;        // [2] an MMA warp's products, at its end
-  uint32_t* holder = reinterpret_cast<uint32_t*>(drained + 2);
+  uint64_t* met = drained + 2;           // [4] the two warps that own the same 32 rows of a tile
+  uint32_t* holder = reinterpret_cast<uint32_t*>(met + 4);
   int4* work = reinterpret_cast<int4*>(sm + F::OFF_WORK);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // as a uniform value, for what follows from it
 
   tc::grid_dep_launch();  // the join's CTAs start as SMs fall free, and wait for this grid's end
-  if (tid == 0) {
+  if (warp == SW && lane == 0) {
+    tc::prefetch_tmap(&mk);
+    tc::prefetch_tmap(&mv);
+    tc::prefetch_tmap(&mq);
     tc::mbar_init(q_full, 1);
     tc::mbar_init(q_empty, 2);
     for (int s = 0; s < SLOTS; ++s) {
@@ -185,6 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::mbar_init(v_tail + s, 1);
     }
     for (int j = 0; j < 4; ++j) {
+      tc::mbar_init(met + j, 2);
       tc::mbar_init(s_full + j, 1);
       tc::mbar_init(p_full + j, SW / 2);
     }
@@ -199,49 +242,59 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::fence_mbar_init();
     start_req = a.n_req;
   }
+  __syncwarp();
+  if (warp == SW + 1) tc::tmem_alloc(holder, 512);
 
   // All requests' work: its sum, and where this CTA's piece begins.
   const int per = (a.n_req + THREADS - 1) / THREADS, r0 = min(tid * per, a.n_req), r1 = min(r0 + per, a.n_req);
-  long long mine = 0;
+  auto sum_of = [&](const Req& q) {
+    int sum = 0;
+    for (int i = 0; i < q.n; i += 2 * a.toks) sum += work_of(a, q, i);
+    return sum * a.Hkv;
+  };
+  Req q0{0, 0, 0};  // the thread's first request
+  int first = 0, mine = 0;
   bool without = false;  // a request has rows without keys
   for (int r = r0; r < r1; ++r) {
     const Req q = request(a, r);
-    long long sum = 0;
-    for (int i = 0; i < q.n; i += 2 * a.toks) sum += work_of(a, q, i);
-    mine += sum * a.Hkv;
+    const int sum = sum_of(q);
+    if (r == r0) {
+      q0 = q;
+      first = sum;
+    }
+    mine += sum;
     without |= q.n > q.kv;
   }
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) sums[warp] = inc;
-  __syncwarp();
-  if (warp == SW + 1) tc::tmem_alloc(holder, 512);
   tc::fence_before_sync();
   without = __syncthreads_or(without);
   tc::fence_after_sync();
-  long long before = inc - mine, total = 0;
+  int before = inc - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < SW + 4; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
+    const int v = sums[w];
+    if (w < warp) before += v;
+    total += v;
   }
-  const long long piece = (total + GRID - 1) / GRID, x0 = piece * blockIdx.x, x1 = min(x0 + piece, total);
+  const int piece = (total - 1) / GRID + 1, x0 = min(piece * (int)blockIdx.x, total), x1 = min(x0 + piece, total);
   if (before <= x0 && x0 < before + mine) {
-    for (int r = r0; r < r1; ++r) {
-      const Req q = request(a, r);
-      long long sum = 0;
-      for (int i = 0; i < q.n; i += 2 * a.toks) sum += work_of(a, q, i);
-      sum *= a.Hkv;
-      if (x0 < before + sum) {
-        start_req = r;
-        start_at = x0 - before;
-        break;
-      }
-      before += sum;
+    int r = r0;
+    while (x0 >= before + first && r + 1 < r1) {
+      before += first;
+      q0 = request(a, ++r);
+      first = sum_of(q0);
     }
+    start_req = r;
+    start_of[0] = q0.row0;
+    start_of[1] = q0.n;
+    start_of[2] = q0.kv;
+    start_at = x0 - before;
   }
   if (without) {  // rows without keys, in requests with more rows than keys
     for (int r = blockIdx.x; r < a.n_req; r += GRID) {
@@ -272,19 +325,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int x = 0; x < 2 * n; ++x) {
           if (!(ok = tc::mbar_wait_warp(empty + slot, ph ^ 1))) break;
           const int key0 = (t.k0 + (x >> 1)) * KT, boxes = (min(t.q.kv - key0, KT) + box - 1) / box;
-          if (tc::elect_one()) tc::mbar_expect_tx(full + slot, boxes * box * D * 2);
-          __syncwarp();
-          uint8_t* dst = sm + F::OFF_KV + slot * TILE_BYTES<D>;
-          for (int b = 0; b < boxes; ++b) {
-            const int key = key0 + b * box, page = pages[key >> a.shift];
-            if (tc::elect_one()) {
+          const int page = key0 >> a.shift;
+          pages.reach(page);
+          int at[8];
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tc::tma_load_4d(dst + c * BOX_BYTES + b * box * 128, x & 1 ? &mv : &mk, c * 64, key & ((1 << a.shift) - 1),
-                                t.head, page, full + slot);
-            }
-            __syncwarp();
+          for (int b = 0; b < 8; ++b)
+            at[b] = x & 1 ? pages.place(page + b, a.v_page, t.head * a.v_head, a.v_units)
+                          : pages.place(page + b, a.k_page, t.head * a.k_head, a.k_units);
+          if (tc::elect_one()) {
+            tc::mbar_expect_tx(full + slot, boxes * box * D * 2);
+            uint8_t* dst = sm + F::OFF_KV + slot * TILE_BYTES<D>;
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+              if (b < boxes)
+                tc::tma_load_5d(dst + b * box * D * 2, x & 1 ? &mv : &mk, 0, 0, 0, (key0 & ((1 << a.shift) - 1)) >> 3, at[b],
+                                full + slot);
           }
+          __syncwarp();
           ++loads;
           if (++slot == SLOTS) { slot = 0; ph ^= 1; }
           if (x == 0) {
@@ -307,8 +364,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       ok = tc::ring_landed(full, SLOTS, loads) && tc::ring_landed(q_full, 1, q_loads) && ok;
     } else if (warp < SW + 3) {
-      const int j = warp - (SW + 1);  // the tile
-      const uint32_t q = tc::smem_u32(sm + F::OFF_Q + j * TILE_BYTES<D>), kv = tc::smem_u32(sm + F::OFF_KV);
+      const int j = warp - (SW + 1);  // the softmax group
+      const uint32_t q = tc::smem_u32(sm + F::OFF_Q), kv = tc::smem_u32(sm + F::OFF_KV);
       const uint32_t s_col = tmem + j * 128, o_col = tmem + F::O_COL + j * D;
       int ring = 0;           // ring position of the item's K(0)
       unsigned tails = 0;     // parity of each slot's ragged tiles so far
@@ -320,53 +377,65 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
-        const int nb = t.blocks(a, j), most = max(t.blocks(a, 0), t.blocks(a, 1)), tail = t.tail();
+        const bool one = t.one(a);
+        const int nb = t.blocks(a, j), most = one ? t.k1 - t.k0 : max(t.blocks(a, 0), t.blocks(a, 1)), tail = t.tail();
         auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
         auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
+        // the K/V tile of the group's block b, and which 64 keys of it
+        auto at = [&](int b) { return one ? b : b >> 1; };
+        auto half = [&](int b) { return one ? j : b & 1; };
+        auto opens = [&](int b) { return one || !(b & 1); };
+        auto closes = [&](int b) { return one || (b & 1) || b + 1 == most; };
         // both MMA warps give a K/V tile back, whether they used it or not
         // (but not before it is there: its barrier is in an older phase)
         auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
+        // scores of block b; then the K tile is free, and at last Q
         auto scores = [&](int b) {
-          mma_rows<D>(s_col + (b & 1) * 64, q, tile_of(2 * (b >> 1)), b & 1);
-          tc::mma_commit(s_full + j * 2 + (b & 1));
-        };
-        // after the scores of block b: the K tile, and at last Q
-        auto release_k = [&](int b) {
-          if ((b & 1) || b + 1 == most) release(2 * (b >> 1));
+          if (b < nb) {
+            mma_scores<D>(s_col + (b & 1) * 64, q + (one ? 0 : j * TILE_BYTES<D>), tile_of(2 * at(b)), half(b));
+            tc::mma_commit(s_full + j * 2 + (b & 1));
+          }
+          if (closes(b)) release(2 * at(b));
           if (b + 1 == most) tc::mma_commit(q_empty);
         };
-        if (!(ok = wait(q_full, i) && wait_full(0))) break;
-        if (tc::elect_one()) {
-          // over P of the last item, whose products were issued before
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (b < nb) scores(b);
-            if (b < most) release_k(b);
+        // the last block's P V, then the V tile is free
+        auto values = [&](int b) {
+          if (b < nb) {
+            mma_values<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * at(b) + 1), half(b), b == 0);
+            tc::mma_commit(o_full + j);
+            if (b + 1 == nb) tc::mma_commit(o_done + j);
           }
-        }
-        __syncwarp();
-        for (int b = 0; b < most; ++b) {
-          if (!(b & 1)) {
-            if (!(ok = wait_full(b + 1))) break;                  // V tile b / 2
-            if (b + 2 < most && !(ok = wait_full(b + 2))) break;  // K tile b / 2 + 1
-            if (b + 2 >= most && tail < KT) {
-              const int slot = (ring + b + 1) % SLOTS;
-              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
-              tails ^= 1u << slot;
+          if (closes(b)) release(2 * at(b) + 1);
+        };
+        if (!(ok = wait(q_full, i))) break;
+        // block -2, -1: scores only (over P of the last item, whose products were issued before)
+        for (int b = -2; b < most; ++b) {
+          if (b >= 0) {
+            if (opens(b)) {
+              const int v = 2 * at(b) + 1;
+              if (!(ok = wait_full(v))) break;
+              if (at(b) + 1 == t.k1 - t.k0 && tail < KT) {
+                const int slot = (ring + v) % SLOTS;
+                if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+                tails ^= 1u << slot;
+              }
+            }
+            if (b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
+            // With one tile the next K tile but one may be on its way still, and the
+            // V tile's slot should not wait for it.
+            if (one || b + 2 >= most) {
+              if (tc::elect_one()) values(b);
+              __syncwarp();
             }
           }
-          if (b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
-          if (tc::elect_one()) {
-            if (b < nb) {
-              mma_add<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * (b >> 1) + 1), b & 1, b == 0);
-              tc::mma_commit(o_full + j);
-              if (b + 1 == nb) tc::mma_commit(o_done + j);
+          if (b + 2 < most) {
+            if (opens(b + 2) && !(ok = wait_full(2 * at(b + 2)))) break;
+            if (tc::elect_one()) {
+              if (!one && b >= 0) values(b);
+              scores(b + 2);
             }
-            if (b + 2 < nb) scores(b + 2);
-            if ((b & 1) || b + 1 == most) release(2 * (b >> 1) + 1);
-            if (b + 2 < most) release_k(b + 2);
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (!ok) break;
         ring += 2 * (t.k1 - t.k0);
@@ -374,33 +443,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = tc::mma_drain(drained + j) && ok;
     } else {
       // The piece's items; and the last V tile of a ragged item: nothing behind the request's keys.
-      int r = min(start_req, a.n_req - 1), h = 0, i = 0, items = 0, ring = 0;
-      long long at = 0, left = start_req < a.n_req ? x1 - x0 : 0;  // within the unit; of the piece
-      Req q = request(a, r);
+      int r = start_req, h = 0, i = 0, items = 0, ring = 0;
+      int at = 0, left = r < a.n_req ? x1 - x0 : 0;  // within the unit; of the piece
+      Req q{0, 0, 0};
       Split split{};
       if (left > 0) {
-        long long sum = 0;  // of one head
-        for (int b = 0; b < q.n; b += 64 * a.toks) {
-          long long v = work_of(a, q, b + lane * 2 * a.toks);
+        q = Req{start_of[0], start_of[1], start_of[2]};
+        at = start_at;
+        if (q.n <= 2 * a.toks) {
+          const int one = work_of(a, q, 0);
+          h = at / one;
+          at -= h * one;
+        } else {
+          // 32 units at a time: the sum of a head's, then the unit
+          int sum = 0;
+          for (int b = 0; b < q.n; b += 64 * a.toks) sum += __reduce_add_sync(0xffffffffu, work_of(a, q, b + lane * 2 * a.toks));
+          h = at / max(sum, 1);
+          at -= h * sum;
+          for (bool found = false; !found && i < q.n;) {
+            const int v = work_of(a, q, i + lane * 2 * a.toks);
+            int upto = v;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          sum += v;
-        }
-        h = (int)(start_at / max(sum, 1ll));
-        at = start_at % max(sum, 1ll);
-        for (bool found = false; !found && i < q.n;) {
-          const long long v = work_of(a, q, i + lane * 2 * a.toks);
-          long long upto = v;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            for (int o = 1; o < 32; o <<= 1) {
+              const int x = __shfl_up_sync(0xffffffffu, upto, o);
+              if (lane >= o) upto += x;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, upto > at);
+            found = past != 0;
+            const int l = found ? __ffs(past) - 1 : 31;
+            at -= __shfl_sync(0xffffffffu, found ? upto - v : upto, l);
+            i += (found ? l : 32) * 2 * a.toks;
           }
-          const unsigned past = __ballot_sync(0xffffffffu, upto > at);
-          found = past != 0;
-          const int l = found ? __ffs(past) - 1 : 31;
-          at -= __shfl_sync(0xffffffffu, found ? upto - v : upto, l);
-          i += (found ? l : 32) * 2 * a.toks;
         }
       }
       auto advance = [&] {  // to the next unit
@@ -417,14 +490,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       while (ok) {
         int k0 = 0, k1 = 0, part = -1;
         while (left > 0) {  // the next unit's piece; a cut may leave no whole tile of it
-          const long long all = work_of(a, q, i);
+          const int all = work_of(a, q, i);
           if (at < all) {
-            const int wt = weight(a, q, i), tiles = (int)(all >> (wt - 1));
-            const long long end = min(at + left, all);
+            const int wt = weight(a, q, i), tiles = all >> (wt - 1), end = at + min(left, all - at);
             k0 = tile_at(at, wt);
             k1 = tile_at(end, wt);
             part = k0 == 0 && k1 == tiles ? -1 : 2 * (int)blockIdx.x + (k0 == 0);
-            if (k0 == 0 && k1 < tiles) split = Split{end, all, piece, q.row0, q.n, q.kv, i, h, wt};
+            if (k0 == 0 && k1 < tiles) split = Split{end, all, piece, q.row0, q.n, q.kv, i, h, wt, {}};
             left -= end - at;
             if (k0 < k1) break;
           }
@@ -446,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tail < KT) {
           const int slot = tail_at % SLOTS;
           if (!(ok = tc::mbar_wait_warp(full + slot, (tail_at / SLOTS) & 1))) break;
-          zero_rows<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, tail);
+          zero_keys<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, tail);
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(v_tail + slot);
@@ -460,21 +532,30 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) a.split[blockIdx.x] = split;
     }
   } else {
-    const int j = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of the tile
+    const int j = warp >> 2, r = (warp & 3) * 32 + lane;  // group, row of its tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tmem + F::O_COL + j * D + lanes;
     const float sl2 = a.scale * LOG2E;
     const int tok_of = r / a.G, head_of = r % a.G;
-    int turn[2] = {0, 0}, outs = 0, done = 0;  // blocks of each buffer, of the tile, and items so far
+    int turn[2] = {0, 0}, outs = 0, done = 0, meets = 0;  // blocks of each buffer, of the group, items and meetings so far
+    auto meet = [&] {  // with the other group's warp of these rows
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(met + (warp & 3));
+      const bool there = tc::mbar_wait_warp(met + (warp & 3), meets++ & 1);
+      tc::fence_after_sync();
+      return there;
+    };
     for (int i = 0; ok && next_item(work, work_full, work_free, i, w, ok); ++i) {
       const Item t(w);
-      const int n = t.tokens(a, j), nb = t.blocks(a, j), row = j * a.toks * a.G + r;
+      const bool one = t.one(a);
+      const int tile = one ? 0 : j, n = t.tokens(a, tile), nb = t.blocks(a, j), row = tile * a.toks * a.G + r;
       const bool mine = tok_of < n, any = (warp & 3) * 32 < n * a.G;  // the thread's row, the warp's
-      if (!nb) {
+      if (!nb && !one) {
         if (t.part >= 0 && mine) a.stat[(size_t)t.part * a.rows + row] = make_float2(0.f, 0.f);
         continue;
       }
-      const int first = t.tok0 + j * a.toks, tok = first + tok_of;
+      const int first = t.tok0 + tile * a.toks, tok = first + tok_of;
       const int see = last_key(a, t.q, tok), least = last_key(a, t.q, first);
       float ref = 0.f, ref2 = 0.f, l = 0.f;    // the exponentials' reference, also times sl2; their sum
       for (int b = 0; b < nb; ++b, ++outs) {
@@ -486,7 +567,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc::tmem_ld32_nowait(ts, u);
           tc::tmem_ld32_nowait(ts + 32, u + 32);
           tc::tmem_wait_ld();
-          const int key0 = (2 * t.k0 + b) * 64;
+          const int key0 = (2 * t.k0 + (one ? 2 * b + j : b)) * 64;
           if (key0 + 63 > least) {  // some row does not read all of these keys
             const int last = see - key0;
 #pragma unroll
@@ -519,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               ref = to_new;
               ref2 = to_new2;
               l *= f;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t x[32];
                 tc::tmem_ld32_nowait(to + c, x);
@@ -551,45 +632,71 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + j * 2 + (b & 1));
       }
-      if (!ok || !(ok = tc::mbar_wait_warp(o_done + j, done++ & 1))) break;
+      if (!ok || (nb && !(ok = tc::mbar_wait_warp(o_done + j, done++ & 1)))) break;
       tc::fence_after_sync();
       if (!any) continue;
-      if (t.part >= 0) {
-        float4* dst = a.part + (size_t)t.part * (D / 4) * a.rows + row;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
-          tc::tmem_ld32_nowait(to + c, x);
+      // The row's O (its columns c0 .. c1 - 1 in this thread), sum and reference.  A tile
+      // that both groups took: the two warps of these rows tell one another theirs, and each
+      // joins half of the columns from both groups' O, which lie in the same lanes.
+      int c0 = 0, c1 = D;
+      float own = 1.f, other = 0.f;
+      if (one) {
+        chain[j][r] = make_float2(ref2, l);
+        if (!(ok = meet())) break;
+        const float2 x = chain[j ^ 1][r];
+        const float top = l == 0.f ? x.x : x.y == 0.f ? ref2 : fmaxf(ref2, x.x);
+        own = l == 0.f ? 0.f : tc::ex2(ref2 - top);
+        other = x.y == 0.f ? 0.f : tc::ex2(x.x - top);
+        l = j ? other * x.y + own * l : own * l + other * x.y;  // in one order
+        ref2 = top;
+        c0 = j * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      const float inv = t.part >= 0 ? 1.f : 1.f / l;
+      const size_t at = (size_t)t.q.row0 + tok, head = t.head * a.G + head_of;
+      const bool out = mine && (t.part >= 0 || see >= 0);
+      float4* part = a.part + (size_t)max(t.part, 0) * (D / 4) * a.rows + row;
+      bf16* dst = a.o + (at * a.Hq + head) * D;
+#pragma unroll 1
+      for (int x0 = c0; x0 < c1; x0 += 32) {  // (unrolled, a call of few keys would wait for its instructions)
+        uint32_t x[32];
+        tc::tmem_ld32_nowait(to + x0, x);
+        if (one) {
+          uint32_t y[32];
+          tc::tmem_ld32_nowait(to + (j ? -D : D) + x0, y);
           tc::tmem_wait_ld();
-          if (mine)
+          // (a group none of whose keys the row reads has nothing there)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float u = own == 0.f ? 0.f : own * __uint_as_float(x[e]), v = other == 0.f ? 0.f : other * __uint_as_float(y[e]);
+            x[e] = __float_as_uint(u + v);
+          }
+        } else {
+          tc::tmem_wait_ld();
+        }
+        if (out) {
+          if (t.part >= 0) {
 #pragma unroll
             for (int g = 0; g < 8; ++g)
-              dst[(size_t)(c / 4 + g) * a.rows] = make_float4(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1]),
-                                                              __uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3]));
-        }
-        if (mine) a.stat[(size_t)t.part * a.rows + row] = make_float2(ref2, l);
-      } else {
-        const float inv = 1.f / l;
-        const size_t at = (size_t)t.q.row0 + tok, head = t.head * a.G + head_of;
-        const bool out = mine && see >= 0;
-        bf16* dst = a.o + (at * a.Hq + head) * D;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
-          tc::tmem_ld32_nowait(to + c, x);
-          tc::tmem_wait_ld();
-          if (out)
+              part[(size_t)(x0 / 4 + g) * a.rows] = make_float4(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1]),
+                                                                __uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3]));
+          } else {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 h[e] = pack2(__uint_as_float(x[g * 8 + 2 * e]) * inv, __uint_as_float(x[g * 8 + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + c + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(dst + x0 + g * 8) = make_uint4(h[0], h[1], h[2], h[3]);
             }
+          }
         }
-        if (out) a.lse[head * a.T + at] = (ref2 + log2f(l)) * LN2;
       }
+      if (out && c0 == 0) {
+        if (t.part >= 0) a.stat[(size_t)t.part * a.rows + row] = make_float2(ref2, l);
+        else a.lse[head * a.T + at] = (ref2 + log2f(l)) * LN2;
+      }
+      if (one && !(ok = meet())) break;  // the other group's next P V waits for its own warps only
       tc::fence_before_sync();  // O has been read before the next item's P V, which waits for its P
     }
   }
@@ -602,50 +709,113 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// The parts of the unit that CTA blockIdx.x of the attention began and did not
-// finish: its own, then the first one of each CTA behind it.  A thread takes eight
-// columns of a row.
-template <int D> __global__ void __launch_bounds__(256) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
+// Joins the parts of the units that cuts divide: the part of the CTA that began
+// the unit, then the first one of each CTA behind it.  A task is some columns (eight a
+// thread) of a unit's rows; warps share a task's parts where there are many.
+constexpr int JOIN_CTAS = 4 * SM_COUNT, JOIN_WARPS = 8;
+
+template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
+  __shared__ int ends[256 + 1];  // tasks of the units before
+  __shared__ Split splits[GRID];
+  __shared__ float sums[JOIN_WARPS][10][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto parts_of = [&](const Split& s) { return 2 + (s.work - s.after - 1) / s.piece; };
+  // warps that share a task's parts: each takes two or more
+  auto share_of = [&](int parts) { return parts >= 16 ? 8 : parts >= 8 ? 4 : parts >= 4 ? 2 : 1; };
+  auto rows_of = [&](const Split& s) { return min(s.n - s.tok0, 2 * a.toks) * a.G; };
   tc::grid_dep_wait();
-  const Split s = a.split[blockIdx.x];
-  if (!s.n) return;
-  const int rows = min(s.n - s.tok0, 2 * a.toks) * a.G, id = blockIdx.y * 256 + threadIdx.x, row = id % rows, c8 = id / rows;
-  if (c8 >= D / 8) return;
-  const Req q{s.row0, s.n, s.kv};
-  const int tok = s.tok0 + row / a.G;
-  if (last_key(a, q, tok) < 0) return;
-  // calls f with each part that holds a tile
-  auto parts = [&](auto f) {
-    f(2 * (int)blockIdx.x + 1);
-    long long at = s.after;
-    for (int c = blockIdx.x + 1; at < s.work && c < GRID; ++c) {
-      const long long end = min(at + s.piece, s.work);
-      if (tile_at(at, s.weight) < tile_at(end, s.weight)) f(2 * c);
-      at = end;
+  static_assert(GRID <= 256, "a thread takes a split");
+  int count = 0;
+  if (tid < GRID) {
+    const Split s = a.split[tid];
+    if (s.n) {
+      splits[tid] = s;
+      const int each = 32 * JOIN_WARPS / share_of(parts_of(s));
+      count = (rows_of(s) * (D / 8) + each - 1) / each;
     }
-  };
-  float top = -INFINITY, sum = 0.f, acc[8] = {};
-  parts([&](int p) {
-    const float2 st = a.stat[(size_t)p * a.rows + row];
-    if (st.y != 0.f) top = fmaxf(top, st.x);
-  });
-  parts([&](int p) {
-    const float2 st = a.stat[(size_t)p * a.rows + row];
-    if (st.y == 0.f) return;  // none of the part's keys is the row's
-    const float f = tc::ex2(st.x - top);
-    const float4* src = a.part + ((size_t)p * (D / 4) + 2 * c8) * a.rows + row;
-    const float4 x = src[0], y = src[a.rows];
-    sum += f * st.y;
-    acc[0] += f * x.x; acc[1] += f * x.y; acc[2] += f * x.z; acc[3] += f * x.w;
-    acc[4] += f * y.x; acc[5] += f * y.y; acc[6] += f * y.z; acc[7] += f * y.w;
-  });
-  const float inv = 1.f / sum;
-  const size_t at = (size_t)s.row0 + tok, head = s.head * a.G + row % a.G;
-  uint32_t h[4];
+  }
+  __shared__ int warp_sums[JOIN_WARPS];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  *reinterpret_cast<uint4*>(a.o + (at * a.Hq + head) * D + c8 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
-  if (c8 == 0) a.lse[head * a.T + at] = (top + log2f(sum)) * LN2;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, count, o);
+    if (lane >= o) count += v;
+  }
+  if (lane == 31) warp_sums[warp] = count;
+  __syncthreads();
+  for (int v = 0; v < warp; ++v) count += warp_sums[v];
+  ends[tid + 1] = count;
+  if (tid == 0) ends[0] = 0;
+  __syncthreads();
+  for (int task = blockIdx.x; task < ends[GRID]; task += JOIN_CTAS) {
+    int c = 0;
+    for (int step = 128; step; step >>= 1)
+      if (c + step < GRID && ends[c + step] <= task) c += step;
+    const Split& s = splits[c];
+    const int n = parts_of(s), share = share_of(n), g = warp % share, rows = rows_of(s);
+    const int id = (task - ends[c]) * (32 * JOIN_WARPS / share) + warp / share * 32 + lane, row = id % rows, c8 = id / rows;
+    const Req q{s.row0, s.n, s.kv};
+    const int tok = s.tok0 + row / a.G;
+    const bool out = c8 < D / 8 && last_key(a, q, tok) >= 0;
+    float top = -INFINITY, sum = 0.f, acc[8] = {};
+    if (out) {
+      for (int p0 = g; p0 < n; p0 += 4 * share) {
+        float2 st[4];
+        float4 x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = p0 + e * share;
+          // (a piece may hold none of the unit's tiles)
+          const int from = s.after + (p - 1) * s.piece, to = from + min(s.piece, s.work - from);
+          const bool there = p < n && (p == 0 || tile_at(from, s.weight) < tile_at(to, s.weight));
+          const size_t at = p == 0 ? 2 * c + 1 : 2 * (c + p);
+          st[e] = there ? a.stat[at * a.rows + row] : make_float2(0.f, 0.f);
+          const float4* src = a.part + (at * (D / 4) + 2 * c8) * a.rows + row;
+          x[e] = y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (there) {
+            x[e] = src[0];
+            y[e] = src[a.rows];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (st[e].y == 0.f) continue;  // none of the part's keys is the row's: it holds nothing
+          const float to = fmaxf(top, st[e].x), f = tc::ex2(st[e].x - to), k = top == -INFINITY ? 0.f : tc::ex2(top - to);
+          top = to;
+          sum = sum * k + f * st[e].y;
+          const float v[8] = {x[e].x, x[e].y, x[e].z, x[e].w, y[e].x, y[e].y, y[e].z, y[e].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = acc[i] * k + f * v[i];
+        }
+      }
+    }
+    if (share > 1) {
+      __syncthreads();
+      sums[warp][8][lane] = sum;
+      sums[warp][9][lane] = top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sums[warp][i][lane] = acc[i];
+      __syncthreads();
+      if (g == 0)
+        for (int w = 1; w < share; ++w) {
+          const float l = sums[warp + w][8][lane], m = sums[warp + w][9][lane];
+          if (l == 0.f) continue;
+          const float to = fmaxf(top, m), f = tc::ex2(m - to), k = top == -INFINITY ? 0.f : tc::ex2(top - to);
+          top = to;
+          sum = sum * k + f * l;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = acc[i] * k + f * sums[warp + w][i][lane];
+        }
+    }
+    if (out && g == 0) {
+      const float inv = 1.f / sum;
+      const size_t at = (size_t)s.row0 + tok, head = s.head * a.G + row % a.G;
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      *reinterpret_cast<uint4*>(a.o + (at * a.Hq + head) * D + c8 * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+      if (c8 == 0) a.lse[head * a.T + at] = (top + log2f(sum)) * LN2;
+    }
+  }
 }
 
 // Rows of a part: two tiles of tokens, or all there are.
@@ -662,20 +832,25 @@ template <int D> int attend(const CUtensorMap* m, const PagedArgs& a, cudaStream
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
   attn_paged_kernel<D><<<GRID, THREADS, F::SMEM, s>>>(m[0], m[1], m[2], a);
   if (int rc = op_launched("attention_paged")) return rc;
-  if (launch_k(attn_paged_join_kernel<D>, dim3(GRID, (a.rows * (D / 8) + 255) / 256), dim3(256), 0, s, true, a) != cudaSuccess)
-    return op_launched("attention_paged's join");
-  return GOCR_OK;
+  launch_k(attn_paged_join_kernel<D>, dim3(JOIN_CTAS), dim3(JOIN_WARPS * 32), 0, s, true, a);
+  return op_launched("attention_paged's join");
 }
 
-// TMA map over the pages of a cache: boxes of 64 columns x the keys of a page
-// that a tile holds.
-bool map_pages(CUtensorMap* m, const void* p, const gocr_paged_kv& kv, const int64_t* st) {
-  const unsigned long long dims[4] = {(unsigned long long)kv.head_dim, (unsigned long long)kv.page_size,
-                                      (unsigned long long)kv.n_kv_heads, (unsigned long long)kv.n_pages};
-  const unsigned long long strides[3] = {(unsigned long long)st[2] * 2, (unsigned long long)st[1] * 2,
-                                         (unsigned long long)st[0] * 2};
-  const unsigned box[4] = {64, (unsigned)(kv.page_size < KT ? kv.page_size : KT), 1, 1};
-  return encode_tmap(m, p, false, 4, dims, strides, box);
+// TMA map over the pages of a cache: a box is all columns of the keys of a page
+// that a tile holds, in groups of 8.  A box's page and head share one dimension,
+// whose stride is the largest that both strides are multiples of.
+bool map_pages(CUtensorMap* m, const void* p, const gocr_paged_kv& kv, const int64_t* st, int& page, int& head, int& units) {
+  const int64_t unit = std::gcd(st[0], st[1]), n = (kv.n_pages - 1) * (st[0] / unit) + (kv.n_kv_heads - 1) * (st[1] / unit) + 1;
+  if (n > 0x7fffffff) return false;
+  page = (int)(st[0] / unit);
+  head = (int)(st[1] / unit);
+  units = (int)n;
+  const unsigned long long dims[5] = {64, 8, (unsigned long long)kv.head_dim / 64, (unsigned long long)kv.page_size / 8,
+                                      (unsigned long long)n};
+  const unsigned long long strides[4] = {(unsigned long long)st[2] * 2, 128, (unsigned long long)st[2] * 16,
+                                         (unsigned long long)unit * 2};
+  const unsigned box[5] = {64, 8, (unsigned)kv.head_dim / 64, (unsigned)(kv.page_size < KT ? kv.page_size : KT) / 8, 1};
+  return encode_tmap(m, p, false, 5, dims, strides, box);
 }
 
 // The same over q: boxes of 64 columns x the G heads of a kv head x the tokens of a tile.
@@ -718,18 +893,23 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
   if (((uintptr_t)table | (uintptr_t)cu_rows | (uintptr_t)kv_len | (uintptr_t)lse) & 3)
     return op_fail(GOCR_EINVAL, "array not 4-byte aligned");
   if (workspace_bytes < gocr_op_attention_paged_workspace(T, Hq, Hkv, d)) return op_fail(GOCR_ECAPACITY, "workspace too small");
+  const int G = Hq / Hkv, rows = part_rows(T, G);
+  // the work of a call is counted in 32 bits: key tiles of pairs of query tiles
+  if ((T / (2 * (128 / G)) + (T < n_req ? T : n_req)) * (long long)Hkv * (((long long)max_pages * kv.page_size - 1) / KT + 1) > 1 << 29)
+    return op_fail(GOCR_EINVAL, "bad shape: T=%d rows of %d requests over %d pages of %d", T, n_req, max_pages, kv.page_size);
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
   if (!T || !n_req) return GOCR_OK;
-  const int G = Hq / Hkv, rows = part_rows(T, G);
   CUtensorMap m[3];
-  if (!map_queries(&m[0], q, T, Hq, G, d, ldq) || !map_pages(&m[1], kv.k, kv, &kv.k_page) || !map_pages(&m[2], kv.v, kv, &kv.v_page))
+  int kp, kh, ku, vp, vh, vu;
+  if (!map_queries(&m[0], q, T, Hq, G, d, ldq) || !map_pages(&m[1], kv.k, kv, &kv.k_page, kp, kh, ku) ||
+      !map_pages(&m[2], kv.v, kv, &kv.v_page, vp, vh, vu))
     return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
   int shift = 4;
   while ((1 << shift) < kv.page_size) ++shift;
   uint8_t* ws = (uint8_t*)workspace;
   const PagedArgs a{table, cu_rows, kv_len, (bf16*)o, lse, (float4*)ws, (float2*)(ws + part_bytes(rows, d)),
                     (Split*)(ws + part_bytes(rows, d) + stat_bytes(rows)), max_pages, kv.n_pages, n_req, T, Hq, Hkv, G,
-                    128 / G, kind == GOCR_FWD_DRAFT, shift, rows, scale};
+                    128 / G, kind == GOCR_FWD_DRAFT, shift, rows, kp, kh, ku, vp, vh, vu, scale};
   return d == 128 ? attend<128>(m, a, s) : attend<64>(m, a, s);
 }

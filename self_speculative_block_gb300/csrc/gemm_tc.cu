@@ -125,8 +125,8 @@ bool encode_tmap(void* out, const void* ptr, bool f32, int rank, const unsigned 
                  const unsigned long long* strides, const unsigned* box) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (!encoder()) return false;
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; }
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
   return g_encode(reinterpret_cast<CUtensorMap*>(out),

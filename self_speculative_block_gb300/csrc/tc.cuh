@@ -124,10 +124,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int x, int y, int z, int u, int v, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(smem_u32(dst)), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(smem_u32(dst)), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -182,11 +182,11 @@ __device__ __forceinline__ void fence_after_sync() {
 
 // Shared-memory matrix descriptor: K-major operand tile in the 128-byte
 // swizzled layout TMA writes (8-row atoms of 1024 bytes).
-__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t atom_bytes = 1024) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);  // start address
   d |= (uint64_t)(16u >> 4) << 16;            // leading byte offset (unused for this layout)
-  d |= (uint64_t)(1024u >> 4) << 32;          // stride byte offset: next 8-row atom
+  d |= (uint64_t)(atom_bytes >> 4) << 32;     // stride byte offset: next 8-row atom
   d |= (uint64_t)1 << 46;                     // descriptor version
   d |= (uint64_t)2 << 61;                     // 128-byte swizzle
   return d;
@@ -194,13 +194,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
 
 // The same for an M- or N-major tile: 64-element (128-byte) row segments, one
 // per k, as TMA writes a box of 64 columns x k rows of a row-major matrix
-// whose rows run along k.  SBO: the next eight k (1024 bytes); LBO: the next
+// whose rows run along k.  SBO: the next eight k (atom_bytes); LBO: the next
 // 64 elements of M or N (one box of block_bytes).
-__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t block_bytes) {
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t block_bytes, uint32_t atom_bytes = 1024) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
   d |= (uint64_t)(block_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)(atom_bytes >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
