@@ -529,8 +529,8 @@ int gocr_op_page_step(const int32_t* held, const int32_t* start, const int32_t* 
  * The angle is exact to 2^-26 turns at any position, values are rounded once
  * to bf16.  q, k and v bf16 with rows ldq, ldk and ldv elements apart, as in
  * gocr_op_attention_packed; pos and slots int32[T] (device).  A row whose slot
- * is outside 0..n_pages*page_size-1 is skipped: it is not read, and its q_out
- * row is left as it was.  The slots of a call are distinct (of two rows with
+ * is outside 0..n_pages*page_size-1 is skipped: whatever it holds, nothing is
+ * written for it, and its q_out row is left as it was.  The slots of a call are distinct (of two rows with
  * one slot, parts of either may be left).  Hq <= 1024, Hq % Hkv == 0, d 64 or
  * 128, T <= 2^24, 1 <= theta <= 1e30. */
 int gocr_op_kv_write_paged(const void* q, const void* k, const void* v, const int32_t* pos, const int32_t* slots,

@@ -38,9 +38,9 @@ static __device__ unsigned g_gave_up;  // threads whose wait gave up, ever
 
 // A unit that its CTA began and did not finish.
 struct Split {
-  int after;  // where the next CTA's piece begins, within the unit
-  int work, piece;
-  int row0, n, kv, tok0, head, weight, pad[3];
+  unsigned after;  // where the next CTA's piece begins, within the unit
+  unsigned work, piece;
+  int row0, n, kv, tok0, head, two, pad[3];
 };
 
 struct PagedArgs {
@@ -78,6 +78,7 @@ template <int D> __device__ __forceinline__ void mma_values(uint32_t dst, uint32
 }
 // Keys n .. 127 of a tile become zero: they are nobody's and may hold anything.  One warp.
 template <int D> __device__ __forceinline__ void zero_keys(uint8_t* tile, int n) {
+#pragma unroll 1
   for (int i = n * 8 + (threadIdx.x & 31); i < KT * 8; i += 32)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
@@ -105,16 +106,24 @@ __device__ __forceinline__ Req request(const PagedArgs& a, int r) {
 __device__ __forceinline__ int last_key(const PagedArgs& a, const Req& q, int i) {
   return a.draft && i > 0 ? q.kv - 1 : q.kv - q.n + i;
 }
-// Work of the two query tiles from token i on: key tiles, twice where both tiles
-// hold tokens.
-__device__ __forceinline__ int weight(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks ? 2 : 1; }
-__device__ __forceinline__ int work_of(const PagedArgs& a, const Req& q, int i) {
-  if (i >= q.n) return 0;
-  const int last = last_key(a, q, min(i + 2 * a.toks, q.n) - 1);
-  return last < 0 ? 0 : (last / KT + 1) * weight(a, q, i);
+// Work of a unit, the two query tiles from token i on: 5 a key tile where both
+// hold tokens, 4 where one does, and 10 for its beginning and end (measured, in cycles:
+// 3,070, 2,480 and 6,500).
+constexpr unsigned START = 10;
+__device__ __forceinline__ bool two_tiles(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks; }
+__device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int i) {
+  const int last = i < q.n ? last_key(a, q, min(i + 2 * a.toks, q.n) - 1) : -1;
+  return last < 0 ? 0 : last / KT + 1;
+}
+__device__ __forceinline__ unsigned work_of(const PagedArgs& a, const Req& q, int i) {
+  const unsigned n = key_tiles(a, q, i);
+  return n ? START + n * (two_tiles(a, q, i) ? 5 : 4) : 0;
 }
 // The key tiles of a unit that lie before its work x.
-__device__ __forceinline__ int tile_at(int x, int weight) { return (x + weight - 1) >> (weight - 1); }
+__device__ __forceinline__ int tile_at(unsigned x, bool two) {
+  x = max(x, START) - START;
+  return two ? (x + 4) / 5 : (x + 3) / 4;
+}
 
 // One work item, as every warp sees it.
 struct Item {
@@ -138,11 +147,27 @@ struct Item {
   __device__ int tail() const { return min(q.kv - (k1 - 1) * KT, KT); }
 };
 
+// tc::mbar_wait_warp in few instructions: the roles' loops together have to stay in
+// the instruction cache (with twenty waits of the longer form a chunk's call takes 6 % more).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  uint32_t t0 = 0, t;  // low words: a wait of two seconds ends before they come round
+  bool there;
+#pragma unroll 1
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 64 && !(there = tc::mbar_try_wait(bar, parity)); ++i) {}
+    if (there) break;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+    if (!t0) t0 = t | 1;
+  } while (t - t0 + 1 < (uint32_t)tc::WAIT_NS);
+  return __all_sync(0xffffffffu, there);
+}
+
 // The warp's next item from the ring of two; false past the last one.
 __device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full, uint64_t* work_free, int i, int4* w,
                                           bool& ok) {
   const int s = i & 1;
-  if (!(ok = tc::mbar_wait_warp(work_full + s, (i >> 1) & 1))) return false;
+  if (!(ok = wait_warp(work_full + s, (i >> 1) & 1))) return false;
 #pragma unroll
   for (int e = 0; e < 3; ++e) {
     w[e] = work[s * 3 + e];
@@ -156,28 +181,29 @@ __device__ __forceinline__ bool next_item(const int4* work, uint64_t* work_full,
   return w[0].y > 0;
 }
 
-// The pages of a request, 32 entries a warp in hand and the next 32 on their way.
+// The pages of a request as the last coordinates of the K and V maps: 32 a warp in
+// hand and the next 32 on their way.
 struct Pages {
   const int* row;
-  int n, n_pages, at, cur, next;
+  int n, at, next, k, v;
   __device__ int entry(int i) const { return i < n ? row[i] : -1; }
-  __device__ Pages(const PagedArgs& a, const Item& t)
-      : row(a.table + (size_t)t.req * a.max_pages), n((t.q.kv + (1 << a.shift) - 1) >> a.shift), n_pages(a.n_pages),
-        at((t.k0 * KT) >> a.shift) {
-    cur = entry(at + (threadIdx.x & 31));
-    next = entry(at + 32 + (threadIdx.x & 31));
+  __device__ void take(const PagedArgs& a, int head, int page) {
+    const bool there = page >= 0 && page < a.n_pages;  // behind a map's end TMA reads zeros
+    k = there ? page * a.k_page + head * a.k_head : a.k_units;
+    v = there ? page * a.v_page + head * a.v_head : a.v_units;
   }
-  // Before pages i .. of a tile are asked for (twice, for K and for V); 32 is a multiple of a tile's pages.
-  __device__ void reach(int i) {
+  __device__ Pages(const PagedArgs& a, const Item& t)
+      : row(a.table + (size_t)t.req * a.max_pages), n((t.q.kv + (1 << a.shift) - 1) >> a.shift), at((t.k0 * KT) >> a.shift) {
+    const int lane = threadIdx.x & 31, first = entry(at + lane);
+    next = entry(at + 32 + lane);
+    take(a, t.head, first);
+  }
+  // Before the pages of a tile, i and behind, are asked for; 32 is a multiple of a tile's pages.
+  __device__ void reach(const PagedArgs& a, int head, int i) {
     if (i < at + 32) return;
     at += 32;
-    cur = next;
+    take(a, head, next);
     next = entry(at + 32 + (threadIdx.x & 31));
-  }
-  // The last coordinate of page i in a map, to all lanes; behind the map's end TMA reads zeros.
-  __device__ int place(int i, int page, int head, int units) const {
-    const int p = __shfl_sync(0xffffffffu, cur, (i - at) & 31);
-    return p >= 0 && p < n_pages ? p * page + head : units;
   }
 };
 
@@ -188,8 +214,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   using F = Lay<D>;
   constexpr int SLOTS = F::SLOTS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) int sums[SW + 4];
-  __shared__ int start_at;                 // where this CTA's piece begins within its first request,
+  __shared__ __align__(16) unsigned sums[SW + 4];
+  __shared__ unsigned start_at;            // where this CTA's piece begins within its first request,
   __shared__ int start_req, start_of[3];   // and that request
   __shared__ float2 chain[2][128];         // of a tile whose keys both softmax groups share: reference and sum
   uint8_t* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -221,6 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::prefetch_tmap(&mq);
     tc::mbar_init(q_full, 1);
     tc::mbar_init(q_empty, 2);
+#pragma unroll 1
     for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(full + s, 1);
       tc::mbar_init(empty + s, 2);
@@ -248,16 +275,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   // All requests' work: its sum, and where this CTA's piece begins.
   const int per = (a.n_req + THREADS - 1) / THREADS, r0 = min(tid * per, a.n_req), r1 = min(r0 + per, a.n_req);
   auto sum_of = [&](const Req& q) {
-    int sum = 0;
+    unsigned sum = 0;
+#pragma unroll 1
     for (int i = 0; i < q.n; i += 2 * a.toks) sum += work_of(a, q, i);
     return sum * a.Hkv;
   };
   Req q0{0, 0, 0};  // the thread's first request
-  int first = 0, mine = 0;
+  unsigned first = 0, mine = 0;
   bool without = false;  // a request has rows without keys
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     const Req q = request(a, r);
-    const int sum = sum_of(q);
+    const unsigned sum = sum_of(q);
     if (r == r0) {
       q0 = q;
       first = sum;
@@ -265,26 +294,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     mine += sum;
     without |= q.n > q.kv;
   }
-  int inc = mine;
+  unsigned inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) sums[warp] = inc;
   tc::fence_before_sync();
   without = __syncthreads_or(without);
   tc::fence_after_sync();
-  int before = inc - mine, total = 0;
+  unsigned before = inc - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < SW + 4; ++w) {
-    const int v = sums[w];
+    const unsigned v = sums[w];
     if (w < warp) before += v;
     total += v;
   }
-  const int piece = (total - 1) / GRID + 1, x0 = min(piece * (int)blockIdx.x, total), x1 = min(x0 + piece, total);
+  const unsigned piece = (total + GRID - 1) / GRID, x0 = min(piece * blockIdx.x, total), x1 = x0 + min(piece, total - x0);
   if (before <= x0 && x0 < before + mine) {
     int r = r0;
+#pragma unroll 1
     while (x0 >= before + first && r + 1 < r1) {
       before += first;
       q0 = request(a, ++r);
@@ -297,12 +327,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     start_at = x0 - before;
   }
   if (without) {  // rows without keys, in requests with more rows than keys
+#pragma unroll 1
     for (int r = blockIdx.x; r < a.n_req; r += GRID) {
       const Req q = request(a, r);
       const int n = q.kv == 0 ? q.n : a.draft ? min(1, q.n - q.kv) : q.n - q.kv;
+#pragma unroll 1
       for (int i = tid; i < n * a.Hq; i += THREADS) {
         const int t = q.row0 + i / a.Hq, h = i % a.Hq;
         a.lse[(size_t)h * a.T + t] = -INFINITY;
+#pragma unroll 1
         for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(a.o + ((size_t)t * a.Hq + h) * D + c) = make_uint4(0, 0, 0, 0);
       }
     }
@@ -322,30 +355,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         const Item t(w);
         Pages pages(a, t);
         const int n = t.k1 - t.k0;
+#pragma unroll 1
         for (int x = 0; x < 2 * n; ++x) {
-          if (!(ok = tc::mbar_wait_warp(empty + slot, ph ^ 1))) break;
+          if (!(ok = wait_warp(empty + slot, ph ^ 1))) break;
           const int key0 = (t.k0 + (x >> 1)) * KT, boxes = (min(t.q.kv - key0, KT) + box - 1) / box;
-          const int page = key0 >> a.shift;
-          pages.reach(page);
-          int at[8];
-#pragma unroll
-          for (int b = 0; b < 8; ++b)
-            at[b] = x & 1 ? pages.place(page + b, a.v_page, t.head * a.v_head, a.v_units)
-                          : pages.place(page + b, a.k_page, t.head * a.k_head, a.k_units);
-          if (tc::elect_one()) {
-            tc::mbar_expect_tx(full + slot, boxes * box * D * 2);
-            uint8_t* dst = sm + F::OFF_KV + slot * TILE_BYTES<D>;
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (b < boxes)
-                tc::tma_load_5d(dst + b * box * D * 2, x & 1 ? &mv : &mk, 0, 0, 0, (key0 & ((1 << a.shift) - 1)) >> 3, at[b],
-                                full + slot);
-          }
+          const int page = key0 >> a.shift, group = (key0 & ((1 << a.shift) - 1)) >> 3;
+          pages.reach(a, t.head, page);
+          const int mine = x & 1 ? pages.v : pages.k;
+          uint8_t* dst = sm + F::OFF_KV + slot * TILE_BYTES<D>;
+          if (tc::elect_one()) tc::mbar_expect_tx(full + slot, boxes * box * D * 2);
           __syncwarp();
+#pragma unroll 1
+          for (int b = 0; b < boxes; ++b) {
+            const int at = __shfl_sync(0xffffffffu, mine, (page - pages.at + b) & 31);
+            if (tc::elect_one()) tc::tma_load_5d(dst + b * box * D * 2, x & 1 ? &mv : &mk, 0, 0, 0, group, at, full + slot);
+            __syncwarp();
+          }
           ++loads;
           if (++slot == SLOTS) { slot = 0; ph ^= 1; }
           if (x == 0) {
-            if (!(ok = tc::mbar_wait_warp(q_empty, (i & 1) ^ 1))) break;
+            if (!(ok = wait_warp(q_empty, (i & 1) ^ 1))) break;
             const int tiles = t.tokens(a, 1) ? 2 : 1;
             if (tc::elect_one()) {
               tc::mbar_expect_tx(q_full, tiles * a.toks * a.G * D * 2);
@@ -362,7 +391,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         if (lane == 0) tc::mbar_arrive(issued + (i & 1));
       }
-      ok = tc::ring_landed(full, SLOTS, loads) && tc::ring_landed(q_full, 1, q_loads) && ok;
+      // a copy that lands after its CTA has left would do so in the shared memory of the next
+      bool landed = !q_loads || wait_warp(q_full, (q_loads - 1) & 1);
+#pragma unroll 1
+      for (int s = 0; s < SLOTS && s < loads; ++s) landed = landed && wait_warp(full + s, ((loads - 1 - s) / SLOTS) & 1);
+      ok = landed && ok;
     } else if (warp < SW + 3) {
       const int j = warp - (SW + 1);  // the softmax group
       const uint32_t q = tc::smem_u32(sm + F::OFF_Q), kv = tc::smem_u32(sm + F::OFF_KV);
@@ -371,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       unsigned tails = 0;     // parity of each slot's ragged tiles so far
       int turn[2] = {0, 0};   // blocks of each buffer so far
       auto wait = [&](uint64_t* bar, int ph) {
-        const bool r = tc::mbar_wait_warp(bar, ph & 1);
+        const bool r = wait_warp(bar, ph & 1);
         tc::fence_after_sync();
         return r;
       };
@@ -389,50 +422,55 @@ __global__ void __launch_bounds__(THREADS, 1)
         // both MMA warps give a K/V tile back, whether they used it or not
         // (but not before it is there: its barrier is in an older phase)
         auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
-        // scores of block b; then the K tile is free, and at last Q
         auto scores = [&](int b) {
-          if (b < nb) {
-            mma_scores<D>(s_col + (b & 1) * 64, q + (one ? 0 : j * TILE_BYTES<D>), tile_of(2 * at(b)), half(b));
-            tc::mma_commit(s_full + j * 2 + (b & 1));
-          }
+          if (b >= nb) return;
+          mma_scores<D>(s_col + (b & 1) * 64, q + (one ? 0 : j * TILE_BYTES<D>), tile_of(2 * at(b)), half(b));
+          tc::mma_commit(s_full + j * 2 + (b & 1));
+        };
+        // after the scores of block b: the K tile, and at last Q
+        auto release_k = [&](int b) {
           if (closes(b)) release(2 * at(b));
           if (b + 1 == most) tc::mma_commit(q_empty);
         };
-        // the last block's P V, then the V tile is free
         auto values = [&](int b) {
-          if (b < nb) {
-            mma_values<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * at(b) + 1), half(b), b == 0);
-            tc::mma_commit(o_full + j);
-            if (b + 1 == nb) tc::mma_commit(o_done + j);
-          }
+          if (b >= nb) return;
+          mma_values<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * at(b) + 1), half(b), b == 0);
+          tc::mma_commit(o_full + j);
+          if (b + 1 == nb) tc::mma_commit(o_done + j);
+        };
+        auto release_v = [&](int b) {
           if (closes(b)) release(2 * at(b) + 1);
         };
         if (!(ok = wait(q_full, i))) break;
         // block -2, -1: scores only (over P of the last item, whose products were issued before)
+#pragma unroll 1
         for (int b = -2; b < most; ++b) {
-          if (b >= 0) {
-            if (opens(b)) {
-              const int v = 2 * at(b) + 1;
-              if (!(ok = wait_full(v))) break;
-              if (at(b) + 1 == t.k1 - t.k0 && tail < KT) {
-                const int slot = (ring + v) % SLOTS;
-                if (!(ok = wait(v_tail + slot, tails >> slot))) break;
-                tails ^= 1u << slot;
-              }
-            }
-            if (b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
-            // With one tile the next K tile but one may be on its way still, and the
-            // V tile's slot should not wait for it.
-            if (one || b + 2 >= most) {
-              if (tc::elect_one()) values(b);
-              __syncwarp();
+          if (b >= 0 && opens(b)) {
+            const int v = 2 * at(b) + 1;
+            if (!(ok = wait_full(v))) break;
+            if (at(b) + 1 == t.k1 - t.k0 && tail < KT) {
+              const int slot = (ring + v) % SLOTS;
+              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+              tails ^= 1u << slot;
             }
           }
-          if (b + 2 < most) {
-            if (opens(b + 2) && !(ok = wait_full(2 * at(b + 2)))) break;
+          // Two tiles: the next K tile is there by now, and is not waited for between P and
+          // its product.  One: it may be on its way still, and the V tile's slot does not wait for it.
+          const bool more = b + 2 < most;
+          if (more && (b < 0 || !one) && opens(b + 2) && !(ok = wait_full(2 * at(b + 2)))) break;
+          if (b >= 0 && b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
+          if (tc::elect_one()) {
+            if (b >= 0) values(b);
+            if (more && (b < 0 || !one)) scores(b + 2);
+            if (b >= 0) release_v(b);
+            if (more && (b < 0 || !one)) release_k(b + 2);
+          }
+          __syncwarp();
+          if (more && b >= 0 && one) {
+            if (!(ok = wait_full(2 * at(b + 2)))) break;
             if (tc::elect_one()) {
-              if (!one && b >= 0) values(b);
               scores(b + 2);
+              release_k(b + 2);
             }
             __syncwarp();
           }
@@ -440,32 +478,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         ring += 2 * (t.k1 - t.k0);
       }
-      ok = tc::mma_drain(drained + j) && ok;
+      if (tc::elect_one()) tc::mma_commit(drained + j);
+      __syncwarp();
+      ok = wait_warp(drained + j, 0) && ok;
     } else {
       // The piece's items; and the last V tile of a ragged item: nothing behind the request's keys.
       int r = start_req, h = 0, i = 0, items = 0, ring = 0;
-      int at = 0, left = r < a.n_req ? x1 - x0 : 0;  // within the unit; of the piece
+      unsigned at = 0, left = r < a.n_req ? x1 - x0 : 0;  // within the unit; of the piece
       Req q{0, 0, 0};
       Split split{};
       if (left > 0) {
         q = Req{start_of[0], start_of[1], start_of[2]};
         at = start_at;
         if (q.n <= 2 * a.toks) {
-          const int one = work_of(a, q, 0);
+          const unsigned one = work_of(a, q, 0);
           h = at / one;
           at -= h * one;
         } else {
           // 32 units at a time: the sum of a head's, then the unit
-          int sum = 0;
+          unsigned sum = 0;
+#pragma unroll 1
           for (int b = 0; b < q.n; b += 64 * a.toks) sum += __reduce_add_sync(0xffffffffu, work_of(a, q, b + lane * 2 * a.toks));
-          h = at / max(sum, 1);
+          h = at / max(sum, 1u);
           at -= h * sum;
+#pragma unroll 1
           for (bool found = false; !found && i < q.n;) {
-            const int v = work_of(a, q, i + lane * 2 * a.toks);
-            int upto = v;
+            const unsigned v = work_of(a, q, i + lane * 2 * a.toks);
+            unsigned upto = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-              const int x = __shfl_up_sync(0xffffffffu, upto, o);
+              const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
               if (lane >= o) upto += x;
             }
             const unsigned past = __ballot_sync(0xffffffffu, upto > at);
@@ -487,23 +529,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         else left = 0;
       };
       int tail = KT, tail_at = 0;  // of the item before
+#pragma unroll 1
       while (ok) {
         int k0 = 0, k1 = 0, part = -1;
+#pragma unroll 1
         while (left > 0) {  // the next unit's piece; a cut may leave no whole tile of it
-          const int all = work_of(a, q, i);
+          const unsigned all = work_of(a, q, i);
           if (at < all) {
-            const int wt = weight(a, q, i), tiles = all >> (wt - 1), end = at + min(left, all - at);
-            k0 = tile_at(at, wt);
-            k1 = tile_at(end, wt);
+            const bool two = two_tiles(a, q, i);
+            const unsigned end = at + min(left, all - at);
+            const int tiles = key_tiles(a, q, i);
+            k0 = tile_at(at, two);
+            k1 = tile_at(end, two);
             part = k0 == 0 && k1 == tiles ? -1 : 2 * (int)blockIdx.x + (k0 == 0);
-            if (k0 == 0 && k1 < tiles) split = Split{end, all, piece, q.row0, q.n, q.kv, i, h, wt, {}};
+            if (k0 == 0 && 0 < k1 && k1 < tiles) split = Split{end, all, piece, q.row0, q.n, q.kv, i, h, two, {}};
             left -= end - at;
             if (k0 < k1) break;
           }
           advance();
         }
         const int s = items & 1;
-        if (!(ok = tc::mbar_wait_warp(work_free + s, ((items >> 1) & 1) ^ 1))) break;
+        if (!(ok = wait_warp(work_free + s, ((items >> 1) & 1) ^ 1))) break;
         if (lane == 0) {
           work[s * 3] = make_int4(q.row0, k0 < k1 ? q.n : 0, q.kv, i);
           work[s * 3 + 1] = make_int4(h, k0, k1, part);
@@ -514,10 +560,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The item before, whose tail the next one's loads need not wait for.  Once its
         // loads are issued the slot's barrier is in their phase or the one before;
         // of the barriers that say so, two in turn, none is asked two phases late.
-        if (items > 1 && !(ok = tc::mbar_wait_warp(issued + (items & 1), ((items - 2) >> 1) & 1))) break;
+        if (items > 1 && !(ok = wait_warp(issued + (items & 1), ((items - 2) >> 1) & 1))) break;
         if (tail < KT) {
           const int slot = tail_at % SLOTS;
-          if (!(ok = tc::mbar_wait_warp(full + slot, (tail_at / SLOTS) & 1))) break;
+          if (!(ok = wait_warp(full + slot, (tail_at / SLOTS) & 1))) break;
           zero_keys<D>(sm + F::OFF_KV + slot * TILE_BYTES<D>, tail);
           tc::fence_proxy_async_smem();
           __syncwarp();
@@ -542,7 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(met + (warp & 3));
-      const bool there = tc::mbar_wait_warp(met + (warp & 3), meets++ & 1);
+      const bool there = wait_warp(met + (warp & 3), meets++ & 1);
       tc::fence_after_sync();
       return there;
     };
@@ -558,9 +604,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int first = t.tok0 + tile * a.toks, tok = first + tok_of;
       const int see = last_key(a, t.q, tok), least = last_key(a, t.q, first);
       float ref = 0.f, ref2 = 0.f, l = 0.f;    // the exponentials' reference, also times sl2; their sum
+#pragma unroll 1
       for (int b = 0; b < nb; ++b, ++outs) {
         const uint32_t ts = tmem + j * 128 + (b & 1) * 64 + lanes;
-        if (!(ok = tc::mbar_wait_warp(s_full + j * 2 + (b & 1), (b & 1 ? turn[1]++ : turn[0]++) & 1))) break;
+        if (!(ok = wait_warp(s_full + j * 2 + (b & 1), (b & 1 ? turn[1]++ : turn[0]++) & 1))) break;
         tc::fence_after_sync();
         if (any) {
           uint32_t u[64];
@@ -590,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (__any_sync(0xffffffffu, grow)) {
               // the last block's P V; these scores vouch for the one before it, and
               // the next one waits for this block's P, so the parity is unambiguous
-              if (!(ok = tc::mbar_wait_warp(o_full + j, (outs - 1) & 1))) break;
+              if (!(ok = wait_warp(o_full + j, (outs - 1) & 1))) break;
               tc::fence_after_sync();
               // a row whose reference stays, beside one whose grows (which may be of the
               // next request), keeps its bits: the products are rounded by themselves,
@@ -632,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + j * 2 + (b & 1));
       }
-      if (!ok || (nb && !(ok = tc::mbar_wait_warp(o_done + j, done++ & 1)))) break;
+      if (!ok || (nb && !(ok = wait_warp(o_done + j, done++ & 1)))) break;
       tc::fence_after_sync();
       if (!any) continue;
       // The row's O (its columns c0 .. c1 - 1 in this thread), sum and reference.  A tile
@@ -719,7 +766,7 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
   __shared__ Split splits[GRID];
   __shared__ float sums[JOIN_WARPS][10][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto parts_of = [&](const Split& s) { return 2 + (s.work - s.after - 1) / s.piece; };
+  auto parts_of = [&](const Split& s) { return 2 + (int)((s.work - s.after - 1) / s.piece); };
   // warps that share a task's parts: each takes two or more
   auto share_of = [&](int parts) { return parts >= 16 ? 8 : parts >= 8 ? 4 : parts >= 4 ? 2 : 1; };
   auto rows_of = [&](const Split& s) { return min(s.n - s.tok0, 2 * a.toks) * a.G; };
@@ -765,8 +812,8 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
         for (int e = 0; e < 4; ++e) {
           const int p = p0 + e * share;
           // (a piece may hold none of the unit's tiles)
-          const int from = s.after + (p - 1) * s.piece, to = from + min(s.piece, s.work - from);
-          const bool there = p < n && (p == 0 || tile_at(from, s.weight) < tile_at(to, s.weight));
+          const unsigned from = s.after + (p - 1) * s.piece, to = from + min(s.piece, s.work - from);
+          const bool there = p < n && (p == 0 || tile_at(from, s.two) < tile_at(to, s.two));
           const size_t at = p == 0 ? 2 * c + 1 : 2 * (c + p);
           st[e] = there ? a.stat[at * a.rows + row] : make_float2(0.f, 0.f);
           const float4* src = a.part + (at * (D / 4) + 2 * c8) * a.rows + row;
@@ -894,8 +941,9 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
     return op_fail(GOCR_EINVAL, "array not 4-byte aligned");
   if (workspace_bytes < gocr_op_attention_paged_workspace(T, Hq, Hkv, d)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   const int G = Hq / Hkv, rows = part_rows(T, G);
-  // the work of a call is counted in 32 bits: key tiles of pairs of query tiles
-  if ((T / (2 * (128 / G)) + (T < n_req ? T : n_req)) * (long long)Hkv * (((long long)max_pages * kv.page_size - 1) / KT + 1) > 1 << 29)
+  // the work of a call, at most 5 a key tile and START for each unit, is counted in 32 bits
+  const long long units = (T / (2 * (128 / G)) + (long long)(T < n_req ? T : n_req)) * Hkv;
+  if (units * (((long long)max_pages * kv.page_size - 1) / KT + 3) > 1 << 29)
     return op_fail(GOCR_EINVAL, "bad shape: T=%d rows of %d requests over %d pages of %d", T, n_req, max_pages, kv.page_size);
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;

@@ -2,12 +2,13 @@
 //
 //   y_i = c u_i - s u_(i+d/2),  y_(i+d/2) = c u_(i+d/2) + s u_i,  (c, s) = (cos, sin)(x theta^(-2i/d))
 //
-// A row's angles serve all of its heads, so a CTA takes a few rows, evaluates
-// their cosines and sines once into shared memory, and its threads then take 8 + 8
-// elements of a head each (both halves of the rotation), 16 bytes a load.  The angle
-// in turns is x f_i mod 1 with f_i = theta^(-2i/d) / 2 pi as a 64-bit fraction:
-// one integer product whose overflow drops the whole turns, exact to x 2^-54 or
-// so (f_i comes from a double), where fp32 would lose 2^-24 of the whole angle.
+// A row's angles serve all of its heads, so a CTA takes a few rows and evaluates
+// their cosines and sines once into shared memory, while its threads' loads are under
+// way: a thread takes 8 + 8 elements of a head (both halves of the rotation), 16 bytes a
+// load, four such pieces at a time.  The angle in turns is x f_i mod 1 with f_i =
+// theta^(-2i/d) / 2 pi as a 64-bit fraction: one integer product whose overflow
+// drops the whole turns, exact to x 2^-54 or so (f_i comes from a double), where
+// fp32 would lose 2^-24 of the whole angle.
 #include "paged.cuh"
 
 #include <cmath>
@@ -17,7 +18,7 @@ using namespace gocr::paged;
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256, BATCH = 2;
 constexpr int MOST_ROWS = 8;  // rows of a CTA
 
 struct WriteArgs {
@@ -39,41 +40,66 @@ __device__ __forceinline__ uint32_t down2(float a, float b) {
 }
 
 template <int D> __global__ void __launch_bounds__(THREADS) kv_write_kernel(const __grid_constant__ WriteArgs a) {
-  constexpr int H = D / 2, P = D / 16;  // pieces of 8 + 8 elements in a head
-  __shared__ float2 cs[MOST_ROWS][H];
-  const int t0 = blockIdx.x * a.rows, n = min(a.rows, a.T - t0), heads = a.Hq + 2 * a.kv.n_kv_heads;
+  constexpr int H = D / 2, P = D / 16, STEP = THREADS / P;  // pieces of a head; heads a step
+  __shared__ __align__(16) float2 cs[MOST_ROWS][H];
+  __shared__ unsigned slot_of[MOST_ROWS];
+  const int t0 = blockIdx.x * a.rows, n = min(a.rows, a.T - t0), Hq = a.Hq, Hkv = a.kv.n_kv_heads, heads = Hq + 2 * Hkv;
   const unsigned n_slots = (unsigned)a.kv.n_pages << a.shift;
-  for (int i = threadIdx.x; i < n * H; i += THREADS) {
-    const unsigned long long turn = (unsigned long long)(long long)a.pos[t0 + i / H] * a.freq[i % H];
-    float s, c;  // half turns in [-1, 1), to 2^-31
-    sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
-    cs[i / H][i % H] = make_float2(c, s);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n * heads * P; i += THREADS) {
-    const int p = i % P, h = i / P % heads, t = t0 + i / (P * heads);
-    const unsigned slot = (unsigned)a.slots[t];
-    if (slot >= n_slots) continue;
-    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.kv.n_kv_heads;
-    const int kh = h - a.Hq - (is_k ? 0 : a.kv.n_kv_heads);
-    const bf16* src = is_q ? a.q + t * a.ldq + h * D : is_k ? a.k + t * a.ldk + kh * D : a.v + t * a.ldv + kh * D;
-    const long long page = slot >> a.shift, off = slot & ((1u << a.shift) - 1);
-    bf16* dst = is_q ? a.q_out + ((size_t)t * a.Hq + h) * D
-                : is_k ? (bf16*)a.kv.k + page * a.kv.k_page + kh * a.kv.k_head + off * a.kv.k_token
-                       : (bf16*)a.kv.v + page * a.kv.v_page + kh * a.kv.v_head + off * a.kv.v_token;
-    uint4 lo = *reinterpret_cast<const uint4*>(src + p * 8), hi = *reinterpret_cast<const uint4*>(src + H + p * 8);
-    if (is_q || is_k) {
-      uint32_t *u = &lo.x, *w = &hi.x;
+  const int p = threadIdx.x % P;
+  int row = 0, h = threadIdx.x / P;
+  for (bool first = true;; first = false) {
+    uint4 lo[BATCH], hi[BATCH];
+    int rows[BATCH], hs[BATCH];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = up2(u[e]), y = up2(w[e]);
-        const float2 c0 = cs[t - t0][p * 8 + 2 * e], c1 = cs[t - t0][p * 8 + 2 * e + 1];
-        u[e] = down2(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
-        w[e] = down2(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+    for (int e = 0; e < BATCH; ++e) {
+      while (h >= heads) {
+        h -= heads;
+        ++row;
       }
+      rows[e] = row;
+      hs[e] = h;
+      if (row < n) {
+        const long long t = t0 + row;
+        const bf16* src = (h < Hq ? a.q + t * a.ldq + h * D : h < Hq + Hkv ? a.k + t * a.ldk + (h - Hq) * D
+                                                                           : a.v + t * a.ldv + (h - Hq - Hkv) * D) + p * 8;
+        lo[e] = *reinterpret_cast<const uint4*>(src);
+        hi[e] = *reinterpret_cast<const uint4*>(src + H);
+      }
+      h += STEP;
     }
-    *reinterpret_cast<uint4*>(dst + p * 8) = lo;
-    *reinterpret_cast<uint4*>(dst + H + p * 8) = hi;
+    if (first) {
+      for (int i = threadIdx.x; i < n * H; i += THREADS) {
+        const unsigned long long turn = (unsigned long long)(long long)a.pos[t0 + i / H] * a.freq[i % H];
+        float s, c;  // half turns in [-1, 1), to 2^-31
+        sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s, &c);
+        cs[i / H][i % H] = make_float2(c, s);
+      }
+      if (threadIdx.x < n) slot_of[threadIdx.x] = (unsigned)a.slots[t0 + threadIdx.x];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < BATCH; ++e) {
+      const int r = rows[e], hh = hs[e];
+      if (r >= n) return;  // (rows do not decrease)
+      const unsigned slot = slot_of[r];
+      if (slot >= n_slots) continue;
+      if (hh < Hq + Hkv) {
+        uint32_t *u = &lo[e].x, *w = &hi[e].x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = up2(u[i]), y = up2(w[i]);
+          const float4 c = *reinterpret_cast<const float4*>(&cs[r][p * 8 + 2 * i]);
+          u[i] = down2(x.x * c.x - y.x * c.y, x.y * c.z - y.y * c.w);
+          w[i] = down2(y.x * c.x + x.x * c.y, y.y * c.z + x.y * c.w);
+        }
+      }
+      const long long page = slot >> a.shift, off = slot & ((1u << a.shift) - 1);
+      bf16* dst = (hh < Hq ? a.q_out + ((size_t)(t0 + r) * Hq + hh) * D
+                   : hh < Hq + Hkv ? (bf16*)a.kv.k + page * a.kv.k_page + (hh - Hq) * a.kv.k_head + off * a.kv.k_token
+                                   : (bf16*)a.kv.v + page * a.kv.v_page + (hh - Hq - Hkv) * a.kv.v_head + off * a.kv.v_token) + p * 8;
+      *reinterpret_cast<uint4*>(dst) = lo[e];
+      *reinterpret_cast<uint4*>(dst + H) = hi[e];
+    }
   }
 }
 
@@ -111,7 +137,10 @@ extern "C" int gocr_op_kv_write_paged(const void* q, const void* k, const void* 
   while ((1 << a.shift) < a.kv.page_size) ++a.shift;
   for (int i = 0; i < d / 2; ++i)  // at most 1 / 2 pi of a turn
     a.freq[i] = (unsigned long long)std::ldexp(std::pow((double)theta, -2.0 * i / d) / 6.283185307179586476925, 64);
-  a.rows = 1;
+  // rows that a CTA's threads take in one batch; fewer where that leaves SMs without a CTA
+  const int fit = THREADS * BATCH / ((Hq + 2 * Hkv) * (d / 16)), spread = (T + 2 * SM_COUNT - 1) / (2 * SM_COUNT);
+  a.rows = fit < spread ? fit : spread;
+  a.rows = a.rows < 1 ? 1 : a.rows > MOST_ROWS ? MOST_ROWS : a.rows;
   const int grid = (T + a.rows - 1) / a.rows;
   if (d == 128) kv_write_kernel<128><<<grid, THREADS, 0, s>>>(a);
   else kv_write_kernel<64><<<grid, THREADS, 0, s>>>(a);
