@@ -106,10 +106,10 @@ __device__ __forceinline__ Req request(const PagedArgs& a, int r) {
 __device__ __forceinline__ int last_key(const PagedArgs& a, const Req& q, int i) {
   return a.draft && i > 0 ? q.kv - 1 : q.kv - q.n + i;
 }
-// Work of a unit, the two query tiles from token i on: 5 a key tile where both
-// hold tokens, 4 where one does, and 10 for its beginning and end (measured, in cycles:
-// 3,070, 2,480 and 6,500).
-constexpr unsigned START = 10;
+// Work of a unit, the two query tiles from token i on: 5 a key tile and 10 for its
+// beginning and end where both hold tokens (3,070 and 6,500 cycles measured); 4 and 2
+// where one does, whose keys' way from HBM hides most of the ends (2,480 cycles a tile;
+// 64 single tokens take 54.3 us with 2, 57.5 with 10).
 __device__ __forceinline__ bool two_tiles(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks; }
 __device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int i) {
   const int last = i < q.n ? last_key(a, q, min(i + 2 * a.toks, q.n) - 1) : -1;
@@ -117,12 +117,11 @@ __device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int i
 }
 __device__ __forceinline__ unsigned work_of(const PagedArgs& a, const Req& q, int i) {
   const unsigned n = key_tiles(a, q, i);
-  return n ? START + n * (two_tiles(a, q, i) ? 5 : 4) : 0;
+  return n ? (two_tiles(a, q, i) ? 10 + 5 * n : 2 + 4 * n) : 0;
 }
 // The key tiles of a unit that lie before its work x.
 __device__ __forceinline__ int tile_at(unsigned x, bool two) {
-  x = max(x, START) - START;
-  return two ? (x + 4) / 5 : (x + 3) / 4;
+  return two ? (max(x, 10u) - 6) / 5 : (max(x, 2u) + 1) / 4;
 }
 
 // One work item, as every warp sees it.
@@ -271,6 +270,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncwarp();
   if (warp == SW + 1) tc::tmem_alloc(holder, 512);
+  tc::grid_dep_wait();  // so far nothing that an earlier kernel may write was read
 
   // All requests' work: its sum, and where this CTA's piece begins.
   const int per = (a.n_req + THREADS - 1) / THREADS, r0 = min(tid * per, a.n_req), r1 = min(r0 + per, a.n_req);
@@ -770,6 +770,7 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
   // warps that share a task's parts: each takes two or more
   auto share_of = [&](int parts) { return parts >= 16 ? 8 : parts >= 8 ? 4 : parts >= 4 ? 2 : 1; };
   auto rows_of = [&](const Split& s) { return min(s.n - s.tok0, 2 * a.toks) * a.G; };
+  tc::grid_dep_launch();
   tc::grid_dep_wait();
   static_assert(GRID <= 256, "a thread takes a split");
   int count = 0;
@@ -877,7 +878,7 @@ template <int D> int attend(const CUtensorMap* m, const PagedArgs& a, cudaStream
   using F = Lay<D>;
   if (!kernel_smem_at_least(reinterpret_cast<const void*>(&attn_paged_kernel<D>), F::SMEM))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
-  attn_paged_kernel<D><<<GRID, THREADS, F::SMEM, s>>>(m[0], m[1], m[2], a);
+  launch_k(attn_paged_kernel<D>, dim3(GRID), dim3(THREADS), F::SMEM, s, true, m[0], m[1], m[2], a);
   if (int rc = op_launched("attention_paged")) return rc;
   launch_k(attn_paged_join_kernel<D>, dim3(JOIN_CTAS), dim3(JOIN_WARPS * 32), 0, s, true, a);
   return op_launched("attention_paged's join");
@@ -941,7 +942,7 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
     return op_fail(GOCR_EINVAL, "array not 4-byte aligned");
   if (workspace_bytes < gocr_op_attention_paged_workspace(T, Hq, Hkv, d)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   const int G = Hq / Hkv, rows = part_rows(T, G);
-  // the work of a call, at most 5 a key tile and START for each unit, is counted in 32 bits
+  // the work of a call, at most 5 a key tile and 10 for each unit, is counted in 32 bits
   const long long units = (T / (2 * (128 / G)) + (long long)(T < n_req ? T : n_req)) * Hkv;
   if (units * (((long long)max_pages * kv.page_size - 1) / KT + 3) > 1 << 29)
     return op_fail(GOCR_EINVAL, "bad shape: T=%d rows of %d requests over %d pages of %d", T, n_req, max_pages, kv.page_size);

@@ -10,6 +10,7 @@
 // drops the whole turns, exact to x 2^-54 or so (f_i comes from a double), where
 // fp32 would lose 2^-24 of the whole angle.
 #include "paged.cuh"
+#include "tc.cuh"
 
 #include <cmath>
 
@@ -46,6 +47,8 @@ template <int D> __global__ void __launch_bounds__(THREADS) kv_write_kernel(cons
   const int t0 = blockIdx.x * a.rows, n = min(a.rows, a.T - t0), Hq = a.Hq, Hkv = a.kv.n_kv_heads, heads = Hq + 2 * Hkv;
   const unsigned n_slots = (unsigned)a.kv.n_pages << a.shift;
   const int p = threadIdx.x % P;
+  tc::grid_dep_launch();  // the next kernel's beginning overlaps this one, this one's the last one's
+  tc::grid_dep_wait();
   int row = 0, h = threadIdx.x / P;
   for (bool first = true;; first = false) {
     uint4 lo[BATCH], hi[BATCH];
@@ -142,7 +145,7 @@ extern "C" int gocr_op_kv_write_paged(const void* q, const void* k, const void* 
   a.rows = fit < spread ? fit : spread;
   a.rows = a.rows < 1 ? 1 : a.rows > MOST_ROWS ? MOST_ROWS : a.rows;
   const int grid = (T + a.rows - 1) / a.rows;
-  if (d == 128) kv_write_kernel<128><<<grid, THREADS, 0, s>>>(a);
-  else kv_write_kernel<64><<<grid, THREADS, 0, s>>>(a);
+  if (d == 128) launch_k(kv_write_kernel<128>, dim3(grid), dim3(THREADS), 0, s, true, a);
+  else launch_k(kv_write_kernel<64>, dim3(grid), dim3(THREADS), 0, s, true, a);
   return op_launched("kv_write_paged");
 }

@@ -10,6 +10,7 @@
 // in shared memory) and does its share of the rows, of the pages taken and of
 // those given back, finding the request of each by bisection.
 #include "paged.cuh"
+#include "tc.cuh"
 
 using namespace gocr;
 using namespace gocr::paged;
@@ -65,6 +66,8 @@ __global__ void __launch_bounds__(THREADS) page_step_kernel(const StepArgs a) {
   extern __shared__ int sh[];
   __shared__ int sums[THREADS / 32];
   const int R = a.n_req, tid = threadIdx.x, cap = a.max_pages << a.shift, round = (1 << a.shift) - 1;
+  tc::grid_dep_launch();  // the next kernel's beginning overlaps this one, this one's the last one's
+  tc::grid_dep_wait();
   int *rows = sh, *need = sh + R + 1, *back = need + R + 1;  // sums over the requests before
   const int per = (R + THREADS - 1) / THREADS, r0 = min(tid * per, R), r1 = min(r0 + per, R);
   auto sane = [&](int h, int s, int e) { return 0 <= s && s <= h && s <= e && h <= cap && e <= cap; };
@@ -173,6 +176,6 @@ extern "C" int gocr_op_page_step(const int32_t* held, const int32_t* start, cons
   const size_t smem = 3 * (size_t)(n_req + 1) * sizeof(int);
   if (smem > 48 * 1024 && !kernel_smem_at_least(reinterpret_cast<const void*>(&page_step_kernel), smem))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
-  page_step_kernel<<<grid > 0 ? grid : 1, THREADS, smem, s>>>(a);
+  launch_k(page_step_kernel, dim3(grid > 0 ? grid : 1), dim3(THREADS), smem, s, true, a);
   return op_launched("page_step");
 }
