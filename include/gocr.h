@@ -526,7 +526,7 @@ int gocr_op_page_step(const int32_t* held, const int32_t* start, const int32_t* 
  *   (y[i], y[i+d/2]) = (c u[i] - s u[i+d/2], c u[i+d/2] + s u[i]),
  * c and s the cosine and sine of x theta^(-2i/d), for each head of q (into
  * q_out[T, Hq, d], dense) and of k (into the cache at slots[t]); v is copied.
- * The angle is exact to 2^-26 turns at any position, values are rounded once
+ * The angle is exact to 2^-26 turns up to position 2^24, values are rounded once
  * to bf16.  q, k and v bf16 with rows ldq, ldk and ldv elements apart, as in
  * gocr_op_attention_packed; pos and slots int32[T] (device).  A row whose slot
  * is outside 0..n_pages*page_size-1 is skipped: whatever it holds, nothing is

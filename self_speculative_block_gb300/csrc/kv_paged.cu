@@ -7,7 +7,7 @@
 // way: a thread takes 8 + 8 elements of a head (both halves of the rotation), 16 bytes a
 // load, four such pieces at a time.  The angle in turns is x f_i mod 1 with f_i =
 // theta^(-2i/d) / 2 pi as a 64-bit fraction: one integer product whose overflow
-// drops the whole turns, exact to x 2^-54 or so (f_i comes from a double), where
+// drops the whole turns, exact to x 2^-52 or so (f_i comes from doubles), where
 // fp32 would lose 2^-24 of the whole angle.
 #include "paged.cuh"
 #include "tc.cuh"
@@ -138,8 +138,13 @@ extern "C" int gocr_op_kv_write_paged(const void* q, const void* k, const void* 
   a.T = T;
   a.Hq = Hq;
   while ((1 << a.shift) < a.kv.page_size) ++a.shift;
-  for (int i = 0; i < d / 2; ++i)  // at most 1 / 2 pi of a turn
-    a.freq[i] = (unsigned long long)std::ldexp(std::pow((double)theta, -2.0 * i / d) / 6.283185307179586476925, 64);
+  // theta^(-2i/d) as the product of its powers of two in i (relative 2^-50); at most 1 / 2 pi of a turn
+  double power[64] = {0x1p64 / 6.283185307179586476925};
+  for (int bit = 1; bit < d / 2; bit *= 2) {
+    const double f = std::pow((double)theta, -2.0 * bit / d);
+    for (int i = 0; i < bit; ++i) power[bit + i] = power[i] * f;
+  }
+  for (int i = 0; i < d / 2; ++i) a.freq[i] = (unsigned long long)power[i];
   // rows that a CTA's threads take in one batch; fewer where that leaves SMs without a CTA
   const int fit = THREADS * BATCH / ((Hq + 2 * Hkv) * (d / 16)), spread = (T + 2 * SM_COUNT - 1) / (2 * SM_COUNT);
   a.rows = fit < spread ? fit : spread;

@@ -521,7 +521,10 @@ def _ready(device, sizes, *operands) -> None:
     """The last checks before device work.  Sizes go to the library as 32-bit
     numbers, which would be cut silently; the calls build no autograd graph, so an
     operand that wants a gradient would lose it silently."""
-    if max(sizes) > 0x7fffffff or min(sizes) < 0:
+    bits = 0
+    for n in sizes:
+        bits |= n
+    if bits >> 31:
         raise ValueError(f"a size of {list(sizes)} is outside 0 .. 2^31 - 1")
     for t in operands:
         if t is not None and t.requires_grad and _torch().is_grad_enabled():
@@ -535,7 +538,8 @@ def _launch(device, fn, *args) -> None:
     """Call a C entry on the device's current stream, with the device current."""
     torch = _torch()
     index = device.index
-    if torch.cuda.current_device() != index:
+    current = getattr(torch._C, "_cuda_getDevice", None)  # (a CUDA tensor in hand: CUDA is initialised)
+    if (current() if current is not None else torch.cuda.current_device()) != index:
         with torch.cuda.device(index):
             return _check(fn(*args, torch.cuda.current_stream().cuda_stream))
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
@@ -734,35 +738,52 @@ def op_page_step(held, start, end, table, free_pages, n_free, page_size: int, ro
     torch = _torch()
     _lead("table", table, 2, torch.int32)
     dev, (R, width), n_pages = table.device, table.shape, free_pages.numel()
-    _want("table", table, (R, width), torch.int32, dev)
-    for name, t in (("held", held), ("start", start), ("end", end)):
-        _want(name, t, (R,), torch.int32, dev)
-    _want("free_pages", free_pages, (n_pages,), torch.int32, dev)
-    _want("n_free", n_free, (1,), torch.int32, dev)
+    _ints(dev, ("held", held, (R,)), ("start", start, (R,)), ("end", end, (R,)), ("table", table, (R, width)),
+          ("free_pages", free_pages, (n_pages,)), ("n_free", n_free, (1,)))
     _ready(dev, (R, width, page_size, n_pages, rows))
-    out = torch.empty((1 + 3 * R + 1 + 2 * rows,), dtype=torch.int32, device=dev).split((1, R, R, R + 1, rows, rows))
+    # (views that share no version counter: half the time of split)
+    out = torch.unsafe_split_with_sizes(torch.empty((2 + 3 * R + 2 * rows,), dtype=torch.int32, device=dev),
+                                        (1, R, R, R + 1, rows, rows))
+    at = out[0].data_ptr()
     _launch(dev, load().gocr_op_page_step, held.data_ptr(), start.data_ptr(), end.data_ptr(), R, table.data_ptr(), width,
-            page_size, free_pages.data_ptr(), n_pages, n_free.data_ptr(), *[t.data_ptr() for t in out], rows)
+            page_size, free_pages.data_ptr(), n_pages, n_free.data_ptr(), at, at + 4, at + 4 * (1 + R),
+            at + 4 * (1 + 2 * R), at + 4 * (2 + 3 * R), at + 4 * (2 + 3 * R + rows), rows)
     return PageStep(*out)
 
 
-def _cache(k_cache, v_cache, device):
-    """Check the pages of a layer, [n_pages, Hkv, page_size, d] bf16 each, in any
-    order of the strides; returns (PagedKV, Hkv, d)."""
-    torch = _torch()
-    _lead("k_cache", k_cache, 4, torch.bfloat16)
-    _lead("v_cache", v_cache, 4, torch.bfloat16)
-    shape, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
-    if v_cache.shape != shape:
-        raise ValueError(f"v_cache must be {list(shape)}, got {list(v_cache.shape)}")
-    if ks[3] != 1 or vs[3] != 1:
+def _ints(device, *operands):
+    """Check int32 operands, (name, tensor, shape) each, as _want does."""
+    i32 = _torch().int32
+    for name, t, shape in operands:
+        if not (t.dtype is i32 and t.shape == shape and t.is_contiguous() and t.device == device):
+            _want(name, t, shape, i32, device)
+
+
+def _cache_args(q, k_cache, v_cache):
+    """Check q [T, Hq, d] and a layer's pages, [n_pages, Hkv, page_size, d] each,
+    in any order of the strides, all bf16; returns (PagedKV, device, T, Hq, Hkv, d, q's row pitch)."""
+    bf16, dev, shape, pages = _torch().bfloat16, q.device, q.shape, k_cache.shape
+    if len(shape) == 3 and len(pages) == 4 and v_cache.shape == pages and k_cache.dtype is v_cache.dtype is q.dtype is bf16:
+        (T, Hq, d), (n, Hkv, ps, dk) = shape, pages
+        qs, ks, vs = q.stride(), k_cache.stride(), v_cache.stride()
+        if (dk == d and qs[2] == ks[3] == vs[3] == 1 and (Hq == 1 or qs[1] == d) and k_cache.device == dev
+                and v_cache.device == dev and not (n | Hkv | ps) >> 31):
+            kv = PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], n, ps, Hkv, d)
+            return kv, dev, T, Hq, Hkv, d, qs[0] if T > 1 else Hq * d
+    # what is wrong
+    _lead("q", q, 3, bf16)
+    _lead("k_cache", k_cache, 4, bf16)
+    _lead("v_cache", v_cache, 4, bf16)
+    if v_cache.shape != pages:
+        raise ValueError(f"v_cache must be {list(pages)}, got {list(v_cache.shape)}")
+    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
         raise ValueError("the elements of a head must be contiguous in k_cache and v_cache")
-    if k_cache.device != device or v_cache.device != device:
-        raise ValueError(f"k_cache is on {k_cache.device}, v_cache on {v_cache.device}, q is on {device}")
-    n, heads, ps, d = shape
-    if max(n, heads, ps) > 0x7fffffff:
-        raise ValueError(f"a size of {list(shape)} is outside 0 .. 2^31 - 1")
-    return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), *ks[:3], *vs[:3], n, ps, heads, d), heads, d
+    if k_cache.device != dev or v_cache.device != dev:
+        raise ValueError(f"k_cache is on {k_cache.device}, v_cache on {v_cache.device}, q is on {dev}")
+    if pages[3] != shape[2]:
+        raise ValueError(f"the cache holds heads of {pages[3]}, q has heads of {shape[2]}")
+    _rows("q", q, shape[0], None, shape[2], dev)
+    raise ValueError(f"a size of {list(pages)} is outside 0 .. 2^31 - 1")
 
 
 def op_kv_write_paged(q, k, v, pos, slots, k_cache, v_cache, theta: float = 10000.0, q_out=None):
@@ -773,21 +794,16 @@ def op_kv_write_paged(q, k, v, pos, slots, k_cache, v_cache, theta: float = 1000
     the rotated q [T, Hq, d], written into q_out when given; rows whose slot is
     outside the cache are skipped."""
     torch = _torch()
-    _lead("q", q, 3, torch.bfloat16)
-    dev, (T, Hq, d) = q.device, q.shape
-    kv, Hkv, dk = _cache(k_cache, v_cache, dev)
-    if dk != d:
-        raise ValueError(f"the cache holds heads of {dk}, q has heads of {d}")
-    ld = (_rows("q", q, T, None, d, dev), _rows("k", k, T, Hkv, d, dev), _rows("v", v, T, Hkv, d, dev))
-    _want("pos", pos, (T,), torch.int32, dev)
-    _want("slots", slots, (T,), torch.int32, dev)
+    kv, dev, T, Hq, Hkv, d, ldq = _cache_args(q, k_cache, v_cache)
+    ldk, ldv = _rows("k", k, T, Hkv, d, dev), _rows("v", v, T, Hkv, d, dev)
+    _ints(dev, ("pos", pos, (T,)), ("slots", slots, (T,)))
     _ready(dev, (T, Hq), q, k, v, k_cache, v_cache)
     if q_out is None:
         q_out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
     else:
         _want("q_out", q_out, (T, Hq, d), torch.bfloat16, dev)
     _launch(dev, load().gocr_op_kv_write_paged, q.data_ptr(), k.data_ptr(), v.data_ptr(), pos.data_ptr(),
-            slots.data_ptr(), q_out.data_ptr(), ctypes.byref(kv), T, Hq, *ld, theta)
+            slots.data_ptr(), q_out.data_ptr(), kv, T, Hq, ldq, ldk, ldv, theta)
     return q_out
 
 
@@ -804,17 +820,10 @@ def op_attention_paged(q, k_cache, v_cache, table, cu_rows, kv_len, kind: int = 
     without keys gets 0 and -inf, rows of no request are not written."""
     torch = _torch()
     lib = load()
-    _lead("q", q, 3, torch.bfloat16)
-    dev, (T, Hq, d) = q.device, q.shape
-    kv, Hkv, dk = _cache(k_cache, v_cache, dev)
-    if dk != d:
-        raise ValueError(f"the cache holds heads of {dk}, q has heads of {d}")
-    ldq = _rows("q", q, T, None, d, dev)
+    kv, dev, T, Hq, Hkv, d, ldq = _cache_args(q, k_cache, v_cache)
     _lead("table", table, 2, torch.int32)
     R, width = table.shape
-    _want("table", table, (R, width), torch.int32, dev)
-    _want("cu_rows", cu_rows, (R + 1,), torch.int32, dev)
-    _want("kv_len", kv_len, (R,), torch.int32, dev)
+    _ints(dev, ("table", table, (R, width)), ("cu_rows", cu_rows, (R + 1,)), ("kv_len", kv_len, (R,)))
     _ready(dev, (R, width, T, Hq), q, k_cache, v_cache)
     if o is None:
         o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
@@ -824,10 +833,11 @@ def op_attention_paged(q, k_cache, v_cache, table, cu_rows, kv_len, kind: int = 
         lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
     else:
         _want("lse", lse, (Hq, T), torch.float32, dev)
-    ws = _workspace(workspace, lib.gocr_op_attention_paged_workspace(T, Hq, Hkv, d), dev)
-    _launch(dev, lib.gocr_op_attention_paged, q.data_ptr(), ctypes.byref(kv), table.data_ptr(), width,
-            cu_rows.data_ptr(), kv_len.data_ptr(), kind, o.data_ptr(), lse.data_ptr(), R, T, Hq, ldq,
-            d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+    need = lib.gocr_op_attention_paged_workspace(T, Hq, Hkv, d)
+    ws = _workspace(workspace, need, dev)
+    _launch(dev, lib.gocr_op_attention_paged, q.data_ptr(), kv, table.data_ptr(), width, cu_rows.data_ptr(),
+            kv_len.data_ptr(), kind, o.data_ptr(), lse.data_ptr(), R, T, Hq, ldq, d ** -0.5 if scale is None else scale,
+            ws.data_ptr(), need if workspace is None else ws.numel())
     return o, lse
 
 
