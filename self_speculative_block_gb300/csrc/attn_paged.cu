@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // as a uniform value, for what follows from it
 
-  tc::grid_dep_launch();  // the join's CTAs start as SMs fall free, and wait for this grid's end
   if (warp == SW && lane == 0) {
     tc::prefetch_tmap(&mk);
     tc::prefetch_tmap(&mv);
@@ -747,6 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc::fence_before_sync();  // O has been read before the next item's P V, which waits for its P
     }
   }
+  tc::grid_dep_launch();  // the join's CTAs start as SMs fall free, and wait for this grid's end
   if (!ok) atomicAdd(&g_gave_up, 1u);
   tc::fence_before_sync();
   __syncthreads();
@@ -758,10 +758,15 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Joins the parts of the units that cuts divide: the part of the CTA that began
 // the unit, then the first one of each CTA behind it.  A task is some columns (eight a
-// thread) of a unit's rows; warps share a task's parts where there are many.
+// thread) of a unit's rows; warps share a task's parts where there are many.  A
+// thread has BATCH parts' loads in flight: 4 for short calls, which wait for one
+// chain of loads (one token 11.4 us with 4, 12.0 with 2), and 2 for long ones, whose
+// parts want the loads of four CTAs an SM (two chunks of 2,048 rows 143 us with 2,
+// 147 with 4).
 constexpr int JOIN_CTAS = 4 * SM_COUNT, JOIN_WARPS = 8;
 
-template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
+template <int D, int BATCH>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 8 / BATCH) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ int ends[256 + 1];  // tasks of the units before
   __shared__ Split splits[GRID];
   __shared__ float sums[JOIN_WARPS][10][32];
@@ -790,12 +795,14 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
   }
   if (lane == 31) warp_sums[warp] = count;
   __syncthreads();
-  for (int v = 0; v < warp; ++v) count += warp_sums[v];
+#pragma unroll
+  for (int v = 0; v < JOIN_WARPS; ++v) count += v < warp ? warp_sums[v] : 0;
   ends[tid + 1] = count;
   if (tid == 0) ends[0] = 0;
   __syncthreads();
   for (int task = blockIdx.x; task < ends[GRID]; task += JOIN_CTAS) {
     int c = 0;
+#pragma unroll 1
     for (int step = 128; step; step >>= 1)
       if (c + step < GRID && ends[c + step] <= task) c += step;
     const Split& s = splits[c];
@@ -806,11 +813,12 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
     const bool out = c8 < D / 8 && last_key(a, q, tok) >= 0;
     float top = -INFINITY, sum = 0.f, acc[8] = {};
     if (out) {
-      for (int p0 = g; p0 < n; p0 += 4 * share) {
-        float2 st[4];
-        float4 x[4], y[4];
+#pragma unroll 1
+      for (int p0 = g; p0 < n; p0 += BATCH * share) {
+        float2 st[BATCH];
+        float4 x[BATCH], y[BATCH];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < BATCH; ++e) {
           const int p = p0 + e * share;
           // (a piece may hold none of the unit's tiles)
           const unsigned from = s.after + (p - 1) * s.piece, to = from + min(s.piece, s.work - from);
@@ -825,7 +833,7 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < BATCH; ++e) {
           if (st[e].y == 0.f) continue;  // none of the part's keys is the row's: it holds nothing
           const float to = fmaxf(top, st[e].x), f = tc::ex2(st[e].x - to), k = top == -INFINITY ? 0.f : tc::ex2(top - to);
           top = to;
@@ -844,6 +852,7 @@ template <int D> __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_paged_j
       for (int i = 0; i < 8; ++i) sums[warp][i][lane] = acc[i];
       __syncthreads();
       if (g == 0)
+#pragma unroll 1
         for (int w = 1; w < share; ++w) {
           const float l = sums[warp + w][8][lane], m = sums[warp + w][9][lane];
           if (l == 0.f) continue;
@@ -880,7 +889,8 @@ template <int D> int attend(const CUtensorMap* m, const PagedArgs& a, cudaStream
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
   launch_k(attn_paged_kernel<D>, dim3(GRID), dim3(THREADS), F::SMEM, s, true, m[0], m[1], m[2], a);
   if (int rc = op_launched("attention_paged")) return rc;
-  launch_k(attn_paged_join_kernel<D>, dim3(JOIN_CTAS), dim3(JOIN_WARPS * 32), 0, s, true, a);
+  launch_k(a.T < 8 * a.toks ? attn_paged_join_kernel<D, 4> : attn_paged_join_kernel<D, 2>, dim3(JOIN_CTAS),
+           dim3(JOIN_WARPS * 32), 0, s, true, a);
   return op_launched("attention_paged's join");
 }
 
