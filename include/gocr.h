@@ -553,10 +553,16 @@ int gocr_op_kv_write_paged(const void* q, const void* k, const void* v, const in
  * are of the same call.  kv_len above max_pages * page_size is taken for that;
  * table entries outside 0..n_pages-1 read as pages of zeros.  Hq / Hkv <= 64, Hq <=
  * 1024, d 64 or 128, T <= 2^24, T Hq <= 2^31 - 1, pitch and scale as in
- * gocr_op_attention_packed.
+ * gocr_op_attention_packed; (T / (2 floor(128 Hkv / Hq)) + n_req) Hkv
+ * (max_pages page_size / 128 + 3) <= 2^29; page and head strides of a cache such
+ * that its extent has fewer than 2^31 of their greatest common divisor.
  * Scores, softmax statistics, sums and the parts of a split key axis are in
  * fp32; exp(scale q k^T - m), with m within 2^8 of the maximum so far, is
- * rounded to bf16 for the product with v. */
+ * rounded to bf16 for the product with v.  The keys of all requests are cut into
+ * equal pieces, so a row's last bits depend on the other requests of the call (the
+ * same call gives the same bits).  The workspace takes up to 304 (2 floor(128
+ * Hkv / Hq) Hq / Hkv) (4 d + 8) bytes, 40 MB with heads of 128, and less for
+ * fewer rows. */
 size_t gocr_op_attention_paged_workspace(int T, int Hq, int Hkv, int d);
 int gocr_op_attention_paged(const void* q, const gocr_paged_kv* kv, const int32_t* table, int max_pages,
                             const int32_t* cu_rows, const int32_t* kv_len, int kind, void* o, float* lse, int n_req,

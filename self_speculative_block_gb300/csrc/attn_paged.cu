@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 8 / BATCH) attn_paged_join_ke
           const int p = p0 + e * share;
           // (a piece may hold none of the unit's tiles)
           const unsigned from = s.after + (p - 1) * s.piece, to = from + min(s.piece, s.work - from);
-          const bool there = p < n && (p == 0 || tile_at(from, s.two) < tile_at(to, s.two));
+          const bool there = p < n && c + p < GRID && (p == 0 || tile_at(from, s.two) < tile_at(to, s.two));
           const size_t at = p == 0 ? 2 * c + 1 : 2 * (c + p);
           st[e] = there ? a.stat[at * a.rows + row] : make_float2(0.f, 0.f);
           const float4* src = a.part + (at * (D / 4) + 2 * c8) * a.rows + row;
@@ -894,22 +894,24 @@ template <int D> int attend(const CUtensorMap* m, const PagedArgs& a, cudaStream
   return op_launched("attention_paged's join");
 }
 
-// TMA map over the pages of a cache: a box is all columns of the keys of a page
-// that a tile holds, in groups of 8.  A box's page and head share one dimension,
-// whose stride is the largest that both strides are multiples of.
-bool map_pages(CUtensorMap* m, const void* p, const gocr_paged_kv& kv, const int64_t* st, int& page, int& head, int& units) {
-  const int64_t unit = std::gcd(st[0], st[1]), n = (kv.n_pages - 1) * (st[0] / unit) + (kv.n_kv_heads - 1) * (st[1] / unit) + 1;
-  if (n > 0x7fffffff) return false;
-  page = (int)(st[0] / unit);
-  head = (int)(st[1] / unit);
-  units = (int)n;
-  const unsigned long long dims[5] = {64, 8, (unsigned long long)kv.head_dim / 64, (unsigned long long)kv.page_size / 8,
-                                      (unsigned long long)n};
-  const unsigned long long strides[4] = {(unsigned long long)st[2] * 2, 128, (unsigned long long)st[2] * 16,
-                                         (unsigned long long)unit * 2};
-  const unsigned box[5] = {64, 8, (unsigned)kv.head_dim / 64, (unsigned)(kv.page_size < KT ? kv.page_size : KT) / 8, 1};
-  return encode_tmap(m, p, false, 5, dims, strides, box);
-}
+// K or V as TMA sees it: a box is all columns of the keys of a page that a tile
+// holds, in groups of 8.  A box's page and head share one dimension, whose stride is the
+// largest that both strides are multiples of.
+struct PageMap {
+  const void* p;
+  int64_t token, unit, page, head, units;  // strides in elements; page and head strides in units, and units in all
+  PageMap(const void* p, const int64_t* st, const gocr_paged_kv& kv)
+      : p(p), token(st[2]), unit(std::gcd(st[0], st[1])), page(st[0] / unit), head(st[1] / unit),
+        units((kv.n_pages - 1) * page + (kv.n_kv_heads - 1) * head + 1) {}
+  bool encode(CUtensorMap* m, const gocr_paged_kv& kv) const {
+    const unsigned long long dims[5] = {64, 8, (unsigned long long)kv.head_dim / 64, (unsigned long long)kv.page_size / 8,
+                                        (unsigned long long)units};
+    const unsigned long long strides[4] = {(unsigned long long)token * 2, 128, (unsigned long long)token * 16,
+                                           (unsigned long long)unit * 2};
+    const unsigned box[5] = {64, 8, (unsigned)kv.head_dim / 64, (unsigned)(kv.page_size < KT ? kv.page_size : KT) / 8, 1};
+    return encode_tmap(m, p, false, 5, dims, strides, box);
+  }
+};
 
 // The same over q: boxes of 64 columns x the G heads of a kv head x the tokens of a tile.
 bool map_queries(CUtensorMap* m, const void* p, int T, int Hq, int G, int D, long long ld) {
@@ -956,19 +958,21 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
   const long long units = (T / (2 * (128 / G)) + (long long)(T < n_req ? T : n_req)) * Hkv;
   if (units * (((long long)max_pages * kv.page_size - 1) / KT + 3) > 1 << 29)
     return op_fail(GOCR_EINVAL, "bad shape: T=%d rows of %d requests over %d pages of %d", T, n_req, max_pages, kv.page_size);
+  const PageMap km(kv.k, &kv.k_page, kv), vm(kv.v, &kv.v_page, kv);
+  if (km.units > 0x7fffffff || vm.units > 0x7fffffff)
+    return op_fail(GOCR_EINVAL, "bad cache strides: %d pages whose strides have no common unit", kv.n_pages);
   cudaStream_t s = (cudaStream_t)stream;
   if (int rc = op_stream_check(s)) return rc;
   if (!T || !n_req) return GOCR_OK;
   CUtensorMap m[3];
-  int kp, kh, ku, vp, vh, vu;
-  if (!map_queries(&m[0], q, T, Hq, G, d, ldq) || !map_pages(&m[1], kv.k, kv, &kv.k_page, kp, kh, ku) ||
-      !map_pages(&m[2], kv.v, kv, &kv.v_page, vp, vh, vu))
+  if (!map_queries(&m[0], q, T, Hq, G, d, ldq) || !km.encode(&m[1], kv) || !vm.encode(&m[2], kv))
     return op_fail(GOCR_ECUDA, "a TMA descriptor was rejected");
   int shift = 4;
   while ((1 << shift) < kv.page_size) ++shift;
   uint8_t* ws = (uint8_t*)workspace;
   const PagedArgs a{table, cu_rows, kv_len, (bf16*)o, lse, (float4*)ws, (float2*)(ws + part_bytes(rows, d)),
                     (Split*)(ws + part_bytes(rows, d) + stat_bytes(rows)), max_pages, kv.n_pages, n_req, T, Hq, Hkv, G,
-                    128 / G, kind == GOCR_FWD_DRAFT, shift, rows, kp, kh, ku, vp, vh, vu, scale};
+                    128 / G, kind == GOCR_FWD_DRAFT, shift, rows, (int)km.page, (int)km.head, (int)km.units, (int)vm.page,
+                    (int)vm.head, (int)vm.units, scale};
   return d == 128 ? attend<128>(m, a, s) : attend<64>(m, a, s);
 }

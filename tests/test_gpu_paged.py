@@ -589,6 +589,62 @@ def test_paged_forward_in_a_graph(g):
             assert torch.equal(a, b)
 
 
+def test_paged_graph_with_copies_between(g):
+    """Fills, copies and another stream's work before each call of a captured forward: the calls wait for them."""
+    Hq, Hkv, d, ps, R, T = 4, 2, 64, 16, 3, 40
+    r = torch.Generator(device="cuda").manual_seed(15)
+    kc, vc = _empty_cache("head", 60, Hkv, ps, d)
+    src = [torch.randn((T, h, d), generator=r, device="cuda").bfloat16() for h in (Hq, Hkv, Hkv)]
+    q, k, v = (torch.zeros_like(x) for x in src)
+    lens = [i32([0, 100, 7]), i32([0, 100, 7]), i32([9, 120, 8])]
+    held, start, end = (torch.zeros_like(x) for x in lens)
+    table, free = torch.arange(60, dtype=torch.int32, device="cuda").view(R, 20), torch.arange(60, dtype=torch.int32, device="cuda")
+    n_free = i32([9])
+    rot, o, lse = torch.zeros_like(q), torch.zeros_like(q), torch.zeros((Hq, T), device="cuda")
+    side = torch.cuda.Stream()
+
+    def forward():
+        main = torch.cuda.current_stream()
+        for a, b in zip((held, start, end), lens):
+            a.copy_(b)
+        s = g.op_page_step(held, start, end, table, free, n_free, ps, T)
+        q.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            k.copy_(src[1])
+            v.copy_(src[2])
+        main.wait_stream(side)
+        q.copy_(src[0])
+        g.op_kv_write_paged(q, k, v, s.pos, s.slots, kc, vc, q_out=rot)
+        o.zero_()
+        g.op_attention_paged(rot, kc, vc, table, s.cu_rows, s.kv_len, o=o, lse=lse)
+        q.zero_()
+        k.zero_()
+    saved = table.clone(), free.clone()
+    forward()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (rot, o, lse, kc, vc, table, free)]
+    capture = torch.cuda.Stream()
+    capture.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(capture):
+        table.copy_(saved[0])
+        free.copy_(saved[1])
+        with torch.cuda.graph(graph, stream=capture):
+            forward()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for x in (rot, o, lse, kc, vc):
+            x.zero_()
+        table.copy_(saved[0])
+        free.copy_(saved[1])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((rot, o, lse, kc, vc, table, free), want):
+            assert torch.equal(a, b)
+
+
 def test_paged_calls_on_two_streams(g):
     """Two programs at once, each with its own cache and workspace."""
     cs = [_case([33] * 6, [1031, 2049, 33, 512, 700, 1500], 12, 4, 128, 16, "head", seed=s) for s in (20, 21)]

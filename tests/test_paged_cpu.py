@@ -120,6 +120,12 @@ def test_attention_paged_refusals(g):
         assert call(kv=bad) == EINVAL and "strides" in _message(g), bad
     assert call(kv=dict(page_size=512)) == EINVAL and call(kv=dict(head_dim=32)) == EINVAL
     assert call(n=need - 1) == ECAPACITY and "workspace" in _message(g)
+    # strides whose common divisor is too small for the cache's extent
+    assert call(kv=dict(n_pages=1 << 26, k_page=4104, v_page=4104)) == EINVAL and "unit" in _message(g)
+    assert call(kv=dict(n_pages=1 << 26, v_page=4104)) == EINVAL and "unit" in _message(g)
+    # more work than 32 bits count
+    big = g.load().gocr_op_attention_paged_workspace(1 << 21, 8, 4, 64)
+    assert call(T=1 << 21, R=4096, width=1 << 16, n=big) == EINVAL and "shape" in _message(g)
 
 
 def test_attention_paged_workspaces_serve_fewer_rows(g):
