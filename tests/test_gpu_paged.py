@@ -645,6 +645,74 @@ def test_paged_graph_with_copies_between(g):
             assert torch.equal(a, b)
 
 
+def test_paged_offsets_past_32_bits(g):
+    """A cache of more than 2^32 elements: pages at both of its ends, and slots of more than 2^22 positions."""
+    Hq, Hkv, d, ps, n_pages = 8, 8, 128, 256, 16500
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    kc, vc = (torch.empty((n_pages, ps, Hkv, d), dtype=torch.bfloat16, device="cuda").transpose(1, 2) for _ in range(2))
+    assert kc.numel() > 1 << 32
+    T = 600
+    pages = [n_pages - 1, 0, n_pages - 2]
+    table = i32([pages])
+    r = torch.Generator(device="cuda").manual_seed(16)
+    qkv = torch.randn((T, Hq + 2 * Hkv, d), generator=r, device="cuda").bfloat16()
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = (table[0].long()[pos.long() // ps] * ps + pos % ps).to(torch.int32)
+    rot = g.op_kv_write_paged(q, k, v, pos, slots, kc, vc)
+    K = torch.cat([kc[p].transpose(0, 1) for p in pages])[:T]
+    assert torch.equal(torch.cat([vc[p].transpose(0, 1) for p in pages])[:T], v)
+    val, tol = _rotated(k, pos, 10000.0)
+    assert ((K.double() - val).abs() <= tol).all()
+    c = dict(q=rot, kc=kc, vc=vc, table=table, cu=i32([0, T]), kv_len=i32([T]), K=[K], V=[v], rows=[T])
+    _check(g, c, g.FWD_VERIFY, *_attend(g, c, g.FWD_VERIFY))
+
+
+def test_attention_paged_most_requests(g):
+    """4,096 requests, single tokens over one to five pages."""
+    R = 4096
+    rng = random.Random(17)
+    kv = [rng.randint(1, 70) for _ in range(R)]
+    c = _case([1] * R, kv, 2, 1, 64, 16, "head", seed=17)
+    o, lse = _attend(g, c, g.FWD_VERIFY)
+    K, V = (torch.zeros((R, 70, 64), dtype=torch.float64, device="cuda") for _ in range(2))
+    for r in range(R):
+        K[r, :kv[r]], V[r, :kv[r]] = c["K"][r][:, 0].double(), c["V"][r][:, 0].double()
+    S = torch.einsum("rhd,rkd->rhk", c["q"].double(), K) * 64 ** -0.5
+    S.masked_fill_(torch.arange(70, device="cuda")[None, None, :] >= i32(kv)[:, None, None], -math.inf)
+    P = torch.softmax(S, -1)
+    O = torch.einsum("rhk,rkd->rhd", P, V)
+    # exponentials to 2^-16: scores of at most some tens, sums 70 long
+    tol = (U + 2.0 ** -16) * torch.einsum("rhk,rkd->rhd", P, V.abs()) + U * O.abs()
+    assert ((o.double() - O).abs() <= tol).all()
+    assert ((lse.T.double() - torch.logsumexp(S, -1)).abs() <= 2.0 ** -16).all()
+
+
+def test_attention_paged_graphs_that_share_a_workspace(g):
+    """Two captured calls of different shapes with one workspace, replayed in turn."""
+    cs = [_case([33] * 4, [700, 1500, 90, 4000], 12, 4, 128, 16, "head", seed=22), _case([1] * 9, [2000] * 9, 12, 4, 128, 16, "token", seed=23)]
+    want = [_attend(g, c, g.FWD_VERIFY) for c in cs]
+    ws = torch.empty((max(g.load().gocr_op_attention_paged_workspace(c["q"].shape[0], 12, 4, 128) for c in cs),),
+                     dtype=torch.uint8, device="cuda")
+    outs, graphs, stream = [], [], torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for c in cs:
+        outs.append((torch.zeros(c["q"].shape, dtype=torch.bfloat16, device="cuda"), torch.zeros((12, c["q"].shape[0]), device="cuda")))
+        graphs.append(torch.cuda.CUDAGraph())
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            _attend(g, c, g.FWD_VERIFY, workspace=ws, o=outs[-1][0], lse=outs[-1][1])
+    for _ in range(4):
+        for x in outs:
+            x[0].zero_()
+        for gr in graphs + graphs[::-1]:
+            gr.replay()
+        torch.cuda.synchronize()
+        for w, x in zip(want, outs):
+            assert torch.equal(w[0], x[0]) and torch.equal(w[1], x[1])
+
+
 def test_paged_calls_on_two_streams(g):
     """Two programs at once, each with its own cache and workspace."""
     cs = [_case([33] * 6, [1031, 2049, 33, 512, 700, 1500], 12, 4, 128, 16, "head", seed=s) for s in (20, 21)]
