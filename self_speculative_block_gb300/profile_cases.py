@@ -40,6 +40,13 @@
         (a third [M]), causal attention over 15 packed sequences and over one
         of 8,192 rows, the cross entropy of 2,048 rows.
 
+    python -m self_speculative_block_gb300.profile_cases paged_kv
+        The paged KV cache at the 0.5B-class decoder's heads, each forward
+        twice: single tokens of 64 requests of 256 to 8,131 keys, draft
+        windows of 33 rows of 16 requests of 545 to 2,930 keys, the last
+        chunks of 2,048 rows of two prompts of 8,192 (page step, write and
+        attention each).
+
 All hold a few GB on the device.  The sweep's shapes and inputs are the ones
 bench.py times for its kernel roofline.
 """
@@ -198,6 +205,33 @@ def train_ops_case(repeat: int = 2):
     gocr.op_status(dev)
 
 
+def paged_kv_case(repeat: int = 2):
+    import torch
+    from . import gocr
+    cfg, dev, ps = synth.BASE, torch.device("cuda:0"), 16
+    g = torch.Generator(device=dev)
+    g.manual_seed(0)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)
+    for lens, rows, kind in (([256 + 125 * r for r in range(64)], 1, gocr.FWD_AR),
+                             ([545 + 159 * r for r in range(16)], 33, gocr.FWD_DRAFT),
+                             ([8192, 8192], 2048, gocr.FWD_VERIFY)):
+        R, T, width = len(lens), rows * len(lens), -(-max(lens) // ps)
+        n_pages = sum(-(-n // ps) for n in lens)
+        cache = [torch.randn((n_pages, cfg.n_kv_heads, ps, cfg.head_dim), generator=g, device=dev).to(torch.bfloat16)
+                 for _ in range(2)]
+        qkv = torch.randn((T, cfg.n_q_heads + 2 * cfg.n_kv_heads, cfg.head_dim), generator=g, device=dev).to(torch.bfloat16)
+        q, k, v = qkv.split((cfg.n_q_heads, cfg.n_kv_heads, cfg.n_kv_heads), 1)
+        table = torch.full((R, width), -1, dtype=torch.int32, device=dev)
+        free = torch.randperm(n_pages, generator=g, device=dev).to(torch.int32)
+        zero, past = i32([0] * R), [n - rows for n in lens]
+        first = gocr.op_page_step(zero, zero, i32(past), table, free, i32([n_pages]), ps, sum(past))
+        for _ in range(repeat):
+            s = gocr.op_page_step(first.held, first.held, i32(lens), table, free, first.n_free, ps, T)
+            rot = gocr.op_kv_write_paged(q, k, v, s.pos, s.slots, *cache, theta=cfg.rope_theta)
+            gocr.op_attention_paged(rot, *cache, table, s.cu_rows, s.kv_len, kind=kind)
+    gocr.op_status(dev)
+
+
 def draft_case(B: int = 32):
     from . import gocr
     cfg = synth.BASE
@@ -238,6 +272,8 @@ def main(argv):
     what = argv[1] if len(argv) > 1 else ""
     if what == "train_ops":
         train_ops_case()
+    elif what == "paged_kv":
+        paged_kv_case()
     elif what == "draft":
         draft_case(int(argv[2]) if len(argv) > 2 else 32)
     elif what == "sweep":
