@@ -20,6 +20,7 @@
 #include "paged.cuh"
 
 #include <numeric>
+#include <type_traits>
 
 using namespace gocr;
 using namespace gocr::packed;
@@ -409,71 +410,77 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
-        const bool one = t.one(a);
-        const int nb = t.blocks(a, j), most = one ? t.k1 - t.k0 : max(t.blocks(a, 0), t.blocks(a, 1)), tail = t.tail();
-        auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
-        auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
-        // the K/V tile of the group's block b, and which 64 keys of it
-        auto at = [&](int b) { return one ? b : b >> 1; };
-        auto half = [&](int b) { return one ? j : b & 1; };
-        auto opens = [&](int b) { return one || !(b & 1); };
-        auto closes = [&](int b) { return one || (b & 1) || b + 1 == most; };
-        // both MMA warps give a K/V tile back, whether they used it or not
-        // (but not before it is there: its barrier is in an older phase)
-        auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
-        auto scores = [&](int b) {
-          if (b >= nb) return;
-          mma_scores<D>(s_col + (b & 1) * 64, q + (one ? 0 : j * TILE_BYTES<D>), tile_of(2 * at(b)), half(b));
-          tc::mma_commit(s_full + j * 2 + (b & 1));
-        };
-        // after the scores of block b: the K tile, and at last Q
-        auto release_k = [&](int b) {
-          if (closes(b)) release(2 * at(b));
-          if (b + 1 == most) tc::mma_commit(q_empty);
-        };
-        auto values = [&](int b) {
-          if (b >= nb) return;
-          mma_values<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * at(b) + 1), half(b), b == 0);
-          tc::mma_commit(o_full + j);
-          if (b + 1 == nb) tc::mma_commit(o_done + j);
-        };
-        auto release_v = [&](int b) {
-          if (closes(b)) release(2 * at(b) + 1);
-        };
-        if (!(ok = wait(q_full, i))) break;
-        // block -2, -1: scores only (over P of the last item, whose products were issued before)
+        // the item's loop, once for one query tile and once for two: an instruction more between a
+        // block's P and its products is time in which the tensor pipe waits
+        auto products = [&](auto lone) {
+          constexpr bool one = decltype(lone)::value;
+          const int nb = t.blocks(a, j), most = one ? t.k1 - t.k0 : max(t.blocks(a, 0), t.blocks(a, 1)), tail = t.tail();
+          auto wait_full = [&](int x) { return wait(full + (ring + x) % SLOTS, (ring + x) / SLOTS); };
+          auto tile_of = [&](int x) { return kv + ((ring + x) % SLOTS) * TILE_BYTES<D>; };
+          // the K/V tile of the group's block b, and which 64 keys of it
+          auto at = [&](int b) { return one ? b : b >> 1; };
+          auto half = [&](int b) { return one ? j : b & 1; };
+          auto opens = [&](int b) { return one || !(b & 1); };
+          auto closes = [&](int b) { return one || (b & 1) || b + 1 == most; };
+          // both MMA warps give a K/V tile back, whether they used it or not
+          // (but not before it is there: its barrier is in an older phase)
+          auto release = [&](int x) { tc::mma_commit(empty + (ring + x) % SLOTS); };
+          auto scores = [&](int b) {
+            if (b >= nb) return;
+            mma_scores<D>(s_col + (b & 1) * 64, q + (one ? 0 : j * TILE_BYTES<D>), tile_of(2 * at(b)), half(b));
+            tc::mma_commit(s_full + j * 2 + (b & 1));
+          };
+          // after the scores of block b: the K tile, and at last Q
+          auto release_k = [&](int b) {
+            if (closes(b)) release(2 * at(b));
+            if (b + 1 == most) tc::mma_commit(q_empty);
+          };
+          auto values = [&](int b) {
+            if (b >= nb) return;
+            mma_values<D>(o_col, s_col + (b & 1) * 64, tile_of(2 * at(b) + 1), half(b), b == 0);
+            tc::mma_commit(o_full + j);
+            if (b + 1 == nb) tc::mma_commit(o_done + j);
+          };
+          auto release_v = [&](int b) {
+            if (closes(b)) release(2 * at(b) + 1);
+          };
+          if (!(ok = wait(q_full, i))) return;
+          // block -2, -1: scores only (over P of the last item, whose products were issued before)
 #pragma unroll 1
-        for (int b = -2; b < most; ++b) {
-          if (b >= 0 && opens(b)) {
-            const int v = 2 * at(b) + 1;
-            if (!(ok = wait_full(v))) break;
-            if (at(b) + 1 == t.k1 - t.k0 && tail < KT) {
-              const int slot = (ring + v) % SLOTS;
-              if (!(ok = wait(v_tail + slot, tails >> slot))) break;
-              tails ^= 1u << slot;
+          for (int b = -2; b < most; ++b) {
+            if (b >= 0 && opens(b)) {
+              const int v = 2 * at(b) + 1;
+              if (!(ok = wait_full(v))) break;
+              if (at(b) + 1 == t.k1 - t.k0 && tail < KT) {
+                const int slot = (ring + v) % SLOTS;
+                if (!(ok = wait(v_tail + slot, tails >> slot))) break;
+                tails ^= 1u << slot;
+              }
             }
-          }
-          // Two tiles: the next K tile is there by now, and is not waited for between P and
-          // its product.  One: it may be on its way still, and the V tile's slot does not wait for it.
-          const bool more = b + 2 < most;
-          if (more && (b < 0 || !one) && opens(b + 2) && !(ok = wait_full(2 * at(b + 2)))) break;
-          if (b >= 0 && b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
-          if (tc::elect_one()) {
-            if (b >= 0) values(b);
-            if (more && (b < 0 || !one)) scores(b + 2);
-            if (b >= 0) release_v(b);
-            if (more && (b < 0 || !one)) release_k(b + 2);
-          }
-          __syncwarp();
-          if (more && b >= 0 && one) {
-            if (!(ok = wait_full(2 * at(b + 2)))) break;
+            // Two tiles: the next K tile is there by now, and is not waited for between P and
+            // its product.  One: it may be on its way still, and the V tile's slot does not wait for it.
+            const bool more = b + 2 < most;
+            if (more && (b < 0 || !one) && opens(b + 2) && !(ok = wait_full(2 * at(b + 2)))) break;
+            if (b >= 0 && b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
             if (tc::elect_one()) {
-              scores(b + 2);
-              release_k(b + 2);
+              if (b >= 0) values(b);
+              if (more && (b < 0 || !one)) scores(b + 2);
+              if (b >= 0) release_v(b);
+              if (more && (b < 0 || !one)) release_k(b + 2);
             }
             __syncwarp();
+            if (more && b >= 0 && one) {
+              if (!(ok = wait_full(2 * at(b + 2)))) break;
+              if (tc::elect_one()) {
+                scores(b + 2);
+                release_k(b + 2);
+              }
+              __syncwarp();
+            }
           }
-        }
+        };
+        if (t.one(a)) products(std::true_type{});
+        else products(std::false_type{});
         if (!ok) break;
         ring += 2 * (t.k1 - t.k0);
       }
@@ -714,7 +721,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           // (a group none of whose keys the row reads has nothing there)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float u = own == 0.f ? 0.f : own * __uint_as_float(x[e]), v = other == 0.f ? 0.f : other * __uint_as_float(y[e]);
+            const float u = own == 0.f ? 0.f : own * __uint_as_float(x[e]);
+            const float v = other == 0.f ? 0.f : other * __uint_as_float(y[e]);
             x[e] = __float_as_uint(u + v);
           }
         } else {
@@ -948,7 +956,8 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
     return op_fail(GOCR_EINVAL, "bad shape: T=%d Hq=%d Hkv=%d", T, Hq, Hkv);
   if (!pitch_ok(ldq, Hq, d)) return op_fail(GOCR_EINVAL, "bad row pitch %lld", ldq);
   if (!(scale > 0.f) || scale > 1e30f) return op_fail(GOCR_EINVAL, "bad scale");
-  if (!cu_rows || (n_req && (!table || !kv_len)) || (T && (!q || !o || !lse)) || !workspace) return op_fail(GOCR_EINVAL, "null pointer");
+  if (!cu_rows || (n_req && (!table || !kv_len)) || (T && (!q || !o || !lse)) || !workspace)
+    return op_fail(GOCR_EINVAL, "null pointer");
   if (((uintptr_t)q | (uintptr_t)o | (uintptr_t)workspace) & 15) return op_fail(GOCR_EINVAL, "operand not 16-byte aligned");
   if (((uintptr_t)table | (uintptr_t)cu_rows | (uintptr_t)kv_len | (uintptr_t)lse) & 3)
     return op_fail(GOCR_EINVAL, "array not 4-byte aligned");
