@@ -350,42 +350,44 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == SW) {
       // K(0), V(0), K(1), V(1), ... through the ring, Q behind the item's K(0)
       int slot = 0, ph = 0, loads = 0, q_loads = 0;
-      const int box = min(1 << a.shift, KT);  // keys of a page that a tile holds
+      const int shift = min(a.shift, 7);  // log2 of the keys of a page that a tile holds
       for (int i = 0; next_item(work, work_full, work_free, i, w, ok); ++i) {
         const Item t(w);
         Pages pages(a, t);
-        const int n = t.k1 - t.k0;
 #pragma unroll 1
-        for (int x = 0; x < 2 * n; ++x) {
-          if (!(ok = wait_warp(empty + slot, ph ^ 1))) break;
-          const int key0 = (t.k0 + (x >> 1)) * KT, boxes = (min(t.q.kv - key0, KT) + box - 1) / box;
+        for (int x = t.k0; ok && x < t.k1; ++x) {
+          const int key0 = x * KT, boxes = (min(t.q.kv - key0, KT) + (1 << shift) - 1) >> shift;
           const int page = key0 >> a.shift, group = (key0 & ((1 << a.shift) - 1)) >> 3;
           pages.reach(a, t.head, page);
-          const int mine = x & 1 ? pages.v : pages.k;
-          uint8_t* dst = sm + F::OFF_KV + slot * TILE_BYTES<D>;
-          if (tc::elect_one()) tc::mbar_expect_tx(full + slot, boxes * box * D * 2);
-          __syncwarp();
-#pragma unroll 1
-          for (int b = 0; b < boxes; ++b) {
-            const int at = __shfl_sync(0xffffffffu, mine, (page - pages.at + b) & 31);
-            if (tc::elect_one()) tc::tma_load_5d(dst + b * box * D * 2, x & 1 ? &mv : &mk, 0, 0, 0, group, at, full + slot);
-            __syncwarp();
-          }
-          ++loads;
-          if (++slot == SLOTS) { slot = 0; ph ^= 1; }
-          if (x == 0) {
-            if (!(ok = wait_warp(q_empty, (i & 1) ^ 1))) break;
-            const int tiles = t.tokens(a, 1) ? 2 : 1;
-            if (tc::elect_one()) {
-              tc::mbar_expect_tx(q_full, tiles * a.toks * a.G * D * 2);
-              for (int j = 0; j < tiles; ++j)
+          // a lane has a page, and loads its keys (a loop over the pages in one lane, which first gets
+          // each page from the lane that has it, takes 5 % more of two chunks' call)
+          const int b = (lane - (page - pages.at)) & 31;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                  tc::tma_load_3d(sm + F::OFF_Q + j * TILE_BYTES<D> + c * BOX_BYTES, &mq, c * 64, t.head * a.G,
-                                  t.q.row0 + t.tok0 + j * a.toks, q_full);
-            }
+          for (int v = 0; v < 2; ++v) {
+            if (!(ok = wait_warp(empty + slot, ph ^ 1))) break;
+            if (tc::elect_one()) tc::mbar_expect_tx(full + slot, boxes << shift + (D == 128 ? 8 : 7));
             __syncwarp();
-            ++q_loads;
+            if (b < boxes)
+              tc::tma_load_5d(sm + F::OFF_KV + slot * TILE_BYTES<D> + (b << shift) * D * 2, v ? &mv : &mk, 0, 0, 0, group,
+                              v ? pages.v : pages.k, full + slot);
+            __syncwarp();
+            ++loads;
+            if (++slot == SLOTS) { slot = 0; ph ^= 1; }
+            if (x == t.k0 && v == 0) {
+              if (!(ok = wait_warp(q_empty, (i & 1) ^ 1))) break;
+              const int tiles = t.tokens(a, 1) ? 2 : 1;
+              if (tc::elect_one()) {
+                tc::mbar_expect_tx(q_full, tiles * a.toks * a.G * D * 2);
+#pragma unroll 1
+                for (int j = 0; j < tiles; ++j)
+#pragma unroll
+                  for (int c = 0; c < D / 64; ++c)
+                    tc::tma_load_3d(sm + F::OFF_Q + j * TILE_BYTES<D> + c * BOX_BYTES, &mq, c * 64, t.head * a.G,
+                                    t.q.row0 + t.tok0 + j * a.toks, q_full);
+              }
+              __syncwarp();
+              ++q_loads;
+            }
           }
         }
         if (!ok) break;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t s_col = tmem + j * 128, o_col = tmem + F::O_COL + j * D;
       int ring = 0;           // ring position of the item's K(0)
       unsigned tails = 0;     // parity of each slot's ragged tiles so far
-      int turn[2] = {0, 0};   // blocks of each buffer so far
+      unsigned turns = 0;     // parity of each buffer's blocks so far
       auto wait = [&](uint64_t* bar, int ph) {
         const bool r = wait_warp(bar, ph & 1);
         tc::fence_after_sync();
@@ -461,7 +463,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             // its product.  One: it may be on its way still, and the V tile's slot does not wait for it.
             const bool more = b + 2 < most;
             if (more && (b < 0 || !one) && opens(b + 2) && !(ok = wait_full(2 * at(b + 2)))) break;
-            if (b >= 0 && b < nb && !(ok = wait(p_full + j * 2 + (b & 1), turn[b & 1]++))) break;
+            if (b >= 0 && b < nb) {
+              if (!(ok = wait(p_full + j * 2 + (b & 1), turns >> (b & 1)))) break;
+              turns ^= 1u << (b & 1);
+            }
             if (tc::elect_one()) {
               if (b >= 0) values(b);
               if (more && (b < 0 || !one)) scores(b + 2);
@@ -589,7 +594,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t to = tmem + F::O_COL + j * D + lanes;
     const float sl2 = a.scale * LOG2E;
     const int tok_of = r / a.G, head_of = r % a.G;
-    int turn[2] = {0, 0}, outs = 0, done = 0, meets = 0;  // blocks of each buffer, of the group, items and meetings so far
+    unsigned turns = 0;  // parity of each buffer's blocks so far
+    int outs = 0, done = 0, meets = 0;  // the group's blocks, items and meetings so far
     auto meet = [&] {  // with the other group's warp of these rows
       tc::fence_before_sync();
       __syncwarp();
@@ -613,7 +619,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
       for (int b = 0; b < nb; ++b, ++outs) {
         const uint32_t ts = tmem + j * 128 + (b & 1) * 64 + lanes;
-        if (!(ok = wait_warp(s_full + j * 2 + (b & 1), (b & 1 ? turn[1]++ : turn[0]++) & 1))) break;
+        if (!(ok = wait_warp(s_full + j * 2 + (b & 1), turns >> (b & 1) & 1))) break;
+        turns ^= 1u << (b & 1);
         tc::fence_after_sync();
         if (any) {
           uint32_t u[64];
