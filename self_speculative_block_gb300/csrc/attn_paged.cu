@@ -515,10 +515,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       Req q{0, 0, 0};
       Split split{};
       if (left > 0) {
-        q = Req{start_of[0], start_of[1], start_of[2]};
+        // (row ranges that overlap may be more work than 32 bits count: whatever the sums
+        // say then, rows and heads stay within the arrays)
+        q = Req{start_of[0], min(start_of[1], a.T - start_of[0]), start_of[2]};
         at = start_at;
         if (q.n <= 2 * a.toks) {
-          const unsigned one = work_of(a, q, 0);
+          const unsigned one = max(work_of(a, q, 0), 1u);
           h = at / one;
           at -= h * one;
         } else {
@@ -544,6 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             i += (found ? l : 32) * 2 * a.toks;
           }
         }
+        if ((unsigned)h >= (unsigned)a.Hkv) left = 0;
       }
       auto advance = [&] {  // to the next unit
         at = 0;
