@@ -689,6 +689,72 @@ def test_attention_paged_most_requests(g):
     assert ((lse.T.double() - torch.logsumexp(S, -1)).abs() <= 2.0 ** -16).all()
 
 
+def test_page_step_most_rows(g):
+    """2^24 rows of 4,096 requests, and the same with a row too few."""
+    R, n, ps, width = 4096, 4096, 256, 17
+    n_pages = R * (n // ps)
+    order = torch.randperm(n_pages, generator=torch.Generator(device="cuda").manual_seed(18), device="cuda").to(torch.int32)
+    for T in (1 << 24, (1 << 24) - 1):
+        table = torch.full((R, width), -1, dtype=torch.int32, device="cuda")
+        zero = torch.zeros((R,), dtype=torch.int32, device="cuda")
+        s = g.op_page_step(zero, zero, zero + n, table, order.clone(), i32([n_pages]), ps, T)
+        ok = R if T == 1 << 24 else R - 1  # requests whose rows fit
+        want = order.flip(0)[:ok * (n // ps)].view(ok, n // ps)
+        assert torch.equal(table[:ok, :n // ps], want) and (table[ok:] == -1).all() and int(s.n_free) == n_pages - want.numel()
+        rows = ok * n
+        pos = torch.arange(n, dtype=torch.int32, device="cuda")
+        assert torch.equal(s.pos[:rows].view(ok, n), pos.expand(ok, n)) and (s.pos[rows:] == -1).all()
+        assert torch.equal(s.slots[:rows].view(ok, n), want.repeat_interleave(ps, 1) * ps + pos % ps) and (s.slots[rows:] == -1).all()
+        assert torch.equal(s.kv_len, torch.where(torch.arange(R, device="cuda") < ok, n, 0).to(torch.int32))
+
+
+def test_attention_paged_most_keys(g):
+    """One token over 2^24 keys: the longest table, a request on all of the device."""
+    n, ps, d = 1 << 24, 256, 64
+    r = torch.Generator(device="cuda").manual_seed(19)
+    kc, vc = (torch.randn((n // ps, 1, ps, d), generator=r, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.randperm(n // ps, generator=r, device="cuda").to(torch.int32)[None]
+    q = torch.randn((1, 2, d), generator=r, device="cuda").bfloat16()
+    o, lse = g.op_attention_paged(q, kc, vc, table, i32([0, 1]), i32([n]))
+    S = torch.cat([torch.einsum("hd,nd->hn", q[0].double(), kc[p:p + 4096, 0].reshape(-1, d).double()) * d ** -0.5
+                   for p in range(0, n // ps, 4096)], 1)  # (the order of the keys does not matter)
+    ref = torch.logsumexp(S, 1)
+    P = torch.exp(S - ref[:, None])
+    V = [vc[p:p + 4096, 0].reshape(-1, d).double() for p in range(0, n // ps, 4096)]
+    parts = P.split(4096 * ps, 1)
+    O, bound = sum(p @ v for p, v in zip(parts, V)), sum(p @ v.abs() for p, v in zip(parts, V))
+    # a piece's keys are summed 16 at a time in each of two chains, the pieces one after the other; exponentials to 2^-17
+    deep = (n / 152 / 32 + 152 + 64) * TC + 2.0 ** -17
+    assert ((o[0].double() - O).abs() <= (U + deep) * bound + U * O.abs()).all()
+    assert ((lse[:, 0].double() - ref).abs() <= deep + 4 * F32 * ref.abs()).all()
+
+
+def test_paged_most_rows(g):
+    """2^20 rows of 4,096 whole prompts of 256: written and attended."""
+    R, n, Hq, Hkv, d, ps = 4096, 256, 2, 1, 64, 64
+    T = R * n
+    r = torch.Generator(device="cuda").manual_seed(20)
+    qkv = torch.randn((T, Hq + 2 * Hkv, d), generator=r, device="cuda", dtype=torch.bfloat16)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    kc, vc = (torch.zeros((T // ps, Hkv, ps, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).view(R, n).flip(1).reshape(-1).contiguous()
+    table = (slots.view(R, n // ps, ps)[:, :, 0] // ps).contiguous()
+    rot = g.op_kv_write_paged(q, k, v, (torch.arange(T, device="cuda") % n).to(torch.int32), slots, kc, vc)
+    cu = (torch.arange(R + 1, device="cuda") * n).to(torch.int32)
+    o, lse = g.op_attention_paged(rot, kc, vc, table, cu, i32([n] * R))
+    seen = torch.tril(torch.ones((n, n), dtype=torch.bool, device="cuda"))
+    for a in range(0, R, 512):
+        K, V = (c[table[a:a + 512].long()].reshape(512, n, d).double() for c in (kc, vc))
+        Q = rot[a * n:(a + 512) * n].view(512, n, Hq, d).double()
+        for h in range(Hq):
+            S = (Q[:, :, h] @ K.transpose(1, 2) * d ** -0.5).masked_fill(~seen, -math.inf)
+            P = torch.softmax(S, -1)
+            O = P @ V
+            tol = (U + 2.0 ** -16) * (P @ V.abs()) + U * O.abs()
+            assert ((o[a * n:(a + 512) * n, h].view(512, n, d).double() - O).abs() <= tol).all()
+            assert ((lse[h, a * n:(a + 512) * n].view(512, n).double() - torch.logsumexp(S, -1)).abs() <= 2.0 ** -16).all()
+
+
 def test_attention_paged_graphs_that_share_a_workspace(g):
     """Two captured calls of different shapes with one workspace, replayed in turn."""
     cs = [_case([33] * 4, [700, 1500, 90, 4000], 12, 4, 128, 16, "head", seed=22), _case([1] * 9, [2000] * 9, 12, 4, 128, 16, "token", seed=23)]
