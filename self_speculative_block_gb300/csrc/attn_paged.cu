@@ -21,7 +21,7 @@
 // What bounds it (12 q and 4 kv heads of 128, pages of 16, times on the device):
 //   few rows: HBM.  256 single tokens of 1,000 to 4,000 keys 181 us (6.1 TB/s, 90 % of a
 //     copy's rate), 64 of 256 to 8,192 51 (4.8 TB/s: 7 us before the first keys are there, 4 for
-//     the join), a window of 33 behind 131,105 keys 56, one token over 1,097 keys 11;
+//     the join), a window of 33 behind 131,105 keys 56, one token over 1,097 keys 12;
 //   many rows: the tensor pipe.  A prompt of 16,384 rows 527 us (1.56 PFLOP/s, 81 % of
 //     the library's product), two last chunks of 2,048 rows over 8,192 keys 133 (1.35);
 //     128 keys of two query tiles pass in 3,000 cycles, 2,590 of them products;
@@ -67,6 +67,7 @@ struct PagedArgs {
   float4* part;   // [2 GRID][D / 4][rows]
   float2* stat;   // [2 GRID][rows]: reference (times scale log2 e) and sum of the exponentials
   Split* split;   // [GRID], n = 0: none
+  int* tasks;     // [GRID], of their joins
   int max_pages, n_pages, n_req, T, Hq, Hkv, G, toks, draft, shift, rows;
   int k_page, k_head, k_units, v_page, v_head, v_units;  // page and head strides of the maps' last dimension, and its size
   float scale;
@@ -139,6 +140,17 @@ __device__ __forceinline__ unsigned work_of(const PagedArgs& a, const Req& q, in
 // The key tiles of a unit that lie before its work x.
 __device__ __forceinline__ int tile_at(unsigned x, bool two) {
   return two ? (max(x, 10u) - 6) / 5 : (max(x, 2u) + 1) / 4;
+}
+
+// The join of a unit: its parts (pieces that may hold a tile of it), the warps that
+// share a task's parts (each takes two or more), and its tasks of JOIN_WARPS warps.
+constexpr int JOIN_CTAS = 4 * SM_COUNT, JOIN_WARPS = 8;
+__device__ __forceinline__ int parts_of(const Split& s) { return 2 + (int)((s.work - s.after - 1) / s.piece); }
+__device__ __forceinline__ int share_of(int parts) { return parts >= 16 ? 8 : parts >= 8 ? 4 : parts >= 4 ? 2 : 1; }
+__device__ __forceinline__ int rows_of(const PagedArgs& a, const Split& s) { return min(s.n - s.tok0, 2 * a.toks) * a.G; }
+template <int D> __device__ __forceinline__ int tasks_of(const PagedArgs& a, const Split& s) {
+  const int each = 32 * JOIN_WARPS / share_of(parts_of(s));
+  return s.n ? (rows_of(a, s) * (D / 8) + each - 1) / each : 0;
 }
 
 // One work item, as every warp sees it.
@@ -605,7 +617,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         tail_at = ring - 1;
         advance();
       }
-      if (lane == 0) a.split[blockIdx.x] = split;
+      if (lane == 0) {
+        a.split[blockIdx.x] = split;
+        a.tasks[blockIdx.x] = split.n ? tasks_of<D>(a, split) : 0;
+      }
     }
   } else {
     const int j = warp >> 2, r = (warp & 3) * 32 + lane;  // group, row of its tile
@@ -797,28 +812,27 @@ __global__ void __launch_bounds__(THREADS, 1)
 // chain of loads (one token 11.4 us with 4, 12.0 with 2), and 2 for long ones, whose
 // parts want the loads of four CTAs an SM (two chunks of 2,048 rows 143 us with 2,
 // 147 with 4).
-constexpr int JOIN_CTAS = 4 * SM_COUNT, JOIN_WARPS = 8;
-
 template <int D, int BATCH>
 __global__ void __launch_bounds__(JOIN_WARPS * 32, 8 / BATCH) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ int ends[256 + 1];  // tasks of the units before
-  __shared__ Split splits[GRID];
   __shared__ float sums[JOIN_WARPS][10][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto parts_of = [&](const Split& s) { return 2 + (int)((s.work - s.after - 1) / s.piece); };
-  // warps that share a task's parts: each takes two or more
-  auto share_of = [&](int parts) { return parts >= 16 ? 8 : parts >= 8 ? 4 : parts >= 4 ? 2 : 1; };
-  auto rows_of = [&](const Split& s) { return min(s.n - s.tok0, 2 * a.toks) * a.G; };
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   static_assert(GRID <= 256, "a thread takes a split");
+  // Long calls read the counts first and a task's split later: 608 CTAs that read all
+  // splits wait for one another's cache lines (16 draft windows 20.8 -> 19.7 us); short
+  // ones would wait for one load more (one token 11.8 -> 12.1).
+  constexpr bool AHEAD = BATCH == 4;
+  __shared__ Split splits[AHEAD ? GRID : 1];
   int count = 0;
   if (tid < GRID) {
-    const Split s = a.split[tid];
-    if (s.n) {
+    if constexpr (AHEAD) {
+      const Split s = a.split[tid];
       splits[tid] = s;
-      const int each = 32 * JOIN_WARPS / share_of(parts_of(s));
-      count = (rows_of(s) * (D / 8) + each - 1) / each;
+      if (s.n) count = tasks_of<D>(a, s);
+    } else {
+      count = a.tasks[tid];
     }
   }
   __shared__ int warp_sums[JOIN_WARPS];
@@ -839,8 +853,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 8 / BATCH) attn_paged_join_ke
 #pragma unroll 1
     for (int step = 128; step; step >>= 1)
       if (c + step < GRID && ends[c + step] <= task) c += step;
-    const Split& s = splits[c];
-    const int n = parts_of(s), share = share_of(n), g = warp % share, rows = rows_of(s);
+    const Split s = AHEAD ? splits[AHEAD ? c : 0] : a.split[c];
+    const int n = parts_of(s), share = share_of(n), g = warp % share, rows = rows_of(a, s);
     const int id = (task - ends[c]) * (32 * JOIN_WARPS / share) + warp / share * 32 + lane, row = id % rows, c8 = id / rows;
     const Req q{s.row0, s.n, s.kv};
     const int tok = s.tok0 + row / a.G;
@@ -966,7 +980,7 @@ cudaError_t attn_paged_gave_up(unsigned* out, cudaStream_t s) {
 extern "C" size_t gocr_op_attention_paged_workspace(int T, int Hq, int Hkv, int d) {
   if (T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 64 || d < 1) return 0;
   const int rows = part_rows(T, Hq / Hkv);
-  return part_bytes(rows, d) + stat_bytes(rows) + GRID * sizeof(Split);
+  return part_bytes(rows, d) + stat_bytes(rows) + GRID * (sizeof(Split) + sizeof(int));
 }
 
 extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache, const int32_t* table, int max_pages,
@@ -1006,7 +1020,8 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
   while ((1 << shift) < kv.page_size) ++shift;
   uint8_t* ws = (uint8_t*)workspace;
   const PagedArgs a{table, cu_rows, kv_len, (bf16*)o, lse, (float4*)ws, (float2*)(ws + part_bytes(rows, d)),
-                    (Split*)(ws + part_bytes(rows, d) + stat_bytes(rows)), max_pages, kv.n_pages, n_req, T, Hq, Hkv, G,
+                    (Split*)(ws + part_bytes(rows, d) + stat_bytes(rows)),
+                    (int*)(ws + part_bytes(rows, d) + stat_bytes(rows) + GRID * sizeof(Split)), max_pages, kv.n_pages, n_req, T, Hq, Hkv, G,
                     128 / G, kind == GOCR_FWD_DRAFT, shift, rows, (int)km.page, (int)km.head, (int)km.units, (int)vm.page,
                     (int)vm.head, (int)vm.units, scale};
   return d == 128 ? attend<128>(m, a, s) : attend<64>(m, a, s);
