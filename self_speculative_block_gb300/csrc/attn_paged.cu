@@ -29,9 +29,9 @@
 //     1,000 tokens of 16 to 400 keys 85 us.
 // The roles' code has to stay in the instruction cache: with waits of twenty sites
 // unrolled, rescaling unrolled and eight boxes a load unrolled (192 KB in all instead
-// of 55) two chunks' call took 207 us.  A piece's end in fp32 costs 0.5 KB a row: the
-// join of the two chunks' 302 parts is 15 us of 133.  No smaller pieces: cuts at unit
-// boundaries only would leave a third of the SMs idle with 200 units.
+// of 55) two chunks' call took 207 us.  A part costs 0.5 KB a row, written and read: the
+// join of the two chunks' 302 parts is 15 us of 133, where cuts at unit boundaries only
+// would leave two thirds of the SMs idle in the second round of their 200 units.
 #include "attn_packed.cuh"
 #include "paged.cuh"
 
