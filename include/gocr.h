@@ -554,7 +554,7 @@ int gocr_op_kv_write_paged(const void* q, const void* k, const void* v, const in
  * table entries outside 0..n_pages-1 read as pages of zeros.  Hq / Hkv <= 64, Hq <=
  * 1024, d 64 or 128, T <= 2^24, T Hq <= 2^31 - 1, pitch and scale as in
  * gocr_op_attention_packed; (T / (2 floor(128 Hkv / Hq)) + n_req) Hkv
- * (max_pages page_size / 128 + 3) <= 2^29; page and head strides of a cache such
+ * (max_pages page_size / 128 + 5) <= 2^29; page and head strides of a cache such
  * that its extent has fewer than 2^31 of their greatest common divisor.
  * Scores, softmax statistics, sums and the parts of a split key axis are in
  * fp32; exp(scale q k^T - m), with m within 2^8 of the maximum so far, is

@@ -22,7 +22,7 @@
 //   few rows: HBM.  256 single tokens of 1,000 to 4,000 keys 181 us (6.1 TB/s, 90 % of a
 //     copy's rate), 64 of 256 to 8,192 51 (4.8 TB/s: 7 us before the first keys are there, 4 for
 //     the join), a window of 33 behind 131,105 keys 56, one token over 1,097 keys 12;
-//   many rows: the tensor pipe.  A prompt of 16,384 rows 527 us (1.56 PFLOP/s, 81 % of
+//   many rows: the tensor pipe.  A prompt of 16,384 rows 511 us (1.61 PFLOP/s, 83 % of
 //     the library's product), two last chunks of 2,048 rows over 8,192 keys 133 (1.35);
 //     128 keys of two query tiles pass in 3,000 cycles, 2,590 of them products;
 //   short requests: the chain of an item (Q, scores, softmax, P V, store), 3 us each:
@@ -124,10 +124,10 @@ __device__ __forceinline__ Req request(const PagedArgs& a, int r) {
 __device__ __forceinline__ int last_key(const PagedArgs& a, const Req& q, int i) {
   return a.draft && i > 0 ? q.kv - 1 : q.kv - q.n + i;
 }
-// Work of a unit, the two query tiles from token i on: 5 a key tile and 10 for its
-// beginning and end where both hold tokens (3,070 and 6,500 cycles measured); 4 and 2
-// where one does, whose keys' way from HBM hides most of the ends (2,480 cycles a tile;
-// 64 single tokens take 54.3 us with 2, 57.5 with 10).
+// Work of a unit, the two query tiles from token i on: 5 a key tile (3,000 cycles) and 16
+// for its beginning and end where both hold tokens (a prompt of 8,192 rows takes 159 us
+// with 10 for the ends, 154 with 16); 4 and 2 where one does, whose keys' way from HBM hides
+// most of the ends (2,480 cycles a tile; 64 single tokens take 54.3 us with 2, 57.5 with 10).
 __device__ __forceinline__ bool two_tiles(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks; }
 __device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int i) {
   const int last = i < q.n ? last_key(a, q, min(i + 2 * a.toks, q.n) - 1) : -1;
@@ -135,11 +135,11 @@ __device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int i
 }
 __device__ __forceinline__ unsigned work_of(const PagedArgs& a, const Req& q, int i) {
   const unsigned n = key_tiles(a, q, i);
-  return n ? (two_tiles(a, q, i) ? 10 + 5 * n : 2 + 4 * n) : 0;
+  return n ? (two_tiles(a, q, i) ? 16 + 5 * n : 2 + 4 * n) : 0;
 }
 // The key tiles of a unit that lie before its work x.
 __device__ __forceinline__ int tile_at(unsigned x, bool two) {
-  return two ? (max(x, 10u) - 6) / 5 : (max(x, 2u) + 1) / 4;
+  return two ? (max(x, 16u) - 12) / 5 : (max(x, 2u) + 1) / 4;
 }
 
 // The join of a unit: its parts (pieces that may hold a tile of it), the warps that
@@ -1003,9 +1003,9 @@ extern "C" int gocr_op_attention_paged(const void* q, const gocr_paged_kv* cache
     return op_fail(GOCR_EINVAL, "array not 4-byte aligned");
   if (workspace_bytes < gocr_op_attention_paged_workspace(T, Hq, Hkv, d)) return op_fail(GOCR_ECAPACITY, "workspace too small");
   const int G = Hq / Hkv, rows = part_rows(T, G);
-  // the work of a call, at most 5 a key tile and 10 for each unit, is counted in 32 bits
+  // the work of a call, at most 5 a key tile and 16 for each unit, is counted in 32 bits
   const long long units = (T / (2 * (128 / G)) + (long long)(T < n_req ? T : n_req)) * Hkv;
-  if (units * (((long long)max_pages * kv.page_size - 1) / KT + 3) > 1 << 29)
+  if (units * (((long long)max_pages * kv.page_size - 1) / KT + 5) > 1 << 29)
     return op_fail(GOCR_EINVAL, "bad shape: T=%d rows of %d requests over %d pages of %d", T, n_req, max_pages, kv.page_size);
   const PageMap km(kv.k, &kv.k_page, kv), vm(kv.v, &kv.v_page, kv);
   if (km.units > 0x7fffffff || vm.units > 0x7fffffff)
