@@ -20,7 +20,7 @@ using namespace gocr::paged;
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MOST = 1 << 30;  // sums end here: above every count that can be served, and 2 * MOST fits an int
+constexpr int MOST = (1 << 30) - 1;  // sums end here: above every count that can be served, and 2 * MOST fits an int
 
 struct StepArgs {
   const int *held, *start, *end, *n_free;
