@@ -20,6 +20,7 @@ using namespace gocr::paged;
 namespace {
 
 constexpr int THREADS = 256;
+constexpr size_t STATIC_SMEM = THREADS / 32 * sizeof(int);  // the scans' sums of warps
 constexpr int MOST = (1 << 30) - 1;  // sums end here: above every count that can be served, and 2 * MOST fits an int
 
 struct StepArgs {
@@ -176,7 +177,8 @@ extern "C" int gocr_op_page_step(const int32_t* held, const int32_t* start, cons
   const long long work = T > 16 * n_req ? T : 16ll * n_req;
   const int grid = (int)((work + THREADS - 1) / THREADS < 2 * SM_COUNT ? (work + THREADS - 1) / THREADS : 2 * SM_COUNT);
   const size_t smem = 3 * (size_t)(n_req + 1) * sizeof(int);
-  if (smem > 48 * 1024 && !kernel_smem_at_least(reinterpret_cast<const void*>(&page_step_kernel), smem))
+  // (the default limit of 48 KB counts the kernel's own 32 bytes, too)
+  if (smem + STATIC_SMEM > 48 * 1024 && !kernel_smem_at_least(reinterpret_cast<const void*>(&page_step_kernel), smem))
     return op_fail(GOCR_ECUDA, "kernel configuration rejected");
   launch_k(page_step_kernel, dim3(grid > 0 ? grid : 1), dim3(THREADS), smem, s, true, a);
   return op_launched("page_step");

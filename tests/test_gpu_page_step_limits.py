@@ -1,4 +1,8 @@
 """The page step where its counts and its shared memory are largest."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +43,29 @@ def test_page_step_more_rows_than_32_bits_count(g, R):
     pos = torch.arange(n, dtype=torch.int32, device="cuda")
     assert torch.equal(s.pos.view(2, n), pos.expand(2, n))
     assert torch.equal(s.slots.view(2, n), pages.repeat_interleave(ps, 1) * ps + pos % ps)
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+# a page each, the last request none: whatever shared memory the sizes before have asked for stays set
+EVERY_REQUEST = """
+import torch
+from self_speculative_block_gb300 import gocr as g
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+for R in (4090, 4091, 4092, 4093, 4094, 4095, 4096):
+    table = torch.full((R, 2), -1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros((R,), dtype=torch.int32, device="cuda")
+    free = torch.arange(R - 1, dtype=torch.int32, device="cuda")
+    s = g.op_page_step(zero, zero, zero + 3, table, free, i32([R - 1]), 16, 3 * R)
+    page = torch.arange(R - 1, device="cuda", dtype=torch.int32).flip(0)
+    assert torch.equal(table[:-1, 0], page) and int(table[-1, 0]) == -1 and (table[:, 1] == -1).all(), R
+    assert int(s.n_free) == 0 and (s.kv_len[:-1] == 3).all() and int(s.kv_len[-1]) == 0, R
+    assert torch.equal(s.slots[:-3].view(R - 1, 3), page[:, None] * 16 + i32([0, 1, 2])) and (s.slots[-3:] == -1).all(), R
+print("served")
+"""
+
+
+def test_page_step_most_requests_in_a_new_process(g):
+    """4,090 to 4,096 requests, the fewest first, where no larger call has raised the kernel's limit before."""
+    r = subprocess.run([sys.executable, "-c", EVERY_REQUEST], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.strip() == "served", r.stdout + r.stderr
