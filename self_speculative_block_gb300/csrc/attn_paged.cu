@@ -354,17 +354,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     start_of[2] = q0.kv;
     start_at = x0 - before;
   }
-  if (without) {  // rows without keys, in requests with more rows than keys
+  if (without) {
+    // Rows without keys, in requests with more rows than keys: a warp finds the requests among its
+    // own and writes a share of each one's rows, so that all CTAs' warps write a request together.
+    // (A refused prompt of 16,384 rows beside 64 tokens: 85 us, 56 without it; with its rows in one CTA 2,770.)
 #pragma unroll 1
-    for (int r = blockIdx.x; r < a.n_req; r += GRID) {
-      const Req q = request(a, r);
-      const int n = q.kv == 0 ? q.n : a.draft ? min(1, q.n - q.kv) : q.n - q.kv;
+    for (int at = warp * 32; at < a.n_req; at += THREADS) {
+      const Req q = at + lane < a.n_req ? request(a, at + lane) : Req{0, 0, 0};
+      const int none = q.kv == 0 ? q.n : a.draft ? min(1, q.n - q.kv) : q.n - q.kv;
 #pragma unroll 1
-      for (int i = tid; i < n * a.Hq; i += THREADS) {
-        const int t = q.row0 + i / a.Hq, h = i % a.Hq;
-        a.lse[(size_t)h * a.T + t] = -INFINITY;
+      for (unsigned some = __ballot_sync(0xffffffffu, none > 0); some; some &= some - 1) {
+        const int l = __ffs(some) - 1, row0 = __shfl_sync(0xffffffffu, q.row0, l), n = __shfl_sync(0xffffffffu, none, l);
+        const unsigned first = (blockIdx.x + at + l) % GRID * 32 + lane, rows = (unsigned)n * a.Hq;
+        uint4* o = reinterpret_cast<uint4*>(a.o + (size_t)row0 * a.Hq * D);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(a.o + ((size_t)t * a.Hq + h) * D + c) = make_uint4(0, 0, 0, 0);
+        for (size_t i = first; i < (size_t)rows * (D / 8); i += GRID * 32) o[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (unsigned i = first; i < rows; i += GRID * 32) a.lse[(size_t)(i / n) * a.T + row0 + i % n] = -INFINITY;
       }
     }
   }
