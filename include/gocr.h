@@ -502,8 +502,10 @@ typedef struct gocr_paged_kv {
  * requests in their order: from the first one on whose need, with the needs of
  * those before it, is more than there is, requests that need pages are refused.
  * Refused too are a request whose lengths do not satisfy 0 <= start <= held, start
- * <= end and held, end <= max_pages * page_size (it has no rows), and one
- * whose rows end behind row T.
+ * <= end and held, end <= max_pages * page_size (it has no rows), and, from the
+ * first one on whose rows end behind row T, all requests, those without rows
+ * among them: an end or a rollback behind it gives nothing back, and is asked for
+ * again with held_out as held.
  *
  * Outputs: table (in place: entries of pages taken; the others, those of pages
  * given back among them, stay as they were), free_pages (in place, entries at

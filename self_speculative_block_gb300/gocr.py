@@ -734,7 +734,9 @@ def op_page_step(held, start, end, table, free_pages, n_free, page_size: int, ro
     stack free_pages [n_pages] (n_free [1] of them free) or those behind given
     back to it.  table [n_req, max_pages] and free_pages are updated in place;
     rows is the number of rows that the forward is laid out for.  A request
-    whose pages or rows do not fit is refused: it keeps what it holds."""
+    whose pages do not fit is refused, and from the first one on whose rows do not
+    fit all are, ends and rollbacks among them: a refused request keeps what it
+    holds, as the returned held says."""
     torch = _torch()
     _lead("table", table, 2, torch.int32)
     dev, (R, width), n_pages = table.device, table.shape, free_pages.numel()

@@ -45,6 +45,25 @@ def test_page_step_more_rows_than_32_bits_count(g, R):
     assert torch.equal(s.slots.view(2, n), pages.repeat_interleave(ps, 1) * ps + pos % ps)
 
 
+def test_page_step_ends_behind_rows_that_do_not_fit(g):
+    """From the first request on whose rows end behind the last row, none gives anything back or takes anything; asked
+    again with what the step says they hold, they do."""
+    ps, order = 16, list(range(12))
+    table, free = torch.full((4, 4), -1, dtype=torch.int32, device="cuda"), i32(order)
+    s = g.op_page_step(i32([0] * 4), i32([0] * 4), i32([16, 32, 40, 33]), table, free, i32([12]), ps, 121)
+    assert int(s.n_free) == 3 and s.held.tolist() == [16, 32, 40, 33]
+    before = table.tolist()
+    # the first grows within the rows, the second does not fit, the third ends, the fourth is rolled back
+    s = g.op_page_step(s.held, i32([16, 32, 0, 10]), i32([18, 35, 0, 10]), table, free, s.n_free, ps, 4)
+    assert s.held.tolist() == [18, 32, 40, 33] and s.kv_len.tolist() == [18, 0, 0, 0] and int(s.n_free) == 2
+    assert s.cu_rows.tolist() == [0, 2, 4, 4, 4] and s.pos.tolist() == [16, 17, -1, -1]
+    before[0][1] = 2
+    assert table.tolist() == before
+    s = g.op_page_step(s.held, i32([18, 32, 0, 10]), i32([18, 32, 0, 10]), table, free, s.n_free, ps, 4)
+    assert s.held.tolist() == [18, 32, 0, 10] and int(s.n_free) == 2 + 3 + 2
+    assert free[:7].tolist() == [0, 1, before[3][2], before[3][1], before[2][2], before[2][1], before[2][0]]
+
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 # a page each, the last request none: whatever shared memory the sizes before have asked for stays set
