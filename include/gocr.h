@@ -528,7 +528,7 @@ int gocr_op_page_step(const int32_t* held, const int32_t* start, const int32_t* 
  *   (y[i], y[i+d/2]) = (c u[i] - s u[i+d/2], c u[i+d/2] + s u[i]),
  * c and s the cosine and sine of x theta^(-2i/d), for each head of q (into
  * q_out[T, Hq, d], dense) and of k (into the cache at slots[t]); v is copied.
- * The angle is exact to 2^-26 turns up to position 2^24, values are rounded once
+ * The angle is exact to 2^-25 turns up to position 2^24, values are rounded once
  * to bf16.  q, k and v bf16 with rows ldq, ldk and ldv elements apart, as in
  * gocr_op_attention_packed; pos and slots int32[T] (device).  A row whose slot
  * is outside 0..n_pages*page_size-1 is skipped: whatever it holds, nothing is
@@ -561,8 +561,10 @@ int gocr_op_kv_write_paged(const void* q, const void* k, const void* v, const in
  * Scores, softmax statistics, sums and the parts of a split key axis are in
  * fp32; exp(scale q k^T - m), with m within 2^8 of the maximum so far, is
  * rounded to bf16 for the product with v.  The keys of all requests are cut into
- * equal pieces, so a row's last bits depend on the other requests of the call (the
- * same call gives the same bits).  The workspace takes up to 304 (2 floor(128
+ * equal pieces, so a row's last bits depend on the lengths of all requests of the
+ * call (on nothing that the others hold; the same call gives the same bits): the row of
+ * a verify window need not equal that of a single token bit for bit, as the rows of
+ * the decoder's own forwards do.  The workspace takes up to 304 (2 floor(128
  * Hkv / Hq) Hq / Hkv) (4 d + 8) bytes, 40 MB with heads of 128, and less for
  * fewer rows. */
 size_t gocr_op_attention_paged_workspace(int T, int Hq, int Hkv, int d);

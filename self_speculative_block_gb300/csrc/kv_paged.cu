@@ -7,13 +7,15 @@
 // way: a thread takes 8 + 8 elements of a head (both halves of the rotation), 16 bytes a
 // load, two such pieces at a time.  The angle in turns is x f_i mod 1 with f_i =
 // theta^(-2i/d) / 2 pi as a 64-bit fraction: one integer product whose overflow
-// drops the whole turns, exact to x 2^-52 or so (f_i comes from doubles), where
-// fp32 would lose 2^-24 of the whole angle.
+// drops the whole turns, where fp32 would lose 2^-24 of the whole angle.  f_i comes from
+// doubles, to 2^-50 of its value and so to x 2^-52.6 turns; the top 32 bits of the product
+// lose 2^-32 and their conversion to fp32 2^-26 more: 2^-25.7 turns up to position 2^24.
 //
-// Bound by HBM: 13,655 rows of 12 + 2 x 4 heads of 128 (140 MB) 28.5 us, 4.9 TB/s
-// (torch's copy of 70 MB takes 47); without the angles the same.  Two
+// Bound by HBM: 13,655 rows of 12 + 2 x 4 heads of 128 (140 MB) 28.7 us, 4.9 TB/s
+// (torch's copy of 70 MB takes 47), of heads of 64 11.5; without the angles the same.  Two
 // pieces a batch and 256 threads: four pieces 30.5, 128 or 512 threads 28.4 to 31,
-// streaming loads and stores 28.3; a row a CTA 36.  528 rows take 3.5 us, 64 2.1.
+// streaming loads and stores 28.3; a row a CTA 36.  528 rows take 3.5 us (heads of
+// 64: 2.5), 64 2.1.
 #include "paged.cuh"
 #include "tc.cuh"
 

@@ -819,7 +819,12 @@ def op_attention_paged(q, k_cache, v_cache, table, cu_rows, kv_len, kind: int = 
     request's n is at position kv_len - n + i and reads the keys up to it;
     kind=FWD_DRAFT: the rows behind the first read all kv_len keys.  Returns (o
     [T, Hq, d] bf16, lse [Hq, T] fp32), written into o and lse when given; a row
-    without keys gets 0 and -inf, rows of no request are not written."""
+    without keys gets 0 and -inf, rows of no request are not written.  The last
+    bits of a row depend on the lengths of all requests of the call, so a verify
+    window's row need not equal a single token's bit for bit: rounds of draft and
+    verify over pages are not bit-identical to a loop of single tokens, as the
+    decoder's are.  A non-finite v of a new row may reach rows before it of the
+    same request."""
     torch = _torch()
     lib = load()
     kv, dev, T, Hq, Hkv, d, ldq = _cache_args(q, k_cache, v_cache)
