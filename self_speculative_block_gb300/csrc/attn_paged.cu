@@ -19,19 +19,27 @@
 // with one token a product of 128 rows takes less time than its keys do from HBM.
 //
 // What bounds it (12 q and 4 kv heads of 128, pages of 16, times on the device):
-//   few rows: HBM.  256 single tokens of 1,000 to 4,000 keys 181 us (6.1 TB/s, 90 % of a
+//   few rows: HBM.  256 single tokens of 1,000 to 4,000 keys 182 us (6.1 TB/s, 90 % of a
 //     copy's rate), 64 of 256 to 8,192 51 (4.8 TB/s: 7 us before the first keys are there, 4 for
 //     the join), a window of 33 behind 131,105 keys 56, one token over 1,097 keys 12;
-//   many rows: the tensor pipe.  A prompt of 16,384 rows 511 us (1.61 PFLOP/s, 83 % of
+//   many rows: the tensor pipe.  A prompt of 16,384 rows 513 us (1.61 PFLOP/s, 85 % of
 //     the library's product), two last chunks of 2,048 rows over 8,192 keys 133 (1.35);
 //     128 keys of two query tiles pass in 3,000 cycles, 2,590 of them products;
+//   heads of 64: the chain of a block of 64 keys (scores, maximum, exponentials, P V), as long
+//     as with heads of 128 for half the products: the prompt 435 us, two chunks 108, with the
+//     tensor pipe 37 % active, the special-function pipe 37 %, the issue slots 46 %;
 //   short requests: the chain of an item (Q, scores, softmax, P V, store), 3 us each:
-//     1,000 tokens of 16 to 400 keys 85 us.
-// The roles' code has to stay in the instruction cache: with waits of twenty sites
-// unrolled, rescaling unrolled and eight boxes a load unrolled (192 KB in all instead
-// of 55) two chunks' call took 207 us.  A part costs 0.5 KB a row, written and read: the
+//     1,000 tokens of 16 to 400 keys 84 us.
+// The roles' code has to stay in the instruction cache: with waits of twenty sites,
+// rescaling and eight boxes a load unrolled, three and a half times as much of it, two chunks'
+// call took 207 us (176 with the waits and the loads rolled up).  A part costs 0.5 KB a row, written and read: the
 // join of the two chunks' 302 parts is 15 us of 133, where cuts at unit boundaries only
 // would leave two thirds of the SMs idle in the second round of their 200 units.
+//
+// P is rounded to bf16 for its product, which runs at the tensor pipe's full rate so (tf32 would
+// halve it, and V would have to be widened first); its sum is taken
+// before the rounding, in fp32, as are scores, statistics and the parts.  Against 64 bits o is
+// off by 0.0021 to 0.0024 of its norm; the rounding of o alone makes 0.0017.
 #include "attn_packed.cuh"
 #include "paged.cuh"
 
@@ -125,9 +133,12 @@ __device__ __forceinline__ int last_key(const PagedArgs& a, const Req& q, int i)
   return a.draft && i > 0 ? q.kv - 1 : q.kv - q.n + i;
 }
 // Work of a unit, the two query tiles from token i on: 5 a key tile (3,000 cycles) and 16
-// for its beginning and end where both hold tokens (a prompt of 8,192 rows takes 159 us
-// with 10 for the ends, 154 with 16); 4 and 2 where one does, whose keys' way from HBM hides
-// most of the ends (2,480 cycles a tile; 64 single tokens take 54.3 us with 2, 57.5 with 10).
+// for its beginning and end where both hold tokens (a prompt of 8,192 rows takes 154.6 us
+// with 16 for the ends, 159.9 with 10); 4 and 2 where one does, whose keys' way from HBM hides
+// most of the ends (2,480 cycles a tile; 64 single tokens take 50.7 us with 2, 53.1 with 10).
+// Weighed with heads of 128; with heads of 64 the same: other ends, or 6 a key tile of two query
+// tiles, change two chunks (108.1 us), a prompt of 16,384 (437) and 64 tokens (33.9) by 1 % at
+// most, and 10 for single tiles' ends takes draft windows from 16.9 to 16.1 and chunks to 109.4.
 __device__ __forceinline__ bool two_tiles(const PagedArgs& a, const Req& q, int i) { return q.n - i > a.toks; }
 __device__ __forceinline__ int key_tiles(const PagedArgs& a, const Req& q, int i) {
   const int last = i < q.n ? last_key(a, q, min(i + 2 * a.toks, q.n) - 1) : -1;
@@ -815,9 +826,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 // the unit, then the first one of each CTA behind it.  A task is some columns (eight a
 // thread) of a unit's rows; warps share a task's parts where there are many.  A
 // thread has BATCH parts' loads in flight: 4 for short calls, which wait for one
-// chain of loads (one token 11.4 us with 4, 12.0 with 2), and 2 for long ones, whose
-// parts want the loads of four CTAs an SM (two chunks of 2,048 rows 143 us with 2,
-// 147 with 4).
+// chain of loads (one token 11.5 us with 4, 12.1 with 2), and 2 for long ones, whose
+// parts want the loads of four CTAs an SM (two chunks of 2,048 rows 133.2 us with 2,
+// 136.7 with 4).
 template <int D, int BATCH>
 __global__ void __launch_bounds__(JOIN_WARPS * 32, 8 / BATCH) attn_paged_join_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ int ends[256 + 1];  // tasks of the units before
@@ -827,8 +838,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 8 / BATCH) attn_paged_join_ke
   tc::grid_dep_wait();
   static_assert(GRID <= 256, "a thread takes a split");
   // Long calls read the counts first and a task's split later: 608 CTAs that read all
-  // splits wait for one another's cache lines (16 draft windows 20.8 -> 19.7 us); short
-  // ones would wait for one load more (one token 11.8 -> 12.1).
+  // splits wait for one another's cache lines (16 draft windows 21.4 us, 19.8 so); short
+  // ones would wait for one load more (64 tokens 51.3 us, 50.8 so).
   constexpr bool AHEAD = BATCH == 4;
   __shared__ Split splits[AHEAD ? GRID : 1];
   int count = 0;

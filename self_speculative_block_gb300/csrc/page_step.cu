@@ -10,7 +10,7 @@
 // in shared memory) and does its share of the rows, of the pages taken and of
 // those given back, finding the request of each by bisection.  A call is a chain of
 // loads, scans and bisections, whatever it moves: 16 windows of 33 rows 3.4 us, 64
-// prompts of 1,537 4.2, 1,000 requests of which a third shrink or end 6.6.
+// prompts of 1,537 4.4, 1,000 requests of which a third shrink or end 6.7.
 #include "paged.cuh"
 #include "tc.cuh"
 

@@ -40,8 +40,8 @@
         (a third [M]), causal attention over 15 packed sequences and over one
         of 8,192 rows, the cross entropy of 2,048 rows.
 
-    python -m self_speculative_block_gb300.profile_cases paged_kv
-        The paged KV cache at the 0.5B-class decoder's heads, each forward
+    python -m self_speculative_block_gb300.profile_cases paged_kv [head_dim]
+        The paged KV cache at the 0.5B-class decoder's heads (or as many of 64), each forward
         twice: single tokens of 64 requests of 256 to 8,131 keys, draft
         windows of 33 rows of 16 requests of 545 to 2,930 keys, the last
         chunks of 2,048 rows of two prompts of 8,192 (page step, write and
@@ -205,7 +205,7 @@ def train_ops_case(repeat: int = 2):
     gocr.op_status(dev)
 
 
-def paged_kv_case(repeat: int = 2):
+def paged_kv_case(head_dim: int = synth.BASE.head_dim, repeat: int = 2):
     import torch
     from . import gocr
     cfg, dev, ps = synth.BASE, torch.device("cuda:0"), 16
@@ -217,9 +217,9 @@ def paged_kv_case(repeat: int = 2):
                              ([8192, 8192], 2048, gocr.FWD_VERIFY)):
         R, T, width = len(lens), rows * len(lens), -(-max(lens) // ps)
         n_pages = sum(-(-n // ps) for n in lens)
-        cache = [torch.randn((n_pages, cfg.n_kv_heads, ps, cfg.head_dim), generator=g, device=dev).to(torch.bfloat16)
+        cache = [torch.randn((n_pages, cfg.n_kv_heads, ps, head_dim), generator=g, device=dev).to(torch.bfloat16)
                  for _ in range(2)]
-        qkv = torch.randn((T, cfg.n_q_heads + 2 * cfg.n_kv_heads, cfg.head_dim), generator=g, device=dev).to(torch.bfloat16)
+        qkv = torch.randn((T, cfg.n_q_heads + 2 * cfg.n_kv_heads, head_dim), generator=g, device=dev).to(torch.bfloat16)
         q, k, v = qkv.split((cfg.n_q_heads, cfg.n_kv_heads, cfg.n_kv_heads), 1)
         table = torch.full((R, width), -1, dtype=torch.int32, device=dev)
         free = torch.randperm(n_pages, generator=g, device=dev).to(torch.int32)
@@ -273,7 +273,7 @@ def main(argv):
     if what == "train_ops":
         train_ops_case()
     elif what == "paged_kv":
-        paged_kv_case()
+        paged_kv_case(*[int(x) for x in argv[2:3]])
     elif what == "draft":
         draft_case(int(argv[2]) if len(argv) > 2 else 32)
     elif what == "sweep":
